@@ -19,7 +19,8 @@ __all__ = [
     "FA_OK", "FA_ERR_INVALID", "FA_ERR_CUDA", "FA_ERR_DEVICE_TIMEOUT", "FA_ERR_UNSUPPORTED",
     "FA_ERR_TOO_LARGE", "FA_ERR_BAD_INPUT", "FaOptions", "FaPagedParams", "paged_attention",
     "fa_paged_attention", "fa_paged_attention_bwd", "fa_train_fwd_ex", "fa_train_bwd_ex", "make_options",
-    "FA_MASK_F32", "FA_MASK_BF16", "FA_MASK_BOOL",
+    "FA_MASK_F32", "FA_MASK_BF16", "FA_MASK_BOOL", "FaQ8Cache", "FaQ8Rows", "make_q8_cache",
+    "q8_cache_write", "q8_cache_read", "q8_paged_attention",
 ]
 
 FA_OK = 0
@@ -94,6 +95,41 @@ class FaParams(ctypes.Structure):
     ]
 
 
+class FaQ8Cache(ctypes.Structure):
+    """Mirror of `fa_q8_cache` in include/fa_train.h."""
+
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("scale_block", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class FaQ8Rows(ctypes.Structure):
+    """Mirror of `fa_q8_rows` in include/fa_train.h."""
+
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_stride", ctypes.c_int64 * 3),
+        ("v_stride", ctypes.c_int64 * 3),
+        ("cu_seqlens", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p),
+        ("lengths", ctypes.c_void_p),
+        ("batch", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("total", ctypes.c_int32),
+        ("new_len", ctypes.c_int32),
+    ]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -133,6 +169,14 @@ def load_library():
             lib.fa_paged_attention_bwd.argtypes = [vp, vp, vp, vp, vp, vp, fp, vp, vp, vp, vp,
                                                    vp, vp]
             lib.fa_paged_attention_bwd.restype = ctypes.c_int
+            pc, pr = ctypes.POINTER(FaQ8Cache), ctypes.POINTER(FaQ8Rows)
+            lib.fa_q8_cache_write.argtypes = [pc, pr, vp]
+            lib.fa_q8_cache_write.restype = ctypes.c_int
+            lib.fa_q8_cache_read.argtypes = [pc, pr, vp]
+            lib.fa_q8_cache_read.restype = ctypes.c_int
+            lib.fa_q8_paged_attention.argtypes = [vp, pc, vp, vp, vp, vp,
+                                                  ctypes.POINTER(FaPagedParams), vp]
+            lib.fa_q8_paged_attention.restype = ctypes.c_int
             lib.fa_device_status.argtypes = [ctypes.c_int]
             lib.fa_device_status.restype = ctypes.c_int
             lib.fa_error_string.argtypes = [ctypes.c_int]
@@ -323,7 +367,7 @@ def fa_device_status(clear: bool = True) -> int:
     return load_library().fa_device_status(int(bool(clear)))
 
 
-FA_NUM_KERNELS = 10
+FA_NUM_KERNELS = 14
 
 
 def fa_profile_enable(on: bool) -> None:
@@ -585,3 +629,194 @@ def varlen_attention_bwd(q, k, v, o, lse, dO, cu_q, cu_k, max_q, max_k, *, scale
                                         dsinks=dsinks, deterministic=deterministic)
     fa_train_bwd_ex(q, k, v, o, lse, dO, None, dq, dk, dv, params, opt, stream)
     return (dq, dk, dv) if sinks is None else (dq, dk, dv, dsinks)
+
+
+# ----------------------------------------------------------------- 8-bit key/value cache
+def make_q8_cache(num_pages, n_kv_heads, page_size, head_dim, scale_block=None, device="cuda"):
+    """An empty 8-bit paged cache: (k_cache, v_cache, k_scale, v_scale), codes float8_e4m3fn
+    [num_pages, Hk, page_size, d] and float32 scales [num_pages, Hk, page_size // scale_block]
+    (by default one scale for each page and head)."""
+    import torch
+
+    block = page_size if scale_block is None else int(scale_block)
+    if block < 1 or page_size % block:
+        raise ValueError("scale_block must divide page_size")
+    codes = [torch.zeros((num_pages, n_kv_heads, page_size, head_dim), dtype=torch.uint8,
+                         device=device).view(torch.float8_e4m3fn) for _ in range(2)]
+    scales = [torch.ones((num_pages, n_kv_heads, page_size // block), dtype=torch.float32,
+                         device=device) for _ in range(2)]
+    return (*codes, *scales)
+
+
+def _q8_need(ok, text):
+    if not ok:
+        raise ValueError(text)
+
+
+def _q8_device(*tensors):
+    """Every tensor must be on the current CUDA device (the one the kernels are launched on)."""
+    import torch
+
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -2
+    for t in tensors:
+        if t.get_device() != dev:
+            raise ValueError("the tensors must be on the current CUDA device")
+
+
+def _q8_cache(k_cache, v_cache, k_scale, v_scale) -> FaQ8Cache:
+    import torch
+
+    _q8_need(k_cache.dtype == v_cache.dtype == torch.float8_e4m3fn and k_cache.dim() == 4
+             and k_cache.shape == v_cache.shape,
+             "k_cache and v_cache must be float8_e4m3fn [num_pages, Hk, page_size, d]")
+    P, Hk, ps, d = k_cache.shape
+    _q8_need(k_scale.dtype == v_scale.dtype == torch.float32 and k_scale.shape == v_scale.shape
+             and k_scale.dim() == 3 and k_scale.shape[:2] == k_cache.shape[:2]
+             and k_scale.shape[2] > 0 and ps % k_scale.shape[2] == 0,
+             "k_scale and v_scale must be float32 [num_pages, Hk, page_size // scale_block]")
+    _q8_need(k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous()
+             and v_scale.is_contiguous(), "the cache's tensors must be contiguous")
+    return FaQ8Cache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                     v_scale.data_ptr(), P, Hk, ps, d, ps // k_scale.shape[2], 0)
+
+
+def _q8_index(t, shape, name):
+    import torch
+
+    _q8_need(t.dtype == torch.int32 and t.is_contiguous() and tuple(t.shape) == shape,
+             f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
+    return t.data_ptr()
+
+
+def _q8_stride(t, name):
+    """(sequence, head, row) strides of bf16 rows [B, Hk, n, d] or [Hk, total, d]: any with the
+    last dimension contiguous and the others multiples of 8 elements."""
+    import torch
+
+    st = [s if n > 1 else 0 for s, n in zip(t.stride(), t.shape)]
+    _q8_need(t.dtype == torch.bfloat16 and t.stride(-1) == 1 and not any(s % 8 for s in st[:-1]),
+             f"{name} must be bfloat16 with contiguous rows and strides that are multiples of 8")
+    return (ctypes.c_int64 * 3)(*((0, *st[:-1]) if t.dim() == 3 else st[:-1]))
+
+
+class _on_stream:
+    """The stream of a call: its handle, and a context in which new outputs belong to it."""
+
+    def __init__(self, stream):
+        import torch
+
+        now = torch.cuda.current_stream()
+        self.handle = now.cuda_stream if stream is None else int(
+            getattr(stream, "cuda_stream", stream))
+        self.ctx = None
+        if self.handle != now.cuda_stream:
+            self.ctx = torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                                         else torch.cuda.ExternalStream(self.handle))
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def q8_cache_write(k, v, k_cache, v_cache, k_scale, v_scale, block_table, lengths, *,
+                   cu_seqlens=None, stream=None) -> None:
+    """Quantise new keys and values into an 8-bit paged cache, in place. k, v: bf16
+    [B, Hk, n, d], n new rows for each sequence, or with cu_seqlens (int32 [B + 1]) packed
+    [Hk, total, d]; any strides with contiguous rows. `lengths` (int32 [B]) counts each sequence's
+    keys with the new rows, which become its last positions; block_table is int32 [B, max_pages].
+    A page written to must belong to one sequence of the call. See fa_q8_cache_write in
+    include/fa_train.h for the rounding and the scales."""
+    cache = _q8_cache(k_cache, v_cache, k_scale, v_scale)
+    _q8_need(block_table.dim() == 2, "block_table must be [B, max_pages]")
+    B, per = block_table.shape
+    rows = FaQ8Rows(k.data_ptr(), v.data_ptr(), _q8_stride(k, "k"), _q8_stride(v, "v"), None,
+                    _q8_index(block_table, (B, per), "block_table"),
+                    _q8_index(lengths, (B,), "lengths"), B, per, 0, 0)
+    _q8_need(k.shape == v.shape, "k and v must have the same shape")
+    if cu_seqlens is None:
+        n = k.shape[2] if k.dim() == 4 else -1
+        _q8_need(tuple(k.shape) == (B, cache.n_kv_heads, n, cache.head_dim),
+                 "k and v must be [B, Hk, n, d]")
+        if n == 0:
+            return
+        rows.new_len = n
+        _q8_device(k, v, k_cache, v_cache, k_scale, v_scale, block_table, lengths)
+    else:
+        n = k.shape[1] if k.dim() == 3 else -1
+        _q8_need(tuple(k.shape) == (cache.n_kv_heads, n, cache.head_dim),
+                 "packed k and v must be [Hk, total, d]")
+        if n == 0:
+            return
+        rows.total = n
+        rows.cu_seqlens = _q8_index(cu_seqlens, (B + 1,), "cu_seqlens")
+        _q8_device(k, v, k_cache, v_cache, k_scale, v_scale, block_table, lengths, cu_seqlens)
+    with _on_stream(stream) as handle:
+        rc = load_library().fa_q8_cache_write(ctypes.byref(cache), ctypes.byref(rows), handle)
+    if rc:
+        raise FaError(rc, "fa_q8_cache_write")
+
+
+def q8_cache_read(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, total, *, out=None,
+                  stream=None):
+    """The keys and values of a batch back from an 8-bit paged cache: (k, v), bf16
+    [Hk, total, d], packed as varlen_attention_fwd takes them. Sequence b's rows
+    cu_seqlens[b] .. cu_seqlens[b + 1] - 1 are its first keys. `out`: a pair of such tensors of
+    any strides with contiguous rows (rows behind cu_seqlens[B] are left as they were)."""
+    import torch
+
+    cache = _q8_cache(k_cache, v_cache, k_scale, v_scale)
+    _q8_need(block_table.dim() == 2, "block_table must be [B, max_pages]")
+    B, per = block_table.shape
+    shape = (cache.n_kv_heads, int(total), cache.head_dim)
+    table = _q8_index(block_table, (B, per), "block_table")
+    cu = _q8_index(cu_seqlens, (B + 1,), "cu_seqlens")
+    _q8_device(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens)
+    with _on_stream(stream) as handle:
+        k, v = out if out is not None else (
+            torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device) for _ in range(2))
+        if out is not None:
+            _q8_need(tuple(k.shape) == tuple(v.shape) == shape, "out must be two [Hk, total, d]")
+            _q8_device(k, v)
+        if shape[1] == 0:
+            return k, v
+        rows = FaQ8Rows(k.data_ptr(), v.data_ptr(), _q8_stride(k, "k"), _q8_stride(v, "v"), cu,
+                        table, None, B, per, shape[1], 0)
+        rc = load_library().fa_q8_cache_read(ctypes.byref(cache), ctypes.byref(rows), handle)
+    if rc:
+        raise FaError(rc, "fa_q8_cache_read")
+    return k, v
+
+
+def q8_paged_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, lengths, *, scale,
+                       causal=True, stream=None):
+    """paged_attention over an 8-bit paged cache: q bf16 [B, H, q_len, d], codes float8_e4m3fn
+    [num_pages, Hk, page_size, d] with float32 scales [num_pages, Hk, page_size // scale_block],
+    block_table [B, max_pages] and lengths [B] (int32): returns (o, lse). The q_len queries are
+    each sequence's last positions (causal: bottom-right per sequence)."""
+    import torch
+
+    cache = _q8_cache(k_cache, v_cache, k_scale, v_scale)
+    _q8_need(q.dtype == torch.bfloat16 and q.dim() == 4 and q.is_contiguous()
+             and q.shape[3] == cache.head_dim, "q must be contiguous bfloat16 [B, H, q_len, d]")
+    B, H, lq, d = q.shape
+    _q8_need(block_table.dim() == 2, "block_table must be [B, max_pages]")
+    per = block_table.shape[1]
+    table = _q8_index(block_table, (B, per), "block_table")
+    lens = _q8_index(lengths, (B,), "lengths")
+    _q8_device(q, k_cache, v_cache, k_scale, v_scale, block_table, lengths)
+    params = FaPagedParams(B, H, cache.n_kv_heads, lq, d, cache.page_size, per, cache.num_pages,
+                           float(scale), int(bool(causal)), 0, 0)
+    with _on_stream(stream) as handle:
+        o = torch.empty_like(q)
+        lse = torch.empty((B, H, lq), dtype=torch.float32, device=q.device)
+        rc = load_library().fa_q8_paged_attention(q.data_ptr(), ctypes.byref(cache), table, lens,
+                                                  o.data_ptr(), lse.data_ptr(),
+                                                  ctypes.byref(params), handle)
+    if rc:
+        raise FaError(rc, "fa_q8_paged_attention")
+    return o, lse

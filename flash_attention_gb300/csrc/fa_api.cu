@@ -292,6 +292,10 @@ const char* fa_kernel_name(int id) {
     case FA_KERNEL_PAGED_DECODE_BWD: return "paged_decode_bwd_kernel";
     case FA_KERNEL_BWD_MAIN: return "bwd_main_kernel";
     case FA_KERNEL_BWD_DQ: return "bwd_dq_kernel";
+    case FA_KERNEL_Q8_WRITE: return "q8_write_kernel";
+    case FA_KERNEL_Q8_READ: return "q8_read_kernel";
+    case FA_KERNEL_Q8_ATTN: return "q8_attn_kernel";
+    case FA_KERNEL_Q8_COMBINE: return "q8_combine_kernel";
     default: return "unknown";
   }
 }
@@ -750,6 +754,142 @@ int fa_paged_attention_bwd(const void* q, const void* k_cache, const void* v_cac
   if ((e = cudaFreeAsync(ws, s)) != cudaSuccess)
     return cuda_fail(e, "cudaFreeAsync (paged backward workspace)");
   return FA_OK;
+}
+
+// ---------------------------------------------------------------- 8-bit key/value cache
+static int log2_of(int x) {
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
+
+static int check_q8_cache(const fa_q8_cache* c) {
+  if (!c) return FA_ERR_INVALID;
+  const int ps = c->page_size, sb = c->scale_block;
+  if (c->num_pages <= 0 || c->n_kv_heads <= 0 || c->reserved != 0) return FA_ERR_INVALID;
+  if ((int64_t)c->num_pages * c->n_kv_heads > INT32_MAX / 2) return FA_ERR_INVALID;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return FA_ERR_INVALID;
+  if (ps < 8 || ps > 256 || (ps & (ps - 1))) return FA_ERR_INVALID;
+  if (sb < 1 || sb > ps || (sb & (sb - 1))) return FA_ERR_INVALID;
+  if (!c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16)) return FA_ERR_INVALID;
+  if (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+    return FA_ERR_INVALID;
+  return FA_OK;
+}
+
+// Checks of fa_q8_cache_write (with lengths) and fa_q8_cache_read, and the kernels' arguments.
+static int prepare_q8_rows(const fa_q8_cache* c, const fa_q8_rows* r, bool write,
+                           fa::Q8RowsArgs* a) {
+  int rc = check_q8_cache(c);
+  if (rc) return rc;
+  if (!r || r->batch <= 0 || r->max_pages <= 0) return FA_ERR_INVALID;
+  if ((int64_t)r->max_pages * c->page_size > kMaxLen) return FA_ERR_INVALID;
+  if (!r->block_table || !aligned(r->block_table, 4)) return FA_ERR_INVALID;
+  if (write ? (!r->lengths || !aligned(r->lengths, 4)) : r->lengths != nullptr)
+    return FA_ERR_INVALID;
+  if (r->cu_seqlens) {
+    if (!aligned(r->cu_seqlens, 4) || r->total < 0 || r->new_len != 0) return FA_ERR_INVALID;
+  } else if (!write || r->total != 0 || r->new_len < 1 || r->new_len > kMaxLen) {
+    return FA_ERR_INVALID;
+  }
+  if ((rc = check_bf16(r->k)) || (rc = check_bf16(r->v))) return rc;
+  for (int i = 0; i < 3; ++i)
+    if (r->k_stride[i] < 0 || r->v_stride[i] < 0 || r->k_stride[i] % 8 || r->v_stride[i] % 8)
+      return FA_ERR_INVALID;
+  a->codes[0] = c->k;
+  a->codes[1] = c->v;
+  a->scales[0] = c->k_scale;
+  a->scales[1] = c->v_scale;
+  a->rows[0] = r->k;
+  a->rows[1] = r->v;
+  for (int w = 0; w < 2; ++w) {
+    const int64_t* st = w ? r->v_stride : r->k_stride;
+    a->st_b[w] = st[0];
+    a->st_h[w] = st[1];
+    a->st_r[w] = st[2];
+  }
+  a->cu = r->cu_seqlens;
+  a->table = r->block_table;
+  a->lens = r->lengths;
+  a->B = r->batch;
+  a->Hk = c->n_kv_heads;
+  a->d = c->head_dim;
+  a->total = r->total;
+  a->new_len = r->new_len;
+  a->max_pages = r->max_pages;
+  a->num_pages = c->num_pages;
+  a->ps_shift = log2_of(c->page_size);
+  a->sb_shift = log2_of(c->scale_block);
+  if (fa::q8_rows_items(*a) > INT32_MAX) return FA_ERR_INVALID;
+  return FA_OK;
+}
+
+static int q8_rows_call(const fa_q8_cache* cache, const fa_q8_rows* rows, bool write,
+                        void* stream) {
+  fa::Q8RowsArgs a;
+  int rc = prepare_q8_rows(cache, rows, write, &a);
+  if (rc) return rc;
+  if ((rc = check_device())) return rc;
+  if (a.cu && a.total == 0) return FA_OK;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  cudaError_t e = device_status_word(dev, &a.status);
+  if (e != cudaSuccess) return cuda_fail(e, "status word");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  e = write ? fa::launch_q8_write(a, s) : fa::launch_q8_read(a, s);
+  return e == cudaSuccess ? FA_OK : cuda_fail(e, write ? "cache write launch" : "cache read launch");
+}
+
+int fa_q8_cache_write(const fa_q8_cache* cache, const fa_q8_rows* rows, void* stream) {
+  return q8_rows_call(cache, rows, true, stream);
+}
+
+int fa_q8_cache_read(const fa_q8_cache* cache, const fa_q8_rows* rows, void* stream) {
+  return q8_rows_call(cache, rows, false, stream);
+}
+
+int fa_q8_paged_attention(const void* q, const fa_q8_cache* cache, const int32_t* block_table,
+                          const int32_t* lengths, void* o, float* lse, const fa_paged_params* p,
+                          void* stream) {
+  int rc;
+  if ((rc = check_q8_cache(cache))) return rc;
+  if ((rc = check_paged(p, q, cache->k, cache->v, block_table, lengths)) || (rc = check_bf16(o)))
+    return rc;
+  if (lse && !aligned(lse, 4)) return FA_ERR_INVALID;
+  if (p->n_kv_heads != cache->n_kv_heads || p->head_dim != cache->head_dim ||
+      p->page_size != cache->page_size || p->num_pages != cache->num_pages || p->num_splits != 0)
+    return FA_ERR_INVALID;
+  if ((int64_t)p->batch * p->n_heads * p->q_len > INT32_MAX / 2) return FA_ERR_INVALID;
+  if ((rc = check_device())) return rc;
+  fa::Q8AttnArgs a;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  cudaError_t e = device_status_word(dev, &a.status);
+  if (e != cudaSuccess) return cuda_fail(e, "status word");
+  a.q = q;
+  a.k = static_cast<const uint8_t*>(cache->k);
+  a.v = static_cast<const uint8_t*>(cache->v);
+  a.k_scale = cache->k_scale;
+  a.v_scale = cache->v_scale;
+  a.table = block_table;
+  a.lens = lengths;
+  a.o = o;
+  a.lse = lse;
+  a.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  a.B = p->batch;
+  a.H = p->n_heads;
+  a.Hk = p->n_kv_heads;
+  a.G = p->n_heads / p->n_kv_heads;
+  a.lq = p->q_len;
+  a.d = p->head_dim;
+  a.max_pages = p->max_pages;
+  a.num_pages = p->num_pages;
+  a.causal = p->causal;
+  a.ps_shift = log2_of(p->page_size);
+  a.sb_shift = log2_of(cache->scale_block);
+  a.scale = p->scale;
+  e = fa::launch_q8_attn(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail(e, "8-bit paged attention launch");
 }
 
 int fa_device_status(int clear) {

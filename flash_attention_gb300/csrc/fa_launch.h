@@ -47,7 +47,11 @@ enum KernelId {
   kKernPagedGather = 7,
   kKernPagedScatter = 8,
   kKernPagedDecodeBwd = 9,
-  kNumKernels = 10
+  kKernQ8Write = 10,
+  kKernQ8Read = 11,
+  kKernQ8Attn = 12,
+  kKernQ8Combine = 13,
+  kNumKernels = 14
 };
 
 // Records a timing event before (end = 0) or after (end = 1) a launch on `s` when timing is
@@ -305,5 +309,41 @@ cudaError_t launch_paged_scatter(const PagedGradArgs& a, cudaStream_t stream);
 bool paged_decode_path(int G, int lq);
 cudaError_t launch_paged_decode_bwd(const PagedGradArgs& a, float* dq_acc, float scale,
                                     cudaStream_t stream);
+
+// The 8-bit key/value cache: writer and reader (fa_q8_cache.cu). Index 0 is K, 1 is V.
+struct Q8RowsArgs {
+  void* codes[2];        // e4m3 [num_pages, Hk, page_size, d]
+  float* scales[2];      // [num_pages, Hk, page_size / scale_block]
+  void* rows[2];         // bf16 rows, written to the cache or read back from it
+  long long st_b[2], st_h[2], st_r[2];  // their strides (sequence, head, row) in elements
+  const int32_t* cu;     // packed batch: [B + 1] row offsets, or nullptr: new_len rows each
+  const int32_t* table;  // [B, max_pages]
+  const int32_t* lens;   // [B] (writer: lengths with the new rows)
+  int* status;
+  int B, Hk, d, total, new_len, max_pages, num_pages;
+  int ps_shift, sb_shift;  // log2 of page_size and scale_block
+};
+long long q8_rows_items(const Q8RowsArgs& a);  // warps of a launch, at most
+cudaError_t launch_q8_write(const Q8RowsArgs& a, cudaStream_t stream);
+cudaError_t launch_q8_read(const Q8RowsArgs& a, cudaStream_t stream);
+
+// Attention over the 8-bit cache (fa_q8_attn.cu).
+struct Q8AttnArgs {
+  const void* q;         // bf16 [B, H, lq, d]
+  const uint8_t* k;      // e4m3 codes and scales, as in Q8RowsArgs
+  const uint8_t* v;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* table;  // [B, max_pages]
+  const int32_t* lens;   // [B]
+  void* o;               // bf16 [B, H, lq, d]
+  float* lse;            // [B, H, lq] or nullptr
+  int* status;
+  uint64_t wait_limit_ns;
+  int B, H, Hk, G, lq, d, max_pages, num_pages, causal;
+  int ps_shift, sb_shift;
+  float scale;
+};
+cudaError_t launch_q8_attn(const Q8AttnArgs& a, cudaStream_t stream);
 
 }  // namespace fa

@@ -220,7 +220,11 @@ int fa_train_bwd(const void* q, const void* k, const void* v, const void* o, con
 #define FA_KERNEL_PAGED_GATHER 7  /* fa_paged_attention_bwd: packed K, V, q side / page owners */
 #define FA_KERNEL_PAGED_SCATTER 8 /* fa_paged_attention_bwd: cache gradients completed, dq */
 #define FA_KERNEL_PAGED_DECODE_BWD 9 /* fa_paged_attention_bwd, few rows: the gradient kernel */
-#define FA_NUM_KERNELS 10
+#define FA_KERNEL_Q8_WRITE 10   /* fa_q8_cache_write */
+#define FA_KERNEL_Q8_READ 11    /* fa_q8_cache_read */
+#define FA_KERNEL_Q8_ATTN 12    /* fa_q8_paged_attention */
+#define FA_KERNEL_Q8_COMBINE 13 /* merge of the key ranges of fa_q8_paged_attention */
+#define FA_NUM_KERNELS 14
 
 /* Turns timing on (1) or off (0). Returns FA_OK. */
 int fa_profile_enable(int on);
@@ -351,6 +355,80 @@ int fa_paged_attention_bwd(const void* q, const void* k_cache, const void* v_cac
                            const int32_t* block_table, const int32_t* lengths, const void* o,
                            const float* lse, const void* dO, void* dq, void* dk_cache,
                            void* dv_cache, const fa_paged_params* p, void* stream);
+
+/* ------------------------------------------------------------------ 8-bit key/value cache
+ * The paged cache in 8 bits: e4m3 codes and one f32 scale for each block of scale_block slots of
+ * a page and each head; a code c with the scale s stands for c * s. Half the bytes of the bf16
+ * cache, for the calls that are bound by them: fa_q8_cache_write quantises new keys and values
+ * into it, fa_q8_paged_attention attends over it (decode and cached prefill), fa_q8_cache_read
+ * reads a batch's keys and values back as bf16, packed as the variable-length batch of
+ * fa_train_fwd_ex takes them (a long prompt against what is cached). No counterpart on the
+ * pages.
+ *
+ * Scales must be finite and > 0 wherever a key is read; what the slots past a sequence's end
+ * hold (codes and scales, NaN included) reaches no result. */
+typedef struct fa_q8_cache {
+  void* k;              /* e4m3 [num_pages, n_kv_heads, page_size, head_dim], 16-byte aligned */
+  void* v;              /* same */
+  float* k_scale;       /* f32 [num_pages, n_kv_heads, page_size / scale_block], 4-byte aligned */
+  float* v_scale;       /* same */
+  int32_t num_pages;    /* >= 1 */
+  int32_t n_kv_heads;   /* >= 1; num_pages * n_kv_heads < 2^30 */
+  int32_t page_size;    /* a power of two in [8, 256] */
+  int32_t head_dim;     /* 64, 128 or 256 */
+  int32_t scale_block;  /* a power of two in [1, page_size] */
+  int32_t reserved;     /* must be 0 */
+} fa_q8_cache;
+
+/* Rows of keys and values, bf16: row i of head h is at h * stride[1] + i * stride[2] elements
+ * (packed: cu_seqlens non-NULL, sequence b owns the rows cu_seqlens[b] .. cu_seqlens[b+1] - 1 of
+ * `total`), or for sequence b at b * stride[0] + h * stride[1] + i * stride[2] (cu_seqlens NULL:
+ * every sequence has `new_len` rows). The head_dim elements of a row are contiguous; strides are
+ * multiples of 8 elements and k, v are 16-byte aligned, so views into a larger tensor (a fused
+ * projection's output) serve as they are. */
+typedef struct fa_q8_rows {
+  void* k;
+  void* v;
+  int64_t k_stride[3];
+  int64_t v_stride[3];
+  const int32_t* cu_seqlens;  /* NULL, or int32 [batch + 1] on the device, 4-byte aligned */
+  const int32_t* block_table; /* int32 [batch, max_pages] on the device, 4-byte aligned */
+  const int32_t* lengths;     /* writer: int32 [batch] on the device; reader: NULL */
+  int32_t batch;              /* >= 1 */
+  int32_t max_pages;          /* columns of the table; max_pages * page_size <= 2^22 */
+  int32_t total;              /* packed: rows for each head, >= 0; otherwise 0 */
+  int32_t new_len;            /* not packed: rows of each sequence, >= 1; packed: 0 */
+} fa_q8_rows;
+
+/* Quantises new rows into the cache. lengths[b] counts the sequence's keys with the new rows: its
+ * n rows become the positions lengths[b] - n .. lengths[b] - 1 (those below 0 are left out, so a
+ * padded entry of length 0 writes nothing). For each scale block that gets a new row, with a the
+ * largest finite |x| of its new rows, s = 2^k with the smallest k >= -100 for which a <= 448 s;
+ * where the block holds earlier tokens of the sequence, s is not below the scale it had, and if
+ * it is above, their codes c become e4m3(c * (old scale / s)). New codes are e4m3(x / s) (nearest,
+ * ties to even; NaN for values that are not finite). Slots at and behind lengths[b] keep their
+ * codes. A page that a call writes must belong to one sequence of the call (pages that are only
+ * read, such as a shared prefix, may be shared). Not checked: two sequences writing one slot race.
+ * The table, lengths and offsets are checked on the device: a sequence whose length is outside
+ * [0, max_pages * page_size] is not written, rows of a page outside the cache are left out,
+ * offsets out of range are clamped, and each makes fa_device_status return FA_ERR_BAD_INPUT.
+ * Every output bit is determined by the inputs. Returns FA_OK, FA_ERR_INVALID,
+ * FA_ERR_UNSUPPORTED or FA_ERR_CUDA. */
+int fa_q8_cache_write(const fa_q8_cache* cache, const fa_q8_rows* rows, void* stream);
+
+/* Reads the first cu_seqlens[b+1] - cu_seqlens[b] keys and values of every sequence back:
+ * bf16(code * scale) into rows->k and rows->v (packed: cu_seqlens is required). Rows of `total`
+ * behind cu_seqlens[batch] are left as they were. Rows of a page outside the cache or past the
+ * table's end become 0 and make fa_device_status return FA_ERR_BAD_INPUT. */
+int fa_q8_cache_read(const fa_q8_cache* cache, const fa_q8_rows* rows, void* stream);
+
+/* fa_paged_attention over the 8-bit cache: same q, block_table, lengths, o, lse, params and
+ * checks (p's n_kv_heads, head_dim, page_size and num_pages must equal the cache's, num_splits
+ * must be 0). Sums and softmax statistics are f32. A query row with an element that is not finite
+ * gives NaN. */
+int fa_q8_paged_attention(const void* q, const fa_q8_cache* cache, const int32_t* block_table,
+                          const int32_t* lengths, void* o, float* lse, const fa_paged_params* p,
+                          void* stream);
 
 /* ------------------------------------------------------------------ bounded waits, diagnostics
  * Sets the limit of one barrier wait inside the kernels launched after this call, from any
