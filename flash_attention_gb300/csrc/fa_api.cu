@@ -86,6 +86,21 @@ bool encode_bf16_3d(CUtensorMap* m, const void* base, int bh, int rows, int d, i
   return r == CUDA_SUCCESS;
 }
 
+// 3-D map over the bytes of a contiguous [bh, rows, d] tensor of 8-bit codes, box (cols, box_rows,
+// 1), rows of cols = 64 or 128 bytes swizzled by their width; reads outside fill with zeros.
+bool encode_u8_3d(CUtensorMap* m, const void* base, int bh, int rows, int d, int cols,
+                  int box_rows) {
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)bh};
+  cuuint64_t strides[2] = {(cuuint64_t)d, (cuuint64_t)rows * (cuuint64_t)d};
+  cuuint32_t box[3] = {(cuuint32_t)cols, (cuuint32_t)box_rows, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims,
+                        strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // The tile map of a q-side or kv-side tensor: 3-D (d, rows, batch * heads) in the default
 // layout, 4-D in the bshd layout (the kernels issue the matching load form).
 bool encode_bf16_map(CUtensorMap* m, const void* base, int d, int rows, int heads, int batch,
@@ -861,10 +876,12 @@ int fa_q8_paged_attention(const void* q, const fa_q8_cache* cache, const int32_t
     return FA_ERR_INVALID;
   if ((int64_t)p->batch * p->n_heads * p->q_len > INT32_MAX / 2) return FA_ERR_INVALID;
   if ((rc = check_device())) return rc;
+  cudaError_t e = get_encoder();
+  if (e != cudaSuccess) return cuda_fail(e, "cuTensorMapEncodeTiled entry point");
   fa::Q8AttnArgs a;
   int dev = 0;
   cudaGetDevice(&dev);
-  cudaError_t e = device_status_word(dev, &a.status);
+  e = device_status_word(dev, &a.status);
   if (e != cudaSuccess) return cuda_fail(e, "status word");
   a.q = q;
   a.k = static_cast<const uint8_t*>(cache->k);
@@ -888,8 +905,21 @@ int fa_q8_paged_attention(const void* q, const fa_q8_cache* cache, const int32_t
   a.ps_shift = log2_of(p->page_size);
   a.sb_shift = log2_of(cache->scale_block);
   a.scale = p->scale;
-  e = fa::launch_q8_attn(a, static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? FA_OK : cuda_fail(e, "8-bit paged attention launch");
+  if (fa::q8_attn_units(a) > INT32_MAX) return FA_ERR_INVALID;
+  fa::Q8AttnMaps m;
+  const int cols = fa::q8_box_cols(a.d), box = fa::q8_box_rows(p->page_size);
+  if (!encode_u8_3d(&m.k, a.k, a.num_pages * a.Hk, p->page_size, a.d, cols, box) ||
+      !encode_u8_3d(&m.v, a.v, a.num_pages * a.Hk, p->page_size, a.d, cols, box))
+    return cuda_fail(cudaErrorInvalidValue, "cuTensorMapEncodeTiled");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  void* ws = nullptr;
+  if ((e = cudaMallocAsync(&ws, fa::q8_attn_workspace_bytes(a), s)) != cudaSuccess)
+    return cuda_fail(e, "cudaMallocAsync (8-bit paged attention workspace)");
+  e = fa::launch_q8_attn(a, m, ws, s);
+  const cudaError_t e2 = cudaFreeAsync(ws, s);
+  if (e != cudaSuccess) return cuda_fail(e, "8-bit paged attention launch");
+  if (e2 != cudaSuccess) return cuda_fail(e2, "cudaFreeAsync (8-bit paged attention workspace)");
+  return FA_OK;
 }
 
 int fa_device_status(int clear) {

@@ -344,6 +344,14 @@ struct Q8AttnArgs {
   int ps_shift, sb_shift;
   float scale;
 };
-cudaError_t launch_q8_attn(const Q8AttnArgs& a, cudaStream_t stream);
+struct Q8AttnMaps {
+  CUtensorMap k, v;  // the codes as [num_pages * Hk, page_size, d] bytes
+};
+int q8_box_rows(int page_size);
+int q8_box_cols(int head_dim);
+long long q8_attn_units(const Q8AttnArgs& a);  // CTAs of the joining kernel
+size_t q8_attn_workspace_bytes(const Q8AttnArgs& a);
+cudaError_t launch_q8_attn(const Q8AttnArgs& a, const Q8AttnMaps& m, void* ws,
+                           cudaStream_t stream);
 
 }  // namespace fa

@@ -6,9 +6,35 @@
 // j iff j < len (and, with the causal rule, j <= len - q_len + i). O = softmax(scale q k^T) v and
 // L = log sum exp; a query that sees no key gives O = 0 and L = -inf.
 //
-// The plainest form: one CTA for each query row, a warp for each key in turn (a lane holds
-// d / 32 columns), an online softmax in each warp, the warps joined in shared memory.
+// Decoding reads every code once, so HBM bounds it; 152 SMs at the measured copy rate take in
+// 23 codes a clock each, too many to widen them on the CUDA cores first. The tensor cores read
+// the codes as they are (tcgen05 kind::f8f6f4), and the bf16 and f32 operands that meet them are
+// split into 8-bit pieces, which cost only columns of an otherwise empty tile:
+//  * q (8 significant bits) = hi + lo / 16, both e4m3 (4 bits each, hi the nearest), after a power
+//    of two for each row that puts its largest element into [128, 256). Exact, except that
+//    elements 2^-14 below the row's largest lose what is under 2^-22 of it.
+//  * a softmax weight = p1 + p2 / 8 + p3 / 64, all e5m2 (3 bits each): 9 bits, and with e5m2's
+//    range weights down to 2^-35 of the row's largest still count, as they do when a key that
+//    takes nearly all of the weight has thousands of small ones beside it.
+// S^T = K q^T has the keys as the M = 128 rows of a tile and R query rows as 2 R columns: a thread
+// owns a key, whose two scales are then the thread's constants, and sees the R scores of it.
+// O^T = V^T w^T has the head dim as M (V is read transposed, MN-major) and 3 R columns; the value
+// scale is part of the weight: w = exp2(score + log2(v_scale) - m), m the running maximum of that
+// sum, so that neither the weights nor O lose range whatever the scales are; the softmax's sum
+// takes w / v_scale.
+//
+// Work: the (sequence, kv head, block of R rows) units, each ceil(len / 128) key tiles, form one
+// list of tiles, cut evenly over persistent CTAs (the lengths are on the device; each CTA finds
+// its part from them). A CTA writes the units it has whole; of the others it leaves its share's
+// O, m and sum, which a second kernel joins in the order of the keys.
+//
+// Warps of a CTA: 0-3 softmax (thread = key of the tile, and head-dim row of O^T), 4 TMA copies of
+// K and V pages (boxes of min(page_size, 128) rows), 5 issues S^T, 6 O^T (and zeroes what a last
+// page holds behind the sequence's end, so that NaN there meets no weight), 7 splits q, 8 fetches
+// the scales. All waits on barriers are bounded.
 #include <float.h>
+
+#include <algorithm>
 
 #include "fa_common.cuh"
 #include "fa_launch.h"
@@ -17,92 +43,940 @@
 namespace fa {
 
 namespace {
-constexpr int kWarps = 8;
+constexpr int kKT = 128;          // keys of a tile (the MMA M of S^T)
+constexpr int kScRing = 2;        // tiles of scales in shared memory
+constexpr int kPageChunk = 128;   // block-table entries staged at a time
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRise = 3.0f;     // m follows a score that is this far (base 2) above it
+constexpr float kWeight = 4096.0f;  // weights are at most 2^3; e5m2 ends at 57344
 
-template <int HD>
-__global__ void __launch_bounds__(kWarps * 32) q8_attn_kernel(const Q8AttnArgs p) {
-  constexpr int CPL = HD / 32;  // columns of a lane
-  __shared__ float acc_s[kWarps][HD], m_s[kWarps], l_s[kWarps];
-  const int warp = warp_id(), lane = lane_id();
-  const long long row = blockIdx.x;  // (b * H + h) * lq + i
-  const int i = (int)(row % p.lq), h = (int)(row / p.lq % p.H), b = (int)(row / p.lq / p.H);
-  const int kh = h / p.G;
-  const int ps = 1 << p.ps_shift;
-  const long long cap = (long long)p.max_pages * ps;
+// R query rows of a unit at a time; ST stages in each of the K and V rings; CTAS per SM.
+template <int HD, int R_>
+struct Q8Layout {
+  static constexpr int R = R_;
+  static constexpr int CTAS = (R == 8 && HD <= 128) ? 2 : 1;
+  static constexpr int ST = HD == 64 ? (CTAS == 2 ? 5 : 6) : HD == 128 ? (CTAS == 2 ? 3 : 5)
+                                                                     : (R == 8 ? 3 : 2);
+  static constexpr int CH = HD <= 128 ? HD : 128;   // columns (bytes) of a swizzled row
+  static constexpr int KCH = HD / CH;               // row chunks: 1, or 2 at head_dim 256
+  static constexpr int NS = 2 * R;                  // columns of S^T: hi rows, lo rows
+  static constexpr int NP = 4 * R;                  // columns of O^T: three pieces, one unused
+  static constexpr int KV_BYTES = kKT * HD;
+  static constexpr int Q_BYTES = NS * HD;
+  static constexpr int P_BYTES = kKT * NP;
+  static constexpr int OFF_K = 0;
+  static constexpr int OFF_V = OFF_K + ST * KV_BYTES;
+  static constexpr int OFF_Q = OFF_V + ST * KV_BYTES;
+  static constexpr int OFF_P = OFF_Q + 2 * Q_BYTES;
+  static constexpr int SMEM_BYTES = OFF_P + 2 * P_BYTES + 1024;
+  static constexpr int COL_S = 0;                   // two S^T buffers, then O^T
+  static constexpr int COL_O = 2 * NS;
+  static constexpr int TMEM_USED = COL_O + KCH * NP;
+  static constexpr int TMEM_COLS = TMEM_USED <= 64 ? 64 : TMEM_USED <= 128 ? 128
+                                   : TMEM_USED <= 256 ? 256 : 512;
+  static constexpr int THREADS = 288;
+  static constexpr int TMA_WARP = 4, S_WARP = 5, O_WARP = 6, Q_WARP = 7, SC_WARP = 8;
+  static_assert(TMEM_USED <= 512 && TMEM_COLS * CTAS <= 512, "TMEM budget");
+  // dynamic, static (pages, scales, barriers, rows: below) and the driver's 1 KB
+  static constexpr int STATIC_BYTES = 4 * kPageChunk + 8 * kScRing * kKT + 64 * R + 512;
+  static_assert((SMEM_BYTES + STATIC_BYTES + 1024) * CTAS <= 228 * 1024, "shared memory budget");
+};
+
+// Swizzle of a row of W bytes (W = 32, 64 or 128): the 16-byte chunk c of row r lies at chunk
+// swz(c, r). (The swizzle XORs address bits 4.. with bits 7.., and tiles start on its period.)
+template <int W>
+__device__ __forceinline__ int swz(int c, int r) {
+  return c ^ (W == 128 ? (r & 7) : W == 64 ? ((r >> 1) & 3) : ((r >> 2) & 1));
+}
+// Descriptor of an operand of rows of W bytes, swizzled by W: the next 8 rows are 8 W away, the
+// next W-byte chunk (where there is one) `lbo`.
+template <int W>
+__device__ __forceinline__ Desc q8_desc(uint32_t saddr, uint32_t lbo) {
+  const uint64_t mode = W == 128 ? 2 : W == 64 ? 4 : 6;
+  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)((8 * W) >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= mode << 61;
+  return Desc{static_cast<uint32_t>(d), static_cast<uint32_t>(d >> 32)};
+}
+// Instruction descriptor, kind::f8f6f4, f32 accumulator; formats: 0 e4m3, 1 e5m2.
+constexpr uint32_t idesc_f8(int a_fmt, int b_fmt, int M, int N, int a_mn, int b_mn) {
+  return (1u << 4) | ((uint32_t)a_fmt << 7) | ((uint32_t)b_fmt << 10) | ((uint32_t)a_mn << 15) |
+         ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint32_t a_lo, uint32_t a_hi,
+                                       uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 ad, bd;\n setp.ne.b32 p, %6, 0;\n"
+      " mov.b64 ad, {%1, %2};\n mov.b64 bd, {%3, %4};\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], ad, bd, %5, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&r)[8]) {
+  uint32_t v[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
+                 "=r"(v[6]), "=r"(v[7])
+               : "r"(taddr));
+#pragma unroll
+  for (int e = 0; e < 8; ++e) r[e] = __uint_as_float(v[e]);
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
+                   taddr),
+               "r"(__float_as_uint(r[0])), "r"(__float_as_uint(r[1])), "r"(__float_as_uint(r[2])),
+               "r"(__float_as_uint(r[3])), "r"(__float_as_uint(r[4])), "r"(__float_as_uint(r[5])),
+               "r"(__float_as_uint(r[6])), "r"(__float_as_uint(r[7]))
+               : "memory");
+}
+// Two floats -> two e5m2 codes (nearest even), and back: e5m2 is the upper half of an f16.
+__device__ __forceinline__ uint32_t e5m2x2_from_f32(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 f32_from_e5m2x2(uint32_t codes) {
+  const uint32_t h = __byte_perm(codes, 0, 0x1404);  // bytes 1 and 0 as the halves' upper bytes
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// The barrier of the 128 softmax threads; true where any of them came with `v`.
+__device__ __forceinline__ bool softmax_any(bool v) {
+  int r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 128, p;\n"
+      " selp.s32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((int)v)
+      : "memory");
+  return r != 0;
+}
+// Largest value of the warp (NaN is passed over), by the integer reduction: floats in the order
+// of their bits once the negative ones are turned around.
+__device__ __forceinline__ float warp_max(float x) {
+  int i = __float_as_int(x != x ? -INFINITY : x);
+  i = i >= 0 ? i : i ^ 0x7fffffff;
+  i = __reduce_max_sync(0xffffffffu, i);
+  return __int_as_float(i >= 0 ? i : i ^ 0x7fffffff);
+}
+
+struct Q8K {
+  const __nv_bfloat16* q;  // [B, H, lq, HD]
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* table;
+  const int32_t* lens;
+  __nv_bfloat16* o;
+  float* lse;
+  float* o_part;   // [2 * grid, R, HD]: O of a share, in units of 2^m
+  float* ml_part;  // [2 * grid, 2, R]: m and the sum
+  int* status;
+  int B, H, Hk, G, lq, rows, rb, max_pages, num_pages, ps_shift, sb_shift, causal;
+  float scale_log2;
+  unsigned long long wait_limit_ns;
+};
+
+__device__ __forceinline__ int q8_len(const Q8K& p, int b) {
+  const long long cap = (long long)p.max_pages << p.ps_shift;
   const int raw = p.lens[b];
-  const int len = raw < 0 ? 0 : raw > cap ? (int)cap : raw;
-  bool bad = raw != len;
-  const int seen = p.causal ? len - p.lq + i + 1 : len;  // keys 0 .. seen - 1
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + row * HD + lane * CPL;
-  float qr[CPL], acc[CPL];
-#pragma unroll
-  for (int c = 0; c < CPL; ++c) {
-    qr[c] = __bfloat162float(q[c]) * p.scale;
-    acc[c] = 0.0f;
-  }
-  float m = -FLT_MAX / 2, l = 0.0f;
-  for (int j = warp; j < seen; j += kWarps) {
-    const int pg = p.table[(size_t)b * p.max_pages + (j >> p.ps_shift)];
-    if (pg < 0 || pg >= p.num_pages) bad = true;
-    float s = 0.0f, vs = 0.0f, vv[CPL] = {};
-    if (pg >= 0 && pg < p.num_pages) {
-      const size_t at = (size_t)pg * p.Hk + kh;
-      const size_t blk = (at << (p.ps_shift - p.sb_shift)) + ((j & (ps - 1)) >> p.sb_shift);
-      const size_t off = ((at << p.ps_shift) + (j & (ps - 1))) * HD + lane * CPL;
-#pragma unroll
-      for (int c = 0; c < CPL; c += 2) {
-        const float2 kc = f32_from_e4m3x2(*reinterpret_cast<const uint16_t*>(p.k + off + c));
-        const float2 vc = f32_from_e4m3x2(*reinterpret_cast<const uint16_t*>(p.v + off + c));
-        s += qr[c] * kc.x + qr[c + 1] * kc.y;
-        vv[c] = vc.x;
-        vv[c + 1] = vc.y;
+  return raw < 0 ? 0 : raw > cap ? (int)cap : raw;
+}
+
+// Tiles of the whole list, per unit of a sequence (times Hk * rb units each), by one warp.
+__device__ __forceinline__ long long q8_all_tiles(const Q8K& p, int lane) {
+  long long sum = 0;
+  for (int b = lane; b < p.B; b += 32) sum += (q8_len(p, b) + kKT - 1) / kKT;
+  for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum * p.Hk * p.rb;
+}
+// Tiles of a CTA: the list cut evenly over the grid.
+__device__ __forceinline__ long long q8_share(long long all, long long grid) {
+  return (all + grid - 1) / grid;
+}
+
+// The units of a CTA's share [t, t1) of the list, in order. Every role walks its own copy.
+struct Walk {
+  long long t, t1;   // next tile of the list, end of the share
+  long long pre;     // tiles of the list before sequence b
+  int b, nt, len;    // sequence, its tiles for each unit, its length
+  // the unit found by next()
+  int kh, rb, ja, jb;  // kv head, row block, tiles [ja, jb) of it (tiles that no row sees left out)
+  int whole;           // the share has all of the unit
+  int first;           // the share has its first tile
+
+  // Starts at tile t0 (warp-wide).
+  __device__ __forceinline__ void init(const Q8K& p, long long t0, long long end, int lane) {
+    t = t0;
+    t1 = end;
+    pre = 0;
+    b = 0;
+    nt = 0;
+    len = 0;
+    if (t >= t1) return;
+    const long long U = (long long)p.Hk * p.rb;
+    for (int base = 0;; base += 32) {  // ends: t lies below the sum over all sequences
+      const int i = base + lane;
+      const long long n = i < p.B ? (long long)((q8_len(p, i) + kKT - 1) / kKT) * U : 0;
+      long long upto = n;
+      for (int o = 1; o < 32; o *= 2) {
+        const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
       }
-      for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-      s *= p.k_scale[blk];
-      vs = p.v_scale[blk];
+      const unsigned beyond = __ballot_sync(0xffffffffu, pre + upto > t);
+      if (beyond || base + 32 >= p.B) {
+        const int at = beyond ? __ffs(beyond) - 1 : 31;
+        b = min(base + at, p.B - 1);
+        pre += __shfl_sync(0xffffffffu, upto - n, at);
+        break;
+      }
+      pre += __shfl_sync(0xffffffffu, upto, 31);
     }
-    const float mn = fmaxf(m, s);
-    const float f = expf(m - mn), w = expf(s - mn);
-    l = l * f + w;
-#pragma unroll
-    for (int c = 0; c < CPL; ++c) acc[c] = acc[c] * f + w * vs * vv[c];
-    m = mn;
+    len = q8_len(p, b);
+    nt = (len + kKT - 1) / kKT;
   }
-#pragma unroll
-  for (int c = 0; c < CPL; ++c) acc_s[warp][lane * CPL + c] = acc[c];
-  if (lane == 0) {
-    m_s[warp] = m;
-    l_s[warp] = l;
+
+  __device__ __forceinline__ bool next(const Q8K& p, int R) {
+    if (t >= t1) return false;
+    const long long U = (long long)p.Hk * p.rb;
+    while (t >= pre + U * nt) {  // the next sequence with keys
+      pre += U * nt;
+      if (++b >= p.B) return false;
+      len = q8_len(p, b);
+      nt = (len + kKT - 1) / kKT;
+    }
+    const long long in = t - pre;
+    const int u = (int)(in / nt);
+    ja = (int)(in % nt);
+    kh = u / p.rb;
+    rb = u % p.rb;
+    const long long left = t1 - t;
+    const int je = left < nt - ja ? ja + (int)left : nt;
+    t += je - ja;
+    first = ja == 0;
+    whole = first && je == nt;
+    // keys that any row of the block sees
+    const int r0 = rb * R, r1 = min(p.rows, r0 + R) - 1;
+    const int imax = r0 / p.lq == r1 / p.lq ? r1 % p.lq : p.lq - 1;
+    const int seen = p.causal ? max(0, len - p.lq + imax + 1) : len;
+    jb = max(ja, min(je, (seen + kKT - 1) / kKT));
+    return true;
   }
+};
+
+template <int HD, int R>
+__global__ void __launch_bounds__(288, Q8Layout<HD, R>::CTAS)
+    q8_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
+                   const Q8K p) {
+  using LY = Q8Layout<HD, R>;
+  constexpr int ST = LY::ST, KCH = LY::KCH, CH = LY::CH, NS = LY::NS, NP = LY::NP;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  __shared__ uint64_t k_full[ST], v_full[ST], k_empty[ST], v_empty[ST];
+  __shared__ uint64_t s_full[2], s_free[2], p_full[2], p_done[2], q_full[2], q_free[2];
+  __shared__ uint64_t sc_full[kScRing], sc_free[kScRing], drain_s, drain_o;
+  __shared__ uint32_t tmem_base_s;
+  __shared__ WaitCtl wctl;
+  __shared__ int bad_input;
+  __shared__ int page_s[kPageChunk];
+  __shared__ float sc_s[kScRing][2][kKT];  // key scale, log2 of the value scale
+  __shared__ __align__(16) float qs_s[2][R];   // rows: score factor, key limit
+  __shared__ __align__(16) int lim_s[2][R];
+  __shared__ __align__(16) float m_s[R], red_s[4][R];
+
+  const int warp = warp_id(), lane = lane_id();
+  if (threadIdx.x == 0) {
+    wait_ctl_init(&wctl, p.wait_limit_ns);
+    bad_input = 0;
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&s_full[s], 1);
+      mbar_init(&s_free[s], 4);
+      mbar_init(&p_full[s], 4);
+      mbar_init(&p_done[s], 1);
+      mbar_init(&q_full[s], 1);
+      mbar_init(&q_free[s], 2);
+    }
+    for (int s = 0; s < kScRing; ++s) {
+      mbar_init(&sc_full[s], 1);
+      mbar_init(&sc_free[s], 4);
+    }
+    mbar_init(&drain_s, 1);
+    mbar_init(&drain_o, 1);
+    fence_barrier_init();
+  }
+  if (warp == LY::S_WARP) {
+    tmem_alloc(&tmem_base_s, LY::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
   __syncthreads();
-  float mt = -FLT_MAX / 2, lt = 0.0f;
-  for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, m_s[w]);
-  for (int w = 0; w < kWarps; ++w) lt += l_s[w] * expf(m_s[w] - mt);
-  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + row * HD;
-  if (threadIdx.x < HD) {
-    float a = 0.0f;
-    for (int w = 0; w < kWarps; ++w) a += acc_s[w][threadIdx.x] * expf(m_s[w] - mt);
-    o[threadIdx.x] = __float2bfloat16(seen > 0 ? a / lt : 0.0f);
+  tc_fence_after();
+  const uint32_t tbase = tmem_base_s;
+  grid_dep_trigger();
+
+  Walk w;
+  {
+    const long long all = q8_all_tiles(p, lane);
+    const long long per = q8_share(all, gridDim.x);
+    const long long t0 = per * blockIdx.x;
+    w.init(p, t0, t0 + per < all ? t0 + per : all, lane);
+    if (warp == 0 && blockIdx.x == 0) {  // lengths out of range are clamped, and reported here
+      bool bad = false;
+      for (int b = lane; b < p.B; b += 32) bad |= p.lens[b] != q8_len(p, b);
+      if (bad) bad_input = 1;
+    }
   }
-  if (threadIdx.x == 0 && p.lse) p.lse[row] = seen > 0 ? mt + logf(lt) : -INFINITY;
-  if (bad && lane == 0 && p.status) atomicCAS(p.status, kStatusOk, kStatusBadInput);
+
+  if (warp == LY::TMA_WARP) {
+    // ------------------------------------------------------------------ K and V copies
+    const bool leader = lane == 0;
+    if (leader) {
+      tma_prefetch_desc(&mK);
+      tma_prefetch_desc(&mV);
+    }
+    const int box = min(1 << p.ps_shift, kKT);  // rows of a box
+    const int nsub = kKT / box;                 // boxes of a tile and chunk (<= 16)
+    const int z_oob = p.num_pages * p.Hk;       // a page past the cache: zero fill
+    const int sub = lane / KCH, c = lane % KCH; // this lane's box
+    int g = 0;                                  // tiles so far
+    int page_b = -1, page_lo = 0;               // page_s holds entries page_lo .. of sequence page_b
+    bool ok = true;
+    while (ok && w.next(p, R)) {
+      const int used = (w.len + (1 << p.ps_shift) - 1) >> p.ps_shift;
+      const int32_t* row = p.table + (size_t)w.b * p.max_pages;
+      for (int j = w.ja; j < w.jb && ok; ++j, ++g) {
+        const int n0 = j * kKT;
+        const int p_lo = n0 >> p.ps_shift, p_hi = min(used - 1, (n0 + kKT - 1) >> p.ps_shift);
+        if (page_b != w.b || p_lo < page_lo || p_hi >= page_lo + kPageChunk) {
+          page_b = w.b;
+          page_lo = p_lo;
+          __syncwarp();
+          const int n = min(kPageChunk, used - page_lo);
+          for (int e = lane; e < n; e += 32) {
+            int pg = row[page_lo + e];
+            if (pg < 0 || pg >= p.num_pages) {
+              pg = -1;
+              bad_input = 1;
+            }
+            page_s[e] = pg;
+          }
+          __syncwarp();
+        }
+        const int key = n0 + sub * box;
+        int z = z_oob, y = 0;
+        if (sub < nsub && key < w.len) {
+          const int pg = page_s[(key >> p.ps_shift) - page_lo];
+          if (pg >= 0) {
+            z = pg * p.Hk + w.kh;
+            y = key & ((1 << p.ps_shift) - 1);
+          }
+        }
+        const int st = g % ST;
+        const uint32_t use = g / ST;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+          uint64_t* full = which ? &v_full[st] : &k_full[st];
+          if (leader) {
+            if (use > 0) ok = mbar_wait(which ? &v_empty[st] : &k_empty[st], (use - 1) & 1, &wctl);
+            if (ok) mbar_arrive_expect_tx(full, LY::KV_BYTES);
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          uint8_t* dst = smem + (which ? LY::OFF_V : LY::OFF_K) + st * LY::KV_BYTES +
+                         c * (kKT * CH) + sub * box * CH;
+          if (sub < nsub) tma_load_3d(dst, which ? &mV : &mK, full, c * CH, y, z);
+        }
+        if (!ok) {  // the K copy of this tile may be under way: let it land
+          if (leader) mbar_wait_drain(&k_full[st], use & 1);
+          break;
+        }
+      }
+    }
+    if (leader)  // no copy may be in flight when the CTA ends
+      for (int s = 0; s < ST; ++s) {
+        const int n = (g - s + ST - 1) / ST;  // copies into stage s
+        if (n > 0) {
+          mbar_wait_drain(&k_full[s], (n - 1) & 1);
+          mbar_wait_drain(&v_full[s], (n - 1) & 1);
+        }
+      }
+  } else if (warp == LY::S_WARP) {
+    // ------------------------------------------------------------------ S^T = K q^T
+    if (elect_one()) {
+      const uint32_t id = idesc_f8(0, 0, kKT, NS, 0, 0);
+      int g = 0, un = 0;
+      bool ok = true;
+      for (; ok && w.next(p, R); ++un) {
+        ok = mbar_wait(&q_full[un & 1], (un >> 1) & 1, &wctl);
+        if (!ok) break;
+        const Desc qb = q8_desc<CH>(smem_u32(smem + LY::OFF_Q + (un & 1) * LY::Q_BYTES), 0);
+        for (int j = w.ja; j < w.jb; ++j, ++g) {
+          const int st = g % ST, buf = g & 1;
+          ok = mbar_wait(&k_full[st], (g / ST) & 1, &wctl);
+          if (ok && g >= 2) ok = mbar_wait(&s_free[buf], ((g >> 1) - 1) & 1, &wctl);
+          if (!ok) break;
+          tc_fence_after();
+          const Desc ka = q8_desc<CH>(smem_u32(smem + LY::OFF_K + st * LY::KV_BYTES), 0);
+          const uint32_t tS = tbase + LY::COL_S + buf * NS;
+#pragma unroll
+          for (int ks = 0; ks < HD / 32; ++ks) {
+            const int ch = ks * 32 / CH, in = ks * 32 % CH;
+            mma_f8(tS, ka.at(ch * (kKT * CH) + in), ka.hi, qb.at(ch * (NS * CH) + in), qb.hi, id,
+                   ks > 0 ? 1u : 0u);
+          }
+          mma_commit(&s_full[buf]);
+          mma_commit(&k_empty[st]);
+        }
+        if (ok) mma_commit(&q_free[un & 1]);  // (arrives at once where the unit had no tile)
+      }
+      mma_commit(&drain_s);
+      mbar_wait_drain(&drain_s, 0);
+    }
+  } else if (warp == LY::O_WARP) {
+    // ------------------------------------------------------------------ O^T += V^T w^T
+    constexpr int MV = HD < 128 ? HD : 128;  // head-dim rows of an MMA
+    const uint32_t id = idesc_f8(0, 1, MV, NP, 1, 1);
+    int g = 0;
+    bool ok = true;
+    while (ok && w.next(p, R)) {
+      for (int j = w.ja; j < w.jb; ++j, ++g) {
+        const int st = g % ST, buf = g & 1, n0 = j * kKT;
+        ok = __all_sync(0xffffffffu, mbar_wait(&p_full[buf], (g >> 1) & 1, &wctl));
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&v_full[st], (g / ST) & 1, &wctl));
+        if (!ok) break;
+        uint8_t* vt = smem + LY::OFF_V + st * LY::KV_BYTES;
+        if (n0 + kKT > w.len) {  // rows behind the sequence's end
+          const int r0 = w.len - n0;
+          for (int e = lane; e < (kKT - r0) * (HD / 16); e += 32) {
+            const int r = r0 + e / (HD / 16), x = e % (HD / 16);
+            *reinterpret_cast<uint4*>(vt + x * 16 / CH * (kKT * CH) + r * CH + x * 16 % CH) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async();
+          __syncwarp();
+        }
+        tc_fence_after();
+        if (lane == 0) {
+          const Desc va = q8_desc<CH>(smem_u32(vt), kKT * CH);
+          const Desc pb = q8_desc<NP>(smem_u32(smem + LY::OFF_P + buf * LY::P_BYTES), 0);
+#pragma unroll
+          for (int h = 0; h < KCH; ++h)
+#pragma unroll
+            for (int ks = 0; ks < kKT / 32; ++ks)
+              mma_f8(tbase + LY::COL_O + h * NP, va.at(h * (kKT * CH) + ks * 32 * CH), va.hi,
+                     pb.at(ks * 32 * NP), pb.hi, id, (j > w.ja || ks > 0) ? 1u : 0u);
+          mma_commit(&p_done[buf]);
+          mma_commit(&v_empty[st]);
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) {
+      mma_commit(&drain_o);
+      mbar_wait_drain(&drain_o, 0);
+    }
+    __syncwarp();
+  } else if (warp == LY::Q_WARP) {
+    // ------------------------------------------------------------------ q in two pieces
+    constexpr int CPL = HD / 32;  // columns of a lane
+    int un = 0;
+    for (; w.next(p, R); ++un) {
+      const int qb = un & 1;
+      if (un >= 2 &&
+          !__all_sync(0xffffffffu, mbar_wait(&q_free[qb], ((un >> 1) - 1) & 1, &wctl)))
+        break;
+      uint8_t* dst = smem + LY::OFF_Q + qb * LY::Q_BYTES;
+      const int r0 = w.rb * R;
+      const __nv_bfloat16* src =
+          p.q + (((size_t)w.b * p.Hk + w.kh) * p.rows + r0) * HD + lane * CPL;
+#pragma unroll 4
+      for (int r = 0; r < R; ++r) {
+        const bool live = r0 + r < p.rows;
+        uint32_t x[CPL / 2];
+#pragma unroll
+        for (int e = 0; e < CPL / 2; ++e)
+          x[e] = live ? reinterpret_cast<const uint32_t*>(src + (size_t)r * HD)[e] : 0u;
+        uint32_t a = 0;
+#pragma unroll
+        for (int e = 0; e < CPL / 2; ++e)
+          a = max(a, max(x[e] & 0x7fffu, (x[e] >> 16) & 0x7fffu));
+        a = __reduce_max_sync(0xffffffffu, a);
+        // 2^sh puts the row's largest element into [128, 256); a row with an element that is not
+        // finite becomes NaN
+        const int sh = 134 - (int)max(a >> 7, 1u);
+        const bool odd = a >= 0x7f80u;
+        const float f0 = __int_as_float((sh / 2 + 127) << 23);
+        const float f1 = __int_as_float((sh - sh / 2 + 127) << 23);
+        uint32_t hi = 0, lo = 0, hi2 = 0, lo2 = 0;
+#pragma unroll
+        for (int e = 0; e < CPL / 2; ++e) {
+          const float u = __uint_as_float(x[e] << 16) * f0 * f1;
+          const float v = __uint_as_float(x[e] & 0xffff0000u) * f0 * f1;
+          const uint32_t h = odd ? 0x7f7fu : e4m3x2_from_f32(u, v);
+          const float2 t = f32_from_e4m3x2(h);
+          const uint32_t l = e4m3x2_from_f32((u - t.x) * 16.0f, (v - t.y) * 16.0f);
+          if (e < 2) {
+            hi |= h << (16 * e);
+            lo |= l << (16 * e);
+          } else {
+            hi2 |= h << (16 * (e - 2));
+            lo2 |= l << (16 * (e - 2));
+          }
+        }
+        const int col = lane * CPL, ch = col / CH, in = col % CH;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {  // hi rows, then lo rows
+          const int n = half * R + r;
+          uint8_t* at = dst + ch * (NS * CH) + n * CH + swz<CH>(in / 16, n) * 16 + in % 16;
+          if constexpr (CPL == 2)
+            *reinterpret_cast<uint16_t*>(at) = (uint16_t)(half ? lo : hi);
+          else if constexpr (CPL == 4)
+            *reinterpret_cast<uint32_t*>(at) = half ? lo : hi;
+          else
+            *reinterpret_cast<uint2*>(at) = half ? make_uint2(lo, lo2) : make_uint2(hi, hi2);
+        }
+        if (lane == 0) {
+          const int i = (r0 + r) % p.lq;
+          qs_s[qb][r] = live ? p.scale_log2 * __int_as_float((127 - sh / 2) << 23) *
+                                   __int_as_float((127 - (sh - sh / 2)) << 23)
+                             : 0.0f;
+          lim_s[qb][r] = !live ? 0 : p.causal ? max(0, w.len - p.lq + i + 1) : w.len;
+        }
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[qb]);
+    }
+  } else if (warp == LY::SC_WARP) {
+    // ------------------------------------------------------------------ scales: those of two
+    // tiles are on their way in registers, and the table entries of the two after them
+    int g = 0;
+    bool ok = true;
+    const int nb_shift = p.ps_shift - p.sb_shift;
+    while (ok && w.next(p, R)) {
+      const int32_t* row = p.table + (size_t)w.b * p.max_pages;
+      int pg[2][4];
+      float ks[2][4], vs[2][4];
+      auto pages = [&](int j, int (&to)[4]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = j * kKT + e * 32 + lane;
+          to[e] = key < w.len && j < w.jb ? row[key >> p.ps_shift] : -1;
+        }
+      };
+      auto scales = [&](int j, const int (&pgs)[4], float (&k)[4], float (&v)[4]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = j * kKT + e * 32 + lane;
+          const bool have = pgs[e] >= 0 && pgs[e] < p.num_pages;
+          const size_t at = (((size_t)(have ? pgs[e] : 0) * p.Hk + w.kh) << nb_shift) +
+                            ((key & ((1 << p.ps_shift) - 1)) >> p.sb_shift);
+          k[e] = have ? __ldg(p.k_scale + at) : 0.0f;
+          v[e] = have ? __ldg(p.v_scale + at) : 1.0f;
+        }
+      };
+      pages(w.ja, pg[0]);
+      pages(w.ja + 1, pg[1]);
+      scales(w.ja, pg[0], ks[0], vs[0]);
+      scales(w.ja + 1, pg[1], ks[1], vs[1]);
+      pages(w.ja + 2, pg[0]);
+      pages(w.ja + 3, pg[1]);
+      for (int j = w.ja; j < w.jb && ok; j += 2) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (j + h >= w.jb) break;
+          const int slot = g % kScRing;
+          if (g >= kScRing)
+            ok = __all_sync(0xffffffffu, mbar_wait(&sc_free[slot], (g / kScRing - 1) & 1, &wctl));
+          if (!ok) break;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            sc_s[slot][0][e * 32 + lane] = ks[h][e];
+            sc_s[slot][1][e * 32 + lane] =
+                log2f(fmaxf(vs[h][e], __int_as_float((kQ8MinExp + 127) << 23)));
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sc_full[slot]);
+          ++g;
+          scales(j + h + 2, pg[h], ks[h], vs[h]);
+          pages(j + h + 4, pg[h]);
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax, and O out
+    const int key = threadIdx.x;  // key of the tile
+    const uint32_t lanes = tbase + ((uint32_t)(warp * 32) << 16);
+    int g = 0, un = 0;
+    bool ok = true;
+    for (; ok && w.next(p, R); ++un) {
+      const int qb = un & 1;
+      ok = mbar_wait(&q_full[qb], (un >> 1) & 1, &wctl);
+      // (a wait that ran out shows at the next softmax_any, where all threads leave together)
+      const int r0 = w.rb * R, live = min(R, p.rows - r0);
+      int lim_min = w.len;  // tiles below it need no test of the keys
+      if (p.causal) lim_min = max(0, w.len - p.lq + 1);
+      float l[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) l[r] = 0.0f;
+      // rows that are not there: m far above every score, so that they weigh nothing
+      if (key < R) m_s[key] = key < live ? 0.0f : 1e30f;
+      if (softmax_any(!ok)) {
+        ok = false;
+        break;
+      }
+      for (int j = w.ja; j < w.jb; ++j, ++g) {
+        const int buf = g & 1, slot = g % kScRing, n0 = j * kKT;
+        ok = ok && mbar_wait(&sc_full[slot], (g / kScRing) & 1, &wctl);
+        const float kc = sc_s[slot][0][key], lsv = sc_s[slot][1][key];
+        const float inv = ex2(-lsv);  // 1 / value scale
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(&s_full[buf], (g >> 1) & 1, &wctl));
+        tc_fence_after();
+        float t[R];
+        const uint32_t tS = lanes + LY::COL_S + buf * NS;
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < R; c += 8) {
+          float hi[8], lo[8];
+          tmem_ld8(tS + c, hi);
+          tmem_ld8(tS + R + c, lo);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float s = fmaf(lo[e], 0.0625f, hi[e]) * kc;
+            t[c + e] = fmaf(s, qs_s[qb][c + e], lsv - m_s[c + e]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&s_free[buf]);
+          mbar_arrive(&sc_free[slot]);
+        }
+        if (n0 + kKT > lim_min) {
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+            if (n0 + key >= lim_s[qb][r]) t[r] = -INFINITY;
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) top = fmaxf(top, t[r]);
+        const bool first = j == w.ja;
+        if (softmax_any(top > kRise || first || !ok)) {
+          // m moves: to the largest score so far, at the first tile to the tile's own
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const float mx = warp_max(t[r]);
+            if (lane == 0) red_s[warp][r] = mx;
+          }
+          if (softmax_any(!ok)) {
+            ok = false;
+            break;
+          }
+          if (!first) {  // O is about to be scaled: the last O^T MMA must be done
+            ok = mbar_wait(&p_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &wctl);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+          }
+#pragma unroll
+          for (int c = 0; c < R; c += 8) {
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int r = c + e;
+              float up = fmaxf(fmaxf(red_s[0][r], red_s[1][r]), fmaxf(red_s[2][r], red_s[3][r]));
+              if (first ? up == -INFINITY || r >= live : !(up > 0.0f)) up = 0.0f;
+              f[e] = ex2(-up);
+              t[r] -= up;
+              if (!first) l[r] *= f[e];
+              if (key == r) m_s[r] += up;
+            }
+            if (!first) {
+#pragma unroll 1
+              for (int h = 0; h < KCH * 3; ++h) {
+                const uint32_t at = lanes + LY::COL_O + h / 3 * NP + h % 3 * R + c;
+                float x[8];
+                tmem_ld8(at, x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] *= f[e];
+                tmem_st8(at, x);
+              }
+            }
+          }
+          if (!first) {
+            tmem_wait_st();
+            tc_fence_before();
+          }
+          softmax_any(false);  // m_s is read, and red_s written, by everyone after this
+        }
+        // weights, their sum, and their pieces into shared memory, the key's row of NP bytes
+        if (g >= 2) ok = ok && mbar_wait(&p_done[buf], ((g >> 1) - 1) & 1, &wctl);
+        uint8_t* prow = smem + LY::OFF_P + buf * LY::P_BYTES + key * NP;
+        uint32_t pc[3][R / 4];
+#pragma unroll
+        for (int r = 0; r < R; r += 2) {
+          float a = ex2(t[r]), b = ex2(t[r + 1]);
+          l[r] = fmaf(a, inv, l[r]);
+          l[r + 1] = fmaf(b, inv, l[r + 1]);
+          a *= kWeight;
+          b *= kWeight;
+          uint32_t x[3];
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            x[i] = e5m2x2_from_f32(a, b);
+            const float2 back = f32_from_e5m2x2(x[i]);
+            a = (a - back.x) * 8.0f;
+            b = (b - back.y) * 8.0f;
+            if (r % 4 == 0)
+              pc[i][r / 4] = x[i];
+            else
+              pc[i][r / 4] |= x[i] << 16;
+          }
+        }
+        if constexpr (R == 8) {
+          *reinterpret_cast<uint4*>(prow + swz<NP>(0, key) * 16) =
+              make_uint4(pc[0][0], pc[0][1], pc[1][0], pc[1][1]);
+          *reinterpret_cast<uint4*>(prow + swz<NP>(1, key) * 16) =
+              make_uint4(pc[2][0], pc[2][1], 0u, 0u);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 3; ++i)
+#pragma unroll
+            for (int x = 0; x < R / 16; ++x)
+              *reinterpret_cast<uint4*>(prow + swz<NP>(i * (R / 16) + x, key) * 16) = make_uint4(
+                  pc[i][4 * x], pc[i][4 * x + 1], pc[i][4 * x + 2], pc[i][4 * x + 3]);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[buf]);
+      }
+      if (!__all_sync(0xffffffffu, ok)) ok = false;
+      // the sums of the 128 keys' threads
+      if (softmax_any(!ok)) {
+        ok = false;
+        break;
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float x = l[r];
+        for (int o = 16; o > 0; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (lane == 0) red_s[warp][r] = x;
+      }
+      const bool any = w.jb > w.ja;
+      if (any) ok = mbar_wait(&p_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &wctl);
+      if (softmax_any(!ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const size_t unit_row = ((size_t)w.b * p.Hk + w.kh) * p.rows + r0;
+      const size_t part = 2 * (size_t)blockIdx.x + (w.first ? 1 : 0);
+      // this thread's head-dim row: a 64-row accumulator lies in lanes 0-15 of each warp
+      const int col = HD == 64 ? warp * 16 + lane : (int)threadIdx.x;
+      const bool mine = HD > 64 || lane < 16;
+#pragma unroll 1
+      for (int c = 0; c < R; c += 8) {
+#pragma unroll 1
+        for (int h = 0; h < KCH; ++h) {
+          float x[8], y[8], z[8];
+          if (any) {
+            const uint32_t at = lanes + LY::COL_O + h * NP + c;
+            tmem_ld8(at, x);
+            tmem_ld8(at + R, y);
+            tmem_ld8(at + 2 * R, z);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int r = c + e;
+            const float sum = red_s[0][r] + red_s[1][r] + red_s[2][r] + red_s[3][r];
+            const float o = any ? fmaf(fmaf(z[e], 0.125f, y[e]), 0.125f, x[e]) / kWeight : 0.0f;
+            if (!mine || r >= live) continue;
+            if (w.whole)
+              p.o[(unit_row + r) * HD + h * 128 + col] =
+                  __float2bfloat16(sum == 0.0f ? 0.0f : o / sum);
+            else
+              p.o_part[(part * R + r) * HD + h * 128 + col] = sum == 0.0f ? 0.0f : o;
+          }
+        }
+      }
+      if (key < live) {
+        const float sum = red_s[0][key] + red_s[1][key] + red_s[2][key] + red_s[3][key];
+        if (!w.whole) {
+          p.ml_part[part * 2 * R + key] = m_s[key];
+          p.ml_part[part * 2 * R + R + key] = sum;
+        } else if (p.lse) {
+          p.lse[unit_row + key] = sum == 0.0f ? -INFINITY : fmaf(m_s[key], kLn2, logf(sum));
+        }
+      }
+      tc_fence_before();
+      if (threadIdx.x == 0) mbar_arrive(&q_free[qb]);
+      softmax_any(false);  // red_s and m_s may be written again
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == LY::S_WARP) tmem_dealloc(tbase, LY::TMEM_COLS);
+  if (threadIdx.x == 0) {
+    report_abort(&wctl, p.status);
+    if (bad_input && p.status) atomicCAS(p.status, kStatusOk, kStatusBadInput);
+  }
+}
+
+// Joins the shares of the units that were cut, and writes those of sequences without keys: one
+// CTA for each unit.
+template <int HD, int R>
+__global__ void __launch_bounds__(256) q8_combine_kernel(const Q8K p, int grid) {
+  const int lane = lane_id();
+  grid_dep_wait();
+  const long long u = blockIdx.x;  // (b * Hk + kh) * rb + row block
+  const int U = p.Hk * p.rb;
+  const int b = (int)(u / U), in = (int)(u % U);
+  const int r0 = in % p.rb * R, live = min(R, p.rows - r0);
+  const size_t unit_row = ((size_t)b * p.Hk + in / p.rb) * p.rows + r0;
+  const int nt = (q8_len(p, b) + kKT - 1) / kKT;
+  if (nt == 0) {
+    for (int e = threadIdx.x; e < live * HD; e += 256) p.o[unit_row * HD + e] = __float2bfloat16(0.f);
+    if (p.lse && threadIdx.x < live) p.lse[unit_row + threadIdx.x] = -INFINITY;
+    return;
+  }
+  // every warp finds the unit's place in the list for itself
+  long long before = 0;
+  for (int i = lane; i < b; i += 32) before += (q8_len(p, i) + kKT - 1) / kKT;
+  for (int o = 16; o > 0; o /= 2) before += __shfl_xor_sync(0xffffffffu, before, o);
+  const long long per = q8_share(q8_all_tiles(p, lane), grid);
+  const long long a = before * U + (long long)in * nt;
+  const int c0 = (int)(a / per), c1 = (int)((a + nt - 1) / per);
+  if (c0 == c1) return;  // written whole
+  // share i: slot 2 c0 + 1 (it begins there), then 2 c of each further CTA
+  auto slot = [&](int c) { return (size_t)2 * c + (c == c0 ? 1 : 0); };
+  for (int r = threadIdx.x / 32; r < live; r += 8) {
+    float m = -FLT_MAX;
+    for (int c = c0 + lane; c <= c1; c += 32) {
+      const float* ml = p.ml_part + slot(c) * 2 * R + r;
+      if (ml[R] != 0.0f) m = fmaxf(m, ml[0]);
+    }
+    for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float sum = 0.0f, acc[HD / 32] = {};
+    for (int c = c0; c <= c1; ++c) {
+      const float* ml = p.ml_part + slot(c) * 2 * R + r;
+      if (ml[R] == 0.0f) continue;
+      const float f = ex2(ml[0] - m);
+      sum = fmaf(ml[R], f, sum);
+      const float* src = p.o_part + (slot(c) * R + r) * HD + lane;
+#pragma unroll
+      for (int e = 0; e < HD / 32; ++e) acc[e] = fmaf(src[e * 32], f, acc[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < HD / 32; ++e)
+      p.o[(unit_row + r) * HD + e * 32 + lane] =
+          __float2bfloat16(sum == 0.0f ? 0.0f : acc[e] / sum);
+    if (p.lse && lane == 0)
+      p.lse[unit_row + r] = sum == 0.0f ? -INFINITY : fmaf(m, kLn2, logf(sum));
+  }
+}
+
+struct Plan {
+  int R, rb, grid;
+};
+
+// Rows of a unit: the smallest block that holds the G * q_len rows of a kv head, 32 at most (more
+// rows take further passes over the keys, from L2). Grid: every CTA slot of the GPU, or one CTA
+// for each tile there can be.
+Plan make_plan(const Q8AttnArgs& a) {
+  Plan pl;
+  const int rows = a.G * a.lq;
+  pl.R = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  pl.rb = (rows + pl.R - 1) / pl.R;
+  const int ctas = 152 * (pl.R == 8 && a.d <= 128 ? 2 : 1);
+  const long long cap = (long long)a.max_pages << a.ps_shift;
+  const long long tiles = (cap + kKT - 1) / kKT * a.B * a.Hk * pl.rb;
+  pl.grid = (int)std::min<long long>(ctas, tiles);
+  return pl;
+}
+
+template <int HD, int R>
+cudaError_t attn_t(const Q8AttnArgs& a, const Q8AttnMaps& m, const Plan& pl, void* ws,
+                   cudaStream_t s) {
+  using LY = Q8Layout<HD, R>;
+  auto kern = q8_attn_kernel<HD, R>;
+  static OncePerKey<> smem_attr;
+  cudaError_t e = set_smem_once(smem_attr, kern, LY::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  Q8K p;
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.k_scale = a.k_scale;
+  p.v_scale = a.v_scale;
+  p.table = a.table;
+  p.lens = a.lens;
+  p.o = static_cast<__nv_bfloat16*>(a.o);
+  p.lse = a.lse;
+  p.ml_part = static_cast<float*>(ws);
+  p.o_part = p.ml_part + (size_t)2 * pl.grid * 2 * R;
+  p.status = a.status;
+  p.B = a.B;
+  p.H = a.H;
+  p.Hk = a.Hk;
+  p.G = a.G;
+  p.lq = a.lq;
+  p.rows = a.G * a.lq;
+  p.rb = pl.rb;
+  p.max_pages = a.max_pages;
+  p.num_pages = a.num_pages;
+  p.ps_shift = a.ps_shift;
+  p.sb_shift = a.sb_shift;
+  p.causal = a.causal;
+  p.scale_log2 = a.scale * kLog2e;
+  p.wait_limit_ns = a.wait_limit_ns;
+  profile_mark(kKernQ8Attn, 0, s);
+  kern<<<pl.grid, LY::THREADS, LY::SMEM_BYTES, s>>>(m.k, m.v, p);
+  e = cudaGetLastError();
+  profile_mark(kKernQ8Attn, 1, s);
+  if (e != cudaSuccess) return e;
+  profile_mark(kKernQ8Combine, 0, s);
+  e = launch_pdl(q8_combine_kernel<HD, R>, dim3((unsigned)((long long)a.B * a.Hk * pl.rb)),
+                 dim3(256), 0, s, p, pl.grid);
+  profile_mark(kKernQ8Combine, 1, s);
+  return e;
 }
 
 template <int HD>
-cudaError_t attn_t(const Q8AttnArgs& a, cudaStream_t s) {
-  profile_mark(kKernQ8Attn, 0, s);
-  q8_attn_kernel<HD><<<(unsigned)((long long)a.B * a.H * a.lq), kWarps * 32, 0, s>>>(a);
-  const cudaError_t e = cudaGetLastError();
-  profile_mark(kKernQ8Attn, 1, s);
-  return e;
+cudaError_t attn_d(const Q8AttnArgs& a, const Q8AttnMaps& m, const Plan& pl, void* ws,
+                   cudaStream_t s) {
+  if (pl.R == 8) return attn_t<HD, 8>(a, m, pl, ws, s);
+  if (pl.R == 16) return attn_t<HD, 16>(a, m, pl, ws, s);
+  return attn_t<HD, 32>(a, m, pl, ws, s);
 }
 }  // namespace
 
-cudaError_t launch_q8_attn(const Q8AttnArgs& a, cudaStream_t s) {
+int q8_box_rows(int page_size) { return page_size < kKT ? page_size : kKT; }
+int q8_box_cols(int head_dim) { return head_dim < 128 ? head_dim : 128; }
+
+long long q8_attn_units(const Q8AttnArgs& a) {
+  return (long long)a.B * a.Hk * make_plan(a).rb;
+}
+
+size_t q8_attn_workspace_bytes(const Q8AttnArgs& a) {
+  const Plan pl = make_plan(a);
+  return (size_t)2 * pl.grid * pl.R * (a.d + 2) * 4;
+}
+
+cudaError_t launch_q8_attn(const Q8AttnArgs& a, const Q8AttnMaps& m, void* ws, cudaStream_t s) {
+  const Plan pl = make_plan(a);
   switch (a.d) {
-    case 64: return attn_t<64>(a, s);
-    case 128: return attn_t<128>(a, s);
-    case 256: return attn_t<256>(a, s);
+    case 64: return attn_d<64>(a, m, pl, ws, s);
+    case 128: return attn_d<128>(a, m, pl, ws, s);
+    case 256: return attn_d<256>(a, m, pl, ws, s);
     default: return cudaErrorInvalidValue;
   }
 }
