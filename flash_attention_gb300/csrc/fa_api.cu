@@ -874,15 +874,7 @@ int fa_q8_paged_attention(const void* q, const fa_q8_cache* cache, const int32_t
   if (p->n_kv_heads != cache->n_kv_heads || p->head_dim != cache->head_dim ||
       p->page_size != cache->page_size || p->num_pages != cache->num_pages || p->num_splits != 0)
     return FA_ERR_INVALID;
-  if ((int64_t)p->batch * p->n_heads * p->q_len > INT32_MAX / 2) return FA_ERR_INVALID;
-  if ((rc = check_device())) return rc;
-  cudaError_t e = get_encoder();
-  if (e != cudaSuccess) return cuda_fail(e, "cuTensorMapEncodeTiled entry point");
   fa::Q8AttnArgs a;
-  int dev = 0;
-  cudaGetDevice(&dev);
-  e = device_status_word(dev, &a.status);
-  if (e != cudaSuccess) return cuda_fail(e, "status word");
   a.q = q;
   a.k = static_cast<const uint8_t*>(cache->k);
   a.v = static_cast<const uint8_t*>(cache->v);
@@ -905,7 +897,14 @@ int fa_q8_paged_attention(const void* q, const fa_q8_cache* cache, const int32_t
   a.ps_shift = log2_of(p->page_size);
   a.sb_shift = log2_of(cache->scale_block);
   a.scale = p->scale;
-  if (fa::q8_attn_units(a) > INT32_MAX) return FA_ERR_INVALID;
+  if (fa::q8_attn_tiles(a) > INT32_MAX / 2) return FA_ERR_INVALID;
+  if ((rc = check_device())) return rc;
+  cudaError_t e = get_encoder();
+  if (e != cudaSuccess) return cuda_fail(e, "cuTensorMapEncodeTiled entry point");
+  int dev = 0;
+  cudaGetDevice(&dev);
+  e = device_status_word(dev, &a.status);
+  if (e != cudaSuccess) return cuda_fail(e, "status word");
   fa::Q8AttnMaps m;
   const int cols = fa::q8_box_cols(a.d), box = fa::q8_box_rows(p->page_size);
   if (!encode_u8_3d(&m.k, a.k, a.num_pages * a.Hk, p->page_size, a.d, cols, box) ||

@@ -349,7 +349,7 @@ struct Q8AttnMaps {
 };
 int q8_box_rows(int page_size);
 int q8_box_cols(int head_dim);
-long long q8_attn_units(const Q8AttnArgs& a);  // CTAs of the joining kernel
+long long q8_attn_tiles(const Q8AttnArgs& a);  // key tiles of all units, at most
 size_t q8_attn_workspace_bytes(const Q8AttnArgs& a);
 cudaError_t launch_q8_attn(const Q8AttnArgs& a, const Q8AttnMaps& m, void* ws,
                            cudaStream_t stream);

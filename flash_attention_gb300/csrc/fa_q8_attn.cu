@@ -13,15 +13,17 @@
 //  * q (8 significant bits) = hi + lo / 16, both e4m3 (4 bits each, hi the nearest), after a power
 //    of two for each row that puts its largest element into [128, 256). Exact, except that
 //    elements 2^-14 below the row's largest lose what is under 2^-22 of it.
-//  * a softmax weight = p1 + p2 / 8 + p3 / 64, all e5m2 (3 bits each): 9 bits, and with e5m2's
-//    range weights down to 2^-35 of the row's largest still count, as they do when a key that
-//    takes nearly all of the weight has thousands of small ones beside it.
+//  * a softmax weight, rounded to 9 bits in f16, = p1 + p2 / 8 + p3 / 64, all e5m2: e5m2 is the
+//    upper byte of an f16 (3 bits of the 9), so a piece is that byte of what the pieces before it
+//    leave, times 8. In steps of 2^-33 of the row's largest weight at least, so that thousands of
+//    small weights beside a key that takes nearly all still count (with the pieces unscaled the
+//    steps are 2^-27, and a case like that was off by 1.3 times its tolerance).
 // S^T = K q^T has the keys as the M = 128 rows of a tile and R query rows as 2 R columns: a thread
 // owns a key, whose two scales are then the thread's constants, and sees the R scores of it.
 // O^T = V^T w^T has the head dim as M (V is read transposed, MN-major) and 3 R columns; the value
 // scale is part of the weight: w = exp2(score + log2(v_scale) - m), m the running maximum of that
-// sum, so that neither the weights nor O lose range whatever the scales are; the softmax's sum
-// takes w / v_scale.
+// sum less 11, so that neither the weights nor O lose range whatever the
+// scales are; the softmax's sum takes w / v_scale.
 //
 // Work: the (sequence, kv head, block of R rows) units, each ceil(len / 128) key tiles, form one
 // list of tiles, cut evenly over persistent CTAs (the lengths are on the device; each CTA finds
@@ -30,7 +32,7 @@
 //
 // Warps of a CTA: 0-3 softmax (thread = key of the tile, and head-dim row of O^T), 4 TMA copies of
 // K and V pages (boxes of min(page_size, 128) rows), 5 issues S^T, 6 O^T (and zeroes what a last
-// page holds behind the sequence's end, so that NaN there meets no weight), 7 splits q, 8 fetches
+// page holds behind the sequence's end, so that NaN there meets no weight), 7 splits q and fetches
 // the scales. All waits on barriers are bounded.
 #include <float.h>
 
@@ -48,16 +50,17 @@ constexpr int kScRing = 2;        // tiles of scales in shared memory
 constexpr int kPageChunk = 128;   // block-table entries staged at a time
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRise = 3.0f;     // m follows a score that is this far (base 2) above it
-constexpr float kWeight = 4096.0f;  // weights are at most 2^3; e5m2 ends at 57344
+// The weight of the score that m was taken from is 2^kTop; m stays until a weight passes
+// 2^kMost (where f16 would not hold 8 times what the first piece leaves).
+constexpr float kTop = 11.0f, kMost = 15.0f;
 
 // R query rows of a unit at a time; ST stages in each of the K and V rings; CTAS per SM.
 template <int HD, int R_>
 struct Q8Layout {
   static constexpr int R = R_;
-  static constexpr int CTAS = (R == 8 && HD <= 128) ? 2 : 1;
-  static constexpr int ST = HD == 64 ? (CTAS == 2 ? 5 : 6) : HD == 128 ? (CTAS == 2 ? 3 : 5)
-                                                                     : (R == 8 ? 3 : 2);
+  static constexpr int CTAS = (R <= 16 && HD <= 128) ? 2 : 1;
+  static constexpr int ST = HD == 64 ? (R == 8 ? 5 : 4) : HD == 128 ? (R == 8 ? 3 : R == 16 ? 2 : 5)
+                                                                    : (R == 8 ? 3 : 2);
   static constexpr int CH = HD <= 128 ? HD : 128;   // columns (bytes) of a swizzled row
   static constexpr int KCH = HD / CH;               // row chunks: 1, or 2 at head_dim 256
   static constexpr int NS = 2 * R;                  // columns of S^T: hi rows, lo rows
@@ -75,8 +78,8 @@ struct Q8Layout {
   static constexpr int TMEM_USED = COL_O + KCH * NP;
   static constexpr int TMEM_COLS = TMEM_USED <= 64 ? 64 : TMEM_USED <= 128 ? 128
                                    : TMEM_USED <= 256 ? 256 : 512;
-  static constexpr int THREADS = 288;
-  static constexpr int TMA_WARP = 4, S_WARP = 5, O_WARP = 6, Q_WARP = 7, SC_WARP = 8;
+  static constexpr int THREADS = 256;
+  static constexpr int TMA_WARP = 4, S_WARP = 5, O_WARP = 6, QS_WARP = 7;
   static_assert(TMEM_USED <= 512 && TMEM_COLS * CTAS <= 512, "TMEM budget");
   // dynamic, static (pages, scales, barriers, rows: below) and the driver's 1 KB
   static constexpr int STATIC_BYTES = 4 * kPageChunk + 8 * kScRing * kKT + 64 * R + 512;
@@ -133,15 +136,29 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&r)[8]) {
                "r"(__float_as_uint(r[6])), "r"(__float_as_uint(r[7]))
                : "memory");
 }
-// Two floats -> two e5m2 codes (nearest even), and back: e5m2 is the upper half of an f16.
-__device__ __forceinline__ uint32_t e5m2x2_from_f32(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
+// N = 16, 32 or 64 columns of a TMEM lane.
+template <int N>
+__device__ __forceinline__ void load_cols(uint32_t taddr, uint32_t (&r)[N]) {
+  if constexpr (N == 16) {
+    tmem_ld16(taddr, r);
+  } else {
+#pragma unroll
+    for (int c = 0; c < N; c += 32) tmem_ld32(taddr + c, *reinterpret_cast<uint32_t(*)[32]>(&r[c]));
+  }
 }
-__device__ __forceinline__ float2 f32_from_e5m2x2(uint32_t codes) {
-  const uint32_t h = __byte_perm(codes, 0, 0x1404);  // bytes 1 and 0 as the halves' upper bytes
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+// Two weights (>= 0, at most 2^15) -> two f16 rounded to 9 bits (half up).
+__device__ __forceinline__ uint32_t weight_f16x2(float lo, float hi) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
+  return (h + 0x00020002u) & 0xfffcfffcu;
+}
+// 8 times what their upper bytes (the e5m2 pieces) leave; exact, and below 2^16.
+__device__ __forceinline__ uint32_t f16x2_rest(uint32_t h) {
+  const uint32_t top = h & 0xff00ff00u;
+  const __half2 r = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&h),
+                                    *reinterpret_cast<const __half2*>(&top)),
+                            __float2half2_rn(8.0f));
+  return *reinterpret_cast<const uint32_t*>(&r);
 }
 // The barrier of the 128 softmax threads; true where any of them came with `v`.
 __device__ __forceinline__ bool softmax_any(bool v) {
@@ -153,6 +170,14 @@ __device__ __forceinline__ bool softmax_any(bool v) {
       : "r"((int)v)
       : "memory");
   return r != 0;
+}
+// mbar_wait with its polling out of line: the roles' loops stay short (they share the SM's
+// instruction cache).
+__device__ __noinline__ bool wait_more(uint64_t* bar, uint32_t parity, WaitCtl* w) {
+  return mbar_wait(bar, parity, w);
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, WaitCtl* w) {
+  return mbar_try_wait(bar, parity) || wait_more(bar, parity, w);
 }
 // Largest value of the warp (NaN is passed over), by the integer reduction: floats in the order
 // of their bits once the negative ones are turned around.
@@ -185,44 +210,47 @@ __device__ __forceinline__ int q8_len(const Q8K& p, int b) {
   return raw < 0 ? 0 : raw > cap ? (int)cap : raw;
 }
 
-// Tiles of the whole list, per unit of a sequence (times Hk * rb units each), by one warp.
-__device__ __forceinline__ long long q8_all_tiles(const Q8K& p, int lane) {
-  long long sum = 0;
-  for (int b = lane; b < p.B; b += 32) sum += (q8_len(p, b) + kKT - 1) / kKT;
-  for (int o = 16; o > 0; o /= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return sum * p.Hk * p.rb;
+__device__ __forceinline__ int q8_tiles(const Q8K& p, int b) {
+  return (q8_len(p, b) + kKT - 1) / kKT;
+}
+// Key tiles of all sequences (of one unit each), by one warp that has those of sequence `lane`.
+// The host has checked that the list of all tiles, Hk * rb times as long, fits 31 bits.
+__device__ __forceinline__ int q8_all_tiles(const Q8K& p, int mine, int lane) {
+  for (int b = lane + 32; b < p.B; b += 32) mine += q8_tiles(p, b);
+  return (int)__reduce_add_sync(0xffffffffu, (unsigned)mine);
 }
 // Tiles of a CTA: the list cut evenly over the grid.
-__device__ __forceinline__ long long q8_share(long long all, long long grid) {
+__device__ __forceinline__ unsigned q8_share(unsigned all, unsigned grid) {
   return (all + grid - 1) / grid;
 }
 
 // The units of a CTA's share [t, t1) of the list, in order. Every role walks its own copy.
 struct Walk {
-  long long t, t1;   // next tile of the list, end of the share
-  long long pre;     // tiles of the list before sequence b
+  unsigned t, t1;    // next tile of the list, end of the share
+  unsigned pre;      // tiles of the list before sequence b
   int b, nt, len;    // sequence, its tiles for each unit, its length
   // the unit found by next()
   int kh, rb, ja, jb;  // kv head, row block, tiles [ja, jb) of it (tiles that no row sees left out)
   int whole;           // the share has all of the unit
   int first;           // the share has its first tile
 
-  // Starts at tile t0 (warp-wide).
-  __device__ __forceinline__ void init(const Q8K& p, long long t0, long long end, int lane) {
-    t = t0;
-    t1 = end;
+  // The share of CTA `cta` (warp-wide).
+  __device__ __forceinline__ void init(const Q8K& p, unsigned cta, unsigned grid, int lane) {
+    const unsigned U = (unsigned)(p.Hk * p.rb);
+    const int mine = lane < p.B ? q8_tiles(p, lane) : 0;
+    const unsigned all = (unsigned)q8_all_tiles(p, mine, lane) * U;
+    const unsigned per = q8_share(all, grid);
+    t = per * cta;  // (below all + grid)
+    t1 = min(t + per, all);
     pre = 0;
-    b = 0;
-    nt = 0;
-    len = 0;
+    b = nt = len = 0;
     if (t >= t1) return;
-    const long long U = (long long)p.Hk * p.rb;
     for (int base = 0;; base += 32) {  // ends: t lies below the sum over all sequences
-      const int i = base + lane;
-      const long long n = i < p.B ? (long long)((q8_len(p, i) + kKT - 1) / kKT) * U : 0;
-      long long upto = n;
+      const unsigned n =
+          (base == 0 ? mine : base + lane < p.B ? q8_tiles(p, base + lane) : 0) * U;
+      unsigned upto = n;
       for (int o = 1; o < 32; o *= 2) {
-        const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+        const unsigned x = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += x;
       }
       const unsigned beyond = __ballot_sync(0xffffffffu, pre + upto > t);
@@ -240,34 +268,39 @@ struct Walk {
 
   __device__ __forceinline__ bool next(const Q8K& p, int R) {
     if (t >= t1) return false;
-    const long long U = (long long)p.Hk * p.rb;
+    const unsigned U = (unsigned)(p.Hk * p.rb);
     while (t >= pre + U * nt) {  // the next sequence with keys
       pre += U * nt;
       if (++b >= p.B) return false;
       len = q8_len(p, b);
       nt = (len + kKT - 1) / kKT;
     }
-    const long long in = t - pre;
-    const int u = (int)(in / nt);
-    ja = (int)(in % nt);
-    kh = u / p.rb;
-    rb = u % p.rb;
-    const long long left = t1 - t;
-    const int je = left < nt - ja ? ja + (int)left : nt;
+    const unsigned in = t - pre, u = in / (unsigned)nt;
+    ja = (int)(in - u * nt);
+    kh = (int)u;
+    rb = 0;
+    if (p.rb > 1) {
+      kh = (int)(u / (unsigned)p.rb);
+      rb = (int)u - kh * p.rb;
+    }
+    const int je = min(nt, ja + (int)(t1 - t));
     t += je - ja;
     first = ja == 0;
     whole = first && je == nt;
     // keys that any row of the block sees
-    const int r0 = rb * R, r1 = min(p.rows, r0 + R) - 1;
-    const int imax = r0 / p.lq == r1 / p.lq ? r1 % p.lq : p.lq - 1;
-    const int seen = p.causal ? max(0, len - p.lq + imax + 1) : len;
-    jb = max(ja, min(je, (seen + kKT - 1) / kKT));
+    jb = je;
+    if (p.causal && p.lq > 1) {
+      const int r0 = rb * R, r1 = min(p.rows, r0 + R) - 1;
+      const int imax = r0 / p.lq == r1 / p.lq ? r1 % p.lq : p.lq - 1;
+      const int seen = max(0, len - p.lq + imax + 1);
+      jb = max(ja, min(je, (seen + kKT - 1) / kKT));
+    }
     return true;
   }
 };
 
 template <int HD, int R>
-__global__ void __launch_bounds__(288, Q8Layout<HD, R>::CTAS)
+__global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
     q8_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
                    const Q8K p) {
   using LY = Q8Layout<HD, R>;
@@ -285,9 +318,11 @@ __global__ void __launch_bounds__(288, Q8Layout<HD, R>::CTAS)
   __shared__ float sc_s[kScRing][2][kKT];  // key scale, log2 of the value scale
   __shared__ __align__(16) float qs_s[2][R];   // rows: score factor, key limit
   __shared__ __align__(16) int lim_s[2][R];
-  __shared__ __align__(16) float m_s[R], red_s[4][R];
+  __shared__ __align__(16) float nm_s[R], red_s[4][R], f_s[R];  // -m; sums or maxima; O's factors
 
   const int warp = warp_id(), lane = lane_id();
+  Walk w;
+  w.init(p, blockIdx.x, gridDim.x, lane);
   if (threadIdx.x == 0) {
     wait_ctl_init(&wctl, p.wait_limit_ns);
     bad_input = 0;
@@ -323,17 +358,10 @@ __global__ void __launch_bounds__(288, Q8Layout<HD, R>::CTAS)
   const uint32_t tbase = tmem_base_s;
   grid_dep_trigger();
 
-  Walk w;
-  {
-    const long long all = q8_all_tiles(p, lane);
-    const long long per = q8_share(all, gridDim.x);
-    const long long t0 = per * blockIdx.x;
-    w.init(p, t0, t0 + per < all ? t0 + per : all, lane);
-    if (warp == 0 && blockIdx.x == 0) {  // lengths out of range are clamped, and reported here
-      bool bad = false;
-      for (int b = lane; b < p.B; b += 32) bad |= p.lens[b] != q8_len(p, b);
-      if (bad) bad_input = 1;
-    }
+  if (warp == 0 && blockIdx.x == 0) {  // lengths out of range are clamped, and reported here
+    bool bad = false;
+    for (int b = lane; b < p.B; b += 32) bad |= p.lens[b] != q8_len(p, b);
+    if (bad) bad_input = 1;
   }
 
   if (warp == LY::TMA_WARP) {
@@ -386,7 +414,7 @@ __global__ void __launch_bounds__(288, Q8Layout<HD, R>::CTAS)
         for (int which = 0; which < 2; ++which) {
           uint64_t* full = which ? &v_full[st] : &k_full[st];
           if (leader) {
-            if (use > 0) ok = mbar_wait(which ? &v_empty[st] : &k_empty[st], (use - 1) & 1, &wctl);
+            if (use > 0) ok = wait(which ? &v_empty[st] : &k_empty[st], (use - 1) & 1, &wctl);
             if (ok) mbar_arrive_expect_tx(full, LY::KV_BYTES);
           }
           ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -416,13 +444,13 @@ __global__ void __launch_bounds__(288, Q8Layout<HD, R>::CTAS)
       int g = 0, un = 0;
       bool ok = true;
       for (; ok && w.next(p, R); ++un) {
-        ok = mbar_wait(&q_full[un & 1], (un >> 1) & 1, &wctl);
+        ok = wait(&q_full[un & 1], (un >> 1) & 1, &wctl);
         if (!ok) break;
         const Desc qb = q8_desc<CH>(smem_u32(smem + LY::OFF_Q + (un & 1) * LY::Q_BYTES), 0);
         for (int j = w.ja; j < w.jb; ++j, ++g) {
           const int st = g % ST, buf = g & 1;
-          ok = mbar_wait(&k_full[st], (g / ST) & 1, &wctl);
-          if (ok && g >= 2) ok = mbar_wait(&s_free[buf], ((g >> 1) - 1) & 1, &wctl);
+          ok = wait(&k_full[st], (g / ST) & 1, &wctl);
+          if (ok && g >= 2) ok = wait(&s_free[buf], ((g >> 1) - 1) & 1, &wctl);
           if (!ok) break;
           tc_fence_after();
           const Desc ka = q8_desc<CH>(smem_u32(smem + LY::OFF_K + st * LY::KV_BYTES), 0);
@@ -450,8 +478,8 @@ __global__ void __launch_bounds__(288, Q8Layout<HD, R>::CTAS)
     while (ok && w.next(p, R)) {
       for (int j = w.ja; j < w.jb; ++j, ++g) {
         const int st = g % ST, buf = g & 1, n0 = j * kKT;
-        ok = __all_sync(0xffffffffu, mbar_wait(&p_full[buf], (g >> 1) & 1, &wctl));
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&v_full[st], (g / ST) & 1, &wctl));
+        ok = __all_sync(0xffffffffu, wait(&p_full[buf], (g >> 1) & 1, &wctl));
+        if (ok) ok = __all_sync(0xffffffffu, wait(&v_full[st], (g / ST) & 1, &wctl));
         if (!ok) break;
         uint8_t* vt = smem + LY::OFF_V + st * LY::KV_BYTES;
         if (n0 + kKT > w.len) {  // rows behind the sequence's end
@@ -485,26 +513,58 @@ __global__ void __launch_bounds__(288, Q8Layout<HD, R>::CTAS)
       mbar_wait_drain(&drain_o, 0);
     }
     __syncwarp();
-  } else if (warp == LY::Q_WARP) {
-    // ------------------------------------------------------------------ q in two pieces
+  } else if (warp == LY::QS_WARP) {
+    // ------------------------------------------------------------------ q in two pieces, and
+    // the keys' scales: those of two tiles are on their way in registers, and the table entries
+    // of the two after them
     constexpr int CPL = HD / 32;  // columns of a lane
-    int un = 0;
-    for (; w.next(p, R); ++un) {
+    int g = 0, un = 0;
+    bool ok = true;
+    const int nb_shift = p.ps_shift - p.sb_shift;
+    for (; ok && w.next(p, R); ++un) {
+      const int32_t* row = p.table + (size_t)w.b * p.max_pages;
+      int pg[2][4];
+      float ks[2][4], vs[2][4];
+      auto pages = [&](int j, int (&to)[4]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = j * kKT + e * 32 + lane;
+          to[e] = key < w.len && j < w.jb ? row[key >> p.ps_shift] : -1;
+        }
+      };
+      auto scales = [&](int j, const int (&pgs)[4], float (&k)[4], float (&v)[4]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = j * kKT + e * 32 + lane;
+          const bool have = pgs[e] >= 0 && pgs[e] < p.num_pages;
+          const size_t at = (((size_t)(have ? pgs[e] : 0) * p.Hk + w.kh) << nb_shift) +
+                            ((key & ((1 << p.ps_shift) - 1)) >> p.sb_shift);
+          k[e] = have ? __ldg(p.k_scale + at) : 0.0f;
+          v[e] = have ? __ldg(p.v_scale + at) : 1.0f;
+        }
+      };
+      pages(w.ja, pg[0]);
+      pages(w.ja + 1, pg[1]);
       const int qb = un & 1;
       if (un >= 2 &&
-          !__all_sync(0xffffffffu, mbar_wait(&q_free[qb], ((un >> 1) - 1) & 1, &wctl)))
+          !__all_sync(0xffffffffu, wait(&q_free[qb], ((un >> 1) - 1) & 1, &wctl)))
         break;
       uint8_t* dst = smem + LY::OFF_Q + qb * LY::Q_BYTES;
       const int r0 = w.rb * R;
       const __nv_bfloat16* src =
           p.q + (((size_t)w.b * p.Hk + w.kh) * p.rows + r0) * HD + lane * CPL;
+      const int live = min(R, p.rows - r0);
+      if (lane < R) {
+        const int i = (r0 + lane) % p.lq;
+        lim_s[qb][lane] = p.causal ? max(0, w.len - p.lq + i + 1) : w.len;
+      }
+      float mine = 0.0f;  // the score factor of row `lane`
 #pragma unroll 4
-      for (int r = 0; r < R; ++r) {
-        const bool live = r0 + r < p.rows;
+      for (int r = 0; r < live; ++r) {
         uint32_t x[CPL / 2];
 #pragma unroll
         for (int e = 0; e < CPL / 2; ++e)
-          x[e] = live ? reinterpret_cast<const uint32_t*>(src + (size_t)r * HD)[e] : 0u;
+          x[e] = reinterpret_cast<const uint32_t*>(src + (size_t)r * HD)[e];
         uint32_t a = 0;
 #pragma unroll
         for (int e = 0; e < CPL / 2; ++e)
@@ -544,48 +604,14 @@ __global__ void __launch_bounds__(288, Q8Layout<HD, R>::CTAS)
           else
             *reinterpret_cast<uint2*>(at) = half ? make_uint2(lo, lo2) : make_uint2(hi, hi2);
         }
-        if (lane == 0) {
-          const int i = (r0 + r) % p.lq;
-          qs_s[qb][r] = live ? p.scale_log2 * __int_as_float((127 - sh / 2) << 23) *
-                                   __int_as_float((127 - (sh - sh / 2)) << 23)
-                             : 0.0f;
-          lim_s[qb][r] = !live ? 0 : p.causal ? max(0, w.len - p.lq + i + 1) : w.len;
-        }
+        if (lane == r)
+          mine = p.scale_log2 * __int_as_float((127 - sh / 2) << 23) *
+                 __int_as_float((127 - (sh - sh / 2)) << 23);
       }
+      if (lane < R) qs_s[qb][lane] = mine;
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[qb]);
-    }
-  } else if (warp == LY::SC_WARP) {
-    // ------------------------------------------------------------------ scales: those of two
-    // tiles are on their way in registers, and the table entries of the two after them
-    int g = 0;
-    bool ok = true;
-    const int nb_shift = p.ps_shift - p.sb_shift;
-    while (ok && w.next(p, R)) {
-      const int32_t* row = p.table + (size_t)w.b * p.max_pages;
-      int pg[2][4];
-      float ks[2][4], vs[2][4];
-      auto pages = [&](int j, int (&to)[4]) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = j * kKT + e * 32 + lane;
-          to[e] = key < w.len && j < w.jb ? row[key >> p.ps_shift] : -1;
-        }
-      };
-      auto scales = [&](int j, const int (&pgs)[4], float (&k)[4], float (&v)[4]) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = j * kKT + e * 32 + lane;
-          const bool have = pgs[e] >= 0 && pgs[e] < p.num_pages;
-          const size_t at = (((size_t)(have ? pgs[e] : 0) * p.Hk + w.kh) << nb_shift) +
-                            ((key & ((1 << p.ps_shift) - 1)) >> p.sb_shift);
-          k[e] = have ? __ldg(p.k_scale + at) : 0.0f;
-          v[e] = have ? __ldg(p.v_scale + at) : 1.0f;
-        }
-      };
-      pages(w.ja, pg[0]);
-      pages(w.ja + 1, pg[1]);
       scales(w.ja, pg[0], ks[0], vs[0]);
       scales(w.ja + 1, pg[1], ks[1], vs[1]);
       pages(w.ja + 2, pg[0]);
@@ -596,7 +622,7 @@ __global__ void __launch_bounds__(288, Q8Layout<HD, R>::CTAS)
           if (j + h >= w.jb) break;
           const int slot = g % kScRing;
           if (g >= kScRing)
-            ok = __all_sync(0xffffffffu, mbar_wait(&sc_free[slot], (g / kScRing - 1) & 1, &wctl));
+            ok = __all_sync(0xffffffffu, wait(&sc_free[slot], (g / kScRing - 1) & 1, &wctl));
           if (!ok) break;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -613,67 +639,68 @@ __global__ void __launch_bounds__(288, Q8Layout<HD, R>::CTAS)
       }
     }
   } else {
-    // ------------------------------------------------------------------ softmax, and O out
+    // ------------------------------------------------------------------ softmax, and O out.
+    // Rows that are not there (live of the R are) are passed over: their columns of q, S, w and O
+    // hold anything and are never used. A wait that runs out shows at the next softmax_any, where all threads leave
+    // together.
     const int key = threadIdx.x;  // key of the tile
     const uint32_t lanes = tbase + ((uint32_t)(warp * 32) << 16);
     int g = 0, un = 0;
     bool ok = true;
     for (; ok && w.next(p, R); ++un) {
       const int qb = un & 1;
-      ok = mbar_wait(&q_full[qb], (un >> 1) & 1, &wctl);
-      // (a wait that ran out shows at the next softmax_any, where all threads leave together)
+      ok = wait(&q_full[qb], (un >> 1) & 1, &wctl);
       const int r0 = w.rb * R, live = min(R, p.rows - r0);
-      int lim_min = w.len;  // tiles below it need no test of the keys
-      if (p.causal) lim_min = max(0, w.len - p.lq + 1);
+      // tiles below lim_min need no test of the keys
+      const int lim_min = p.causal ? max(0, w.len - p.lq + 1) : w.len;
       float l[R];
 #pragma unroll
       for (int r = 0; r < R; ++r) l[r] = 0.0f;
-      // rows that are not there: m far above every score, so that they weigh nothing
-      if (key < R) m_s[key] = key < live ? 0.0f : 1e30f;
+      if (key < R) nm_s[key] = key < live ? 0.0f : -1e30f;  // (an odd live has a neighbour)
       if (softmax_any(!ok)) {
         ok = false;
         break;
       }
       for (int j = w.ja; j < w.jb; ++j, ++g) {
         const int buf = g & 1, slot = g % kScRing, n0 = j * kKT;
-        ok = ok && mbar_wait(&sc_full[slot], (g / kScRing) & 1, &wctl);
+        ok = ok && wait(&sc_full[slot], (g / kScRing) & 1, &wctl);
         const float kc = sc_s[slot][0][key], lsv = sc_s[slot][1][key];
-        const float inv = ex2(-lsv);  // 1 / value scale
-        ok = __all_sync(0xffffffffu, ok && mbar_wait(&s_full[buf], (g >> 1) & 1, &wctl));
+        ok = __all_sync(0xffffffffu, ok && wait(&s_full[buf], (g >> 1) & 1, &wctl));
         tc_fence_after();
-        float t[R];
-        const uint32_t tS = lanes + LY::COL_S + buf * NS;
-        float top = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < R; c += 8) {
-          float hi[8], lo[8];
-          tmem_ld8(tS + c, hi);
-          tmem_ld8(tS + R + c, lo);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float s = fmaf(lo[e], 0.0625f, hi[e]) * kc;
-            t[c + e] = fmaf(s, qs_s[qb][c + e], lsv - m_s[c + e]);
-          }
-        }
+        uint32_t sr[NS];
+        load_cols<NS>(lanes + LY::COL_S + buf * NS, sr);
+        tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&s_free[buf]);
           mbar_arrive(&sc_free[slot]);
         }
-        if (n0 + kKT > lim_min) {
+        float t[R];
+        float top = -INFINITY;
+        const uint64_t kc2 = f2_pack(kc, kc), lsv2 = f2_pack(lsv, lsv);
+        const uint64_t sixteenth = f2_pack(0.0625f, 0.0625f);
 #pragma unroll
-          for (int r = 0; r < R; ++r)
+        for (int r = 0; r < R; r += 2) {
+          if (r >= live) break;
+          const uint64_t hi = f2_pack(__uint_as_float(sr[r]), __uint_as_float(sr[r + 1]));
+          const uint64_t lo = f2_pack(__uint_as_float(sr[R + r]), __uint_as_float(sr[R + r + 1]));
+          const uint64_t s = f2_mul(f2_fma(lo, sixteenth, hi), kc2);
+          const uint64_t qs = *reinterpret_cast<const uint64_t*>(&qs_s[qb][r]);
+          const uint64_t nm = *reinterpret_cast<const uint64_t*>(&nm_s[r]);
+          f2_unpack(f2_fma(s, qs, f2_add(lsv2, nm)), t[r], t[r + 1]);
+          if (n0 + kKT > lim_min) {
             if (n0 + key >= lim_s[qb][r]) t[r] = -INFINITY;
+            if (n0 + key >= lim_s[qb][r + 1]) t[r + 1] = -INFINITY;
+          }
+          top = fmax3(top, t[r], t[r + 1]);
         }
-#pragma unroll
-        for (int r = 0; r < R; ++r) top = fmaxf(top, t[r]);
         const bool first = j == w.ja;
-        if (softmax_any(top > kRise || first || !ok)) {
+        if (softmax_any(top > kMost || first || !ok)) {
           // m moves: to the largest score so far, at the first tile to the tile's own
 #pragma unroll
           for (int r = 0; r < R; ++r) {
+            if (r >= live) break;
             const float mx = warp_max(t[r]);
             if (lane == 0) red_s[warp][r] = mx;
           }
@@ -681,25 +708,25 @@ __global__ void __launch_bounds__(288, Q8Layout<HD, R>::CTAS)
             ok = false;
             break;
           }
-          if (!first) {  // O is about to be scaled: the last O^T MMA must be done
-            ok = mbar_wait(&p_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &wctl);
-            ok = __all_sync(0xffffffffu, ok);
-            tc_fence_after();
+          float f[R];
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            if (r >= live) break;
+            const float mx = fmaxf(fmaxf(red_s[0][r], red_s[1][r]),
+                                   fmaxf(red_s[2][r], red_s[3][r]));
+            float up = mx - kTop;
+            if (first ? mx == -INFINITY : !(up > 0.0f)) up = 0.0f;
+            t[r] -= up;
+            f[r] = first ? 1.0f : ex2(-up);
+            l[r] *= f[r];
+            if (key == r) nm_s[r] -= up;
           }
+          if (!first) {  // O is scaled, once the last O^T MMA is done
+            ok = __all_sync(0xffffffffu, wait(&p_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &wctl));
+            tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < R; c += 8) {
-            float f[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int r = c + e;
-              float up = fmaxf(fmaxf(red_s[0][r], red_s[1][r]), fmaxf(red_s[2][r], red_s[3][r]));
-              if (first ? up == -INFINITY || r >= live : !(up > 0.0f)) up = 0.0f;
-              f[e] = ex2(-up);
-              t[r] -= up;
-              if (!first) l[r] *= f[e];
-              if (key == r) m_s[r] += up;
-            }
-            if (!first) {
+            for (int c = 0; c < R; c += 8) {
+              if (c >= live) break;
 #pragma unroll 1
               for (int h = 0; h < KCH * 3; ++h) {
                 const uint32_t at = lanes + LY::COL_O + h / 3 * NP + h % 3 * R + c;
@@ -707,39 +734,36 @@ __global__ void __launch_bounds__(288, Q8Layout<HD, R>::CTAS)
                 tmem_ld8(at, x);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] *= f[e];
+                for (int e = 0; e < 8; ++e) x[e] *= f[c + e];
                 tmem_st8(at, x);
               }
             }
-          }
-          if (!first) {
             tmem_wait_st();
             tc_fence_before();
           }
-          softmax_any(false);  // m_s is read, and red_s written, by everyone after this
+          softmax_any(false);  // nm_s is read, and red_s written, by everyone after this
         }
         // weights, their sum, and their pieces into shared memory, the key's row of NP bytes
-        if (g >= 2) ok = ok && mbar_wait(&p_done[buf], ((g >> 1) - 1) & 1, &wctl);
+        const float inv = ex2(-lsv);  // 1 / value scale
+        if (g >= 2) ok = ok && wait(&p_done[buf], ((g >> 1) - 1) & 1, &wctl);
         uint8_t* prow = smem + LY::OFF_P + buf * LY::P_BYTES + key * NP;
         uint32_t pc[3][R / 4];
 #pragma unroll
-        for (int r = 0; r < R; r += 2) {
-          float a = ex2(t[r]), b = ex2(t[r + 1]);
-          l[r] = fmaf(a, inv, l[r]);
-          l[r + 1] = fmaf(b, inv, l[r + 1]);
-          a *= kWeight;
-          b *= kWeight;
-          uint32_t x[3];
+        for (int r = 0; r < R; r += 4) {
+          if (r >= live) break;
+          uint32_t h[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float a = ex2(t[r + 2 * e]), b = ex2(t[r + 2 * e + 1]);
+            l[r + 2 * e] = fmaf(a, inv, l[r + 2 * e]);
+            l[r + 2 * e + 1] = fmaf(b, inv, l[r + 2 * e + 1]);
+            h[e] = weight_f16x2(a, b);
+          }
 #pragma unroll
           for (int i = 0; i < 3; ++i) {
-            x[i] = e5m2x2_from_f32(a, b);
-            const float2 back = f32_from_e5m2x2(x[i]);
-            a = (a - back.x) * 8.0f;
-            b = (b - back.y) * 8.0f;
-            if (r % 4 == 0)
-              pc[i][r / 4] = x[i];
-            else
-              pc[i][r / 4] |= x[i] << 16;
+            pc[i][r / 4] = __byte_perm(h[0], h[1], 0x7531);
+            h[0] = f16x2_rest(h[0]);
+            h[1] = f16x2_rest(h[1]);
           }
         }
         if constexpr (R == 8) {
@@ -749,17 +773,18 @@ __global__ void __launch_bounds__(288, Q8Layout<HD, R>::CTAS)
               make_uint4(pc[2][0], pc[2][1], 0u, 0u);
         } else {
 #pragma unroll
-          for (int i = 0; i < 3; ++i)
+          for (int x = 0; x < R / 16; ++x) {
+            if (16 * x >= live) break;
 #pragma unroll
-            for (int x = 0; x < R / 16; ++x)
+            for (int i = 0; i < 3; ++i)
               *reinterpret_cast<uint4*>(prow + swz<NP>(i * (R / 16) + x, key) * 16) = make_uint4(
                   pc[i][4 * x], pc[i][4 * x + 1], pc[i][4 * x + 2], pc[i][4 * x + 3]);
+          }
         }
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[buf]);
       }
-      if (!__all_sync(0xffffffffu, ok)) ok = false;
       // the sums of the 128 keys' threads
       if (softmax_any(!ok)) {
         ok = false;
@@ -767,12 +792,13 @@ __global__ void __launch_bounds__(288, Q8Layout<HD, R>::CTAS)
       }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
+        if (r >= live) break;
         float x = l[r];
         for (int o = 16; o > 0; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
         if (lane == 0) red_s[warp][r] = x;
       }
       const bool any = w.jb > w.ja;
-      if (any) ok = mbar_wait(&p_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &wctl);
+      if (any) ok = wait(&p_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &wctl);
       if (softmax_any(!ok)) {
         ok = false;
         break;
@@ -780,11 +806,23 @@ __global__ void __launch_bounds__(288, Q8Layout<HD, R>::CTAS)
       tc_fence_after();
       const size_t unit_row = ((size_t)w.b * p.Hk + w.kh) * p.rows + r0;
       const size_t part = 2 * (size_t)blockIdx.x + (w.first ? 1 : 0);
+      // a row without keys: sum 0, and O (which may hold anything then) 0
+      if (key < live) {
+        const float sum = red_s[0][key] + red_s[1][key] + red_s[2][key] + red_s[3][key];
+        f_s[key] = sum == 0.0f ? 0.0f : w.whole ? 1.0f / sum : 1.0f;
+        if (!w.whole) {
+          p.ml_part[part * 2 * R + key] = -nm_s[key];
+          p.ml_part[part * 2 * R + R + key] = sum;
+        } else if (p.lse) {
+          p.lse[unit_row + key] = sum == 0.0f ? -INFINITY : fmaf(-nm_s[key], kLn2, logf(sum));
+        }
+      }
+      softmax_any(false);
       // this thread's head-dim row: a 64-row accumulator lies in lanes 0-15 of each warp
       const int col = HD == 64 ? warp * 16 + lane : (int)threadIdx.x;
       const bool mine = HD > 64 || lane < 16;
 #pragma unroll 1
-      for (int c = 0; c < R; c += 8) {
+      for (int c = 0; c < live; c += 8) {
 #pragma unroll 1
         for (int h = 0; h < KCH; ++h) {
           float x[8], y[8], z[8];
@@ -795,32 +833,23 @@ __global__ void __launch_bounds__(288, Q8Layout<HD, R>::CTAS)
             tmem_ld8(at + 2 * R, z);
             tmem_wait_ld();
           }
+          const size_t row0 = (w.whole ? unit_row : part * R) + c;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const int r = c + e;
-            const float sum = red_s[0][r] + red_s[1][r] + red_s[2][r] + red_s[3][r];
-            const float o = any ? fmaf(fmaf(z[e], 0.125f, y[e]), 0.125f, x[e]) / kWeight : 0.0f;
-            if (!mine || r >= live) continue;
+            if (!mine || c + e >= live) break;
+            const float f = f_s[c + e];
+            const float o = f == 0.0f ? 0.0f : fmaf(fmaf(z[e], 0.125f, y[e]), 0.125f, x[e]) * f;
+            const size_t at = (row0 + e) * HD + h * 128 + col;
             if (w.whole)
-              p.o[(unit_row + r) * HD + h * 128 + col] =
-                  __float2bfloat16(sum == 0.0f ? 0.0f : o / sum);
+              p.o[at] = __float2bfloat16(o);
             else
-              p.o_part[(part * R + r) * HD + h * 128 + col] = sum == 0.0f ? 0.0f : o;
+              p.o_part[at] = o;
           }
-        }
-      }
-      if (key < live) {
-        const float sum = red_s[0][key] + red_s[1][key] + red_s[2][key] + red_s[3][key];
-        if (!w.whole) {
-          p.ml_part[part * 2 * R + key] = m_s[key];
-          p.ml_part[part * 2 * R + R + key] = sum;
-        } else if (p.lse) {
-          p.lse[unit_row + key] = sum == 0.0f ? -INFINITY : fmaf(m_s[key], kLn2, logf(sum));
         }
       }
       tc_fence_before();
       if (threadIdx.x == 0) mbar_arrive(&q_free[qb]);
-      softmax_any(false);  // red_s and m_s may be written again
+      softmax_any(false);  // what is in shared memory may be written again
     }
   }
 
@@ -839,23 +868,23 @@ template <int HD, int R>
 __global__ void __launch_bounds__(256) q8_combine_kernel(const Q8K p, int grid) {
   const int lane = lane_id();
   grid_dep_wait();
-  const long long u = blockIdx.x;  // (b * Hk + kh) * rb + row block
-  const int U = p.Hk * p.rb;
-  const int b = (int)(u / U), in = (int)(u % U);
+  const unsigned U = (unsigned)(p.Hk * p.rb);  // blockIdx.x: (b * Hk + kh) * rb + row block
+  const int b = (int)(blockIdx.x / U), in = (int)(blockIdx.x % U);
   const int r0 = in % p.rb * R, live = min(R, p.rows - r0);
   const size_t unit_row = ((size_t)b * p.Hk + in / p.rb) * p.rows + r0;
-  const int nt = (q8_len(p, b) + kKT - 1) / kKT;
+  const int nt = q8_tiles(p, b);
   if (nt == 0) {
     for (int e = threadIdx.x; e < live * HD; e += 256) p.o[unit_row * HD + e] = __float2bfloat16(0.f);
     if (p.lse && threadIdx.x < live) p.lse[unit_row + threadIdx.x] = -INFINITY;
     return;
   }
   // every warp finds the unit's place in the list for itself
-  long long before = 0;
-  for (int i = lane; i < b; i += 32) before += (q8_len(p, i) + kKT - 1) / kKT;
-  for (int o = 16; o > 0; o /= 2) before += __shfl_xor_sync(0xffffffffu, before, o);
-  const long long per = q8_share(q8_all_tiles(p, lane), grid);
-  const long long a = before * U + (long long)in * nt;
+  unsigned before = 0;
+  for (int i = lane; i < b; i += 32) before += q8_tiles(p, i);
+  before = __reduce_add_sync(0xffffffffu, before);
+  const int mine = lane < p.B ? q8_tiles(p, lane) : 0;
+  const unsigned per = q8_share((unsigned)q8_all_tiles(p, mine, lane) * U, grid);
+  const unsigned a = before * U + (unsigned)in * nt;
   const int c0 = (int)(a / per), c1 = (int)((a + nt - 1) / per);
   if (c0 == c1) return;  // written whole
   // share i: slot 2 c0 + 1 (it begins there), then 2 c of each further CTA
@@ -898,7 +927,7 @@ Plan make_plan(const Q8AttnArgs& a) {
   const int rows = a.G * a.lq;
   pl.R = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
   pl.rb = (rows + pl.R - 1) / pl.R;
-  const int ctas = 152 * (pl.R == 8 && a.d <= 128 ? 2 : 1);
+  const int ctas = 152 * (pl.R <= 16 && a.d <= 128 ? 2 : 1);
   const long long cap = (long long)a.max_pages << a.ps_shift;
   const long long tiles = (cap + kKT - 1) / kKT * a.B * a.Hk * pl.rb;
   pl.grid = (int)std::min<long long>(ctas, tiles);
@@ -962,8 +991,9 @@ cudaError_t attn_d(const Q8AttnArgs& a, const Q8AttnMaps& m, const Plan& pl, voi
 int q8_box_rows(int page_size) { return page_size < kKT ? page_size : kKT; }
 int q8_box_cols(int head_dim) { return head_dim < 128 ? head_dim : 128; }
 
-long long q8_attn_units(const Q8AttnArgs& a) {
-  return (long long)a.B * a.Hk * make_plan(a).rb;
+long long q8_attn_tiles(const Q8AttnArgs& a) {
+  const long long cap = (long long)a.max_pages << a.ps_shift;
+  return (long long)a.B * a.Hk * make_plan(a).rb * ((cap + kKT - 1) / kKT);
 }
 
 size_t q8_attn_workspace_bytes(const Q8AttnArgs& a) {
