@@ -648,79 +648,66 @@ def make_q8_cache(num_pages, n_kv_heads, page_size, head_dim, scale_block=None, 
     return (*codes, *scales)
 
 
-def _q8_need(ok, text):
-    if not ok:
-        raise ValueError(text)
+# These calls are short (a decoding step's take microseconds), so their checks are written to cost
+# little where they pass.
+def _q8_cache(k, v, ks, vs, torch) -> FaQ8Cache:
+    shape, blocks = k.shape, ks.shape
+    if not (k.dtype is v.dtype is torch.float8_e4m3fn and len(shape) == 4 and v.shape == shape):
+        raise ValueError("k_cache and v_cache must be float8_e4m3fn [num_pages, Hk, page_size, d]")
+    P, Hk, ps, d = shape
+    if not (ks.dtype is vs.dtype is torch.float32 and len(blocks) == 3 and vs.shape == blocks
+            and blocks[0] == P and blocks[1] == Hk and blocks[2] > 0 and ps % blocks[2] == 0):
+        raise ValueError("k_scale and v_scale must be float32 "
+                         "[num_pages, Hk, page_size // scale_block]")
+    if not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous()
+            and vs.is_contiguous()):
+        raise ValueError("the cache's tensors must be contiguous")
+    return FaQ8Cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), P, Hk, ps, d,
+                     ps // blocks[2], 0)
 
 
-def _q8_device(*tensors):
-    """Every tensor must be on the current CUDA device (the one the kernels are launched on)."""
-    import torch
-
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -2
-    for t in tensors:
-        if t.get_device() != dev:
-            raise ValueError("the tensors must be on the current CUDA device")
+def _q8_table(table, torch):
+    if not (table.dtype is torch.int32 and table.dim() == 2 and table.is_contiguous()):
+        raise ValueError("block_table must be a contiguous int32 tensor [B, max_pages]")
+    return table.shape
 
 
-def _q8_cache(k_cache, v_cache, k_scale, v_scale) -> FaQ8Cache:
-    import torch
-
-    _q8_need(k_cache.dtype == v_cache.dtype == torch.float8_e4m3fn and k_cache.dim() == 4
-             and k_cache.shape == v_cache.shape,
-             "k_cache and v_cache must be float8_e4m3fn [num_pages, Hk, page_size, d]")
-    P, Hk, ps, d = k_cache.shape
-    _q8_need(k_scale.dtype == v_scale.dtype == torch.float32 and k_scale.shape == v_scale.shape
-             and k_scale.dim() == 3 and k_scale.shape[:2] == k_cache.shape[:2]
-             and k_scale.shape[2] > 0 and ps % k_scale.shape[2] == 0,
-             "k_scale and v_scale must be float32 [num_pages, Hk, page_size // scale_block]")
-    _q8_need(k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous()
-             and v_scale.is_contiguous(), "the cache's tensors must be contiguous")
-    return FaQ8Cache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-                     v_scale.data_ptr(), P, Hk, ps, d, ps // k_scale.shape[2], 0)
-
-
-def _q8_index(t, shape, name):
-    import torch
-
-    _q8_need(t.dtype == torch.int32 and t.is_contiguous() and tuple(t.shape) == shape,
-             f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
+def _q8_index(t, n, name, torch):
+    if not (t.dtype is torch.int32 and t.dim() == 1 and t.shape[0] == n and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} entries")
     return t.data_ptr()
 
 
-def _q8_stride(t, name):
+def _q8_rows(t, name, torch):
     """(sequence, head, row) strides of bf16 rows [B, Hk, n, d] or [Hk, total, d]: any with the
     last dimension contiguous and the others multiples of 8 elements."""
-    import torch
+    st = t.stride()
+    if st[0] % 8 or st[1] % 8 or st[-2] % 8:  # a dimension of one element may have any stride
+        st = tuple(s if n > 1 else 0 for s, n in zip(st[:-1], t.shape)) + st[-1:]
+    if t.dtype is not torch.bfloat16 or st[-1] != 1 or st[0] % 8 or st[1] % 8 or st[-2] % 8:
+        raise ValueError(f"{name} must be bfloat16 with contiguous rows and strides that are "
+                         "multiples of 8 elements")
+    return (0, st[0], st[1]) if len(st) == 3 else st[:3]
 
-    st = [s if n > 1 else 0 for s, n in zip(t.stride(), t.shape)]
-    _q8_need(t.dtype == torch.bfloat16 and t.stride(-1) == 1 and not any(s % 8 for s in st[:-1]),
-             f"{name} must be bfloat16 with contiguous rows and strides that are multiples of 8")
-    return (ctypes.c_int64 * 3)(*((0, *st[:-1]) if t.dim() == 3 else st[:-1]))
 
-
-class _on_stream:
-    """The stream of a call: its handle, and a context in which new outputs belong to it."""
-
-    def __init__(self, stream):
-        import torch
-
-        now = torch.cuda.current_stream()
-        self.handle = now.cuda_stream if stream is None else int(
-            getattr(stream, "cuda_stream", stream))
-        self.ctx = None
-        if self.handle != now.cuda_stream:
-            self.ctx = torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
-                                         else torch.cuda.ExternalStream(self.handle))
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _q8_stream(stream, torch, *tensors):
+    """(handle, context) of a call's stream: new outputs are made in the context, so that they
+    belong to that stream (None: it is the current one). Every tensor must be on the current CUDA
+    device, the one the kernels are launched on."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != dev or dev < 0:
+            raise ValueError("the tensors must be on the current CUDA device")
+    if torch.cuda.current_device() != dev:
+        raise ValueError("the tensors must be on the current CUDA device")
+    now = torch._C._cuda_getCurrentRawStream(dev)
+    if stream is None:
+        return now, None
+    handle = int(getattr(stream, "cuda_stream", stream))
+    if handle == now:
+        return now, None
+    return handle, torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                                     else torch.cuda.ExternalStream(handle))
 
 
 def q8_cache_write(k, v, k_cache, v_cache, k_scale, v_scale, block_table, lengths, *,
@@ -731,32 +718,31 @@ def q8_cache_write(k, v, k_cache, v_cache, k_scale, v_scale, block_table, length
     keys with the new rows, which become its last positions; block_table is int32 [B, max_pages].
     A page written to must belong to one sequence of the call. See fa_q8_cache_write in
     include/fa_train.h for the rounding and the scales."""
-    cache = _q8_cache(k_cache, v_cache, k_scale, v_scale)
-    _q8_need(block_table.dim() == 2, "block_table must be [B, max_pages]")
-    B, per = block_table.shape
-    rows = FaQ8Rows(k.data_ptr(), v.data_ptr(), _q8_stride(k, "k"), _q8_stride(v, "v"), None,
-                    _q8_index(block_table, (B, per), "block_table"),
-                    _q8_index(lengths, (B,), "lengths"), B, per, 0, 0)
-    _q8_need(k.shape == v.shape, "k and v must have the same shape")
+    import torch
+
+    cache = _q8_cache(k_cache, v_cache, k_scale, v_scale, torch)
+    B, per = _q8_table(block_table, torch)
+    shape = k.shape
+    if v.shape != shape:
+        raise ValueError("k and v must have the same shape")
     if cu_seqlens is None:
-        n = k.shape[2] if k.dim() == 4 else -1
-        _q8_need(tuple(k.shape) == (B, cache.n_kv_heads, n, cache.head_dim),
-                 "k and v must be [B, Hk, n, d]")
-        if n == 0:
-            return
-        rows.new_len = n
-        _q8_device(k, v, k_cache, v_cache, k_scale, v_scale, block_table, lengths)
+        if not (len(shape) == 4 and shape[0] == B and shape[1] == cache.n_kv_heads
+                and shape[3] == cache.head_dim):
+            raise ValueError("k and v must be [B, Hk, n, d]")
+        cu, total, n = None, 0, shape[2]
     else:
-        n = k.shape[1] if k.dim() == 3 else -1
-        _q8_need(tuple(k.shape) == (cache.n_kv_heads, n, cache.head_dim),
-                 "packed k and v must be [Hk, total, d]")
-        if n == 0:
-            return
-        rows.total = n
-        rows.cu_seqlens = _q8_index(cu_seqlens, (B + 1,), "cu_seqlens")
-        _q8_device(k, v, k_cache, v_cache, k_scale, v_scale, block_table, lengths, cu_seqlens)
-    with _on_stream(stream) as handle:
-        rc = load_library().fa_q8_cache_write(ctypes.byref(cache), ctypes.byref(rows), handle)
+        if not (len(shape) == 3 and shape[0] == cache.n_kv_heads and shape[2] == cache.head_dim):
+            raise ValueError("packed k and v must be [Hk, total, d]")
+        cu, total, n = _q8_index(cu_seqlens, B + 1, "cu_seqlens", torch), shape[1], 0
+    rows = FaQ8Rows(k.data_ptr(), v.data_ptr(), _q8_rows(k, "k", torch), _q8_rows(v, "v", torch),
+                    cu, block_table.data_ptr(), _q8_index(lengths, B, "lengths", torch), B, per,
+                    total, n)
+    handle, _ = _q8_stream(stream, torch, k, v, k_cache, v_cache, k_scale, v_scale, block_table,
+                           lengths, *(() if cu is None else (cu_seqlens,)))
+    if total == 0 and n == 0:
+        return
+    rc = (_lib or load_library()).fa_q8_cache_write(ctypes.byref(cache), ctypes.byref(rows),
+                                                    handle)
     if rc:
         raise FaError(rc, "fa_q8_cache_write")
 
@@ -769,24 +755,32 @@ def q8_cache_read(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, t
     any strides with contiguous rows (rows behind cu_seqlens[B] are left as they were)."""
     import torch
 
-    cache = _q8_cache(k_cache, v_cache, k_scale, v_scale)
-    _q8_need(block_table.dim() == 2, "block_table must be [B, max_pages]")
-    B, per = block_table.shape
-    shape = (cache.n_kv_heads, int(total), cache.head_dim)
-    table = _q8_index(block_table, (B, per), "block_table")
-    cu = _q8_index(cu_seqlens, (B + 1,), "cu_seqlens")
-    _q8_device(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens)
-    with _on_stream(stream) as handle:
-        k, v = out if out is not None else (
-            torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device) for _ in range(2))
-        if out is not None:
-            _q8_need(tuple(k.shape) == tuple(v.shape) == shape, "out must be two [Hk, total, d]")
-            _q8_device(k, v)
-        if shape[1] == 0:
-            return k, v
-        rows = FaQ8Rows(k.data_ptr(), v.data_ptr(), _q8_stride(k, "k"), _q8_stride(v, "v"), cu,
-                        table, None, B, per, shape[1], 0)
-        rc = load_library().fa_q8_cache_read(ctypes.byref(cache), ctypes.byref(rows), handle)
+    cache = _q8_cache(k_cache, v_cache, k_scale, v_scale, torch)
+    B, per = _q8_table(block_table, torch)
+    cu = _q8_index(cu_seqlens, B + 1, "cu_seqlens", torch)
+    total = int(total)
+    shape = (cache.n_kv_heads, total, cache.head_dim)
+    handle, ctx = _q8_stream(stream, torch, k_cache, v_cache, k_scale, v_scale, block_table,
+                             cu_seqlens, *(out or ()))
+    if out is not None:
+        k, v = out
+        if not (k.shape == v.shape == shape):
+            raise ValueError("out must be two tensors [Hk, total, d]")
+        ks, vs = _q8_rows(k, "out[0]", torch), _q8_rows(v, "out[1]", torch)
+    else:
+        if ctx is None:
+            k = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device)
+            v = torch.empty_like(k)
+        else:
+            with ctx:
+                k = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device)
+                v = torch.empty_like(k)
+        ks = vs = (0, total * shape[2], shape[2])
+    if total == 0:
+        return k, v
+    rows = FaQ8Rows(k.data_ptr(), v.data_ptr(), ks, vs, cu, block_table.data_ptr(), None, B, per,
+                    total, 0)
+    rc = (_lib or load_library()).fa_q8_cache_read(ctypes.byref(cache), ctypes.byref(rows), handle)
     if rc:
         raise FaError(rc, "fa_q8_cache_read")
     return k, v
@@ -800,23 +794,30 @@ def q8_paged_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, lengt
     each sequence's last positions (causal: bottom-right per sequence)."""
     import torch
 
-    cache = _q8_cache(k_cache, v_cache, k_scale, v_scale)
-    _q8_need(q.dtype == torch.bfloat16 and q.dim() == 4 and q.is_contiguous()
-             and q.shape[3] == cache.head_dim, "q must be contiguous bfloat16 [B, H, q_len, d]")
-    B, H, lq, d = q.shape
-    _q8_need(block_table.dim() == 2, "block_table must be [B, max_pages]")
-    per = block_table.shape[1]
-    table = _q8_index(block_table, (B, per), "block_table")
-    lens = _q8_index(lengths, (B,), "lengths")
-    _q8_device(q, k_cache, v_cache, k_scale, v_scale, block_table, lengths)
+    cache = _q8_cache(k_cache, v_cache, k_scale, v_scale, torch)
+    shape = q.shape
+    if not (q.dtype is torch.bfloat16 and len(shape) == 4 and q.is_contiguous()
+            and shape[3] == cache.head_dim):
+        raise ValueError("q must be contiguous bfloat16 [B, H, q_len, d]")
+    B, H, lq, d = shape
+    rows, per = _q8_table(block_table, torch)
+    if rows != B:
+        raise ValueError("block_table must have a row for each sequence of q")
+    lens = _q8_index(lengths, B, "lengths", torch)
+    handle, ctx = _q8_stream(stream, torch, q, k_cache, v_cache, k_scale, v_scale, block_table,
+                             lengths)
     params = FaPagedParams(B, H, cache.n_kv_heads, lq, d, cache.page_size, per, cache.num_pages,
-                           float(scale), int(bool(causal)), 0, 0)
-    with _on_stream(stream) as handle:
+                           float(scale), 1 if causal else 0, 0, 0)
+    if ctx is None:
         o = torch.empty_like(q)
         lse = torch.empty((B, H, lq), dtype=torch.float32, device=q.device)
-        rc = load_library().fa_q8_paged_attention(q.data_ptr(), ctypes.byref(cache), table, lens,
-                                                  o.data_ptr(), lse.data_ptr(),
-                                                  ctypes.byref(params), handle)
+    else:
+        with ctx:
+            o = torch.empty_like(q)
+            lse = torch.empty((B, H, lq), dtype=torch.float32, device=q.device)
+    rc = (_lib or load_library()).fa_q8_paged_attention(
+        q.data_ptr(), ctypes.byref(cache), block_table.data_ptr(), lens, o.data_ptr(),
+        lse.data_ptr(), ctypes.byref(params), handle)
     if rc:
         raise FaError(rc, "fa_q8_paged_attention")
     return o, lse

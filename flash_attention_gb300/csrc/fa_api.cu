@@ -778,6 +778,31 @@ static int log2_of(int x) {
   return s;
 }
 
+// Scratch of the 8-bit attention comes from a pool of the library's own on each device that keeps
+// what is freed (a few MB at most): the device's default pool gives memory back whenever the
+// stream has been waited for, and the next call then takes 200 us to get it again, many times
+// what a decoding step's attention runs.
+static cudaError_t scratch_pool(int dev, cudaMemPool_t* out) {
+  static cudaMemPool_t pools[64] = {};
+  static fa::OncePerKey<> once;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  const cudaError_t e = once.run(dev, [dev] {
+    cudaMemPoolProps props = {};
+    props.allocType = cudaMemAllocationTypePinned;
+    props.location.type = cudaMemLocationTypeDevice;
+    props.location.id = dev;
+    cudaMemPool_t pool = nullptr;
+    cudaError_t err = cudaMemPoolCreate(&pool, &props);
+    uint64_t keep = UINT64_MAX;
+    if (err == cudaSuccess)
+      err = cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
+    if (err == cudaSuccess) pools[dev] = pool;
+    return err;
+  });
+  *out = pools[dev];
+  return e;
+}
+
 static int check_q8_cache(const fa_q8_cache* c) {
   if (!c) return FA_ERR_INVALID;
   const int ps = c->page_size, sb = c->scale_block;
@@ -912,8 +937,10 @@ int fa_q8_paged_attention(const void* q, const fa_q8_cache* cache, const int32_t
     return cuda_fail(cudaErrorInvalidValue, "cuTensorMapEncodeTiled");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   void* ws = nullptr;
-  if ((e = cudaMallocAsync(&ws, fa::q8_attn_workspace_bytes(a), s)) != cudaSuccess)
-    return cuda_fail(e, "cudaMallocAsync (8-bit paged attention workspace)");
+  cudaMemPool_t pool = nullptr;
+  if ((e = scratch_pool(dev, &pool)) != cudaSuccess) return cuda_fail(e, "scratch pool");
+  if ((e = cudaMallocFromPoolAsync(&ws, fa::q8_attn_workspace_bytes(a), pool, s)) != cudaSuccess)
+    return cuda_fail(e, "cudaMallocFromPoolAsync (8-bit paged attention workspace)");
   e = fa::launch_q8_attn(a, m, ws, s);
   const cudaError_t e2 = cudaFreeAsync(ws, s);
   if (e != cudaSuccess) return cuda_fail(e, "8-bit paged attention launch");
