@@ -78,141 +78,188 @@ __device__ __forceinline__ float2 bf16x2_f32(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
-// x / s for 8 values of a row as codes. inv: 1 / s where s is a power of two (then exact), else 0.
-__device__ __forceinline__ uint2 quantise8(const uint4& x, float s, float inv, bool odd) {
+// x / s for 8 values of a row as codes, where s = 1 / inv is a power of two (x * inv is exact).
+__device__ __forceinline__ uint2 quantise8(const uint4& x, float inv) {
+  const float2 a = bf16x2_f32(x.x), b = bf16x2_f32(x.y), c = bf16x2_f32(x.z), d = bf16x2_f32(x.w);
+  return make_uint2(e4m3x4_from_f32(a.x * inv, a.y * inv, b.x * inv, b.y * inv),
+                    e4m3x4_from_f32(c.x * inv, c.y * inv, d.x * inv, d.y * inv));
+}
+// The same for any s and any values (the cases that are rare: a scale that another writer chose
+// stays, or a value is not finite): NaN where the conversion would saturate an infinity.
+__device__ __noinline__ uint2 quantise8_any(uint4 x, float s) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   float y[8];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float2 f = bf16x2_f32(w[e]);
-    y[2 * e] = inv != 0.0f ? f.x * inv : f.x / s;
-    y[2 * e + 1] = inv != 0.0f ? f.y * inv : f.y / s;
-  }
-  if (odd) {  // a value that is not finite: NaN, where the conversion would saturate infinities
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (!isfinite(y[e])) y[e] = NAN;
+    y[2 * e] = isfinite(f.x) ? f.x / s : NAN;
+    y[2 * e + 1] = isfinite(f.y) ? f.y / s : NAN;
   }
   return make_uint2(e4m3x4_from_f32(y[0], y[1], y[2], y[3]),
                     e4m3x4_from_f32(y[4], y[5], y[6], y[7]));
 }
+// Codes times a ratio below 1, rounded again.
+__device__ __noinline__ uint2 requantise8(uint2 c, float ratio) {
+  const float2 f0 = f32_from_e4m3x2(c.x), f1 = f32_from_e4m3x2(c.x >> 16);
+  const float2 f2 = f32_from_e4m3x2(c.y), f3 = f32_from_e4m3x2(c.y >> 16);
+  return make_uint2(e4m3x4_from_f32(f0.x * ratio, f0.y * ratio, f1.x * ratio, f1.y * ratio),
+                    e4m3x4_from_f32(f2.x * ratio, f2.y * ratio, f3.x * ratio, f3.y * ratio));
+}
+// |x| of 8 values, the largest in each half (the order of bf16 bits is that of their absolute
+// values; infinities and NaN lie at and above 0x7f80).
+__device__ __forceinline__ uint32_t absmax8(const uint4& x, uint32_t m) {
+  m = __vmaxu2(m, x.x & 0x7fff7fffu);
+  m = __vmaxu2(m, x.y & 0x7fff7fffu);
+  m = __vmaxu2(m, x.z & 0x7fff7fffu);
+  return __vmaxu2(m, x.w & 0x7fff7fffu);
+}
+__device__ __forceinline__ uint4 finite8(uint4 x) {  // 0 for what is not finite
+  x.x &= ~__vcmpgeu2(x.x & 0x7fff7fffu, 0x7f807f80u);
+  x.y &= ~__vcmpgeu2(x.y & 0x7fff7fffu, 0x7f807f80u);
+  x.z &= ~__vcmpgeu2(x.z & 0x7fff7fffu, 0x7f807f80u);
+  x.w &= ~__vcmpgeu2(x.w & 0x7fff7fffu, 0x7f807f80u);
+  return x;
+}
 
 // SPB: steps of a scale block inside a warp (1: a block of at most one step). `wpb` warps of
-// the CTA share a unit of max(rows of a warp, scale block) positions.
-template <int HD, int SPB>
-__global__ void __launch_bounds__(1024)
-    q8_write_kernel(const Q8RowsK p, long long items, int wpb) {
+// the CTA share a unit of max(rows of a warp, scale block) positions. An item is a unit of K or V
+// of `heads` heads in turn, which share the way to the unit (offsets, length, table).
+// THREADS: 256, or up to 1024 where a scale block takes more than 8 warps.
+template <int HD, int SPB, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1)
+    q8_write_kernel(const Q8RowsK p, long long items, int wpb, int heads) {
   using RL = RowLanes<HD>;
+  constexpr int GROUPS = kSteps / SPB;
   __shared__ uint32_t warp_max[32];
   const int warp = warp_id(), lane = lane_id();
-  const int sb = 1 << p.sb_shift;
+  const int sb = 1 << p.sb_shift, ps_mask = (1 << p.ps_shift) - 1;
+  const int nb_shift = p.ps_shift - p.sb_shift;
   const int unit = RL::TR * wpb;
-  // the items of a CTA: K and V of a head, then the next head, then the next unit
   const long long item = (long long)blockIdx.x * (blockDim.x / 32 / wpb) + warp / wpb;
   const int which = (int)(item & 1);
-  const int head = (int)((item >> 1) % p.Hk);
-  const long long slot = (item >> 1) / p.Hk;
+  const int hgroups = (p.Hk + heads - 1) / heads;
+  const int h0 = (int)((item >> 1) % hgroups) * heads;
+  const long long slot = (item >> 1) / hgroups;
   bool live = item < items, bad = false;
-  int b = 0, start = 0, n = 0, len = 0, first = 0;
-  long long p0 = 0;
+  int b = 0, start = 0, n = 0, len = 0, first = 0, p0 = 0;
   if (live) {
     auto offset = [&](int i) { return p.cu ? (long long)p.cu[i] : (long long)i * p.new_len; };
     b = q8_slot_owner(slot, p.B, unit, lane, offset);
-    bad |= seq_rows(p, b, start, n);
     len = p.lens[b];
+    bad |= seq_rows(p, b, start, n);
     if (len < 0 || len > (long long)p.max_pages << p.ps_shift) {  // no place is the right one
       bad = true;
       live = false;
     }
     first = len - n;
     const long long u = slot - (offset(b) / unit + 2ll * b);
-    p0 = (long long)(max(first, 0) / unit + u) * unit;  // first position of this unit
-    live = live && u >= 0 && p0 < len && n > 0;
+    const long long at = (max(first, 0) / unit + u) * unit;  // first position of this unit
+    live = live && u >= 0 && at < len && n > 0;
+    p0 = (int)at + (warp % wpb) * RL::TR;
   }
-  p0 += (warp % wpb) * RL::TR;
   const int lo = max(first, 0);  // new rows are the positions lo .. len - 1
   const int r = lane / RL::LPR, col = lane % RL::LPR * 8;
-  const __nv_bfloat16* src = p.rows[which] + head * p.st_h[which] + col +
-                             (p.cu ? (long long)start * p.st_r[which] : b * p.st_b[which]);
-  uint4 x[kSteps];
-  int pg[kSteps];
-  uint32_t amax[kSteps / SPB];
-  float old[kSteps / SPB];
-  bool odd = false;
+  // pages of the warp's rows: lane i holds that of entry (p0 >> ps_shift) + i
+  int page = -1;
+  if (live && lane <= (RL::TR - 1) >> p.ps_shift && ((p0 >> p.ps_shift) + lane) << p.ps_shift < len)
+    page = p.table[(size_t)b * p.max_pages + (p0 >> p.ps_shift) + lane];
+  int at[kSteps];  // page of the row; -1: left out
+  bool isnew[kSteps];
 #pragma unroll
   for (int t = 0; t < kSteps; ++t) {
-    const long long pos = p0 + t * RL::RPS + r;
-    x[t] = make_uint4(0u, 0u, 0u, 0u);
-    pg[t] = -1;
-    if (live && pos >= lo && pos < len)
-      x[t] = __ldg(reinterpret_cast<const uint4*>(src + (pos - first) * p.st_r[which]));
+    const int pos = p0 + t * RL::RPS + r;
+    at[t] = __shfl_sync(0xffffffffu, page, (pos >> p.ps_shift) - (p0 >> p.ps_shift));
+    isnew[t] = live && pos >= lo && pos < len;
     // earlier rows of a block that gets a new one are looked at too
-    if (live && pos < len && (pos | (sb - 1)) >= lo) pg[t] = page_of(p, b, (int)pos, bad);
+    const bool look = live && pos < len && (pos | (sb - 1)) >= lo;
+    if (look && (at[t] < 0 || at[t] >= p.num_pages)) bad = true;
+    if (!look || at[t] < 0 || at[t] >= p.num_pages) at[t] = -1;
   }
+  // earlier tokens of a block: only the block that `first` lies in has some
+  const bool has_old = live && p0 < first;
+  const int lanes = min(32, RL::LPR << p.sb_shift);  // lanes of a block
+  for (int h = 0; h < heads; ++h) {
+    const int head = h0 + h;
+    const bool on = live && head < p.Hk;
+    const __nv_bfloat16* src = p.rows[which] + head * p.st_h[which] + col +
+                               (p.cu ? (long long)start * p.st_r[which] : b * p.st_b[which]);
+    uint4 x[kSteps];
+    uint32_t m[GROUPS];
 #pragma unroll
-  for (int g = 0; g < kSteps / SPB; ++g) {
-    uint32_t m2 = 0;
-    old[g] = 0.0f;
-#pragma unroll
-    for (int t = g * SPB; t < (g + 1) * SPB; ++t) {
-      const uint32_t w[4] = {x[t].x, x[t].y, x[t].z, x[t].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t a = w[e] & 0x7fff7fffu;
-        const uint32_t inf = __vcmpgeu2(a, 0x7f807f80u);
-        odd |= inf != 0;
-        m2 = __vmaxu2(m2, a & ~inf);
-      }
-      // the block's scale, where it holds earlier tokens: those of the one block with `first`
-      // inside, read before any warp writes it
-      const long long pos = p0 + t * RL::RPS + r;
-      if (pg[t] >= 0 && (pos & ~(long long)(sb - 1)) < first)
-        old[g] = p.scales[which][(((size_t)pg[t] * p.Hk + head) << (p.ps_shift - p.sb_shift)) +
-                                 ((pos & ((1 << p.ps_shift) - 1)) >> p.sb_shift)];
+    for (int t = 0; t < kSteps; ++t) {
+      x[t] = make_uint4(0u, 0u, 0u, 0u);
+      if (on && isnew[t])
+        x[t] = __ldg(reinterpret_cast<const uint4*>(
+            src + (long long)(p0 - first + t * RL::RPS + r) * p.st_r[which]));
     }
-    amax[g] = max(m2 & 0xffffu, m2 >> 16);
-    const int lanes = min(32, RL::LPR << p.sb_shift);  // lanes of a block
-    for (int o = lanes / 2; o > 0; o /= 2)
-      amax[g] = max(amax[g], __shfl_xor_sync(0xffffffffu, amax[g], o));
-  }
-  if (wpb > 1) {  // (then SPB = kSteps: one block for each unit)
-    if (lane == 0) warp_max[warp] = amax[0];
-    __syncthreads();
-    for (int w = warp / wpb * wpb; w < (warp / wpb + 1) * wpb; ++w)
-      amax[0] = max(amax[0], warp_max[w]);
-  }
-  odd = __any_sync(0xffffffffu, odd);
+    uint32_t odd = 0;
 #pragma unroll
-  for (int g = 0; g < kSteps / SPB; ++g) {
-    // lanes of rows past the end hold no old scale; the block's first rows do
-    float was = old[g];
-    const int lanes = min(32, RL::LPR << p.sb_shift);
-    for (int o = lanes / 2; o > 0; o /= 2)
-      was = fmaxf(was, __shfl_xor_sync(0xffffffffu, was, o));
-    const float s = fmaxf(exp2i(scale_exp(amax[g])), was);
-    const bool pow2 = (__float_as_uint(s) & 0x7fffffu) == 0;
-    const float inv = pow2 ? 1.0f / s : 0.0f;
-    const bool grew = was > 0.0f && s > was;
-    const float ratio = grew ? was / s : 1.0f;
+    for (int g = 0; g < GROUPS; ++g) {
+      m[g] = 0;
 #pragma unroll
-    for (int t = g * SPB; t < (g + 1) * SPB; ++t) {
-      if (pg[t] < 0) continue;
-      const long long pos = p0 + t * RL::RPS + r;
-      const int slot_in = (int)pos & ((1 << p.ps_shift) - 1);
-      const size_t at = (size_t)pg[t] * p.Hk + head;
-      uint2* dst = reinterpret_cast<uint2*>(p.codes[which] +
-                                            ((at << p.ps_shift) + slot_in) * HD + col);
-      if (pos >= lo) {
-        *dst = quantise8(x[t], s, inv, odd);
-        // the block's scale, by its first new row
-        if (col == 0 && ((slot_in & (sb - 1)) == 0 || pos == lo))
-          p.scales[which][(at << (p.ps_shift - p.sb_shift)) + (slot_in >> p.sb_shift)] = s;
-      } else if (grew) {
-        const uint2 c = *dst;
-        const float2 f0 = f32_from_e4m3x2(c.x), f1 = f32_from_e4m3x2(c.x >> 16);
-        const float2 f2 = f32_from_e4m3x2(c.y), f3 = f32_from_e4m3x2(c.y >> 16);
-        *dst = make_uint2(e4m3x4_from_f32(f0.x * ratio, f0.y * ratio, f1.x * ratio, f1.y * ratio),
-                          e4m3x4_from_f32(f2.x * ratio, f2.y * ratio, f3.x * ratio, f3.y * ratio));
+      for (int t = g * SPB; t < (g + 1) * SPB; ++t) m[g] = absmax8(x[t], m[g]);
+      odd = __vmaxu2(odd, m[g]);
+    }
+    odd = max(odd & 0xffffu, odd >> 16);
+    const bool any = __any_sync(0xffffffffu, odd >= 0x7f80u);  // a value is not finite
+    if (any) {
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g) {
+        m[g] = 0;
+#pragma unroll
+        for (int t = g * SPB; t < (g + 1) * SPB; ++t) m[g] = absmax8(finite8(x[t]), m[g]);
+      }
+    }
+    float was[GROUPS];
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) {
+      m[g] = max(m[g] & 0xffffu, m[g] >> 16);
+      if (lanes == 32) {
+        m[g] = __reduce_max_sync(0xffffffffu, m[g]);
+      } else {
+        for (int o = lanes / 2; o > 0; o /= 2)
+          m[g] = max(m[g], __shfl_xor_sync(0xffffffffu, m[g], o));
+      }
+      // the block's scale where it holds earlier tokens, read before any warp writes it
+      was[g] = 0.0f;
+      if (has_old) {
+#pragma unroll
+        for (int t = g * SPB; t < (g + 1) * SPB; ++t) {
+          const int pos = p0 + t * RL::RPS + r;
+          if (on && at[t] >= 0 && (pos & ~(sb - 1)) < first)
+            was[g] = p.scales[which][(((size_t)at[t] * p.Hk + head) << nb_shift) +
+                                     ((pos & ps_mask) >> p.sb_shift)];
+        }
+        for (int o = lanes / 2; o > 0; o /= 2)
+          was[g] = fmaxf(was[g], __shfl_xor_sync(0xffffffffu, was[g], o));
+      }
+    }
+    if (wpb > 1) {  // (then GROUPS = 1: one block for each unit)
+      if (lane == 0) warp_max[warp] = m[0];
+      __syncthreads();
+      for (int i = warp / wpb * wpb; i < (warp / wpb + 1) * wpb; ++i) m[0] = max(m[0], warp_max[i]);
+      __syncthreads();
+    }
+    if (!on) continue;
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) {
+      const float s = fmaxf(exp2i(scale_exp(m[g])), was[g]);
+      const bool plain = !any && (__float_as_uint(s) & 0x7fffffu) == 0;
+      const float inv = __uint_as_float(0x7f000000u - __float_as_uint(s));  // (a power of two's)
+#pragma unroll
+      for (int t = g * SPB; t < (g + 1) * SPB; ++t) {
+        if (at[t] < 0) continue;
+        const int pos = p0 + t * RL::RPS + r, in = pos & ps_mask;
+        const size_t row = (size_t)at[t] * p.Hk + head;
+        uint2* dst = reinterpret_cast<uint2*>(p.codes[which] + ((row << p.ps_shift) + in) * HD + col);
+        if (isnew[t]) {
+          *dst = plain ? quantise8(x[t], inv) : quantise8_any(x[t], s);
+          // the block's scale, by its first new row
+          if (col == 0 && ((in & (sb - 1)) == 0 || pos == lo))
+            p.scales[which][(row << nb_shift) + (in >> p.sb_shift)] = s;
+        } else if (was[g] > 0.0f && s > was[g]) {
+          *dst = requantise8(*dst, was[g] / s);
+        }
       }
     }
   }
@@ -305,11 +352,19 @@ cudaError_t write_t(const Q8RowsArgs& a, cudaStream_t s) {
   const int wpb = sb > RL::TR ? sb / RL::TR : 1;
   const int warps = wpb > 8 ? wpb : 8;
   const long long total = a.cu ? a.total : (long long)a.B * a.new_len;
-  const long long items = q8_unit_slots(total, a.B, RL::TR * wpb) * a.Hk * 2;
+  const long long slots = q8_unit_slots(total, a.B, RL::TR * wpb);
+  // heads of an item: four, where that still leaves 16 warps for each SM
+  const int heads = a.Hk >= 4 && slots * wpb * a.Hk / 4 * 2 >= 152 * 16 ? 4 : 1;
+  const long long items = slots * ((a.Hk + heads - 1) / heads) * 2;
   const long long per = warps / wpb;
   profile_mark(kKernQ8Write, 0, s);
-  q8_write_kernel<HD, SPB><<<(unsigned)((items + per - 1) / per), warps * 32, 0, s>>>(
-      rows_params(a), items, wpb);
+  const unsigned grid = (unsigned)((items + per - 1) / per);
+  if constexpr (SPB == 8 && HD >= 128) {
+    if (warps > 8)
+      q8_write_kernel<HD, SPB, 1024><<<grid, warps * 32, 0, s>>>(rows_params(a), items, wpb, heads);
+  }
+  if (warps == 8)
+    q8_write_kernel<HD, SPB, 256><<<grid, 256, 0, s>>>(rows_params(a), items, wpb, heads);
   const cudaError_t e = cudaGetLastError();
   profile_mark(kKernQ8Write, 1, s);
   return e;
