@@ -53,14 +53,20 @@ constexpr float kLn2 = 0.6931471805599453f;
 // The weight of the score that m was taken from is 2^kTop; m stays until a weight passes
 // 2^kMost (where f16 would not hold 8 times what the first piece leaves).
 constexpr float kTop = 11.0f, kMost = 15.0f;
+// The softmax's sums are held in units of 2^16: with value scales from 2^-100 to 2^100 neither
+// w / v_scale nor 2^22 of them leave f32.
+constexpr float kSumExp = 16.0f, kSumUnit = 65536.0f;
 
-// R query rows of a unit at a time; ST stages in each of the K and V rings; CTAS per SM.
+// R query rows of a unit at a time. KST, VST: stages of the K and V rings; V has more, as a V tile
+// stays until the weights of its keys are there (3 and 3 of 16 KB: 167 us, 2 and 4: 162 us for 64
+// sequences of up to 16k keys).
 template <int HD, int R_>
 struct Q8Layout {
   static constexpr int R = R_;
-  static constexpr int CTAS = (R <= 16 && HD <= 128) ? 2 : 1;
-  static constexpr int ST = HD == 64 ? (R == 8 ? 5 : 4) : HD == 128 ? (R == 8 ? 3 : R == 16 ? 2 : 5)
-                                                                    : (R == 8 ? 3 : 2);
+  static constexpr int CTAS = R > 8 || HD > 128 ? 1 : HD == 64 ? 3 : 2;  // resident on an SM
+  static constexpr int KST = HD == 64 ? (R == 8 ? 2 : 6) : HD == 128 ? (R == 8 ? 2 : 5) : 2;
+  static constexpr int VST = HD == 64 ? (R == 8 ? 4 : 8) : HD == 128 ? (R == 8 ? 4 : R == 16 ? 6 : 5)
+                                                         : (R == 8 ? 4 : R == 16 ? 3 : 2);
   static constexpr int CH = HD <= 128 ? HD : 128;   // columns (bytes) of a swizzled row
   static constexpr int KCH = HD / CH;               // row chunks: 1, or 2 at head_dim 256
   static constexpr int NS = 2 * R;                  // columns of S^T: hi rows, lo rows
@@ -69,8 +75,8 @@ struct Q8Layout {
   static constexpr int Q_BYTES = NS * HD;
   static constexpr int P_BYTES = kKT * NP;
   static constexpr int OFF_K = 0;
-  static constexpr int OFF_V = OFF_K + ST * KV_BYTES;
-  static constexpr int OFF_Q = OFF_V + ST * KV_BYTES;
+  static constexpr int OFF_V = OFF_K + KST * KV_BYTES;
+  static constexpr int OFF_Q = OFF_V + VST * KV_BYTES;
   static constexpr int OFF_P = OFF_Q + 2 * Q_BYTES;
   static constexpr int SMEM_BYTES = OFF_P + 2 * P_BYTES + 1024;
   static constexpr int COL_S = 0;                   // two S^T buffers, then O^T
@@ -171,21 +177,36 @@ __device__ __forceinline__ bool softmax_any(bool v) {
       : "memory");
   return r != 0;
 }
-// mbar_wait with its polling out of line: the roles' loops stay short (they share the SM's
-// instruction cache).
+// mbar_wait with its polling out of line, and each poll suspended for up to 20 us: with 8 warps a
+// CTA of which most wait most of the time, the polls were the larger part of all instructions,
+// and they share the SM's instruction cache with the softmax.
 __device__ __noinline__ bool wait_more(uint64_t* bar, uint32_t parity, WaitCtl* w) {
-  return mbar_wait(bar, parity, w);
+  const uint64_t t0 = globaltimer();
+  const uint32_t hint = w->limit_ns < 20000 ? (uint32_t)w->limit_ns : 20000u;
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(hint)
+        : "memory");
+    if (ok) return true;
+    if (*reinterpret_cast<volatile int*>(&w->abort)) return false;
+    if (globaltimer() - t0 > w->limit_ns) {
+      *reinterpret_cast<volatile int*>(&w->abort) = 1;
+      return false;
+    }
+  }
 }
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, WaitCtl* w) {
   return mbar_try_wait(bar, parity) || wait_more(bar, parity, w);
 }
-// Largest value of the warp (NaN is passed over), by the integer reduction: floats in the order
-// of their bits once the negative ones are turned around.
+// Largest value of the warp (NaN is passed over).
 __device__ __forceinline__ float warp_max(float x) {
-  int i = __float_as_int(x != x ? -INFINITY : x);
-  i = i >= 0 ? i : i ^ 0x7fffffff;
-  i = __reduce_max_sync(0xffffffffu, i);
-  return __int_as_float(i >= 0 ? i : i ^ 0x7fffffff);
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 struct Q8K {
@@ -299,16 +320,19 @@ struct Walk {
   }
 };
 
-template <int HD, int R>
+// RL: the rows of a unit that there can be (of the R that a tile has columns for): the softmax's
+// arithmetic runs on these alone.
+template <int HD, int R, int RL>
 __global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
     q8_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
                    const Q8K p) {
   using LY = Q8Layout<HD, R>;
-  constexpr int ST = LY::ST, KCH = LY::KCH, CH = LY::CH, NS = LY::NS, NP = LY::NP;
+  constexpr int KST = LY::KST, VST = LY::VST;
+  constexpr int KCH = LY::KCH, CH = LY::CH, NS = LY::NS, NP = LY::NP;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  __shared__ uint64_t k_full[ST], v_full[ST], k_empty[ST], v_empty[ST];
+  __shared__ uint64_t k_full[KST], v_full[VST], k_empty[KST], v_empty[VST];
   __shared__ uint64_t s_full[2], s_free[2], p_full[2], p_done[2], q_full[2], q_free[2];
   __shared__ uint64_t sc_full[kScRing], sc_free[kScRing], drain_s, drain_o;
   __shared__ uint32_t tmem_base_s;
@@ -318,7 +342,7 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
   __shared__ float sc_s[kScRing][2][kKT];  // key scale, log2 of the value scale
   __shared__ __align__(16) float qs_s[2][R];   // rows: score factor, key limit
   __shared__ __align__(16) int lim_s[2][R];
-  __shared__ __align__(16) float nm_s[R], red_s[4][R], f_s[R];  // -m; sums or maxima; O's factors
+  __shared__ __align__(16) float nm_s[2][R], red_s[4][R];  // -m; maxima or sums of the warps
 
   const int warp = warp_id(), lane = lane_id();
   Walk w;
@@ -326,10 +350,12 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
   if (threadIdx.x == 0) {
     wait_ctl_init(&wctl, p.wait_limit_ns);
     bad_input = 0;
-    for (int s = 0; s < ST; ++s) {
+    for (int s = 0; s < KST; ++s) {
       mbar_init(&k_full[s], 1);
-      mbar_init(&v_full[s], 1);
       mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < VST; ++s) {
+      mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -375,7 +401,7 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
     const int nsub = kKT / box;                 // boxes of a tile and chunk (<= 16)
     const int z_oob = p.num_pages * p.Hk;       // a page past the cache: zero fill
     const int sub = lane / KCH, c = lane % KCH; // this lane's box
-    int g = 0;                                  // tiles so far
+    int g = 0, gk = 0, gv = 0;                  // tiles, and copies of K and V, so far
     int page_b = -1, page_lo = 0;               // page_s holds entries page_lo .. of sequence page_b
     bool ok = true;
     while (ok && w.next(p, R)) {
@@ -408,10 +434,10 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
             y = key & ((1 << p.ps_shift) - 1);
           }
         }
-        const int st = g % ST;
-        const uint32_t use = g / ST;
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
+          const int st = g % (which ? VST : KST);
+          const uint32_t use = g / (which ? VST : KST);
           uint64_t* full = which ? &v_full[st] : &k_full[st];
           if (leader) {
             if (use > 0) ok = wait(which ? &v_empty[st] : &k_empty[st], (use - 1) & 1, &wctl);
@@ -422,21 +448,21 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
           uint8_t* dst = smem + (which ? LY::OFF_V : LY::OFF_K) + st * LY::KV_BYTES +
                          c * (kKT * CH) + sub * box * CH;
           if (sub < nsub) tma_load_3d(dst, which ? &mV : &mK, full, c * CH, y, z);
+          ++(which ? gv : gk);
         }
-        if (!ok) {  // the K copy of this tile may be under way: let it land
-          if (leader) mbar_wait_drain(&k_full[st], use & 1);
-          break;
-        }
+        if (!ok) break;
       }
     }
-    if (leader)  // no copy may be in flight when the CTA ends
-      for (int s = 0; s < ST; ++s) {
-        const int n = (g - s + ST - 1) / ST;  // copies into stage s
-        if (n > 0) {
-          mbar_wait_drain(&k_full[s], (n - 1) & 1);
-          mbar_wait_drain(&v_full[s], (n - 1) & 1);
-        }
+    if (leader) {  // no copy may be in flight when the CTA ends
+      for (int s = 0; s < KST; ++s) {
+        const int n = (gk - s + KST - 1) / KST;  // copies into stage s
+        if (n > 0) mbar_wait_drain(&k_full[s], (n - 1) & 1);
       }
+      for (int s = 0; s < VST; ++s) {
+        const int n = (gv - s + VST - 1) / VST;
+        if (n > 0) mbar_wait_drain(&v_full[s], (n - 1) & 1);
+      }
+    }
   } else if (warp == LY::S_WARP) {
     // ------------------------------------------------------------------ S^T = K q^T
     if (elect_one()) {
@@ -448,8 +474,8 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
         if (!ok) break;
         const Desc qb = q8_desc<CH>(smem_u32(smem + LY::OFF_Q + (un & 1) * LY::Q_BYTES), 0);
         for (int j = w.ja; j < w.jb; ++j, ++g) {
-          const int st = g % ST, buf = g & 1;
-          ok = wait(&k_full[st], (g / ST) & 1, &wctl);
+          const int st = g % KST, buf = g & 1;
+          ok = wait(&k_full[st], (g / KST) & 1, &wctl);
           if (ok && g >= 2) ok = wait(&s_free[buf], ((g >> 1) - 1) & 1, &wctl);
           if (!ok) break;
           tc_fence_after();
@@ -477,9 +503,9 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
     bool ok = true;
     while (ok && w.next(p, R)) {
       for (int j = w.ja; j < w.jb; ++j, ++g) {
-        const int st = g % ST, buf = g & 1, n0 = j * kKT;
-        ok = __all_sync(0xffffffffu, wait(&p_full[buf], (g >> 1) & 1, &wctl));
-        if (ok) ok = __all_sync(0xffffffffu, wait(&v_full[st], (g / ST) & 1, &wctl));
+        const int st = g % VST, buf = g & 1, n0 = j * kKT;
+        ok = __all_sync(0xffffffffu, wait(&v_full[st], (g / VST) & 1, &wctl));
+        if (ok) ok = __all_sync(0xffffffffu, wait(&p_full[buf], (g >> 1) & 1, &wctl));
         if (!ok) break;
         uint8_t* vt = smem + LY::OFF_V + st * LY::KV_BYTES;
         if (n0 + kKT > w.len) {  // rows behind the sequence's end
@@ -556,7 +582,7 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
       const int live = min(R, p.rows - r0);
       if (lane < R) {
         const int i = (r0 + lane) % p.lq;
-        lim_s[qb][lane] = p.causal ? max(0, w.len - p.lq + i + 1) : w.len;
+        lim_s[qb][lane] = min(p.causal ? max(0, w.len - p.lq + i + 1) : w.len, w.jb * kKT);
       }
       float mine = 0.0f;  // the score factor of row `lane`
 #pragma unroll 4
@@ -628,7 +654,7 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
           for (int e = 0; e < 4; ++e) {
             sc_s[slot][0][e * 32 + lane] = ks[h][e];
             sc_s[slot][1][e * 32 + lane] =
-                log2f(fmaxf(vs[h][e], __int_as_float((kQ8MinExp + 127) << 23)));
+                __log2f(fmaxf(vs[h][e], __int_as_float((kQ8MinExp + 127) << 23)));
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&sc_full[slot]);
@@ -640,32 +666,29 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
     }
   } else {
     // ------------------------------------------------------------------ softmax, and O out.
-    // Rows that are not there (live of the R are) are passed over: their columns of q, S, w and O
-    // hold anything and are never used. A wait that runs out shows at the next softmax_any, where all threads leave
-    // together.
+    // Rows that are not there (live of the RL are) have the score factor 0, and columns of q, S, w
+    // and O that hold anything (NaN too) and are never used. A wait that runs out shows at the
+    // next softmax_any, where all threads leave together.
     const int key = threadIdx.x;  // key of the tile
     const uint32_t lanes = tbase + ((uint32_t)(warp * 32) << 16);
+    const uint64_t sixteenth = f2_pack(0.0625f, 0.0625f);
     int g = 0, un = 0;
     bool ok = true;
     for (; ok && w.next(p, R); ++un) {
       const int qb = un & 1;
       ok = wait(&q_full[qb], (un >> 1) & 1, &wctl);
-      const int r0 = w.rb * R, live = min(R, p.rows - r0);
+      const int r0 = w.rb * R, live = min(RL, p.rows - r0);
       // tiles below lim_min need no test of the keys
-      const int lim_min = p.causal ? max(0, w.len - p.lq + 1) : w.len;
-      float l[R];
+      const int lim_min = min(p.causal ? max(0, w.len - p.lq + 1) : w.len, w.jb * kKT);
+      float l[RL];
 #pragma unroll
-      for (int r = 0; r < R; ++r) l[r] = 0.0f;
-      if (key < R) nm_s[key] = key < live ? 0.0f : -1e30f;  // (an odd live has a neighbour)
-      if (softmax_any(!ok)) {
-        ok = false;
-        break;
-      }
+      for (int r = 0; r < RL; ++r) l[r] = 0.0f;
       for (int j = w.ja; j < w.jb; ++j, ++g) {
-        const int buf = g & 1, slot = g % kScRing, n0 = j * kKT;
-        ok = ok && wait(&sc_full[slot], (g / kScRing) & 1, &wctl);
-        const float kc = sc_s[slot][0][key], lsv = sc_s[slot][1][key];
-        ok = __all_sync(0xffffffffu, ok && wait(&s_full[buf], (g >> 1) & 1, &wctl));
+        const int buf = g & 1;
+        const uint32_t ph = (g >> 1) & 1;  // (kScRing = 2 too)
+        ok = ok && wait(&sc_full[buf], ph, &wctl);
+        const float kc = sc_s[buf][0][key], lsv = sc_s[buf][1][key];
+        ok = __all_sync(0xffffffffu, ok && wait(&s_full[buf], ph, &wctl));
         tc_fence_after();
         uint32_t sr[NS];
         load_cols<NS>(lanes + LY::COL_S + buf * NS, sr);
@@ -674,33 +697,33 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&s_free[buf]);
-          mbar_arrive(&sc_free[slot]);
+          mbar_arrive(&sc_free[buf]);
         }
-        float t[R];
-        float top = -INFINITY;
+        const bool first = j == w.ja;
+        float t[RL];
         const uint64_t kc2 = f2_pack(kc, kc), lsv2 = f2_pack(lsv, lsv);
-        const uint64_t sixteenth = f2_pack(0.0625f, 0.0625f);
 #pragma unroll
-        for (int r = 0; r < R; r += 2) {
-          if (r >= live) break;
+        for (int r = 0; r < RL; r += 2) {
+          const uint64_t qs = *reinterpret_cast<const uint64_t*>(&qs_s[qb][r]);
+          const uint64_t nm = first ? 0ull : *reinterpret_cast<const uint64_t*>(&nm_s[qb][r]);
           const uint64_t hi = f2_pack(__uint_as_float(sr[r]), __uint_as_float(sr[r + 1]));
           const uint64_t lo = f2_pack(__uint_as_float(sr[R + r]), __uint_as_float(sr[R + r + 1]));
           const uint64_t s = f2_mul(f2_fma(lo, sixteenth, hi), kc2);
-          const uint64_t qs = *reinterpret_cast<const uint64_t*>(&qs_s[qb][r]);
-          const uint64_t nm = *reinterpret_cast<const uint64_t*>(&nm_s[r]);
           f2_unpack(f2_fma(s, qs, f2_add(lsv2, nm)), t[r], t[r + 1]);
-          if (n0 + kKT > lim_min) {
-            if (n0 + key >= lim_s[qb][r]) t[r] = -INFINITY;
-            if (n0 + key >= lim_s[qb][r + 1]) t[r + 1] = -INFINITY;
-          }
-          top = fmax3(top, t[r], t[r + 1]);
         }
-        const bool first = j == w.ja;
-        if (softmax_any(top > kMost || first || !ok)) {
-          // m moves: to the largest score so far, at the first tile to the tile's own
+        if (j * kKT + kKT > lim_min) {
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            if (r >= live) break;
+          for (int r = 0; r < RL; ++r)
+            if (j * kKT + key >= lim_s[qb][r]) t[r] = -INFINITY;
+        }
+        float top = t[0];
+#pragma unroll
+        for (int r = 1; r < RL; r += 2)
+          top = r + 1 < RL ? fmax3(top, t[r], t[r + 1]) : fmaxf(top, t[r]);
+        if (softmax_any(top > kMost || first || !ok)) {
+          // m moves: to the largest score so far, at a unit's first tile to the tile's own
+#pragma unroll
+          for (int r = 0; r < RL; ++r) {
             const float mx = warp_max(t[r]);
             if (lane == 0) red_s[warp][r] = mx;
           }
@@ -708,10 +731,9 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
             ok = false;
             break;
           }
-          float f[R];
+          float f[RL];
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            if (r >= live) break;
+          for (int r = 0; r < RL; ++r) {
             const float mx = fmaxf(fmaxf(red_s[0][r], red_s[1][r]),
                                    fmaxf(red_s[2][r], red_s[3][r]));
             float up = mx - kTop;
@@ -719,23 +741,23 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
             t[r] -= up;
             f[r] = first ? 1.0f : ex2(-up);
             l[r] *= f[r];
-            if (key == r) nm_s[r] -= up;
+            if (key == r) nm_s[qb][r] = first ? -up : nm_s[qb][r] - up;
           }
           if (!first) {  // O is scaled, once the last O^T MMA is done
             ok = __all_sync(0xffffffffu, wait(&p_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &wctl));
             tc_fence_after();
-#pragma unroll
-            for (int c = 0; c < R; c += 8) {
-              if (c >= live) break;
 #pragma unroll 1
-              for (int h = 0; h < KCH * 3; ++h) {
-                const uint32_t at = lanes + LY::COL_O + h / 3 * NP + h % 3 * R + c;
-                float x[8];
-                tmem_ld8(at, x);
+            for (int h = 0; h < KCH; ++h) {
+#pragma unroll
+              for (int c = 0; c < NP; c += 32) {  // (R columns a piece)
+                uint32_t x[32];
+                tmem_ld32(lanes + LY::COL_O + h * NP + c, x);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] *= f[c + e];
-                tmem_st8(at, x);
+                for (int e = 0; e < 32; ++e)
+                  if ((c + e) % R < RL)
+                    x[e] = __float_as_uint(__uint_as_float(x[e]) * f[(c + e) % R]);
+                tmem_st32(lanes + LY::COL_O + h * NP + c, x);
               }
             }
             tmem_wait_st();
@@ -743,84 +765,72 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
           }
           softmax_any(false);  // nm_s is read, and red_s written, by everyone after this
         }
-        // weights, their sum, and their pieces into shared memory, the key's row of NP bytes
-        const float inv = ex2(-lsv);  // 1 / value scale
-        if (g >= 2) ok = ok && wait(&p_done[buf], ((g >> 1) - 1) & 1, &wctl);
-        uint8_t* prow = smem + LY::OFF_P + buf * LY::P_BYTES + key * NP;
+        // weights, their sum, and their pieces into shared memory, a key's row of NP bytes
+        const float inv = ex2(-lsv - kSumExp);  // 1 / value scale, in the sum's unit
+        if (g >= 2) ok = ok && wait(&p_done[buf], ph ^ 1, &wctl);
         uint32_t pc[3][R / 4];
 #pragma unroll
-        for (int r = 0; r < R; r += 4) {
-          if (r >= live) break;
-          uint32_t h[2];
+        for (int r = 0; r < RL; r += 4) {
+          uint32_t x[2];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float a = ex2(t[r + 2 * e]), b = ex2(t[r + 2 * e + 1]);
-            l[r + 2 * e] = fmaf(a, inv, l[r + 2 * e]);
-            l[r + 2 * e + 1] = fmaf(b, inv, l[r + 2 * e + 1]);
-            h[e] = weight_f16x2(a, b);
+          for (int e = 0; e < 4; e += 2) {
+            if (r + e >= RL) {
+              x[e / 2] = 0u;
+              continue;
+            }
+            const float a = ex2(t[r + e]), b = ex2(t[r + e + 1]);
+            l[r + e] = fmaf(a, inv, l[r + e]);
+            l[r + e + 1] = fmaf(b, inv, l[r + e + 1]);
+            x[e / 2] = weight_f16x2(a, b);
           }
 #pragma unroll
           for (int i = 0; i < 3; ++i) {
-            pc[i][r / 4] = __byte_perm(h[0], h[1], 0x7531);
-            h[0] = f16x2_rest(h[0]);
-            h[1] = f16x2_rest(h[1]);
+            pc[i][r / 4] = __byte_perm(x[0], x[1], 0x7531);
+            x[0] = f16x2_rest(x[0]);
+            x[1] = f16x2_rest(x[1]);
           }
         }
+        uint8_t* prow = smem + LY::OFF_P + buf * LY::P_BYTES + key * NP;
         if constexpr (R == 8) {
+          if constexpr (RL <= 4) pc[0][1] = pc[1][1] = pc[2][1] = 0u;
           *reinterpret_cast<uint4*>(prow + swz<NP>(0, key) * 16) =
               make_uint4(pc[0][0], pc[0][1], pc[1][0], pc[1][1]);
-          *reinterpret_cast<uint4*>(prow + swz<NP>(1, key) * 16) =
-              make_uint4(pc[2][0], pc[2][1], 0u, 0u);
+          *reinterpret_cast<uint2*>(prow + swz<NP>(1, key) * 16) = make_uint2(pc[2][0], pc[2][1]);
         } else {
 #pragma unroll
-          for (int x = 0; x < R / 16; ++x) {
-            if (16 * x >= live) break;
+          for (int x = 0; x < R / 16; ++x)
 #pragma unroll
             for (int i = 0; i < 3; ++i)
               *reinterpret_cast<uint4*>(prow + swz<NP>(i * (R / 16) + x, key) * 16) = make_uint4(
                   pc[i][4 * x], pc[i][4 * x + 1], pc[i][4 * x + 2], pc[i][4 * x + 3]);
-          }
         }
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[buf]);
       }
-      // the sums of the 128 keys' threads
-      if (softmax_any(!ok)) {
-        ok = false;
-        break;
-      }
+      // the sums of the 128 threads
+      const bool any = w.jb > w.ja;
+      if (!any) softmax_any(false);  // (no vote since the last unit's red_s was read)
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        if (r >= live) break;
+      for (int r = 0; r < RL; ++r) {
         float x = l[r];
+#pragma unroll
         for (int o = 16; o > 0; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
         if (lane == 0) red_s[warp][r] = x;
       }
-      const bool any = w.jb > w.ja;
-      if (any) ok = wait(&p_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &wctl);
+      if (any && ok) ok = wait(&p_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &wctl);
       if (softmax_any(!ok)) {
         ok = false;
         break;
       }
       tc_fence_after();
+      // a row without keys: sum 0, and O (whose columns may hold anything then) 0
       const size_t unit_row = ((size_t)w.b * p.Hk + w.kh) * p.rows + r0;
       const size_t part = 2 * (size_t)blockIdx.x + (w.first ? 1 : 0);
-      // a row without keys: sum 0, and O (which may hold anything then) 0
-      if (key < live) {
-        const float sum = red_s[0][key] + red_s[1][key] + red_s[2][key] + red_s[3][key];
-        f_s[key] = sum == 0.0f ? 0.0f : w.whole ? 1.0f / sum : 1.0f;
-        if (!w.whole) {
-          p.ml_part[part * 2 * R + key] = -nm_s[key];
-          p.ml_part[part * 2 * R + R + key] = sum;
-        } else if (p.lse) {
-          p.lse[unit_row + key] = sum == 0.0f ? -INFINITY : fmaf(-nm_s[key], kLn2, logf(sum));
-        }
-      }
-      softmax_any(false);
       // this thread's head-dim row: a 64-row accumulator lies in lanes 0-15 of each warp
       const int col = HD == 64 ? warp * 16 + lane : (int)threadIdx.x;
       const bool mine = HD > 64 || lane < 16;
+      const size_t row0 = w.whole ? unit_row : part * R;
 #pragma unroll 1
       for (int c = 0; c < live; c += 8) {
 #pragma unroll 1
@@ -833,23 +843,36 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
             tmem_ld8(at + 2 * R, z);
             tmem_wait_ld();
           }
-          const size_t row0 = (w.whole ? unit_row : part * R) + c;
+          size_t at = (row0 + c) * HD + h * 128 + col;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (!mine || c + e >= live) break;
-            const float f = f_s[c + e];
-            const float o = f == 0.0f ? 0.0f : fmaf(fmaf(z[e], 0.125f, y[e]), 0.125f, x[e]) * f;
-            const size_t at = (row0 + e) * HD + h * 128 + col;
-            if (w.whole)
-              p.o[at] = __float2bfloat16(o);
-            else
-              p.o_part[at] = o;
+          for (int e = 0; e < (RL < 8 ? RL : 8); ++e, at += HD) {
+            const float sum = (red_s[0][c + e] + red_s[1][c + e]) +
+                              (red_s[2][c + e] + red_s[3][c + e]);
+            float o = fmaf(fmaf(z[e], 0.125f, y[e]), 0.125f, x[e]);
+            if (w.whole) o = __fdividef(o, sum) / kSumUnit;  // (2 ulp; o is rounded to bf16)
+            if (sum == 0.0f) o = 0.0f;
+            if (c + e < live && mine) {
+              if (w.whole)
+                p.o[at] = __float2bfloat16(o);
+              else
+                p.o_part[at] = o;
+            }
           }
         }
       }
+      if (key < live) {
+        const float sum = (red_s[0][key] + red_s[1][key]) + (red_s[2][key] + red_s[3][key]);
+        const float m = any ? -nm_s[qb][key] : 0.0f;
+        if (!w.whole) {
+          p.ml_part[part * 2 * R + key] = m;
+          p.ml_part[part * 2 * R + R + key] = sum;
+        } else if (p.lse) {
+          p.lse[unit_row + key] = sum == 0.0f ? -INFINITY : fmaf(m + kSumExp, kLn2, logf(sum));
+        }
+      }
+      // (the next unit has the other half of nm_s, and writes red_s behind its first vote)
       tc_fence_before();
       if (threadIdx.x == 0) mbar_arrive(&q_free[qb]);
-      softmax_any(false);  // what is in shared memory may be written again
     }
   }
 
@@ -909,14 +932,14 @@ __global__ void __launch_bounds__(256) q8_combine_kernel(const Q8K p, int grid) 
 #pragma unroll
     for (int e = 0; e < HD / 32; ++e)
       p.o[(unit_row + r) * HD + e * 32 + lane] =
-          __float2bfloat16(sum == 0.0f ? 0.0f : acc[e] / sum);
+          __float2bfloat16(sum == 0.0f ? 0.0f : acc[e] / sum / kSumUnit);
     if (p.lse && lane == 0)
-      p.lse[unit_row + r] = sum == 0.0f ? -INFINITY : fmaf(m, kLn2, logf(sum));
+      p.lse[unit_row + r] = sum == 0.0f ? -INFINITY : fmaf(m + kSumExp, kLn2, logf(sum));
   }
 }
 
 struct Plan {
-  int R, rb, grid;
+  int R, RL, rb, grid;
 };
 
 // Rows of a unit: the smallest block that holds the G * q_len rows of a kv head, 32 at most (more
@@ -926,19 +949,20 @@ Plan make_plan(const Q8AttnArgs& a) {
   Plan pl;
   const int rows = a.G * a.lq;
   pl.R = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  pl.RL = rows <= 2 ? 2 : rows <= 4 ? 4 : pl.R;
   pl.rb = (rows + pl.R - 1) / pl.R;
-  const int ctas = 152 * (pl.R <= 16 && a.d <= 128 ? 2 : 1);
+  const int ctas = 152 * (pl.R > 8 || a.d > 128 ? 1 : a.d == 64 ? 3 : 2);
   const long long cap = (long long)a.max_pages << a.ps_shift;
   const long long tiles = (cap + kKT - 1) / kKT * a.B * a.Hk * pl.rb;
   pl.grid = (int)std::min<long long>(ctas, tiles);
   return pl;
 }
 
-template <int HD, int R>
+template <int HD, int R, int RL>
 cudaError_t attn_t(const Q8AttnArgs& a, const Q8AttnMaps& m, const Plan& pl, void* ws,
                    cudaStream_t s) {
   using LY = Q8Layout<HD, R>;
-  auto kern = q8_attn_kernel<HD, R>;
+  auto kern = q8_attn_kernel<HD, R, RL>;
   static OncePerKey<> smem_attr;
   cudaError_t e = set_smem_once(smem_attr, kern, LY::SMEM_BYTES);
   if (e != cudaSuccess) return e;
@@ -982,9 +1006,13 @@ cudaError_t attn_t(const Q8AttnArgs& a, const Q8AttnMaps& m, const Plan& pl, voi
 template <int HD>
 cudaError_t attn_d(const Q8AttnArgs& a, const Q8AttnMaps& m, const Plan& pl, void* ws,
                    cudaStream_t s) {
-  if (pl.R == 8) return attn_t<HD, 8>(a, m, pl, ws, s);
-  if (pl.R == 16) return attn_t<HD, 16>(a, m, pl, ws, s);
-  return attn_t<HD, 32>(a, m, pl, ws, s);
+  switch (pl.RL) {
+    case 2: return attn_t<HD, 8, 2>(a, m, pl, ws, s);
+    case 4: return attn_t<HD, 8, 4>(a, m, pl, ws, s);
+    case 8: return attn_t<HD, 8, 8>(a, m, pl, ws, s);
+    case 16: return attn_t<HD, 16, 16>(a, m, pl, ws, s);
+    default: return attn_t<HD, 32, 32>(a, m, pl, ws, s);
+  }
 }
 }  // namespace
 

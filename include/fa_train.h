@@ -365,7 +365,8 @@ int fa_paged_attention_bwd(const void* q, const void* k_cache, const void* v_cac
  * fa_train_fwd_ex takes them (a long prompt against what is cached). No counterpart on the
  * pages.
  *
- * Scales must be finite and > 0 wherever a key is read; what the slots past a sequence's end
+ * Scales must lie in (0, 2^100] wherever a key is read (value scales below 2^-100, the writer's
+ * smallest, are read as 2^-100); what the slots past a sequence's end
  * hold (codes and scales, NaN included) reaches no result. */
 typedef struct fa_q8_cache {
   void* k;              /* e4m3 [num_pages, n_kv_heads, page_size, head_dim], 16-byte aligned */
