@@ -46,7 +46,6 @@ namespace fa {
 
 namespace {
 constexpr int kKT = 128;          // keys of a tile (the MMA M of S^T)
-constexpr int kScRing = 2;        // tiles of scales in shared memory
 constexpr int kPageChunk = 128;   // block-table entries staged at a time
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -60,10 +59,10 @@ constexpr float kSumExp = 16.0f, kSumUnit = 65536.0f;
 // R query rows of a unit at a time. KST, VST: stages of the K and V rings; V has more, as a V tile
 // stays until the weights of its keys are there (3 and 3 of 16 KB: 167 us, 2 and 4: 162 us for 64
 // sequences of up to 16k keys).
-template <int HD, int R_>
+template <int HD, int R_, int RL>
 struct Q8Layout {
   static constexpr int R = R_;
-  static constexpr int CTAS = R > 8 || HD > 128 ? 1 : HD == 64 ? 3 : 2;  // resident on an SM
+  static constexpr int CTAS = R > 8 || HD > 128 ? 1 : HD == 64 && RL <= 4 ? 3 : 2;  // resident on an SM
   static constexpr int KST = HD == 64 ? (R == 8 ? 2 : 6) : HD == 128 ? (R == 8 ? 2 : 5) : 2;
   static constexpr int VST = HD == 64 ? (R == 8 ? 4 : 8) : HD == 128 ? (R == 8 ? 4 : R == 16 ? 6 : 5)
                                                          : (R == 8 ? 4 : R == 16 ? 3 : 2);
@@ -88,7 +87,7 @@ struct Q8Layout {
   static constexpr int TMA_WARP = 4, S_WARP = 5, O_WARP = 6, QS_WARP = 7;
   static_assert(TMEM_USED <= 512 && TMEM_COLS * CTAS <= 512, "TMEM budget");
   // dynamic, static (pages, scales, barriers, rows: below) and the driver's 1 KB
-  static constexpr int STATIC_BYTES = 4 * kPageChunk + 8 * kScRing * kKT + 64 * R + 512;
+  static constexpr int STATIC_BYTES = 4 * kPageChunk + 16 * kKT + 72 * R + 512;
   static_assert((SMEM_BYTES + STATIC_BYTES + 1024) * CTAS <= 228 * 1024, "shared memory budget");
 };
 
@@ -141,6 +140,11 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&r)[8]) {
                "r"(__float_as_uint(r[3])), "r"(__float_as_uint(r[4])), "r"(__float_as_uint(r[5])),
                "r"(__float_as_uint(r[6])), "r"(__float_as_uint(r[7]))
                : "memory");
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 // N = 16, 32 or 64 columns of a TMEM lane.
 template <int N>
@@ -201,6 +205,11 @@ __device__ __noinline__ bool wait_more(uint64_t* bar, uint32_t parity, WaitCtl* 
 }
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, WaitCtl* w) {
   return mbar_try_wait(bar, parity) || wait_more(bar, parity, w);
+}
+// The wait of a whole warp, that does not part its lanes: true for all or none.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, WaitCtl* w) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, wait_more(bar, parity, w));
 }
 // Largest value of the warp (NaN is passed over).
 __device__ __forceinline__ float warp_max(float x) {
@@ -323,10 +332,10 @@ struct Walk {
 // RL: the rows of a unit that there can be (of the R that a tile has columns for): the softmax's
 // arithmetic runs on these alone.
 template <int HD, int R, int RL>
-__global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
+__global__ void __launch_bounds__(256, Q8Layout<HD, R, RL>::CTAS)
     q8_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
                    const Q8K p) {
-  using LY = Q8Layout<HD, R>;
+  using LY = Q8Layout<HD, R, RL>;
   constexpr int KST = LY::KST, VST = LY::VST;
   constexpr int KCH = LY::KCH, CH = LY::CH, NS = LY::NS, NP = LY::NP;
   extern __shared__ uint8_t smem_raw[];
@@ -334,15 +343,16 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
                                              ~uintptr_t(1023));
   __shared__ uint64_t k_full[KST], v_full[VST], k_empty[KST], v_empty[VST];
   __shared__ uint64_t s_full[2], s_free[2], p_full[2], p_done[2], q_full[2], q_free[2];
-  __shared__ uint64_t sc_full[kScRing], sc_free[kScRing], drain_s, drain_o;
+  __shared__ uint64_t drain_s, drain_o;
   __shared__ uint32_t tmem_base_s;
   __shared__ WaitCtl wctl;
   __shared__ int bad_input;
   __shared__ int page_s[kPageChunk];
-  __shared__ float sc_s[kScRing][2][kKT];  // key scale, log2 of the value scale
+  __shared__ float sc_s[2][2][kKT];  // key scale, log2 of the value scale
   __shared__ __align__(16) float qs_s[2][R];   // rows: score factor, key limit
   __shared__ __align__(16) int lim_s[2][R];
   __shared__ __align__(16) float nm_s[2][R], red_s[4][R];  // -m; maxima or sums of the warps
+  __shared__ __align__(16) float up_s[R], f_s[R];  // how far m moves, and O's factors then
 
   const int warp = warp_id(), lane = lane_id();
   Walk w;
@@ -359,16 +369,12 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
       mbar_init(&v_empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&s_full[s], 1);
+      mbar_init(&s_full[s], 2);  // the MMA, and the scales of its keys
       mbar_init(&s_free[s], 4);
       mbar_init(&p_full[s], 4);
       mbar_init(&p_done[s], 1);
       mbar_init(&q_full[s], 1);
       mbar_init(&q_free[s], 2);
-    }
-    for (int s = 0; s < kScRing; ++s) {
-      mbar_init(&sc_full[s], 1);
-      mbar_init(&sc_free[s], 4);
     }
     mbar_init(&drain_s, 1);
     mbar_init(&drain_o, 1);
@@ -504,8 +510,8 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
     while (ok && w.next(p, R)) {
       for (int j = w.ja; j < w.jb; ++j, ++g) {
         const int st = g % VST, buf = g & 1, n0 = j * kKT;
-        ok = __all_sync(0xffffffffu, wait(&v_full[st], (g / VST) & 1, &wctl));
-        if (ok) ok = __all_sync(0xffffffffu, wait(&p_full[buf], (g >> 1) & 1, &wctl));
+        ok = wait_warp(&v_full[st], (g / VST) & 1, &wctl) &&
+             wait_warp(&p_full[buf], (g >> 1) & 1, &wctl);
         if (!ok) break;
         uint8_t* vt = smem + LY::OFF_V + st * LY::KV_BYTES;
         if (n0 + kKT > w.len) {  // rows behind the sequence's end
@@ -547,8 +553,10 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
     int g = 0, un = 0;
     bool ok = true;
     const int nb_shift = p.ps_shift - p.sb_shift;
+    const unsigned page_scales = (unsigned)p.Hk << nb_shift;  // of a page's heads
     for (; ok && w.next(p, R); ++un) {
       const int32_t* row = p.table + (size_t)w.b * p.max_pages;
+      const unsigned head_scales = (unsigned)w.kh << nb_shift;
       int pg[2][4];
       float ks[2][4], vs[2][4];
       auto pages = [&](int j, int (&to)[4]) {
@@ -563,8 +571,8 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
         for (int e = 0; e < 4; ++e) {
           const int key = j * kKT + e * 32 + lane;
           const bool have = pgs[e] >= 0 && pgs[e] < p.num_pages;
-          const size_t at = (((size_t)(have ? pgs[e] : 0) * p.Hk + w.kh) << nb_shift) +
-                            ((key & ((1 << p.ps_shift) - 1)) >> p.sb_shift);
+          const size_t at = (size_t)(unsigned)pgs[e] * page_scales +
+                            (head_scales + ((key & ((1 << p.ps_shift) - 1)) >> p.sb_shift));
           k[e] = have ? __ldg(p.k_scale + at) : 0.0f;
           v[e] = have ? __ldg(p.v_scale + at) : 1.0f;
         }
@@ -572,9 +580,7 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
       pages(w.ja, pg[0]);
       pages(w.ja + 1, pg[1]);
       const int qb = un & 1;
-      if (un >= 2 &&
-          !__all_sync(0xffffffffu, wait(&q_free[qb], ((un >> 1) - 1) & 1, &wctl)))
-        break;
+      if (un >= 2 && !wait_warp(&q_free[qb], ((un >> 1) - 1) & 1, &wctl)) break;
       uint8_t* dst = smem + LY::OFF_Q + qb * LY::Q_BYTES;
       const int r0 = w.rb * R;
       const __nv_bfloat16* src =
@@ -585,7 +591,7 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
         lim_s[qb][lane] = min(p.causal ? max(0, w.len - p.lq + i + 1) : w.len, w.jb * kKT);
       }
       float mine = 0.0f;  // the score factor of row `lane`
-#pragma unroll 4
+#pragma unroll 2
       for (int r = 0; r < live; ++r) {
         uint32_t x[CPL / 2];
 #pragma unroll
@@ -646,18 +652,17 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (j + h >= w.jb) break;
-          const int slot = g % kScRing;
-          if (g >= kScRing)
-            ok = __all_sync(0xffffffffu, wait(&sc_free[slot], (g / kScRing - 1) & 1, &wctl));
+          const int slot = g & 1;
+          if (g >= 2) ok = wait_warp(&s_free[slot], ((g >> 1) - 1) & 1, &wctl);
           if (!ok) break;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             sc_s[slot][0][e * 32 + lane] = ks[h][e];
             sc_s[slot][1][e * 32 + lane] =
-                __log2f(fmaxf(vs[h][e], __int_as_float((kQ8MinExp + 127) << 23)));
+                lg2(fmaxf(vs[h][e], __int_as_float((kQ8MinExp + 127) << 23)));
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sc_full[slot]);
+          if (lane == 0) mbar_arrive(&s_full[slot]);
           ++g;
           scales(j + h + 2, pg[h], ks[h], vs[h]);
           pages(j + h + 4, pg[h]);
@@ -676,7 +681,7 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
     bool ok = true;
     for (; ok && w.next(p, R); ++un) {
       const int qb = un & 1;
-      ok = wait(&q_full[qb], (un >> 1) & 1, &wctl);
+      ok = wait_warp(&q_full[qb], (un >> 1) & 1, &wctl);
       const int r0 = w.rb * R, live = min(RL, p.rows - r0);
       // tiles below lim_min need no test of the keys
       const int lim_min = min(p.causal ? max(0, w.len - p.lq + 1) : w.len, w.jb * kKT);
@@ -685,20 +690,16 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
       for (int r = 0; r < RL; ++r) l[r] = 0.0f;
       for (int j = w.ja; j < w.jb; ++j, ++g) {
         const int buf = g & 1;
-        const uint32_t ph = (g >> 1) & 1;  // (kScRing = 2 too)
-        ok = ok && wait(&sc_full[buf], ph, &wctl);
-        const float kc = sc_s[buf][0][key], lsv = sc_s[buf][1][key];
-        ok = __all_sync(0xffffffffu, ok && wait(&s_full[buf], ph, &wctl));
+        const uint32_t ph = (g >> 1) & 1;
+        ok = ok && wait_warp(&s_full[buf], ph, &wctl);
         tc_fence_after();
         uint32_t sr[NS];
         load_cols<NS>(lanes + LY::COL_S + buf * NS, sr);
+        const float kc = sc_s[buf][0][key], lsv = sc_s[buf][1][key];
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&s_free[buf]);
-          mbar_arrive(&sc_free[buf]);
-        }
+        if (lane == 0) mbar_arrive(&s_free[buf]);
         const bool first = j == w.ja;
         float t[RL];
         const uint64_t kc2 = f2_pack(kc, kc), lsv2 = f2_pack(lsv, lsv);
@@ -731,43 +732,43 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
             ok = false;
             break;
           }
-          float f[RL];
-#pragma unroll
-          for (int r = 0; r < RL; ++r) {
-            const float mx = fmaxf(fmaxf(red_s[0][r], red_s[1][r]),
-                                   fmaxf(red_s[2][r], red_s[3][r]));
+          if (key < RL) {
+            const float mx = fmaxf(fmaxf(red_s[0][key], red_s[1][key]),
+                                   fmaxf(red_s[2][key], red_s[3][key]));
             float up = mx - kTop;
             if (first ? mx == -INFINITY : !(up > 0.0f)) up = 0.0f;
-            t[r] -= up;
-            f[r] = first ? 1.0f : ex2(-up);
-            l[r] *= f[r];
-            if (key == r) nm_s[qb][r] = first ? -up : nm_s[qb][r] - up;
+            nm_s[qb][key] = first ? -up : nm_s[qb][key] - up;
+            up_s[key] = up;
+            f_s[key] = ex2(-up);
           }
-          if (!first) {  // O is scaled, once the last O^T MMA is done
-            ok = __all_sync(0xffffffffu, wait(&p_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &wctl));
+          if (!first) {  // O is scaled too, once the last O^T MMA is done
+            ok = wait_warp(&p_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &wctl);
             tc_fence_after();
+          }
+          softmax_any(false);
+#pragma unroll
+          for (int r = 0; r < RL; ++r) {
+            t[r] -= up_s[r];
+            if (!first) l[r] *= f_s[r];
+          }
+          if (!first) {
 #pragma unroll 1
-            for (int h = 0; h < KCH; ++h) {
+            for (int c = 0; c < KCH * NP; c += 32) {  // (R columns a piece; f_s beyond RL: any)
+              uint32_t x[32];
+              tmem_ld32(lanes + LY::COL_O + c, x);
+              tmem_wait_ld();
 #pragma unroll
-              for (int c = 0; c < NP; c += 32) {  // (R columns a piece)
-                uint32_t x[32];
-                tmem_ld32(lanes + LY::COL_O + h * NP + c, x);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if ((c + e) % R < RL)
-                    x[e] = __float_as_uint(__uint_as_float(x[e]) * f[(c + e) % R]);
-                tmem_st32(lanes + LY::COL_O + h * NP + c, x);
-              }
+              for (int e = 0; e < 32; ++e)
+                x[e] = __float_as_uint(__uint_as_float(x[e]) * f_s[e % R]);
+              tmem_st32(lanes + LY::COL_O + c, x);
             }
             tmem_wait_st();
             tc_fence_before();
           }
-          softmax_any(false);  // nm_s is read, and red_s written, by everyone after this
         }
         // weights, their sum, and their pieces into shared memory, a key's row of NP bytes
         const float inv = ex2(-lsv - kSumExp);  // 1 / value scale, in the sum's unit
-        if (g >= 2) ok = ok && wait(&p_done[buf], ph ^ 1, &wctl);
+        if (g >= 2) ok = ok && wait_warp(&p_done[buf], ph ^ 1, &wctl);
         uint32_t pc[3][R / 4];
 #pragma unroll
         for (int r = 0; r < RL; r += 4) {
@@ -818,7 +819,7 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R>::CTAS)
         for (int o = 16; o > 0; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
         if (lane == 0) red_s[warp][r] = x;
       }
-      if (any && ok) ok = wait(&p_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &wctl);
+      if (any && ok) ok = wait_warp(&p_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &wctl);
       if (softmax_any(!ok)) {
         ok = false;
         break;
@@ -951,7 +952,7 @@ Plan make_plan(const Q8AttnArgs& a) {
   pl.R = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
   pl.RL = rows <= 2 ? 2 : rows <= 4 ? 4 : pl.R;
   pl.rb = (rows + pl.R - 1) / pl.R;
-  const int ctas = 152 * (pl.R > 8 || a.d > 128 ? 1 : a.d == 64 ? 3 : 2);
+  const int ctas = 152 * (pl.R > 8 || a.d > 128 ? 1 : a.d == 64 && pl.RL <= 4 ? 3 : 2);
   const long long cap = (long long)a.max_pages << a.ps_shift;
   const long long tiles = (cap + kKT - 1) / kKT * a.B * a.Hk * pl.rb;
   pl.grid = (int)std::min<long long>(ctas, tiles);
@@ -961,7 +962,7 @@ Plan make_plan(const Q8AttnArgs& a) {
 template <int HD, int R, int RL>
 cudaError_t attn_t(const Q8AttnArgs& a, const Q8AttnMaps& m, const Plan& pl, void* ws,
                    cudaStream_t s) {
-  using LY = Q8Layout<HD, R>;
+  using LY = Q8Layout<HD, R, RL>;
   auto kern = q8_attn_kernel<HD, R, RL>;
   static OncePerKey<> smem_attr;
   cudaError_t e = set_smem_once(smem_attr, kern, LY::SMEM_BYTES);
