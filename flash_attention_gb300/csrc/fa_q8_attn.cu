@@ -62,10 +62,11 @@ constexpr float kSumExp = 16.0f, kSumUnit = 65536.0f;
 template <int HD, int R_, int RL>
 struct Q8Layout {
   static constexpr int R = R_;
-  static constexpr int CTAS = R > 8 || HD > 128 ? 1 : HD == 64 && RL <= 4 ? 3 : 2;  // resident on an SM
-  static constexpr int KST = HD == 64 ? (R == 8 ? 2 : 6) : HD == 128 ? (R == 8 ? 2 : 5) : 2;
-  static constexpr int VST = HD == 64 ? (R == 8 ? 4 : 8) : HD == 128 ? (R == 8 ? 4 : R == 16 ? 6 : 5)
-                                                         : (R == 8 ? 4 : R == 16 ? 3 : 2);
+  static constexpr int CTAS = R > 16 || HD > 128 ? 1 : HD == 64 && RL <= 4 ? 3 : 2;  // resident on an SM
+  static constexpr int KST = HD == 64 ? (R == 8 ? 2 : 4) : HD == 128 ? (R <= 16 ? 2 : 5) : 2;
+  static constexpr int VST = HD == 64    ? (R <= 16 ? 4 : 8)
+                             : HD == 128 ? (R == 8 ? 4 : R == 16 ? 2 : 5)
+                                         : (R == 8 ? 4 : R == 16 ? 3 : 2);
   static constexpr int CH = HD <= 128 ? HD : 128;   // columns (bytes) of a swizzled row
   static constexpr int KCH = HD / CH;               // row chunks: 1, or 2 at head_dim 256
   static constexpr int NS = 2 * R;                  // columns of S^T: hi rows, lo rows
@@ -132,14 +133,6 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&r)[8]) {
                : "r"(taddr));
 #pragma unroll
   for (int e = 0; e < 8; ++e) r[e] = __uint_as_float(v[e]);
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
-                   taddr),
-               "r"(__float_as_uint(r[0])), "r"(__float_as_uint(r[1])), "r"(__float_as_uint(r[2])),
-               "r"(__float_as_uint(r[3])), "r"(__float_as_uint(r[4])), "r"(__float_as_uint(r[5])),
-               "r"(__float_as_uint(r[6])), "r"(__float_as_uint(r[7]))
-               : "memory");
 }
 __device__ __forceinline__ float lg2(float x) {
   float y;
@@ -246,6 +239,7 @@ __device__ __forceinline__ int q8_tiles(const Q8K& p, int b) {
 // Key tiles of all sequences (of one unit each), by one warp that has those of sequence `lane`.
 // The host has checked that the list of all tiles, Hk * rb times as long, fits 31 bits.
 __device__ __forceinline__ int q8_all_tiles(const Q8K& p, int mine, int lane) {
+#pragma unroll 1
   for (int b = lane + 32; b < p.B; b += 32) mine += q8_tiles(p, b);
   return (int)__reduce_add_sync(0xffffffffu, (unsigned)mine);
 }
@@ -254,7 +248,8 @@ __device__ __forceinline__ unsigned q8_share(unsigned all, unsigned grid) {
   return (all + grid - 1) / grid;
 }
 
-// The units of a CTA's share [t, t1) of the list, in order. Every role walks its own copy.
+// The units of a CTA's share [t, t1) of the list, in order: warp 7 walks it and publishes the units
+// in shared memory, where the other roles take them from.
 struct Walk {
   unsigned t, t1;    // next tile of the list, end of the share
   unsigned pre;      // tiles of the list before sequence b
@@ -275,10 +270,12 @@ struct Walk {
     pre = 0;
     b = nt = len = 0;
     if (t >= t1) return;
+#pragma unroll 1
     for (int base = 0;; base += 32) {  // ends: t lies below the sum over all sequences
       const unsigned n =
           (base == 0 ? mine : base + lane < p.B ? q8_tiles(p, base + lane) : 0) * U;
       unsigned upto = n;
+#pragma unroll 1
       for (int o = 1; o < 32; o *= 2) {
         const unsigned x = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += x;
@@ -299,6 +296,7 @@ struct Walk {
   __device__ __forceinline__ bool next(const Q8K& p, int R) {
     if (t >= t1) return false;
     const unsigned U = (unsigned)(p.Hk * p.rb);
+#pragma unroll 1
     while (t >= pre + U * nt) {  // the next sequence with keys
       pre += U * nt;
       if (++b >= p.B) return false;
@@ -329,6 +327,28 @@ struct Walk {
   }
 };
 
+struct Unit {
+  int b, kh, rb, ja, jb, len, whole, first;
+};
+// Units in shared memory: warp 7 publishes, the others read and free (7 warps).
+constexpr int kUnits = 4;
+struct UnitRing {
+  int4 at[kUnits][2];
+  uint64_t full[kUnits], free[kUnits];
+};
+// The next unit, for a whole warp: false where a wait ran out. end: there is none.
+__device__ __forceinline__ bool take_unit(UnitRing* ring, int un, Unit& u, bool& end, int lane,
+                                          WaitCtl* wctl) {
+  const int slot = un % kUnits;
+  if (!wait_warp(&ring->full[slot], (un / kUnits) & 1, wctl)) return false;
+  const int4 a = ring->at[slot][0], c = ring->at[slot][1];
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&ring->free[slot]);
+  u = Unit{a.x, a.y, a.z, a.w, c.x, c.y, c.z & 1, c.z & 2};
+  end = c.z < 0;
+  return true;
+}
+
 // RL: the rows of a unit that there can be (of the R that a tile has columns for): the softmax's
 // arithmetic runs on these alone.
 template <int HD, int R, int RL>
@@ -344,11 +364,12 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R, RL>::CTAS)
   __shared__ uint64_t k_full[KST], v_full[VST], k_empty[KST], v_empty[VST];
   __shared__ uint64_t s_full[2], s_free[2], p_full[2], p_done[2], q_full[2], q_free[2];
   __shared__ uint64_t drain_s, drain_o;
+  __shared__ __align__(16) UnitRing units;
   __shared__ uint32_t tmem_base_s;
   __shared__ WaitCtl wctl;
   __shared__ int bad_input;
   __shared__ int page_s[kPageChunk];
-  __shared__ float sc_s[2][2][kKT];  // key scale, log2 of the value scale
+  __shared__ __align__(16) float sc_s[2][2][kKT];  // key scale, log2 of the value scale
   __shared__ __align__(16) float qs_s[2][R];   // rows: score factor, key limit
   __shared__ __align__(16) int lim_s[2][R];
   __shared__ __align__(16) float nm_s[2][R], red_s[4][R];  // -m; maxima or sums of the warps
@@ -356,18 +377,21 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R, RL>::CTAS)
 
   const int warp = warp_id(), lane = lane_id();
   Walk w;
-  w.init(p, blockIdx.x, gridDim.x, lane);
+  if (warp == LY::QS_WARP) w.init(p, blockIdx.x, gridDim.x, lane);
   if (threadIdx.x == 0) {
     wait_ctl_init(&wctl, p.wait_limit_ns);
     bad_input = 0;
+#pragma unroll 1
     for (int s = 0; s < KST; ++s) {
       mbar_init(&k_full[s], 1);
       mbar_init(&k_empty[s], 1);
     }
+#pragma unroll 1
     for (int s = 0; s < VST; ++s) {
       mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], 1);
     }
+#pragma unroll 1
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 2);  // the MMA, and the scales of its keys
       mbar_init(&s_free[s], 4);
@@ -375,6 +399,11 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R, RL>::CTAS)
       mbar_init(&p_done[s], 1);
       mbar_init(&q_full[s], 1);
       mbar_init(&q_free[s], 2);
+    }
+#pragma unroll 1
+    for (int s = 0; s < kUnits; ++s) {
+      mbar_init(&units.full[s], 1);
+      mbar_init(&units.free[s], 7);
     }
     mbar_init(&drain_s, 1);
     mbar_init(&drain_o, 1);
@@ -392,6 +421,7 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R, RL>::CTAS)
 
   if (warp == 0 && blockIdx.x == 0) {  // lengths out of range are clamped, and reported here
     bool bad = false;
+#pragma unroll 1
     for (int b = lane; b < p.B; b += 32) bad |= p.lens[b] != q8_len(p, b);
     if (bad) bad_input = 1;
   }
@@ -409,10 +439,13 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R, RL>::CTAS)
     const int sub = lane / KCH, c = lane % KCH; // this lane's box
     int g = 0, gk = 0, gv = 0;                  // tiles, and copies of K and V, so far
     int page_b = -1, page_lo = 0;               // page_s holds entries page_lo .. of sequence page_b
-    bool ok = true;
-    while (ok && w.next(p, R)) {
+    Unit w;
+    bool ok = true, end = false;
+#pragma unroll 1
+    for (int un = 0; ok && (ok = take_unit(&units, un, w, end, lane, &wctl)) && !end; ++un) {
       const int used = (w.len + (1 << p.ps_shift) - 1) >> p.ps_shift;
       const int32_t* row = p.table + (size_t)w.b * p.max_pages;
+#pragma unroll 1
       for (int j = w.ja; j < w.jb && ok; ++j, ++g) {
         const int n0 = j * kKT;
         const int p_lo = n0 >> p.ps_shift, p_hi = min(used - 1, (n0 + kKT - 1) >> p.ps_shift);
@@ -421,6 +454,7 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R, RL>::CTAS)
           page_lo = p_lo;
           __syncwarp();
           const int n = min(kPageChunk, used - page_lo);
+#pragma unroll 1
           for (int e = lane; e < n; e += 32) {
             int pg = row[page_lo + e];
             if (pg < 0 || pg >= p.num_pages) {
@@ -460,10 +494,12 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R, RL>::CTAS)
       }
     }
     if (leader) {  // no copy may be in flight when the CTA ends
+#pragma unroll 1
       for (int s = 0; s < KST; ++s) {
         const int n = (gk - s + KST - 1) / KST;  // copies into stage s
         if (n > 0) mbar_wait_drain(&k_full[s], (n - 1) & 1);
       }
+#pragma unroll 1
       for (int s = 0; s < VST; ++s) {
         const int n = (gv - s + VST - 1) / VST;
         if (n > 0) mbar_wait_drain(&v_full[s], (n - 1) & 1);
@@ -471,20 +507,22 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R, RL>::CTAS)
     }
   } else if (warp == LY::S_WARP) {
     // ------------------------------------------------------------------ S^T = K q^T
-    if (elect_one()) {
-      const uint32_t id = idesc_f8(0, 0, kKT, NS, 0, 0);
-      int g = 0, un = 0;
-      bool ok = true;
-      for (; ok && w.next(p, R); ++un) {
-        ok = wait(&q_full[un & 1], (un >> 1) & 1, &wctl);
+    const uint32_t id = idesc_f8(0, 0, kKT, NS, 0, 0);
+    int g = 0;
+    Unit w;
+    bool ok = true, end = false;
+#pragma unroll 1
+    for (int un = 0; ok && (ok = take_unit(&units, un, w, end, lane, &wctl)) && !end; ++un) {
+      ok = wait_warp(&q_full[un & 1], (un >> 1) & 1, &wctl);
+      const Desc qb = q8_desc<CH>(smem_u32(smem + LY::OFF_Q + (un & 1) * LY::Q_BYTES), 0);
+#pragma unroll 1
+      for (int j = w.ja; j < w.jb && ok; ++j, ++g) {
+        const int st = g % KST, buf = g & 1;
+        ok = wait_warp(&k_full[st], (g / KST) & 1, &wctl) &&
+             (g < 2 || wait_warp(&s_free[buf], ((g >> 1) - 1) & 1, &wctl));
         if (!ok) break;
-        const Desc qb = q8_desc<CH>(smem_u32(smem + LY::OFF_Q + (un & 1) * LY::Q_BYTES), 0);
-        for (int j = w.ja; j < w.jb; ++j, ++g) {
-          const int st = g % KST, buf = g & 1;
-          ok = wait(&k_full[st], (g / KST) & 1, &wctl);
-          if (ok && g >= 2) ok = wait(&s_free[buf], ((g >> 1) - 1) & 1, &wctl);
-          if (!ok) break;
-          tc_fence_after();
+        tc_fence_after();
+        if (lane == 0) {
           const Desc ka = q8_desc<CH>(smem_u32(smem + LY::OFF_K + st * LY::KV_BYTES), 0);
           const uint32_t tS = tbase + LY::COL_S + buf * NS;
 #pragma unroll
@@ -496,18 +534,26 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R, RL>::CTAS)
           mma_commit(&s_full[buf]);
           mma_commit(&k_empty[st]);
         }
-        if (ok) mma_commit(&q_free[un & 1]);  // (arrives at once where the unit had no tile)
+        __syncwarp();
       }
+      // (arrives at once where the unit had no tile)
+      if (ok && lane == 0) mma_commit(&q_free[un & 1]);
+    }
+    if (lane == 0) {
       mma_commit(&drain_s);
       mbar_wait_drain(&drain_s, 0);
     }
+    __syncwarp();
   } else if (warp == LY::O_WARP) {
     // ------------------------------------------------------------------ O^T += V^T w^T
     constexpr int MV = HD < 128 ? HD : 128;  // head-dim rows of an MMA
     const uint32_t id = idesc_f8(0, 1, MV, NP, 1, 1);
     int g = 0;
-    bool ok = true;
-    while (ok && w.next(p, R)) {
+    Unit w;
+    bool ok = true, end = false;
+#pragma unroll 1
+    for (int un = 0; ok && (ok = take_unit(&units, un, w, end, lane, &wctl)) && !end; ++un) {
+#pragma unroll 1
       for (int j = w.ja; j < w.jb; ++j, ++g) {
         const int st = g % VST, buf = g & 1, n0 = j * kKT;
         ok = wait_warp(&v_full[st], (g / VST) & 1, &wctl) &&
@@ -516,6 +562,7 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R, RL>::CTAS)
         uint8_t* vt = smem + LY::OFF_V + st * LY::KV_BYTES;
         if (n0 + kKT > w.len) {  // rows behind the sequence's end
           const int r0 = w.len - n0;
+#pragma unroll 1
           for (int e = lane; e < (kKT - r0) * (HD / 16); e += 32) {
             const int r = r0 + e / (HD / 16), x = e % (HD / 16);
             *reinterpret_cast<uint4*>(vt + x * 16 / CH * (kKT * CH) + r * CH + x * 16 % CH) =
@@ -546,126 +593,146 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R, RL>::CTAS)
     }
     __syncwarp();
   } else if (warp == LY::QS_WARP) {
-    // ------------------------------------------------------------------ q in two pieces, and
-    // the keys' scales: those of two tiles are on their way in registers, and the table entries
-    // of the two after them
-    constexpr int CPL = HD / 32;  // columns of a lane
-    int g = 0, un = 0;
-    bool ok = true;
-    const int nb_shift = p.ps_shift - p.sb_shift;
+    // ------------------------------------------------------------------ the units, their q in
+    // two pieces and their keys' scales
+    constexpr int LPR = HD / 8, RPS = 32 / LPR;  // lanes of a row (8 columns each), rows of a step
+    constexpr int QSTEPS = RL <= RPS ? 1 : RL / RPS;
+    const int nb_shift = p.ps_shift - p.sb_shift, ps_mask = (1 << p.ps_shift) - 1;
     const unsigned page_scales = (unsigned)p.Hk << nb_shift;  // of a page's heads
-    for (; ok && w.next(p, R); ++un) {
-      const int32_t* row = p.table + (size_t)w.b * p.max_pages;
-      const unsigned head_scales = (unsigned)w.kh << nb_shift;
-      int pg[2][4];
-      float ks[2][4], vs[2][4];
-      auto pages = [&](int j, int (&to)[4]) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = j * kKT + e * 32 + lane;
-          to[e] = key < w.len && j < w.jb ? row[key >> p.ps_shift] : -1;
-        }
-      };
-      auto scales = [&](int j, const int (&pgs)[4], float (&k)[4], float (&v)[4]) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = j * kKT + e * 32 + lane;
-          const bool have = pgs[e] >= 0 && pgs[e] < p.num_pages;
-          const size_t at = (size_t)(unsigned)pgs[e] * page_scales +
-                            (head_scales + ((key & ((1 << p.ps_shift) - 1)) >> p.sb_shift));
-          k[e] = have ? __ldg(p.k_scale + at) : 0.0f;
-          v[e] = have ? __ldg(p.v_scale + at) : 1.0f;
-        }
-      };
-      pages(w.ja, pg[0]);
-      pages(w.ja + 1, pg[1]);
-      const int qb = un & 1;
-      if (un >= 2 && !wait_warp(&q_free[qb], ((un >> 1) - 1) & 1, &wctl)) break;
-      uint8_t* dst = smem + LY::OFF_Q + qb * LY::Q_BYTES;
-      const int r0 = w.rb * R;
-      const __nv_bfloat16* src =
-          p.q + (((size_t)w.b * p.Hk + w.kh) * p.rows + r0) * HD + lane * CPL;
-      const int live = min(R, p.rows - r0);
-      if (lane < R) {
-        const int i = (r0 + lane) % p.lq;
-        lim_s[qb][lane] = min(p.causal ? max(0, w.len - p.lq + i + 1) : w.len, w.jb * kKT);
+    int g = 0, published = 0;
+    bool ok = true, ended = false;
+#pragma unroll 1
+    for (int un = -1; ok; ++un) {  // (-1: nothing but the first unit's publication)
+      int4 ua = make_int4(0, 0, 0, 0), uc = ua;
+      if (un >= 0) {
+        ua = units.at[un % kUnits][0];
+        uc = units.at[un % kUnits][1];
+        if (uc.z < 0) break;  // the end
       }
-      float mine = 0.0f;  // the score factor of row `lane`
-#pragma unroll 2
-      for (int r = 0; r < live; ++r) {
-        uint32_t x[CPL / 2];
-#pragma unroll
-        for (int e = 0; e < CPL / 2; ++e)
-          x[e] = reinterpret_cast<const uint32_t*>(src + (size_t)r * HD)[e];
-        uint32_t a = 0;
-#pragma unroll
-        for (int e = 0; e < CPL / 2; ++e)
-          a = max(a, max(x[e] & 0x7fffu, (x[e] >> 16) & 0x7fffu));
-        a = __reduce_max_sync(0xffffffffu, a);
-        // 2^sh puts the row's largest element into [128, 256); a row with an element that is not
-        // finite becomes NaN
-        const int sh = 134 - (int)max(a >> 7, 1u);
-        const bool odd = a >= 0x7f80u;
-        const float f0 = __int_as_float((sh / 2 + 127) << 23);
-        const float f1 = __int_as_float((sh - sh / 2 + 127) << 23);
-        uint32_t hi = 0, lo = 0, hi2 = 0, lo2 = 0;
-#pragma unroll
-        for (int e = 0; e < CPL / 2; ++e) {
-          const float u = __uint_as_float(x[e] << 16) * f0 * f1;
-          const float v = __uint_as_float(x[e] & 0xffff0000u) * f0 * f1;
-          const uint32_t h = odd ? 0x7f7fu : e4m3x2_from_f32(u, v);
-          const float2 t = f32_from_e4m3x2(h);
-          const uint32_t l = e4m3x2_from_f32((u - t.x) * 16.0f, (v - t.y) * 16.0f);
-          if (e < 2) {
-            hi |= h << (16 * e);
-            lo |= l << (16 * e);
-          } else {
-            hi2 |= h << (16 * (e - 2));
-            lo2 |= l << (16 * (e - 2));
-          }
+      const int kh = ua.y, ja = ua.w, jb = uc.x, len = uc.y;
+      if (un >= 0) {
+        // ---- q: row r of the block in pieces hi (row r of the operand) and lo (row R + r)
+        const int qb = un & 1;
+        if (un >= 2 && !wait_warp(&q_free[qb], ((un >> 1) - 1) & 1, &wctl)) break;
+        uint8_t* dst = smem + LY::OFF_Q + qb * LY::Q_BYTES;
+        const int r0 = ua.z * R, live = min(RL, p.rows - r0);
+        const int col = lane % LPR * 8, ch = col / CH, in = col % CH;
+        const __nv_bfloat16* src = p.q + (((size_t)ua.x * p.Hk + kh) * p.rows + r0) * HD + col;
+        auto row_of = [&](int step) { return step * RPS + lane / LPR; };
+        auto load = [&](int step) {
+          return row_of(step) < live
+                     ? __ldg(reinterpret_cast<const uint4*>(src + (size_t)row_of(step) * HD))
+                     : make_uint4(0u, 0u, 0u, 0u);
+        };
+        if (lane < R) {
+          const int i = p.lq == 1 ? 0 : (r0 + lane) % p.lq;
+          lim_s[qb][lane] = min(p.causal ? max(0, len - p.lq + i + 1) : len, jb * kKT);
         }
-        const int col = lane * CPL, ch = col / CH, in = col % CH;
+        uint4 x = load(0), x1 = QSTEPS > 1 ? load(1) : x;
+#pragma unroll 1
+        for (int step = 0; step < QSTEPS; ++step) {
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+          x = x1;
+          if (QSTEPS > 2) x1 = load(step + 2);
+          uint32_t m = 0;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {  // hi rows, then lo rows
-          const int n = half * R + r;
-          uint8_t* at = dst + ch * (NS * CH) + n * CH + swz<CH>(in / 16, n) * 16 + in % 16;
-          if constexpr (CPL == 2)
-            *reinterpret_cast<uint16_t*>(at) = (uint16_t)(half ? lo : hi);
-          else if constexpr (CPL == 4)
-            *reinterpret_cast<uint32_t*>(at) = half ? lo : hi;
-          else
-            *reinterpret_cast<uint2*>(at) = half ? make_uint2(lo, lo2) : make_uint2(hi, hi2);
-        }
-        if (lane == r)
-          mine = p.scale_log2 * __int_as_float((127 - sh / 2) << 23) *
-                 __int_as_float((127 - (sh - sh / 2)) << 23);
-      }
-      if (lane < R) qs_s[qb][lane] = mine;
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full[qb]);
-      scales(w.ja, pg[0], ks[0], vs[0]);
-      scales(w.ja + 1, pg[1], ks[1], vs[1]);
-      pages(w.ja + 2, pg[0]);
-      pages(w.ja + 3, pg[1]);
-      for (int j = w.ja; j < w.jb && ok; j += 2) {
+          for (int e = 0; e < 4; ++e) m = __vmaxu2(m, xs[e] & 0x7fff7fffu);
+          m = max(m & 0xffffu, m >> 16);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (j + h >= w.jb) break;
-          const int slot = g & 1;
-          if (g >= 2) ok = wait_warp(&s_free[slot], ((g >> 1) - 1) & 1, &wctl);
-          if (!ok) break;
+          for (int o = LPR / 2; o > 0; o /= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+          // 2^sh puts the row's largest element into [128, 256); a row with an element that is not
+          // finite becomes NaN
+          const int sh = 134 - (int)max(m >> 7, 1u), r = row_of(step);
+          const float f0 = __int_as_float((sh / 2 + 127) << 23);
+          const float f1 = __int_as_float((sh - sh / 2 + 127) << 23);
+          uint32_t hi[4], lo[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            sc_s[slot][0][e * 32 + lane] = ks[h][e];
-            sc_s[slot][1][e * 32 + lane] =
-                lg2(fmaxf(vs[h][e], __int_as_float((kQ8MinExp + 127) << 23)));
+            const float u = __uint_as_float(xs[e] << 16) * f0 * f1;
+            const float v = __uint_as_float(xs[e] & 0xffff0000u) * f0 * f1;
+            hi[e] = m >= 0x7f80u ? 0x7f7fu : e4m3x2_from_f32(u, v);
+            const float2 h = f32_from_e4m3x2(hi[e]);
+            lo[e] = e4m3x2_from_f32((u - h.x) * 16.0f, (v - h.y) * 16.0f);
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s_full[slot]);
-          ++g;
-          scales(j + h + 2, pg[h], ks[h], vs[h]);
-          pages(j + h + 4, pg[h]);
+          if (r < RL) {
+            uint8_t* at = dst + ch * (NS * CH) + in % 16;
+            *reinterpret_cast<uint2*>(at + r * CH + swz<CH>(in / 16, r) * 16) =
+                make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+            *reinterpret_cast<uint2*>(at + (R + r) * CH + swz<CH>(in / 16, R + r) * 16) =
+                make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+            if (lane % LPR == 0)
+              qs_s[qb][r] = p.scale_log2 * __int_as_float((127 - sh / 2) << 23) *
+                            __int_as_float((127 - (sh - sh / 2)) << 23);
+          }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[qb]);
+      }
+      // ---- two units ahead, so that the copies of the next units' keys can start
+#pragma unroll 1
+      while (!ended && published < un + (un < 0 ? 2 : 3)) {
+        const int slot = published % kUnits;
+        if (published >= kUnits)
+          ok = wait_warp(&units.free[slot], (published / kUnits - 1) & 1, &wctl);
+        if (!ok) break;
+        ended = !w.next(p, R);
+        if (lane == 0) {
+          units.at[slot][0] = make_int4(w.b, w.kh, w.rb, w.ja);
+          units.at[slot][1] = make_int4(w.jb, w.len, ended ? -1 : w.whole | w.first << 1, 0);
+          mbar_arrive(&units.full[slot]);
+        }
+        ++published;
+      }
+      __syncwarp();
+      if (un < 0) continue;
+      // ---- scales: a lane has four keys in a row. Those of two tiles are on their way in
+      // registers (used where they were loaded to: a copy would wait for the load), and the table
+      // entries of the two after them
+      const int32_t* table = p.table + (size_t)ua.x * p.max_pages;
+      const unsigned head_scales = (unsigned)kh << nb_shift;
+      const int end_key = min(len, jb * kKT);
+      const bool wide = p.sb_shift >= 2;  // the four keys have one scale
+      float ks[2][4], vs[2][4];
+      int page[2] = {-1, -1};
+#pragma unroll 1
+      for (int j = ja - 4; j < jb && ok; j += 2) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (j + h >= ja && j + h < jb) {
+            const int buf = g & 1;
+            if (g >= 2) ok = ok && wait_warp(&s_free[buf], ((g >> 1) - 1) & 1, &wctl);
+            ++g;
+            const float least = __int_as_float((kQ8MinExp + 127) << 23);
+            float4 k4 = make_float4(ks[h][0], ks[h][0], ks[h][0], ks[h][0]);
+            const float l0 = lg2(fmaxf(vs[h][0], least));
+            float4 l4 = make_float4(l0, l0, l0, l0);
+            if (!wide) {
+              k4 = make_float4(ks[h][0], ks[h][1], ks[h][2], ks[h][3]);
+              l4 = make_float4(l0, lg2(fmaxf(vs[h][1], least)), lg2(fmaxf(vs[h][2], least)),
+                               lg2(fmaxf(vs[h][3], least)));
+            }
+            *reinterpret_cast<float4*>(&sc_s[buf][0][lane * 4]) = k4;
+            *reinterpret_cast<float4*>(&sc_s[buf][1][lane * 4]) = l4;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_full[buf]);
+          }
+          const int key = (j + h + 2) * kKT + lane * 4;
+          const bool have = page[h] >= 0 && page[h] < p.num_pages;  // (else a key of zeros, or none)
+          const size_t at = (size_t)(unsigned)page[h] * page_scales +
+                            (head_scales + ((key & ps_mask) >> p.sb_shift));
+          ks[h][0] = have ? __ldg(p.k_scale + at) : 0.0f;
+          vs[h][0] = have ? __ldg(p.v_scale + at) : 1.0f;
+          if (!wide) {
+#pragma unroll
+            for (int e = 1; e < 4; ++e) {
+              const bool here = have && key + e < end_key;
+              ks[h][e] = here ? __ldg(p.k_scale + at + (e >> p.sb_shift)) : 0.0f;
+              vs[h][e] = here ? __ldg(p.v_scale + at + (e >> p.sb_shift)) : 1.0f;
+            }
+          }
+          page[h] = key + 2 * kKT < end_key && j + h + 4 >= ja
+                        ? table[(key + 2 * kKT) >> p.ps_shift] : -1;
         }
       }
     }
@@ -677,17 +744,22 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R, RL>::CTAS)
     const int key = threadIdx.x;  // key of the tile
     const uint32_t lanes = tbase + ((uint32_t)(warp * 32) << 16);
     const uint64_t sixteenth = f2_pack(0.0625f, 0.0625f);
-    int g = 0, un = 0;
-    bool ok = true;
-    for (; ok && w.next(p, R); ++un) {
+    int g = 0;
+    Unit w;
+    bool ok = true, end = false;
+#pragma unroll 1
+    for (int un = 0;; ++un) {
       const int qb = un & 1;
-      ok = wait_warp(&q_full[qb], (un >> 1) & 1, &wctl);
+      ok = take_unit(&units, un, w, end, lane, &wctl);
+      if (ok && !end) ok = wait_warp(&q_full[qb], (un >> 1) & 1, &wctl);
+      if (softmax_any(!ok) || end) break;
       const int r0 = w.rb * R, live = min(RL, p.rows - r0);
       // tiles below lim_min need no test of the keys
       const int lim_min = min(p.causal ? max(0, w.len - p.lq + 1) : w.len, w.jb * kKT);
       float l[RL];
 #pragma unroll
       for (int r = 0; r < RL; ++r) l[r] = 0.0f;
+#pragma unroll 1
       for (int j = w.ja; j < w.jb; ++j, ++g) {
         const int buf = g & 1;
         const uint32_t ph = (g >> 1) & 1;
@@ -811,7 +883,6 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R, RL>::CTAS)
       }
       // the sums of the 128 threads
       const bool any = w.jb > w.ja;
-      if (!any) softmax_any(false);  // (no vote since the last unit's red_s was read)
 #pragma unroll
       for (int r = 0; r < RL; ++r) {
         float x = l[r];
@@ -952,7 +1023,7 @@ Plan make_plan(const Q8AttnArgs& a) {
   pl.R = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
   pl.RL = rows <= 2 ? 2 : rows <= 4 ? 4 : pl.R;
   pl.rb = (rows + pl.R - 1) / pl.R;
-  const int ctas = 152 * (pl.R > 8 || a.d > 128 ? 1 : a.d == 64 && pl.RL <= 4 ? 3 : 2);
+  const int ctas = 152 * (pl.R > 16 || a.d > 128 ? 1 : a.d == 64 && pl.RL <= 4 ? 3 : 2);
   const long long cap = (long long)a.max_pages << a.ps_shift;
   const long long tiles = (cap + kKT - 1) / kKT * a.B * a.Hk * pl.rb;
   pl.grid = (int)std::min<long long>(ctas, tiles);
