@@ -62,11 +62,9 @@ constexpr float kSumExp = 16.0f, kSumUnit = 65536.0f;
 template <int HD, int R_, int RL>
 struct Q8Layout {
   static constexpr int R = R_;
-  static constexpr int CTAS = R > 16 || HD > 128 ? 1 : HD == 64 && RL <= 4 ? 3 : 2;  // resident on an SM
-  static constexpr int KST = HD == 64 ? (R == 8 ? 2 : 4) : HD == 128 ? (R <= 16 ? 2 : 5) : 2;
-  static constexpr int VST = HD == 64    ? (R <= 16 ? 4 : 8)
-                             : HD == 128 ? (R == 8 ? 4 : R == 16 ? 2 : 5)
-                                         : (R == 8 ? 4 : R == 16 ? 3 : 2);
+  static constexpr int CTAS = HD > 128 ? 1 : HD == 64 && RL <= 4 ? 3 : 2;  // resident on an SM
+  static constexpr int KST = HD == 64 && R == 16 ? 4 : 2;
+  static constexpr int VST = HD == 64 || R == 8 ? 4 : HD == 128 ? 2 : 3;
   static constexpr int CH = HD <= 128 ? HD : 128;   // columns (bytes) of a swizzled row
   static constexpr int KCH = HD / CH;               // row chunks: 1, or 2 at head_dim 256
   static constexpr int NS = 2 * R;                  // columns of S^T: hi rows, lo rows
@@ -139,15 +137,13 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// N = 16, 32 or 64 columns of a TMEM lane.
+// N = 16 or 32 columns of a TMEM lane.
 template <int N>
 __device__ __forceinline__ void load_cols(uint32_t taddr, uint32_t (&r)[N]) {
-  if constexpr (N == 16) {
+  if constexpr (N == 16)
     tmem_ld16(taddr, r);
-  } else {
-#pragma unroll
-    for (int c = 0; c < N; c += 32) tmem_ld32(taddr + c, *reinterpret_cast<uint32_t(*)[32]>(&r[c]));
-  }
+  else
+    tmem_ld32(taddr, r);
 }
 // Two weights (>= 0, at most 2^15) -> two f16 rounded to 9 bits (half up).
 __device__ __forceinline__ uint32_t weight_f16x2(float lo, float hi) {
@@ -871,11 +867,9 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R, RL>::CTAS)
           *reinterpret_cast<uint2*>(prow + swz<NP>(1, key) * 16) = make_uint2(pc[2][0], pc[2][1]);
         } else {
 #pragma unroll
-          for (int x = 0; x < R / 16; ++x)
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-              *reinterpret_cast<uint4*>(prow + swz<NP>(i * (R / 16) + x, key) * 16) = make_uint4(
-                  pc[i][4 * x], pc[i][4 * x + 1], pc[i][4 * x + 2], pc[i][4 * x + 3]);
+          for (int i = 0; i < 3; ++i)
+            *reinterpret_cast<uint4*>(prow + swz<NP>(i, key) * 16) =
+                make_uint4(pc[i][0], pc[i][1], pc[i][2], pc[i][3]);
         }
         fence_proxy_async();
         __syncwarp();
@@ -958,53 +952,64 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R, RL>::CTAS)
 }
 
 // Joins the shares of the units that were cut, and writes those of sequences without keys: one
-// CTA for each unit.
+// CTA for each unit, one warp for each row in turn. Launched early: what it needs to know of the
+// lengths it works out while the attention still runs.
 template <int HD, int R>
 __global__ void __launch_bounds__(256) q8_combine_kernel(const Q8K p, int grid) {
-  const int lane = lane_id();
-  grid_dep_wait();
+  const int warp = warp_id(), lane = lane_id();
   const unsigned U = (unsigned)(p.Hk * p.rb);  // blockIdx.x: (b * Hk + kh) * rb + row block
   const int b = (int)(blockIdx.x / U), in = (int)(blockIdx.x % U);
-  const int r0 = in % p.rb * R, live = min(R, p.rows - r0);
-  const size_t unit_row = ((size_t)b * p.Hk + in / p.rb) * p.rows + r0;
+  const int kh = p.rb == 1 ? in : in / p.rb, rb = in - kh * p.rb;
+  const int r0 = rb * R, live = min(R, p.rows - r0);
+  const size_t unit_row = ((size_t)b * p.Hk + kh) * p.rows + r0;
+  // every warp finds the unit's place in the list for itself
+  unsigned before = 0;
+  int mine = lane < p.B ? q8_tiles(p, lane) : 0;
   const int nt = q8_tiles(p, b);
+  before = lane < b ? mine : 0;
+#pragma unroll 1
+  for (int i = lane + 32; i < b; i += 32) before += q8_tiles(p, i);
+  before = __reduce_add_sync(0xffffffffu, before);
+  const unsigned per = q8_share((unsigned)q8_all_tiles(p, mine, lane) * U, grid);
   if (nt == 0) {
     for (int e = threadIdx.x; e < live * HD; e += 256) p.o[unit_row * HD + e] = __float2bfloat16(0.f);
     if (p.lse && threadIdx.x < live) p.lse[unit_row + threadIdx.x] = -INFINITY;
-    return;
   }
-  // every warp finds the unit's place in the list for itself
-  unsigned before = 0;
-  for (int i = lane; i < b; i += 32) before += q8_tiles(p, i);
-  before = __reduce_add_sync(0xffffffffu, before);
-  const int mine = lane < p.B ? q8_tiles(p, lane) : 0;
-  const unsigned per = q8_share((unsigned)q8_all_tiles(p, mine, lane) * U, grid);
+  // (by every CTA: what follows this kernel must find the attention done)
+  grid_dep_wait();
+  if (nt == 0) return;
   const unsigned a = before * U + (unsigned)in * nt;
   const int c0 = (int)(a / per), c1 = (int)((a + nt - 1) / per);
   if (c0 == c1) return;  // written whole
   // share i: slot 2 c0 + 1 (it begins there), then 2 c of each further CTA
   auto slot = [&](int c) { return (size_t)2 * c + (c == c0 ? 1 : 0); };
-  for (int r = threadIdx.x / 32; r < live; r += 8) {
+#pragma unroll 1
+  for (int r = warp; r < live; r += 8) {
     float m = -FLT_MAX;
+#pragma unroll 1
     for (int c = c0 + lane; c <= c1; c += 32) {
       const float* ml = p.ml_part + slot(c) * 2 * R + r;
       if (ml[R] != 0.0f) m = fmaxf(m, ml[0]);
     }
+#pragma unroll
     for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float sum = 0.0f, acc[HD / 32] = {};
+#pragma unroll 4
     for (int c = c0; c <= c1; ++c) {
       const float* ml = p.ml_part + slot(c) * 2 * R + r;
-      if (ml[R] == 0.0f) continue;
-      const float f = ex2(ml[0] - m);
-      sum = fmaf(ml[R], f, sum);
       const float* src = p.o_part + (slot(c) * R + r) * HD + lane;
+      float x[HD / 32];
 #pragma unroll
-      for (int e = 0; e < HD / 32; ++e) acc[e] = fmaf(src[e * 32], f, acc[e]);
+      for (int e = 0; e < HD / 32; ++e) x[e] = src[e * 32];
+      const float l = ml[R], f = l == 0.0f ? 0.0f : ex2(ml[0] - m);  // (no key: m is none)
+      sum = fmaf(l, f, sum);
+#pragma unroll
+      for (int e = 0; e < HD / 32; ++e) acc[e] = fmaf(x[e], f, acc[e]);
     }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum / kSumUnit;
 #pragma unroll
     for (int e = 0; e < HD / 32; ++e)
-      p.o[(unit_row + r) * HD + e * 32 + lane] =
-          __float2bfloat16(sum == 0.0f ? 0.0f : acc[e] / sum / kSumUnit);
+      p.o[(unit_row + r) * HD + e * 32 + lane] = __float2bfloat16(acc[e] * inv);
     if (p.lse && lane == 0)
       p.lse[unit_row + r] = sum == 0.0f ? -INFINITY : fmaf(m + kSumExp, kLn2, logf(sum));
   }
@@ -1014,16 +1019,17 @@ struct Plan {
   int R, RL, rb, grid;
 };
 
-// Rows of a unit: the smallest block that holds the G * q_len rows of a kv head, 32 at most (more
-// rows take further passes over the keys, from L2). Grid: every CTA slot of the GPU, or one CTA
+// Rows of a unit: the smallest block that holds the G * q_len rows of a kv head, 16 at most; more
+// rows take further passes over the keys, from L2 (blocks of 32, with one CTA an SM: 83 us against
+// 74 for 128 rows a kv head). Grid: every CTA slot of the GPU, or one CTA
 // for each tile there can be.
 Plan make_plan(const Q8AttnArgs& a) {
   Plan pl;
   const int rows = a.G * a.lq;
-  pl.R = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  pl.R = rows <= 8 ? 8 : 16;
   pl.RL = rows <= 2 ? 2 : rows <= 4 ? 4 : pl.R;
   pl.rb = (rows + pl.R - 1) / pl.R;
-  const int ctas = 152 * (pl.R > 16 || a.d > 128 ? 1 : a.d == 64 && pl.RL <= 4 ? 3 : 2);
+  const int ctas = 152 * (a.d > 128 ? 1 : a.d == 64 && pl.RL <= 4 ? 3 : 2);
   const long long cap = (long long)a.max_pages << a.ps_shift;
   const long long tiles = (cap + kKT - 1) / kKT * a.B * a.Hk * pl.rb;
   pl.grid = (int)std::min<long long>(ctas, tiles);
@@ -1082,8 +1088,7 @@ cudaError_t attn_d(const Q8AttnArgs& a, const Q8AttnMaps& m, const Plan& pl, voi
     case 2: return attn_t<HD, 8, 2>(a, m, pl, ws, s);
     case 4: return attn_t<HD, 8, 4>(a, m, pl, ws, s);
     case 8: return attn_t<HD, 8, 8>(a, m, pl, ws, s);
-    case 16: return attn_t<HD, 16, 16>(a, m, pl, ws, s);
-    default: return attn_t<HD, 32, 32>(a, m, pl, ws, s);
+    default: return attn_t<HD, 16, 16>(a, m, pl, ws, s);
   }
 }
 }  // namespace

@@ -427,7 +427,7 @@ int fa_q8_cache_read(const fa_q8_cache* cache, const fa_q8_rows* rows, void* str
  * checks (p's n_kv_heads, head_dim, page_size and num_pages must equal the cache's, num_splits
  * must be 0). Sums and softmax statistics are f32. A query row with an element that is not finite
  * gives NaN. At most 2^30 tiles of work: batch * n_kv_heads * ceil(max_pages * page_size / 128),
- * times ceil((n_heads / n_kv_heads) * q_len / 32), or FA_ERR_INVALID. */
+ * times ceil((n_heads / n_kv_heads) * q_len / 16), or FA_ERR_INVALID. */
 int fa_q8_paged_attention(const void* q, const fa_q8_cache* cache, const int32_t* block_table,
                           const int32_t* lengths, void* o, float* lse, const fa_paged_params* p,
                           void* stream);
