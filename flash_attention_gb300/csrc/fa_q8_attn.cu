@@ -951,9 +951,10 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R, RL>::CTAS)
   }
 }
 
-// Joins the shares of the units that were cut, and writes those of sequences without keys: one
-// CTA for each unit, one warp for each row in turn. Launched early: what it needs to know of the
-// lengths it works out while the attention still runs.
+// Joins the shares of the units that were cut, and writes those of sequences without keys: a warp
+// for each row, a CTA for (up to) 8 rows of a unit. Launched early: what it needs to know of the
+// lengths it works out while the attention still runs. Then only latency counts (a few KB): a lane
+// reads one share's m and sum, and the first shares' O is on its way before their weights are known.
 template <int HD, int R>
 __global__ void __launch_bounds__(256) q8_combine_kernel(const Q8K p, int grid) {
   const int warp = warp_id(), lane = lane_id();
@@ -971,9 +972,10 @@ __global__ void __launch_bounds__(256) q8_combine_kernel(const Q8K p, int grid) 
   for (int i = lane + 32; i < b; i += 32) before += q8_tiles(p, i);
   before = __reduce_add_sync(0xffffffffu, before);
   const unsigned per = q8_share((unsigned)q8_all_tiles(p, mine, lane) * U, grid);
-  if (nt == 0) {
-    for (int e = threadIdx.x; e < live * HD; e += 256) p.o[unit_row * HD + e] = __float2bfloat16(0.f);
-    if (p.lse && threadIdx.x < live) p.lse[unit_row + threadIdx.x] = -INFINITY;
+  if (nt == 0 && blockIdx.y == 0) {
+    for (int e = threadIdx.x; e < live * HD; e += blockDim.x)
+      p.o[unit_row * HD + e] = __float2bfloat16(0.f);
+    if (p.lse && lane < live && warp == 0) p.lse[unit_row + lane] = -INFINITY;
   }
   // (by every CTA: what follows this kernel must find the attention done)
   grid_dep_wait();
@@ -983,36 +985,77 @@ __global__ void __launch_bounds__(256) q8_combine_kernel(const Q8K p, int grid) 
   if (c0 == c1) return;  // written whole
   // share i: slot 2 c0 + 1 (it begins there), then 2 c of each further CTA
   auto slot = [&](int c) { return (size_t)2 * c + (c == c0 ? 1 : 0); };
-#pragma unroll 1
-  for (int r = warp; r < live; r += 8) {
-    float m = -FLT_MAX;
-#pragma unroll 1
-    for (int c = c0 + lane; c <= c1; c += 32) {
-      const float* ml = p.ml_part + slot(c) * 2 * R + r;
-      if (ml[R] != 0.0f) m = fmaxf(m, ml[0]);
+  const int r = (int)blockIdx.y * 8 + warp;
+  if (r >= live) return;
+  constexpr int CPL = HD / 32, AHEAD = 4;  // columns of a lane
+  struct Part {
+    float x[CPL];
+  };
+  auto load = [&](int c) {
+    Part v;
+    const float* src = p.o_part + (slot(min(c, c1)) * R + r) * HD + lane * CPL;
+    if constexpr (CPL == 2) {
+      const float2 f = *reinterpret_cast<const float2*>(src);
+      v.x[0] = f.x, v.x[1] = f.y;
+    } else {
+#pragma unroll
+      for (int e = 0; e < CPL; e += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(src + e);
+        v.x[e] = f.x, v.x[e + 1] = f.y, v.x[e + 2] = f.z, v.x[e + 3] = f.w;
+      }
     }
-#pragma unroll
-    for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float sum = 0.0f, acc[HD / 32] = {};
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-      const float* ml = p.ml_part + slot(c) * 2 * R + r;
-      const float* src = p.o_part + (slot(c) * R + r) * HD + lane;
-      float x[HD / 32];
-#pragma unroll
-      for (int e = 0; e < HD / 32; ++e) x[e] = src[e * 32];
-      const float l = ml[R], f = l == 0.0f ? 0.0f : ex2(ml[0] - m);  // (no key: m is none)
-      sum = fmaf(l, f, sum);
-#pragma unroll
-      for (int e = 0; e < HD / 32; ++e) acc[e] = fmaf(x[e], f, acc[e]);
+    return v;
+  };
+  float m = -FLT_MAX, sum = 0.0f, acc[CPL] = {};
+#pragma unroll 1
+  for (int base = c0; base <= c1; base += 32) {
+    const int n = min(32, c1 - base + 1);
+    float mi = -FLT_MAX, li = 0.0f;
+    if (lane < n) {
+      const float* ml = p.ml_part + slot(base + lane) * 2 * R + r;
+      li = ml[R];
+      if (li != 0.0f) mi = ml[0];
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum / kSumUnit;
+    Part v[AHEAD];
 #pragma unroll
-    for (int e = 0; e < HD / 32; ++e)
-      p.o[(unit_row + r) * HD + e * 32 + lane] = __float2bfloat16(acc[e] * inv);
-    if (p.lse && lane == 0)
-      p.lse[unit_row + r] = sum == 0.0f ? -INFINITY : fmaf(m + kSumExp, kLn2, logf(sum));
+    for (int k = 0; k < AHEAD; ++k) v[k] = load(base + k);
+    float top = fmaxf(m, mi);
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float f = li == 0.0f ? 0.0f : ex2(mi - top), old = ex2(m - top);
+    m = top;
+    float part = li * f;
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) part += __shfl_xor_sync(0xffffffffu, part, o);
+    sum = fmaf(sum, old, part);
+#pragma unroll
+    for (int e = 0; e < CPL; ++e) acc[e] *= old;
+#pragma unroll 1
+    for (int k0 = 0; k0 < n; k0 += AHEAD) {
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        const float fk = __shfl_sync(0xffffffffu, f, k0 + k);  // (0 behind the last share)
+        if (fk != 0.0f) {
+#pragma unroll
+          for (int e = 0; e < CPL; ++e) acc[e] = fmaf(v[k].x[e], fk, acc[e]);
+        }
+        v[k] = load(base + k0 + AHEAD + k);
+      }
+    }
   }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum / kSumUnit;
+  uint32_t out[CPL / 2];
+#pragma unroll
+  for (int e = 0; e < CPL / 2; ++e) out[e] = pack_bf16(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  __nv_bfloat16* dst = p.o + (unit_row + r) * HD + lane * CPL;
+  if constexpr (CPL == 2)
+    *reinterpret_cast<uint32_t*>(dst) = out[0];
+  else if constexpr (CPL == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+  else
+    *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
+  if (p.lse && lane == 0)
+    p.lse[unit_row + r] = sum == 0.0f ? -INFINITY : fmaf(m + kSumExp, kLn2, logf(sum));
 }
 
 struct Plan {
@@ -1075,8 +1118,10 @@ cudaError_t attn_t(const Q8AttnArgs& a, const Q8AttnMaps& m, const Plan& pl, voi
   profile_mark(kKernQ8Attn, 1, s);
   if (e != cudaSuccess) return e;
   profile_mark(kKernQ8Combine, 0, s);
-  e = launch_pdl(q8_combine_kernel<HD, R>, dim3((unsigned)((long long)a.B * a.Hk * pl.rb)),
-                 dim3(256), 0, s, p, pl.grid);
+  const int rows = p.rows < R ? p.rows : R;
+  e = launch_pdl(q8_combine_kernel<HD, R>,
+                 dim3((unsigned)(a.B * a.Hk * pl.rb), (unsigned)((rows + 7) / 8)),
+                 dim3((unsigned)(32 * (rows < 8 ? rows : 8))), 0, s, p, pl.grid);
   profile_mark(kKernQ8Combine, 1, s);
   return e;
 }
