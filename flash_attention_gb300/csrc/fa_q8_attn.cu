@@ -27,7 +27,7 @@
 //
 // Work: the (sequence, kv head, block of R rows) units, each ceil(len / 128) key tiles, form one
 // list of tiles, cut evenly over persistent CTAs (the lengths are on the device; each CTA finds
-// its part from them). A CTA writes the units it has whole; of the others it leaves its share's
+// its part from them). A unit counts kUnitCost tiles more than it has, what its start and end cost. A CTA writes the units it has whole; of the others it leaves its share's
 // O, m and sum, which a second kernel joins in the order of the keys.
 //
 // Warps of a CTA: 0-3 softmax (thread = key of the tile, and head-dim row of O^T), 4 TMA copies of
@@ -46,6 +46,9 @@ namespace fa {
 
 namespace {
 constexpr int kKT = 128;          // keys of a tile (the MMA M of S^T)
+// Tiles' worth of a unit's start and end (128 sequences of up to 2k keys, head_dim 64: 51 us with 0,
+// 40 with 2, 37 with 4; long sequences do not tell).
+constexpr int kUnitCost = 4;
 constexpr int kPageChunk = 128;   // block-table entries staged at a time
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -229,17 +232,19 @@ __device__ __forceinline__ int q8_len(const Q8K& p, int b) {
   return raw < 0 ? 0 : raw > cap ? (int)cap : raw;
 }
 
-__device__ __forceinline__ int q8_tiles(const Q8K& p, int b) {
-  return (q8_len(p, b) + kKT - 1) / kKT;
+// What a unit of sequence b counts in the list: kUnitCost and its tiles; 0 without keys.
+__device__ __forceinline__ int q8_cost(const Q8K& p, int b) {
+  const int len = q8_len(p, b);
+  return len > 0 ? (len + kKT - 1) / kKT + kUnitCost : 0;
 }
-// Key tiles of all sequences (of one unit each), by one warp that has those of sequence `lane`.
-// The host has checked that the list of all tiles, Hk * rb times as long, fits 31 bits.
-__device__ __forceinline__ int q8_all_tiles(const Q8K& p, int mine, int lane) {
+// The sum over all sequences (of one unit each), by one warp that has that of sequence `lane`.
+// The host has checked that the whole list, Hk * rb times as long, fits 31 bits.
+__device__ __forceinline__ int q8_all_costs(const Q8K& p, int mine, int lane) {
 #pragma unroll 1
-  for (int b = lane + 32; b < p.B; b += 32) mine += q8_tiles(p, b);
+  for (int b = lane + 32; b < p.B; b += 32) mine += q8_cost(p, b);
   return (int)__reduce_add_sync(0xffffffffu, (unsigned)mine);
 }
-// Tiles of a CTA: the list cut evenly over the grid.
+// A CTA's share: the list cut evenly over the grid.
 __device__ __forceinline__ unsigned q8_share(unsigned all, unsigned grid) {
   return (all + grid - 1) / grid;
 }
@@ -247,29 +252,29 @@ __device__ __forceinline__ unsigned q8_share(unsigned all, unsigned grid) {
 // The units of a CTA's share [t, t1) of the list, in order: warp 7 walks it and publishes the units
 // in shared memory, where the other roles take them from.
 struct Walk {
-  unsigned t, t1;    // next tile of the list, end of the share
-  unsigned pre;      // tiles of the list before sequence b
-  int b, nt, len;    // sequence, its tiles for each unit, its length
+  unsigned t, t1;    // next place in the list, end of the share
+  unsigned pre;      // the list before sequence b
+  int b, cost, len;  // sequence, what each of its units counts, its length
   // the unit found by next()
   int kh, rb, ja, jb;  // kv head, row block, tiles [ja, jb) of it (tiles that no row sees left out)
-  int whole;           // the share has all of the unit
+  int whole;           // the share has all of the unit's tiles
   int first;           // the share has its first tile
 
   // The share of CTA `cta` (warp-wide).
   __device__ __forceinline__ void init(const Q8K& p, unsigned cta, unsigned grid, int lane) {
     const unsigned U = (unsigned)(p.Hk * p.rb);
-    const int mine = lane < p.B ? q8_tiles(p, lane) : 0;
-    const unsigned all = (unsigned)q8_all_tiles(p, mine, lane) * U;
+    const int mine = lane < p.B ? q8_cost(p, lane) : 0;
+    const unsigned all = (unsigned)q8_all_costs(p, mine, lane) * U;
     const unsigned per = q8_share(all, grid);
     t = per * cta;  // (below all + grid)
     t1 = min(t + per, all);
     pre = 0;
-    b = nt = len = 0;
+    b = cost = len = 0;
     if (t >= t1) return;
 #pragma unroll 1
     for (int base = 0;; base += 32) {  // ends: t lies below the sum over all sequences
       const unsigned n =
-          (base == 0 ? mine : base + lane < p.B ? q8_tiles(p, base + lane) : 0) * U;
+          (base == 0 ? mine : base + lane < p.B ? q8_cost(p, base + lane) : 0) * U;
       unsigned upto = n;
 #pragma unroll 1
       for (int o = 1; o < 32; o *= 2) {
@@ -286,31 +291,36 @@ struct Walk {
       pre += __shfl_sync(0xffffffffu, upto, 31);
     }
     len = q8_len(p, b);
-    nt = (len + kKT - 1) / kKT;
+    cost = q8_cost(p, b);
   }
 
   __device__ __forceinline__ bool next(const Q8K& p, int R) {
-    if (t >= t1) return false;
     const unsigned U = (unsigned)(p.Hk * p.rb);
+    int je;
+    do {  // (a share may end within what a unit counts before its tiles)
+      if (t >= t1) return false;
 #pragma unroll 1
-    while (t >= pre + U * nt) {  // the next sequence with keys
-      pre += U * nt;
-      if (++b >= p.B) return false;
-      len = q8_len(p, b);
-      nt = (len + kKT - 1) / kKT;
-    }
-    const unsigned in = t - pre, u = in / (unsigned)nt;
-    ja = (int)(in - u * nt);
-    kh = (int)u;
+      while (t >= pre + U * cost) {  // the next sequence with keys
+        pre += U * cost;
+        if (++b >= p.B) return false;
+        len = q8_len(p, b);
+        cost = q8_cost(p, b);
+      }
+      const unsigned in = t - pre, u = in / (unsigned)cost;
+      kh = (int)u;
+      const int from = (int)(in - u * cost), to = min(cost, from + (int)(t1 - t));
+      t += to - from;
+      ja = max(0, from - kUnitCost);
+      je = max(0, to - kUnitCost);
+    } while (je == 0);
     rb = 0;
     if (p.rb > 1) {
-      kh = (int)(u / (unsigned)p.rb);
-      rb = (int)u - kh * p.rb;
+      const int u = kh;
+      kh = (int)((unsigned)u / (unsigned)p.rb);
+      rb = u - kh * p.rb;
     }
-    const int je = min(nt, ja + (int)(t1 - t));
-    t += je - ja;
     first = ja == 0;
-    whole = first && je == nt;
+    whole = first && je == cost - kUnitCost;
     // keys that any row of the block sees
     jb = je;
     if (p.causal && p.lq > 1) {
@@ -965,23 +975,23 @@ __global__ void __launch_bounds__(256) q8_combine_kernel(const Q8K p, int grid) 
   const size_t unit_row = ((size_t)b * p.Hk + kh) * p.rows + r0;
   // every warp finds the unit's place in the list for itself
   unsigned before = 0;
-  int mine = lane < p.B ? q8_tiles(p, lane) : 0;
-  const int nt = q8_tiles(p, b);
+  int mine = lane < p.B ? q8_cost(p, lane) : 0;
+  const int cost = q8_cost(p, b);
   before = lane < b ? mine : 0;
 #pragma unroll 1
-  for (int i = lane + 32; i < b; i += 32) before += q8_tiles(p, i);
+  for (int i = lane + 32; i < b; i += 32) before += q8_cost(p, i);
   before = __reduce_add_sync(0xffffffffu, before);
-  const unsigned per = q8_share((unsigned)q8_all_tiles(p, mine, lane) * U, grid);
-  if (nt == 0 && blockIdx.y == 0) {
+  const unsigned per = q8_share((unsigned)q8_all_costs(p, mine, lane) * U, grid);
+  if (cost == 0 && blockIdx.y == 0) {
     for (int e = threadIdx.x; e < live * HD; e += blockDim.x)
       p.o[unit_row * HD + e] = __float2bfloat16(0.f);
     if (p.lse && lane < live && warp == 0) p.lse[unit_row + lane] = -INFINITY;
   }
   // (by every CTA: what follows this kernel must find the attention done)
   grid_dep_wait();
-  if (nt == 0) return;
-  const unsigned a = before * U + (unsigned)in * nt;
-  const int c0 = (int)(a / per), c1 = (int)((a + nt - 1) / per);
+  if (cost == 0) return;
+  const unsigned a = before * U + (unsigned)in * cost;  // of its first tile and of its last:
+  const int c0 = (int)((a + kUnitCost) / per), c1 = (int)((a + cost - 1) / per);
   if (c0 == c1) return;  // written whole
   // share i: slot 2 c0 + 1 (it begins there), then 2 c of each further CTA
   auto slot = [&](int c) { return (size_t)2 * c + (c == c0 ? 1 : 0); };
@@ -1074,7 +1084,7 @@ Plan make_plan(const Q8AttnArgs& a) {
   pl.rb = (rows + pl.R - 1) / pl.R;
   const int ctas = 152 * (a.d > 128 ? 1 : a.d == 64 && pl.RL <= 4 ? 3 : 2);
   const long long cap = (long long)a.max_pages << a.ps_shift;
-  const long long tiles = (cap + kKT - 1) / kKT * a.B * a.Hk * pl.rb;
+  const long long tiles = ((cap + kKT - 1) / kKT + kUnitCost) * a.B * a.Hk * pl.rb;
   pl.grid = (int)std::min<long long>(ctas, tiles);
   return pl;
 }
@@ -1143,7 +1153,7 @@ int q8_box_cols(int head_dim) { return head_dim < 128 ? head_dim : 128; }
 
 long long q8_attn_tiles(const Q8AttnArgs& a) {
   const long long cap = (long long)a.max_pages << a.ps_shift;
-  return (long long)a.B * a.Hk * make_plan(a).rb * ((cap + kKT - 1) / kKT);
+  return (long long)a.B * a.Hk * make_plan(a).rb * ((cap + kKT - 1) / kKT + kUnitCost);
 }
 
 size_t q8_attn_workspace_bytes(const Q8AttnArgs& a) {
