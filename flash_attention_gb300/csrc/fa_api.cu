@@ -811,6 +811,7 @@ static int check_q8_cache(const fa_q8_cache* c) {
   if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return FA_ERR_INVALID;
   if (ps < 8 || ps > 256 || (ps & (ps - 1))) return FA_ERR_INVALID;
   if (sb < 1 || sb > ps || (sb & (sb - 1))) return FA_ERR_INVALID;
+  if ((int64_t)c->n_kv_heads * ps * c->head_dim > INT32_MAX) return FA_ERR_INVALID;
   if (!c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16)) return FA_ERR_INVALID;
   if (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
     return FA_ERR_INVALID;

@@ -13,9 +13,13 @@
 // the binade (448 = 1.75 * 2^8), so the rule runs on integers.
 //
 // Both kernels move bytes (2 in and 1 out for an element, or 1 in and 2 out) and are bound by
-// HBM. A lane holds 8 columns of a row; a warp takes 8 steps of 32 / (d / 8) rows, all of them
-// loaded before the first is used, so that 4 KB of bf16 are in flight for each warp. A scale
-// block up to that size is reduced inside its warp, a larger one over the warps of its CTA.
+// HBM as long as they spend few instructions on an element: at 164 and 138 for 8 elements they
+// were bound by issue (85 and 66 us for 16 prompts of up to 8k tokens). So a lane holds 8 columns
+// of a row, a warp takes 8 steps of 32 / (d / 8) rows, all loaded before the first is used (4 KB
+// of bf16), and the way to them (sequence, length, table) is gone once for four heads. Where the
+// rows of a warp lie in one page (page_size >= 2048 / d) they are one run of bytes; smaller pages
+// are looked up row by row. A scale block up to a warp's rows is reduced inside the warp, a larger
+// one over the warps of its CTA.
 #include <math.h>
 
 #include "fa_common.cuh"
@@ -44,6 +48,7 @@ struct Q8RowsK {
   const int32_t* lens;   // [B] (writer)
   int* status;
   int B, Hk, total, new_len, max_pages, num_pages, ps_shift, sb_shift;
+  unsigned page_bytes, page_scales;  // of the codes and scales of a page's heads
 };
 
 __device__ __forceinline__ void flag_bad(int* status) {
@@ -60,9 +65,16 @@ __device__ __forceinline__ bool seq_rows(const Q8RowsK& p, int b, int& start, in
   return varlen_seq(p.cu, b, p.total, p.total, start, n);
 }
 
-// Page of a position, or -1 (and a flag) where the table names none.
-__device__ __forceinline__ int page_of(const Q8RowsK& p, int b, int pos, bool& bad) {
-  const int pg = p.table[(size_t)b * p.max_pages + (pos >> p.ps_shift)];
+// Pages of a warp's `rows` rows from position p0 on: lane i holds that of entry
+// (p0 >> ps_shift) + i, -1 where the table names none of the cache. Entries whose positions all
+// lie outside [from, end) are not read.
+__device__ __forceinline__ int lane_page(const Q8RowsK& p, int b, int p0, int rows, int from, int end,
+                                         int lane, bool& bad) {
+  const int entry = (p0 >> p.ps_shift) + lane;
+  if (lane > (rows - 1) >> p.ps_shift || (long long)entry << p.ps_shift >= end ||
+      (long long)(entry + 1) << p.ps_shift <= from)
+    return -1;
+  const int pg = p.table[(size_t)b * p.max_pages + entry];
   if (pg >= 0 && pg < p.num_pages) return pg;
   bad = true;
   return -1;
@@ -80,9 +92,17 @@ __device__ __forceinline__ float2 bf16x2_f32(uint32_t w) {
 
 // x / s for 8 values of a row as codes, where s = 1 / inv is a power of two (x * inv is exact).
 __device__ __forceinline__ uint2 quantise8(const uint4& x, float inv) {
-  const float2 a = bf16x2_f32(x.x), b = bf16x2_f32(x.y), c = bf16x2_f32(x.z), d = bf16x2_f32(x.w);
-  return make_uint2(e4m3x4_from_f32(a.x * inv, a.y * inv, b.x * inv, b.y * inv),
-                    e4m3x4_from_f32(c.x * inv, c.y * inv, d.x * inv, d.y * inv));
+  const uint64_t inv2 = f2_pack(inv, inv);
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t c[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float lo, hi;
+    f2_unpack(f2_mul(f2_pack(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u)),
+                     inv2), lo, hi);
+    c[e] = e4m3x2_from_f32(lo, hi);
+  }
+  return make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
 }
 // The same for any s and any values (the cases that are rare: a scale that another writer chose
 // stays, or a value is not finite): NaN where the conversion would saturate an infinity.
@@ -113,7 +133,7 @@ __device__ __forceinline__ uint32_t absmax8(const uint4& x, uint32_t m) {
   m = __vmaxu2(m, x.z & 0x7fff7fffu);
   return __vmaxu2(m, x.w & 0x7fff7fffu);
 }
-__device__ __forceinline__ uint4 finite8(uint4 x) {  // 0 for what is not finite
+__device__ __noinline__ uint4 finite8(uint4 x) {  // 0 for what is not finite
   x.x &= ~__vcmpgeu2(x.x & 0x7fff7fffu, 0x7f807f80u);
   x.y &= ~__vcmpgeu2(x.y & 0x7fff7fffu, 0x7f807f80u);
   x.z &= ~__vcmpgeu2(x.z & 0x7fff7fffu, 0x7f807f80u);
@@ -123,9 +143,9 @@ __device__ __forceinline__ uint4 finite8(uint4 x) {  // 0 for what is not finite
 
 // SPB: steps of a scale block inside a warp (1: a block of at most one step). `wpb` warps of
 // the CTA share a unit of max(rows of a warp, scale block) positions. An item is a unit of K or V
-// of `heads` heads in turn, which share the way to the unit (offsets, length, table).
-// THREADS: 256, or up to 1024 where a scale block takes more than 8 warps.
-template <int HD, int SPB, int THREADS>
+// of `heads` heads in turn. ONE: the rows of a warp lie in one page. THREADS: 256, or up to 1024
+// where a scale block takes more than 8 warps.
+template <int HD, int SPB, bool ONE, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1)
     q8_write_kernel(const Q8RowsK p, long long items, int wpb, int heads) {
   using RL = RowLanes<HD>;
@@ -133,7 +153,6 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1)
   __shared__ uint32_t warp_max[32];
   const int warp = warp_id(), lane = lane_id();
   const int sb = 1 << p.sb_shift, ps_mask = (1 << p.ps_shift) - 1;
-  const int nb_shift = p.ps_shift - p.sb_shift;
   const int unit = RL::TR * wpb;
   const long long item = (long long)blockIdx.x * (blockDim.x / 32 / wpb) + warp / wpb;
   const int which = (int)(item & 1);
@@ -155,42 +174,48 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1)
     const long long u = slot - (offset(b) / unit + 2ll * b);
     const long long at = (max(first, 0) / unit + u) * unit;  // first position of this unit
     live = live && u >= 0 && at < len && n > 0;
-    p0 = (int)at + (warp % wpb) * RL::TR;
+    p0 = live ? (int)at + (warp % wpb) * RL::TR : 0;
   }
   const int lo = max(first, 0);  // new rows are the positions lo .. len - 1
   const int r = lane / RL::LPR, col = lane % RL::LPR * 8;
-  // pages of the warp's rows: lane i holds that of entry (p0 >> ps_shift) + i
-  int page = -1;
-  if (live && lane <= (RL::TR - 1) >> p.ps_shift && ((p0 >> p.ps_shift) + lane) << p.ps_shift < len)
-    page = p.table[(size_t)b * p.max_pages + (p0 >> p.ps_shift) + lane];
-  int at[kSteps];  // page of the row; -1: left out
-  bool isnew[kSteps];
+  // what the rows p0 + t * RPS + r are, bit t: new, or written or looked at (earlier rows of a
+  // block that gets a new one are); `page`: theirs, ONE: that of them all
+  const int lane_pg = live ? lane_page(p, b, p0, RL::TR, lo & ~(sb - 1), len, lane, bad) : -1;
+  uint32_t isnew = 0, look = 0;
+  int page[ONE ? 1 : kSteps];
 #pragma unroll
   for (int t = 0; t < kSteps; ++t) {
     const int pos = p0 + t * RL::RPS + r;
-    at[t] = __shfl_sync(0xffffffffu, page, (pos >> p.ps_shift) - (p0 >> p.ps_shift));
-    isnew[t] = live && pos >= lo && pos < len;
-    // earlier rows of a block that gets a new one are looked at too
-    const bool look = live && pos < len && (pos | (sb - 1)) >= lo;
-    if (look && (at[t] < 0 || at[t] >= p.num_pages)) bad = true;
-    if (!look || at[t] < 0 || at[t] >= p.num_pages) at[t] = -1;
+    const int pg = __shfl_sync(0xffffffffu, lane_pg, ONE ? 0 : (pos >> p.ps_shift) - (p0 >> p.ps_shift));
+    page[ONE ? 0 : t] = pg;
+    isnew |= (uint32_t)(live && pos >= lo && pos < len) << t;
+    look |= (uint32_t)(live && pos < len && (pos | (sb - 1)) >= lo && pg >= 0) << t;
   }
   // earlier tokens of a block: only the block that `first` lies in has some
-  const bool has_old = live && p0 < first;
+  const bool has_old = live && (p0 & ~(sb - 1)) < first && sb > 1;
   const int lanes = min(32, RL::LPR << p.sb_shift);  // lanes of a block
-  for (int h = 0; h < heads; ++h) {
+  // most warps: nothing but new rows
+  const bool full = ONE && !has_old && __all_sync(0xffffffffu, isnew == 0xffu && look == 0xffu);
+  const long long row_step = RL::RPS * p.st_r[which];
+  const __nv_bfloat16* src =
+      p.rows[which] + h0 * p.st_h[which] + col +
+      (p.cu ? (long long)start * p.st_r[which] : b * p.st_b[which]) +
+      (long long)(p0 - first + r) * p.st_r[which];
+  for (int h = 0; h < heads; ++h, src += p.st_h[which]) {
     const int head = h0 + h;
     const bool on = live && head < p.Hk;
-    const __nv_bfloat16* src = p.rows[which] + head * p.st_h[which] + col +
-                               (p.cu ? (long long)start * p.st_r[which] : b * p.st_b[which]);
     uint4 x[kSteps];
     uint32_t m[GROUPS];
+    if (full && on) {
 #pragma unroll
-    for (int t = 0; t < kSteps; ++t) {
-      x[t] = make_uint4(0u, 0u, 0u, 0u);
-      if (on && isnew[t])
-        x[t] = __ldg(reinterpret_cast<const uint4*>(
-            src + (long long)(p0 - first + t * RL::RPS + r) * p.st_r[which]));
+      for (int t = 0; t < kSteps; ++t)
+        x[t] = __ldg(reinterpret_cast<const uint4*>(src + t * row_step));
+    } else {
+#pragma unroll
+      for (int t = 0; t < kSteps; ++t) {
+        x[t] = make_uint4(0u, 0u, 0u, 0u);
+        if (on && (isnew >> t & 1)) x[t] = __ldg(reinterpret_cast<const uint4*>(src + t * row_step));
+      }
     }
     uint32_t odd = 0;
 #pragma unroll
@@ -210,6 +235,17 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1)
         for (int t = g * SPB; t < (g + 1) * SPB; ++t) m[g] = absmax8(finite8(x[t]), m[g]);
       }
     }
+    // of a row's lanes: the page's codes of this head, and its scales
+    auto codes = [&](int t) {
+      const int in = (p0 & ps_mask) + t * RL::RPS + r;  // (ONE: no wrap)
+      return p.codes[which] + (size_t)(unsigned)page[ONE ? 0 : t] * p.page_bytes +
+             ((unsigned)((head << p.ps_shift) + (ONE ? in : in & ps_mask)) * HD + col);
+    };
+    auto scale = [&](int t) {
+      const int in = ((p0 & ps_mask) + t * RL::RPS + r) & ps_mask;
+      return p.scales[which] + (size_t)(unsigned)page[ONE ? 0 : t] * p.page_scales +
+             (unsigned)((head << (p.ps_shift - p.sb_shift)) + (in >> p.sb_shift));
+    };
     float was[GROUPS];
 #pragma unroll
     for (int g = 0; g < GROUPS; ++g) {
@@ -224,12 +260,9 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1)
       was[g] = 0.0f;
       if (has_old) {
 #pragma unroll
-        for (int t = g * SPB; t < (g + 1) * SPB; ++t) {
-          const int pos = p0 + t * RL::RPS + r;
-          if (on && at[t] >= 0 && (pos & ~(sb - 1)) < first)
-            was[g] = p.scales[which][(((size_t)at[t] * p.Hk + head) << nb_shift) +
-                                     ((pos & ps_mask) >> p.sb_shift)];
-        }
+        for (int t = g * SPB; t < (g + 1) * SPB; ++t)
+          if (on && (look >> t & 1) && ((p0 + t * RL::RPS + r) & ~(sb - 1)) < first)
+            was[g] = *scale(t);
         for (int o = lanes / 2; o > 0; o /= 2)
           was[g] = fmaxf(was[g], __shfl_xor_sync(0xffffffffu, was[g], o));
       }
@@ -241,6 +274,21 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1)
       __syncthreads();
     }
     if (!on) continue;
+    if (full && !any) {
+      uint8_t* dst = codes(0);
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g) {
+        const float s = exp2i(scale_exp(m[g]));
+        const float inv = __uint_as_float(0x7f000000u - __float_as_uint(s));
+#pragma unroll
+        for (int t = g * SPB; t < (g + 1) * SPB; ++t)
+          *reinterpret_cast<uint2*>(dst + t * (RL::RPS * HD)) = quantise8(x[t], inv);
+        // (a block of several steps begins with the first one's first row)
+        if (col == 0 && (SPB > 1 ? r == 0 : (r & (sb - 1)) == 0) && ((p0 & (sb - 1)) == 0 || SPB < 8))
+          *scale(g * SPB) = s;
+      }
+      continue;
+    }
 #pragma unroll
     for (int g = 0; g < GROUPS; ++g) {
       const float s = fmaxf(exp2i(scale_exp(m[g])), was[g]);
@@ -248,15 +296,13 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1)
       const float inv = __uint_as_float(0x7f000000u - __float_as_uint(s));  // (a power of two's)
 #pragma unroll
       for (int t = g * SPB; t < (g + 1) * SPB; ++t) {
-        if (at[t] < 0) continue;
-        const int pos = p0 + t * RL::RPS + r, in = pos & ps_mask;
-        const size_t row = (size_t)at[t] * p.Hk + head;
-        uint2* dst = reinterpret_cast<uint2*>(p.codes[which] + ((row << p.ps_shift) + in) * HD + col);
-        if (isnew[t]) {
+        if (!(look >> t & 1)) continue;
+        uint2* dst = reinterpret_cast<uint2*>(codes(t));
+        if (isnew >> t & 1) {
           *dst = plain ? quantise8(x[t], inv) : quantise8_any(x[t], s);
           // the block's scale, by its first new row
-          if (col == 0 && ((in & (sb - 1)) == 0 || pos == lo))
-            p.scales[which][(row << nb_shift) + (in >> p.sb_shift)] = s;
+          const int pos = p0 + t * RL::RPS + r;
+          if (col == 0 && ((pos & (sb - 1)) == 0 || pos == lo)) *scale(t) = s;
         } else if (was[g] > 0.0f && s > was[g]) {
           *dst = requantise8(*dst, was[g] / s);
         }
@@ -266,16 +312,19 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1)
   if (bad) flag_bad(p.status);
 }
 
-// Row i of sequence b is its key i: bf16(code * scale).
-template <int HD>
-__global__ void __launch_bounds__(256) q8_read_kernel(const Q8RowsK p, long long items) {
+// Row i of sequence b is its key i: bf16(code * scale). ONE, `heads`: as for the writer.
+template <int HD, bool ONE>
+__global__ void __launch_bounds__(256, 4)
+    q8_read_kernel(const Q8RowsK p, long long items, int heads) {
   using RL = RowLanes<HD>;
   const int warp = warp_id(), lane = lane_id();
+  const int ps_mask = (1 << p.ps_shift) - 1;
   const long long item = (long long)blockIdx.x * 8 + warp;
   if (item >= items) return;
   const int which = (int)(item & 1);
-  const int head = (int)((item >> 1) % p.Hk);
-  const long long slot = (item >> 1) / p.Hk;
+  const int hgroups = (p.Hk + heads - 1) / heads;
+  const int h0 = (int)((item >> 1) % hgroups) * heads;
+  const long long slot = (item >> 1) / hgroups;
   auto offset = [&](int i) { return (long long)p.cu[i]; };
   const int b = q8_slot_owner(slot, p.B, RL::TR, lane, offset);
   int start, n;
@@ -283,38 +332,61 @@ __global__ void __launch_bounds__(256) q8_read_kernel(const Q8RowsK p, long long
   const long long cap = (long long)p.max_pages << p.ps_shift;
   bad |= n > cap;
   const long long u = slot - (offset(b) / RL::TR + 2ll * b);
-  const long long p0 = u * RL::TR;
-  const int r = lane / RL::LPR, col = lane % RL::LPR * 8;
-  if (u >= 0 && p0 < n) {
-    __nv_bfloat16* dst = p.rows[which] + head * p.st_h[which] + start * p.st_r[which] + col;
-    uint2 c[kSteps];
-    float s[kSteps];
+  if (u >= 0 && u * RL::TR < n) {
+    const int p0 = (int)(u * RL::TR), end = (int)(n < cap ? n : cap);
+    const int r = lane / RL::LPR, col = lane % RL::LPR * 8;
+    const int lane_pg = lane_page(p, b, p0, RL::TR, 0, end, lane, bad);
+    // bit t: row p0 + t * RPS + r is there (else zeros: past the table's end, or of no page)
+    uint32_t have = 0;
+    int page[ONE ? 1 : kSteps];
 #pragma unroll
     for (int t = 0; t < kSteps; ++t) {
-      const long long pos = p0 + t * RL::RPS + r;
-      c[t] = make_uint2(0u, 0u);
-      s[t] = 0.0f;
-      if (pos >= n || pos >= cap) continue;  // (rows past the table's end: zeros, flagged)
-      const int pg = page_of(p, b, (int)pos, bad);
-      if (pg < 0) continue;
-      const int slot_in = (int)pos & ((1 << p.ps_shift) - 1);
-      const size_t at = (size_t)pg * p.Hk + head;
-      c[t] = __ldg(reinterpret_cast<const uint2*>(p.codes[which] +
-                                                  ((at << p.ps_shift) + slot_in) * HD + col));
-      s[t] = __ldg(p.scales[which] + (at << (p.ps_shift - p.sb_shift)) + (slot_in >> p.sb_shift));
+      const int pos = p0 + t * RL::RPS + r;
+      const int pg =
+          __shfl_sync(0xffffffffu, lane_pg, ONE ? 0 : (pos >> p.ps_shift) - (p0 >> p.ps_shift));
+      page[ONE ? 0 : t] = pg;
+      have |= (uint32_t)(pos < end && pg >= 0) << t;
     }
+    const long long row_step = RL::RPS * p.st_r[which];
+    __nv_bfloat16* dst = p.rows[which] + h0 * p.st_h[which] + col +
+                         (long long)(start + p0 + r) * p.st_r[which];
+    const int stop = min(p.Hk, h0 + heads);
+    const bool one_scale = ONE && (1 << p.sb_shift) >= RL::TR;  // of all the warp's rows
+    for (int head = h0; head < stop; ++head, dst += p.st_h[which]) {
+      uint2 c[kSteps];
+      float s[kSteps];
 #pragma unroll
-    for (int t = 0; t < kSteps; ++t) {
-      const long long pos = p0 + t * RL::RPS + r;
-      if (pos >= n) continue;
-      const float2 f0 = f32_from_e4m3x2(c[t].x), f1 = f32_from_e4m3x2(c[t].x >> 16);
-      const float2 f2 = f32_from_e4m3x2(c[t].y), f3 = f32_from_e4m3x2(c[t].y >> 16);
-      uint4 out;
-      out.x = pack_bf16(f0.x * s[t], f0.y * s[t]);
-      out.y = pack_bf16(f1.x * s[t], f1.y * s[t]);
-      out.z = pack_bf16(f2.x * s[t], f2.y * s[t]);
-      out.w = pack_bf16(f3.x * s[t], f3.y * s[t]);
-      *reinterpret_cast<uint4*>(dst + pos * p.st_r[which]) = out;
+      for (int t = 0; t < kSteps; ++t) {
+        const int in = (p0 & ps_mask) + t * RL::RPS + r;
+        c[t] = make_uint2(0u, 0u);
+        if (have >> t & 1)
+          c[t] = __ldg(reinterpret_cast<const uint2*>(
+              p.codes[which] + (size_t)(unsigned)page[ONE ? 0 : t] * p.page_bytes +
+              ((unsigned)((head << p.ps_shift) + (ONE ? in : in & ps_mask)) * HD + col)));
+      }
+#pragma unroll
+      for (int t = 0; t < kSteps; ++t) {
+        const int in = ((p0 & ps_mask) + t * RL::RPS + r) & ps_mask;
+        s[t] = t > 0 && one_scale ? s[0] : 0.0f;
+        if ((t == 0 || !one_scale) && (have >> t & 1))
+          s[t] = __ldg(p.scales[which] + (size_t)(unsigned)page[ONE ? 0 : t] * p.page_scales +
+                       (unsigned)((head << (p.ps_shift - p.sb_shift)) + (in >> p.sb_shift)));
+      }
+#pragma unroll
+      for (int t = 0; t < kSteps; ++t) {
+        if (p0 + t * RL::RPS + r >= n) continue;
+        const uint64_t s2 = f2_pack(s[t], s[t]);
+        const uint32_t w[4] = {c[t].x, c[t].x >> 16, c[t].y, c[t].y >> 16};
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = f32_from_e4m3x2(w[e]);
+          float x, y;
+          f2_unpack(f2_mul(f2_pack(f.x, f.y), s2), x, y);
+          o[e] = pack_bf16(x, y);
+        }
+        __stcs(reinterpret_cast<uint4*>(dst + t * row_step), make_uint4(o[0], o[1], o[2], o[3]));
+      }
     }
   }
   if (bad) flag_bad(p.status);
@@ -342,10 +414,17 @@ Q8RowsK rows_params(const Q8RowsArgs& a) {
   p.num_pages = a.num_pages;
   p.ps_shift = a.ps_shift;
   p.sb_shift = a.sb_shift;
+  p.page_bytes = (unsigned)a.Hk * a.d << a.ps_shift;  // (checked to fit)
+  p.page_scales = (unsigned)a.Hk << (a.ps_shift - a.sb_shift);
   return p;
 }
 
-template <int HD, int SPB>
+// Heads of an item: four, where that still leaves 16 warps for each SM.
+int heads_of(long long warps_per_head, int Hk) {
+  return Hk >= 4 && warps_per_head * Hk / 4 >= 152 * 16 ? 4 : 1;
+}
+
+template <int HD, int SPB, bool ONE>
 cudaError_t write_t(const Q8RowsArgs& a, cudaStream_t s) {
   using RL = RowLanes<HD>;
   const int sb = 1 << a.sb_shift;
@@ -353,37 +432,51 @@ cudaError_t write_t(const Q8RowsArgs& a, cudaStream_t s) {
   const int warps = wpb > 8 ? wpb : 8;
   const long long total = a.cu ? a.total : (long long)a.B * a.new_len;
   const long long slots = q8_unit_slots(total, a.B, RL::TR * wpb);
-  // heads of an item: four, where that still leaves 16 warps for each SM
-  const int heads = a.Hk >= 4 && slots * wpb * a.Hk / 4 * 2 >= 152 * 16 ? 4 : 1;
+  const int heads = heads_of(slots * wpb * 2, a.Hk);
   const long long items = slots * ((a.Hk + heads - 1) / heads) * 2;
   const long long per = warps / wpb;
-  profile_mark(kKernQ8Write, 0, s);
   const unsigned grid = (unsigned)((items + per - 1) / per);
-  if constexpr (SPB == 8 && HD >= 128) {
+  profile_mark(kKernQ8Write, 0, s);
+  if constexpr (SPB == 8 && ONE && HD >= 128) {
     if (warps > 8)
-      q8_write_kernel<HD, SPB, 1024><<<grid, warps * 32, 0, s>>>(rows_params(a), items, wpb, heads);
+      q8_write_kernel<HD, SPB, ONE, 1024><<<grid, warps * 32, 0, s>>>(rows_params(a), items, wpb,
+                                                                      heads);
   }
   if (warps == 8)
-    q8_write_kernel<HD, SPB, 256><<<grid, 256, 0, s>>>(rows_params(a), items, wpb, heads);
+    q8_write_kernel<HD, SPB, ONE, 256><<<grid, 256, 0, s>>>(rows_params(a), items, wpb, heads);
   const cudaError_t e = cudaGetLastError();
   profile_mark(kKernQ8Write, 1, s);
   return e;
 }
 
+template <int HD, int SPB>
+cudaError_t write_s(const Q8RowsArgs& a, cudaStream_t s) {
+  // (a block of 8 steps is all of a warp's rows, and a page holds whole blocks)
+  if constexpr (SPB < 8)
+    if ((1 << a.ps_shift) < RowLanes<HD>::TR) return write_t<HD, SPB, false>(a, s);
+  return write_t<HD, SPB, true>(a, s);
+}
+
 template <int HD>
 cudaError_t write_d(const Q8RowsArgs& a, cudaStream_t s) {
   const int spb = (1 << a.sb_shift) / RowLanes<HD>::RPS;  // steps of a block (0: less than one)
-  if (spb >= 8) return write_t<HD, 8>(a, s);
-  if (spb == 4) return write_t<HD, 4>(a, s);
-  if (spb == 2) return write_t<HD, 2>(a, s);
-  return write_t<HD, 1>(a, s);
+  if (spb >= 8) return write_s<HD, 8>(a, s);
+  if (spb == 4) return write_s<HD, 4>(a, s);
+  if (spb == 2) return write_s<HD, 2>(a, s);
+  return write_s<HD, 1>(a, s);
 }
 
 template <int HD>
 cudaError_t read_d(const Q8RowsArgs& a, cudaStream_t s) {
-  const long long items = q8_unit_slots(a.total, a.B, RowLanes<HD>::TR) * a.Hk * 2;
+  const long long slots = q8_unit_slots(a.total, a.B, RowLanes<HD>::TR);
+  const int heads = heads_of(slots * 2, a.Hk);
+  const long long items = slots * ((a.Hk + heads - 1) / heads) * 2;
+  const unsigned grid = (unsigned)((items + 7) / 8);
   profile_mark(kKernQ8Read, 0, s);
-  q8_read_kernel<HD><<<(unsigned)((items + 7) / 8), 256, 0, s>>>(rows_params(a), items);
+  if ((1 << a.ps_shift) < RowLanes<HD>::TR)
+    q8_read_kernel<HD, false><<<grid, 256, 0, s>>>(rows_params(a), items, heads);
+  else
+    q8_read_kernel<HD, true><<<grid, 256, 0, s>>>(rows_params(a), items, heads);
   const cudaError_t e = cudaGetLastError();
   profile_mark(kKernQ8Read, 1, s);
   return e;

@@ -374,7 +374,7 @@ typedef struct fa_q8_cache {
   float* k_scale;       /* f32 [num_pages, n_kv_heads, page_size / scale_block], 4-byte aligned */
   float* v_scale;       /* same */
   int32_t num_pages;    /* >= 1 */
-  int32_t n_kv_heads;   /* >= 1; num_pages * n_kv_heads < 2^30 */
+  int32_t n_kv_heads;   /* >= 1; num_pages * n_kv_heads < 2^30, a page's codes < 2^31 bytes */
   int32_t page_size;    /* a power of two in [8, 256] */
   int32_t head_dim;     /* 64, 128 or 256 */
   int32_t scale_block;  /* a power of two in [1, page_size] */

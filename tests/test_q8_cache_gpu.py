@@ -145,6 +145,32 @@ def test_write_token_by_token_keeps_a_monotone_scale():
             np.testing.assert_array_equal(got[2 + w].cpu().numpy(), cache[2 + w])
 
 
+@pytest.mark.parametrize("d,ps,block", [(64, 256, 256), (128, 256, 256), (256, 256, 256),
+                                        (128, 256, 32), (128, 16, 16), (64, 8, 4)])
+@pytest.mark.parametrize("size", [2.0 ** -12, 2.0 ** 12])
+def test_write_into_a_block_with_another_scale(d, ps, block, size):
+    """New tokens far smaller than a block's earlier ones keep its scale, far larger ones raise it,
+    wherever in the block they begin."""
+    import flash_attention_gb300 as fa
+
+    rng = np.random.default_rng(d + ps + block)
+    past = [1, block // 2, block - 1, block + 3, 2 * block + block // 4]
+    new = [3 * block + 1, block, 1, 2, block]
+    lengths = np.array(past) + new
+    per = int(-(-lengths.max() // ps))
+    table, P = plain.make_table(rng, 5, per)
+    cache = plain.make_cache(rng, P, 2, ps, d, block, spread=0.3)
+    got = dev_cache(*cache)
+    cu = np.concatenate([[0], np.cumsum(new)])
+    x = [bf16(rng.standard_normal((2, cu[-1], d)) * size) for _ in range(2)]
+    fa.q8_cache_write(x[0][0], x[1][0], *got, ints(table), ints(lengths), cu_seqlens=ints(cu))
+    for w in range(2):
+        plain.write(cache[w], cache[2 + w], [x[w][1][:, cu[b]:cu[b + 1]] for b in range(5)], table,
+                    lengths, block)
+        np.testing.assert_array_equal(host_codes(got[w]), cache[w])
+        np.testing.assert_array_equal(got[2 + w].cpu().numpy(), cache[2 + w])
+
+
 def test_write_every_bf16_value_rounds_once():
     """All finite bf16 values of one binade range as single-token blocks: the scale is the smallest
     power of two that fits, at the border 448 * 2^k too."""
