@@ -30,10 +30,10 @@
 // its part from them). A unit counts kUnitCost tiles more than it has, what its start and end cost. A CTA writes the units it has whole; of the others it leaves its share's
 // O, m and sum, which a second kernel joins in the order of the keys.
 //
-// Warps of a CTA: 0-3 softmax (thread = key of the tile, and head-dim row of O^T), 4 TMA copies of
-// K and V pages (boxes of min(page_size, 128) rows), 5 issues S^T, 6 O^T (and zeroes what a last
-// page holds behind the sequence's end, so that NaN there meets no weight), 7 splits q and fetches
-// the scales. All waits on barriers are bounded.
+// Warps of a CTA: one or two softmax warpgroups of 8 rows (thread = key of the tile, and head-dim
+// row of O^T), then one warp each for the TMA copies of K and V pages (boxes of min(page_size, 128)
+// rows), for issuing S^T, for O^T (it zeroes what a last page holds behind the sequence's end, so
+// that NaN there meets no weight), and for the list: it walks it, splits q and fetches the scales. All waits on barriers are bounded.
 #include <float.h>
 
 #include <algorithm>
@@ -85,8 +85,10 @@ struct Q8Layout {
   static constexpr int TMEM_USED = COL_O + KCH * NP;
   static constexpr int TMEM_COLS = TMEM_USED <= 64 ? 64 : TMEM_USED <= 128 ? 128
                                    : TMEM_USED <= 256 ? 256 : 512;
-  static constexpr int THREADS = 256;
-  static constexpr int TMA_WARP = 4, S_WARP = 5, O_WARP = 6, QS_WARP = 7;
+  static constexpr int NWG = R / 8;                 // softmax warpgroups, 8 rows each
+  static constexpr int THREADS = 128 * NWG + 128;
+  static constexpr int TMA_WARP = 4 * NWG, S_WARP = TMA_WARP + 1, O_WARP = TMA_WARP + 2,
+                       QS_WARP = TMA_WARP + 3;
   static_assert(TMEM_USED <= 512 && TMEM_COLS * CTAS <= 512, "TMEM budget");
   // dynamic, static (pages, scales, barriers, rows: below) and the driver's 1 KB
   static constexpr int STATIC_BYTES = 4 * kPageChunk + 16 * kKT + 72 * R + 512;
@@ -140,13 +142,29 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// N = 16 or 32 columns of a TMEM lane.
-template <int N>
-__device__ __forceinline__ void load_cols(uint32_t taddr, uint32_t (&r)[N]) {
-  if constexpr (N == 16)
-    tmem_ld16(taddr, r);
-  else
-    tmem_ld32(taddr, r);
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
+                   taddr),
+               "r"(__float_as_uint(r[0])), "r"(__float_as_uint(r[1])), "r"(__float_as_uint(r[2])),
+               "r"(__float_as_uint(r[3])), "r"(__float_as_uint(r[4])), "r"(__float_as_uint(r[5])),
+               "r"(__float_as_uint(r[6])), "r"(__float_as_uint(r[7]))
+               : "memory");
+}
+// Scores of 8 rows: their hi columns, and the lo columns R further on.
+template <int R>
+__device__ __forceinline__ void load_scores(uint32_t taddr, uint32_t (&s)[16]) {
+  if constexpr (R == 8) {
+    tmem_ld16(taddr, s);
+  } else {
+    float a[8], b[8];
+    tmem_ld8(taddr, a);
+    tmem_ld8(taddr + R, b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      s[e] = __float_as_uint(a[e]);
+      s[8 + e] = __float_as_uint(b[e]);
+    }
+  }
 }
 // Two weights (>= 0, at most 2^15) -> two f16 rounded to 9 bits (half up).
 __device__ __forceinline__ uint32_t weight_f16x2(float lo, float hi) {
@@ -162,14 +180,14 @@ __device__ __forceinline__ uint32_t f16x2_rest(uint32_t h) {
                             __float2half2_rn(8.0f));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
-// The barrier of the 128 softmax threads; true where any of them came with `v`.
-__device__ __forceinline__ bool softmax_any(bool v) {
+// The barrier of the 128 threads of softmax warpgroup `wg`; true where any of them came with `v`.
+__device__ __forceinline__ bool softmax_any(int wg, bool v) {
   int r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 128, p;\n"
+      "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n"
       " selp.s32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
-      : "r"((int)v)
+      : "r"((int)v), "r"(wg + 1)
       : "memory");
   return r != 0;
 }
@@ -249,8 +267,8 @@ __device__ __forceinline__ unsigned q8_share(unsigned all, unsigned grid) {
   return (all + grid - 1) / grid;
 }
 
-// The units of a CTA's share [t, t1) of the list, in order: warp 7 walks it and publishes the units
-// in shared memory, where the other roles take them from.
+// The units of a CTA's share [t, t1) of the list, in order: the last warp walks it and publishes the
+// units in shared memory, where the other roles take them from.
 struct Walk {
   unsigned t, t1;    // next place in the list, end of the share
   unsigned pre;      // the list before sequence b
@@ -336,7 +354,7 @@ struct Walk {
 struct Unit {
   int b, kh, rb, ja, jb, len, whole, first;
 };
-// Units in shared memory: warp 7 publishes, the others read and free (7 warps).
+// Units in shared memory: the last warp publishes, the others read and free.
 constexpr int kUnits = 4;
 struct UnitRing {
   int4 at[kUnits][2];
@@ -358,7 +376,7 @@ __device__ __forceinline__ bool take_unit(UnitRing* ring, int un, Unit& u, bool&
 // RL: the rows of a unit that there can be (of the R that a tile has columns for): the softmax's
 // arithmetic runs on these alone.
 template <int HD, int R, int RL>
-__global__ void __launch_bounds__(256, Q8Layout<HD, R, RL>::CTAS)
+__global__ void __launch_bounds__(Q8Layout<HD, R, RL>::THREADS, Q8Layout<HD, R, RL>::CTAS)
     q8_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
                    const Q8K p) {
   using LY = Q8Layout<HD, R, RL>;
@@ -400,16 +418,16 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R, RL>::CTAS)
 #pragma unroll 1
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 2);  // the MMA, and the scales of its keys
-      mbar_init(&s_free[s], 4);
-      mbar_init(&p_full[s], 4);
+      mbar_init(&s_free[s], 4 * LY::NWG);
+      mbar_init(&p_full[s], 4 * LY::NWG);
       mbar_init(&p_done[s], 1);
       mbar_init(&q_full[s], 1);
-      mbar_init(&q_free[s], 2);
+      mbar_init(&q_free[s], 1 + LY::NWG);
     }
 #pragma unroll 1
     for (int s = 0; s < kUnits; ++s) {
       mbar_init(&units.full[s], 1);
-      mbar_init(&units.free[s], 7);
+      mbar_init(&units.free[s], 3 + 4 * LY::NWG);
     }
     mbar_init(&drain_s, 1);
     mbar_init(&drain_o, 1);
@@ -744,11 +762,15 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R, RL>::CTAS)
     }
   } else {
     // ------------------------------------------------------------------ softmax, and O out.
-    // Rows that are not there (live of the RL are) have the score factor 0, and columns of q, S, w
+    // A warpgroup has the rows row0 .. row0 + 7 of the block (RW of them at most; with 16 rows two
+    // groups share the latency of a tile: one group of 16 took 69 us for four new positions of 16
+    // sequences). Rows that are not there (live of the RW are) have the score factor 0, and columns of q, S, w
     // and O that hold anything (NaN too) and are never used. A wait that runs out shows at the
     // next softmax_any, where all threads leave together.
-    const int key = threadIdx.x;  // key of the tile
-    const uint32_t lanes = tbase + ((uint32_t)(warp * 32) << 16);
+    constexpr int RW = RL < 8 ? RL : 8;
+    const int wg = LY::NWG == 1 ? 0 : warp >> 2, wl = warp & 3, row0 = wg * 8;
+    const int key = threadIdx.x & 127;  // key of the tile
+    const uint32_t lanes = tbase + ((uint32_t)(wl * 32) << 16);
     const uint64_t sixteenth = f2_pack(0.0625f, 0.0625f);
     int g = 0;
     Unit w;
@@ -758,87 +780,88 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R, RL>::CTAS)
       const int qb = un & 1;
       ok = take_unit(&units, un, w, end, lane, &wctl);
       if (ok && !end) ok = wait_warp(&q_full[qb], (un >> 1) & 1, &wctl);
-      if (softmax_any(!ok) || end) break;
-      const int r0 = w.rb * R, live = min(RL, p.rows - r0);
+      if (softmax_any(wg, !ok) || end) break;
+      const int r0 = w.rb * R + row0, live = min(RW, p.rows - r0);
       // tiles below lim_min need no test of the keys
       const int lim_min = min(p.causal ? max(0, w.len - p.lq + 1) : w.len, w.jb * kKT);
-      float l[RL];
+      float l[RW];
 #pragma unroll
-      for (int r = 0; r < RL; ++r) l[r] = 0.0f;
+      for (int r = 0; r < RW; ++r) l[r] = 0.0f;
 #pragma unroll 1
       for (int j = w.ja; j < w.jb; ++j, ++g) {
         const int buf = g & 1;
         const uint32_t ph = (g >> 1) & 1;
         ok = ok && wait_warp(&s_full[buf], ph, &wctl);
         tc_fence_after();
-        uint32_t sr[NS];
-        load_cols<NS>(lanes + LY::COL_S + buf * NS, sr);
+        uint32_t sr[16];  // hi of the 8 rows, lo
+        load_scores<R>(lanes + LY::COL_S + buf * NS + row0, sr);
         const float kc = sc_s[buf][0][key], lsv = sc_s[buf][1][key];
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_free[buf]);
         const bool first = j == w.ja;
-        float t[RL];
+        float t[RW];
         const uint64_t kc2 = f2_pack(kc, kc), lsv2 = f2_pack(lsv, lsv);
 #pragma unroll
-        for (int r = 0; r < RL; r += 2) {
-          const uint64_t qs = *reinterpret_cast<const uint64_t*>(&qs_s[qb][r]);
-          const uint64_t nm = first ? 0ull : *reinterpret_cast<const uint64_t*>(&nm_s[qb][r]);
+        for (int r = 0; r < RW; r += 2) {
+          const uint64_t qs = *reinterpret_cast<const uint64_t*>(&qs_s[qb][row0 + r]);
+          const uint64_t nm =
+              first ? 0ull : *reinterpret_cast<const uint64_t*>(&nm_s[qb][row0 + r]);
           const uint64_t hi = f2_pack(__uint_as_float(sr[r]), __uint_as_float(sr[r + 1]));
-          const uint64_t lo = f2_pack(__uint_as_float(sr[R + r]), __uint_as_float(sr[R + r + 1]));
+          const uint64_t lo = f2_pack(__uint_as_float(sr[8 + r]), __uint_as_float(sr[9 + r]));
           const uint64_t s = f2_mul(f2_fma(lo, sixteenth, hi), kc2);
           f2_unpack(f2_fma(s, qs, f2_add(lsv2, nm)), t[r], t[r + 1]);
         }
         if (j * kKT + kKT > lim_min) {
 #pragma unroll
-          for (int r = 0; r < RL; ++r)
-            if (j * kKT + key >= lim_s[qb][r]) t[r] = -INFINITY;
+          for (int r = 0; r < RW; ++r)
+            if (j * kKT + key >= lim_s[qb][row0 + r]) t[r] = -INFINITY;
         }
         float top = t[0];
 #pragma unroll
-        for (int r = 1; r < RL; r += 2)
-          top = r + 1 < RL ? fmax3(top, t[r], t[r + 1]) : fmaxf(top, t[r]);
-        if (softmax_any(top > kMost || first || !ok)) {
+        for (int r = 1; r < RW; r += 2)
+          top = r + 1 < RW ? fmax3(top, t[r], t[r + 1]) : fmaxf(top, t[r]);
+        if (softmax_any(wg, top > kMost || first || !ok)) {
           // m moves: to the largest score so far, at a unit's first tile to the tile's own
 #pragma unroll
-          for (int r = 0; r < RL; ++r) {
+          for (int r = 0; r < RW; ++r) {
             const float mx = warp_max(t[r]);
-            if (lane == 0) red_s[warp][r] = mx;
+            if (lane == 0) red_s[wl][row0 + r] = mx;
           }
-          if (softmax_any(!ok)) {
+          if (softmax_any(wg, !ok)) {
             ok = false;
             break;
           }
-          if (key < RL) {
-            const float mx = fmaxf(fmaxf(red_s[0][key], red_s[1][key]),
-                                   fmaxf(red_s[2][key], red_s[3][key]));
+          if (key < RW) {
+            const int r = row0 + key;
+            const float mx = fmaxf(fmaxf(red_s[0][r], red_s[1][r]), fmaxf(red_s[2][r], red_s[3][r]));
             float up = mx - kTop;
             if (first ? mx == -INFINITY : !(up > 0.0f)) up = 0.0f;
-            nm_s[qb][key] = first ? -up : nm_s[qb][key] - up;
-            up_s[key] = up;
-            f_s[key] = ex2(-up);
+            nm_s[qb][r] = first ? -up : nm_s[qb][r] - up;
+            up_s[r] = up;
+            f_s[r] = ex2(-up);
           }
           if (!first) {  // O is scaled too, once the last O^T MMA is done
             ok = wait_warp(&p_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &wctl);
             tc_fence_after();
           }
-          softmax_any(false);
+          softmax_any(wg, false);
 #pragma unroll
-          for (int r = 0; r < RL; ++r) {
-            t[r] -= up_s[r];
-            if (!first) l[r] *= f_s[r];
+          for (int r = 0; r < RW; ++r) {
+            t[r] -= up_s[row0 + r];
+            if (!first) l[r] *= f_s[row0 + r];
           }
           if (!first) {
 #pragma unroll 1
-            for (int c = 0; c < KCH * NP; c += 32) {  // (R columns a piece; f_s beyond RL: any)
-              uint32_t x[32];
-              tmem_ld32(lanes + LY::COL_O + c, x);
+            for (int h = 0; h < 3 * KCH; ++h) {  // (f_s beyond RW: any)
+              const uint32_t at = lanes + LY::COL_O + h / 3 * NP + h % 3 * R + row0;
+              float x[8];
+              tmem_ld8(at, x);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                x[e] = __float_as_uint(__uint_as_float(x[e]) * f_s[e % R]);
-              tmem_st32(lanes + LY::COL_O + c, x);
+              for (int e = 0; e < 8; ++e) x[e] *= f_s[row0 + e];
+              tmem_st8(at, x);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -847,13 +870,13 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R, RL>::CTAS)
         // weights, their sum, and their pieces into shared memory, a key's row of NP bytes
         const float inv = ex2(-lsv - kSumExp);  // 1 / value scale, in the sum's unit
         if (g >= 2) ok = ok && wait_warp(&p_done[buf], ph ^ 1, &wctl);
-        uint32_t pc[3][R / 4];
+        uint32_t pc[3][2];
 #pragma unroll
-        for (int r = 0; r < RL; r += 4) {
+        for (int r = 0; r < RW; r += 4) {
           uint32_t x[2];
 #pragma unroll
           for (int e = 0; e < 4; e += 2) {
-            if (r + e >= RL) {
+            if (r + e >= RW) {
               x[e / 2] = 0u;
               continue;
             }
@@ -870,16 +893,16 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R, RL>::CTAS)
           }
         }
         uint8_t* prow = smem + LY::OFF_P + buf * LY::P_BYTES + key * NP;
+        if constexpr (RW <= 4) pc[0][1] = pc[1][1] = pc[2][1] = 0u;
         if constexpr (R == 8) {
-          if constexpr (RL <= 4) pc[0][1] = pc[1][1] = pc[2][1] = 0u;
           *reinterpret_cast<uint4*>(prow + swz<NP>(0, key) * 16) =
               make_uint4(pc[0][0], pc[0][1], pc[1][0], pc[1][1]);
           *reinterpret_cast<uint2*>(prow + swz<NP>(1, key) * 16) = make_uint2(pc[2][0], pc[2][1]);
         } else {
 #pragma unroll
           for (int i = 0; i < 3; ++i)
-            *reinterpret_cast<uint4*>(prow + swz<NP>(i, key) * 16) =
-                make_uint4(pc[i][0], pc[i][1], pc[i][2], pc[i][3]);
+            *reinterpret_cast<uint2*>(prow + swz<NP>(i, key) * 16 + row0) =
+                make_uint2(pc[i][0], pc[i][1]);
         }
         fence_proxy_async();
         __syncwarp();
@@ -888,14 +911,14 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R, RL>::CTAS)
       // the sums of the 128 threads
       const bool any = w.jb > w.ja;
 #pragma unroll
-      for (int r = 0; r < RL; ++r) {
+      for (int r = 0; r < RW; ++r) {
         float x = l[r];
 #pragma unroll
         for (int o = 16; o > 0; o /= 2) x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (lane == 0) red_s[warp][r] = x;
+        if (lane == 0) red_s[wl][row0 + r] = x;
       }
       if (any && ok) ok = wait_warp(&p_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &wctl);
-      if (softmax_any(!ok)) {
+      if (softmax_any(wg, !ok)) {
         ok = false;
         break;
       }
@@ -904,51 +927,49 @@ __global__ void __launch_bounds__(256, Q8Layout<HD, R, RL>::CTAS)
       const size_t unit_row = ((size_t)w.b * p.Hk + w.kh) * p.rows + r0;
       const size_t part = 2 * (size_t)blockIdx.x + (w.first ? 1 : 0);
       // this thread's head-dim row: a 64-row accumulator lies in lanes 0-15 of each warp
-      const int col = HD == 64 ? warp * 16 + lane : (int)threadIdx.x;
+      const int col = HD == 64 ? wl * 16 + lane : key;
       const bool mine = HD > 64 || lane < 16;
-      const size_t row0 = w.whole ? unit_row : part * R;
+      const size_t out_row = w.whole ? unit_row : part * R + row0;
 #pragma unroll 1
-      for (int c = 0; c < live; c += 8) {
-#pragma unroll 1
-        for (int h = 0; h < KCH; ++h) {
-          float x[8], y[8], z[8];
-          if (any) {
-            const uint32_t at = lanes + LY::COL_O + h * NP + c;
-            tmem_ld8(at, x);
-            tmem_ld8(at + R, y);
-            tmem_ld8(at + 2 * R, z);
-            tmem_wait_ld();
-          }
-          size_t at = (row0 + c) * HD + h * 128 + col;
+      for (int h = 0; h < KCH; ++h) {
+        float x[8], y[8], z[8];
+        if (any) {
+          const uint32_t at = lanes + LY::COL_O + h * NP + row0;
+          tmem_ld8(at, x);
+          tmem_ld8(at + R, y);
+          tmem_ld8(at + 2 * R, z);
+          tmem_wait_ld();
+        }
+        size_t at = out_row * HD + h * 128 + col;
 #pragma unroll
-          for (int e = 0; e < (RL < 8 ? RL : 8); ++e, at += HD) {
-            const float sum = (red_s[0][c + e] + red_s[1][c + e]) +
-                              (red_s[2][c + e] + red_s[3][c + e]);
-            float o = fmaf(fmaf(z[e], 0.125f, y[e]), 0.125f, x[e]);
-            if (w.whole) o = __fdividef(o, sum) / kSumUnit;  // (2 ulp; o is rounded to bf16)
-            if (sum == 0.0f) o = 0.0f;
-            if (c + e < live && mine) {
-              if (w.whole)
-                p.o[at] = __float2bfloat16(o);
-              else
-                p.o_part[at] = o;
-            }
+        for (int e = 0; e < RW; ++e, at += HD) {
+          const int r = row0 + e;
+          const float sum = (red_s[0][r] + red_s[1][r]) + (red_s[2][r] + red_s[3][r]);
+          float o = fmaf(fmaf(z[e], 0.125f, y[e]), 0.125f, x[e]);
+          if (w.whole) o = __fdividef(o, sum) / kSumUnit;  // (2 ulp; o is rounded to bf16)
+          if (sum == 0.0f) o = 0.0f;
+          if (e < live && mine) {
+            if (w.whole)
+              p.o[at] = __float2bfloat16(o);
+            else
+              p.o_part[at] = o;
           }
         }
       }
       if (key < live) {
-        const float sum = (red_s[0][key] + red_s[1][key]) + (red_s[2][key] + red_s[3][key]);
-        const float m = any ? -nm_s[qb][key] : 0.0f;
+        const int r = row0 + key;
+        const float sum = (red_s[0][r] + red_s[1][r]) + (red_s[2][r] + red_s[3][r]);
+        const float m = any ? -nm_s[qb][r] : 0.0f;
         if (!w.whole) {
-          p.ml_part[part * 2 * R + key] = m;
-          p.ml_part[part * 2 * R + R + key] = sum;
+          p.ml_part[part * 2 * R + r] = m;
+          p.ml_part[part * 2 * R + R + r] = sum;
         } else if (p.lse) {
           p.lse[unit_row + key] = sum == 0.0f ? -INFINITY : fmaf(m + kSumExp, kLn2, logf(sum));
         }
       }
       // (the next unit has the other half of nm_s, and writes red_s behind its first vote)
       tc_fence_before();
-      if (threadIdx.x == 0) mbar_arrive(&q_free[qb]);
+      if (key == 0) mbar_arrive(&q_free[qb]);
     }
   }
 
