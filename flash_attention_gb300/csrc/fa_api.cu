@@ -837,6 +837,12 @@ static int prepare_q8_rows(const fa_q8_cache* c, const fa_q8_rows* r, bool write
   for (int i = 0; i < 3; ++i)
     if (r->k_stride[i] < 0 || r->v_stride[i] < 0 || r->k_stride[i] % 8 || r->v_stride[i] % 8)
       return FA_ERR_INVALID;
+  if (!write) {  // rows that are written must not lie on one another
+    const int64_t d = c->head_dim;
+    if ((r->total > 1 && (r->k_stride[2] < d || r->v_stride[2] < d)) ||
+        (c->n_kv_heads > 1 && (r->k_stride[1] < d || r->v_stride[1] < d)))
+      return FA_ERR_INVALID;
+  }
   a->codes[0] = c->k;
   a->codes[1] = c->v;
   a->scales[0] = c->k_scale;

@@ -191,20 +191,26 @@ __device__ __forceinline__ bool softmax_any(int wg, bool v) {
       : "memory");
   return r != 0;
 }
-// mbar_wait with its polling out of line, and each poll suspended for up to 20 us: with 8 warps a
-// CTA of which most wait most of the time, the polls were the larger part of all instructions,
-// and they share the SM's instruction cache with the softmax.
+// Bounded waits of this kernel. A first poll in line (suspended for as long as the hardware likes);
+// what follows is out of line, with polls suspended for up to 20 us. (8 warps a CTA, most of which
+// wait most of the time: short polls were the larger part of all instructions, and share the SM's
+// instruction cache with the softmax.) Under a limit below 100 us, which exists to make waits run
+// out, those polls are not suspended, and S^T's wait for a unit's q, which always lasts a while at
+// the start, begins with one that is not (elsewhere that costs 2 %).
 __device__ __noinline__ bool wait_more(uint64_t* bar, uint32_t parity, WaitCtl* w) {
   const uint64_t t0 = globaltimer();
-  const uint32_t hint = w->limit_ns < 20000 ? (uint32_t)w->limit_ns : 20000u;
+  const bool brief = w->limit_ns < 100000ull;
   for (;;) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(hint)
-        : "memory");
+    uint32_t ok = 0;
+    if (brief)
+      ok = mbar_test_wait(bar, parity);
+    else
+      asm volatile(
+          "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n"
+          " selp.u32 %0, 1, 0, p;\n}\n"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"(parity)
+          : "memory");
     if (ok) return true;
     if (*reinterpret_cast<volatile int*>(&w->abort)) return false;
     if (globaltimer() - t0 > w->limit_ns) {
@@ -217,8 +223,11 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, WaitCtl* w)
   return mbar_try_wait(bar, parity) || wait_more(bar, parity, w);
 }
 // The wait of a whole warp, that does not part its lanes: true for all or none.
+template <bool SUSPEND = true>
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, WaitCtl* w) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  if (__all_sync(0xffffffffu,
+                 SUSPEND ? mbar_try_wait(bar, parity) : mbar_test_wait(bar, parity)))
+    return true;
   return __all_sync(0xffffffffu, wait_more(bar, parity, w));
 }
 // Largest value of the warp (NaN is passed over).
@@ -537,7 +546,7 @@ __global__ void __launch_bounds__(Q8Layout<HD, R, RL>::THREADS, Q8Layout<HD, R, 
     bool ok = true, end = false;
 #pragma unroll 1
     for (int un = 0; ok && (ok = take_unit(&units, un, w, end, lane, &wctl)) && !end; ++un) {
-      ok = wait_warp(&q_full[un & 1], (un >> 1) & 1, &wctl);
+      ok = wait_warp<false>(&q_full[un & 1], (un >> 1) & 1, &wctl);
       const Desc qb = q8_desc<CH>(smem_u32(smem + LY::OFF_Q + (un & 1) * LY::Q_BYTES), 0);
 #pragma unroll 1
       for (int j = w.ja; j < w.jb && ok; ++j, ++g) {

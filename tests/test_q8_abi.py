@@ -28,7 +28,8 @@ BAD_WRITE = [dict(lengths=None), dict(lengths=FAKE + 2),
              dict(cu_seqlens=None, total=0, new_len=0),
              dict(cu_seqlens=None, total=0, new_len=1 << 23),
              dict(cu_seqlens=None, total=0, new_len=1 << 22, batch=1 << 20)]
-BAD_READ = [dict(), dict(lengths=None, cu_seqlens=None, total=0, new_len=3)]
+BAD_READ = [dict(), dict(lengths=None, cu_seqlens=None, total=0, new_len=3),
+            dict(lengths=None, k_stride=(0, 1024, 0)), dict(lengths=None, v_stride=(0, 64, 256))]
 
 
 @pytest.fixture(scope="module")

@@ -335,6 +335,7 @@ ATTEND = [
     A("all_empty", 2, 4, 2, 2, 128, 16, 16, [0, 0]),
     A("long", 2, 8, 2, 1, 128, 16, 16, [5000, 3000]),
     A("one_long", 1, 1, 1, 1, 128, 256, 256, [16000]),
+    A("very_long", 1, 2, 1, 1, 64, 64, 16, [150_001]),
     A("many_short", 100, 4, 2, 1, 64, 16, 4, [(i * 37) % 200 for i in range(100)]),
 ]
 
@@ -376,7 +377,7 @@ def check_attend(c, table, cache, q, o, lse):
     used = np.max(np.abs(o - want) / tol)
     l_used = 0.0
     if not dead.all():
-        d = np.abs(lse - l_want)[~dead] / np.maximum(1, np.abs(l_want[~dead]))
+        d = np.abs(lse[~dead] - l_want[~dead]) / np.maximum(1, np.abs(l_want[~dead]))
         l_used = float(np.max(d) * 2 ** 17)
     assert used <= 1 and l_used <= 1, (c["name"], used, l_used)
     return used, l_used
@@ -500,6 +501,90 @@ def test_attention_is_bitwise_reproducible():
     for _ in range(5):
         again = attend(c, table, got, qt)
         assert all(torch.equal(x, y) for x, y in zip(first, again))
+
+
+def test_attention_writes_its_outputs_and_nothing_else():
+    """Through the C ABI, with o and lse inside filled buffers: every element of them is written, and
+    none around them, for whole and cut units, empty sequences and head dims of every width."""
+    import ctypes
+
+    import torch
+
+    import flash_attention_gb300 as fa
+
+    for d, lq, lengths in ((64, 1, [5, 0, 900]), (128, 3, [2000, 1, 0]), (256, 5, [300, 0, 700])):
+        c = A("guard", 3, 8, 2, lq, d, 16, 16, lengths)
+        _, table, P, cache, q = make_attend(c)
+        got, (qt, q64) = dev_cache(*cache), bf16(q)
+        n, m, pad = qt.numel(), 3 * 8 * lq, 512
+        for with_lse in (True, False):
+            o = torch.full((n + 2 * pad,), -7.0, dtype=torch.bfloat16, device="cuda")
+            lse = torch.full((m + 2 * pad,), -7.0, device="cuda")
+            tb, ln = ints(table), ints(lengths)
+            s = fa._q8_cache(*got, torch)
+            p = fa.FaPagedParams(3, 8, 2, lq, d, 16, table.shape[1], P, d ** -0.5, 1, 0, 0)
+            rc = fa.load_library().fa_q8_paged_attention(
+                qt.data_ptr(), ctypes.byref(s), tb.data_ptr(), ln.data_ptr(),
+                o.data_ptr() + 2 * pad, lse.data_ptr() + 4 * pad if with_lse else None,
+                ctypes.byref(p), torch.cuda.current_stream().cuda_stream)
+            assert rc == fa.FA_OK and fa.fa_device_status(True) == fa.FA_OK
+            for x in (o, lse):
+                assert (x[:pad] == -7).all() and (x[-pad:] == -7).all()
+            inner = lse[pad:-pad].view(3, 8, lq)
+            if with_lse:
+                check_attend(c, table, cache, q64, o[pad:-pad].view(qt.shape), inner)
+            else:
+                assert (inner == -7).all()
+
+
+def test_caches_beyond_32_bits():
+    """The last pages of caches of over 4 GB, against the same pages in a small cache."""
+    import torch
+
+    import flash_attention_gb300 as fa
+
+    rng = np.random.default_rng(31)
+    Hk, ps, d, block, B = 8, 16, 128, 4, 3
+    lengths = [200, 33, 130]
+    table, P = plain.make_table(rng, B, 13)
+    small = fa.make_q8_cache(P, Hk, ps, d, block)
+    big_pages = (1 << 32) // (Hk * ps * d) + P
+    big = (*(torch.empty((big_pages, Hk, ps, d), dtype=torch.uint8, device="cuda")
+             .view(torch.float8_e4m3fn) for _ in range(2)),
+           *(torch.empty((big_pages, Hk, ps // block), device="cuda") for _ in range(2)))
+    off = big_pages - P
+    cu = np.concatenate([[0], np.cumsum(lengths)])
+    x = [bf16(rng.standard_normal((Hk, cu[-1], d)))[0] for _ in range(2)]
+    q = bf16(rng.standard_normal((B, 16, 1, d)))[0]
+    got = []
+    for cache, t in ((small, table), (big, table + off)):
+        fa.q8_cache_write(*x, *cache, ints(t), ints(lengths), cu_seqlens=ints(cu))
+        got.append((*fa.q8_cache_read(*cache, ints(t), ints(cu), int(cu[-1])),
+                    *fa.q8_paged_attention(q, *cache, ints(t), ints(lengths), scale=0.1)))
+    assert fa.fa_device_status(True) == fa.FA_OK
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def test_attention_waits_that_run_out_are_reported():
+    """With a limit of 1 ns the kernel's ordinary waits run out: it winds down, the status says so,
+    and with the default limit the same calls are right again."""
+    import flash_attention_gb300 as fa
+
+    cases = [A("long", 2, 8, 2, 1, 128, 16, 16, [5000, 3000]),
+             A("rows16", 3, 16, 2, 2, 64, 16, 16, [500, 100, 1]),
+             A("d256", 2, 4, 2, 3, 256, 32, 8, [700, 300])]
+    for c in cases:
+        _, table, P, cache, q = make_attend(c)
+        got, (qt, q64) = dev_cache(*cache), bf16(q)
+        try:
+            fa.fa_set_wait_limit_ns(1)
+            attend(c, table, got, qt)
+            assert fa.fa_device_status(True) == fa.FA_ERR_DEVICE_TIMEOUT
+        finally:
+            fa.fa_set_wait_limit_ns(0)
+        o, lse = attend(c, table, got, qt)
+        assert fa.fa_device_status(True) == fa.FA_OK
+        check_attend(c, table, cache, q64, o, lse)
 
 
 # ------------------------------------------------------------------- together, and captured
