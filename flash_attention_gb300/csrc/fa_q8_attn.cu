@@ -237,6 +237,46 @@ __device__ __forceinline__ float warp_max(float x) {
   return r;
 }
 
+// The bytes of a word that are e4m3 NaN (0x7F, 0xFF): bit 7 of each.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t x) {
+  return ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+// Rows r0 .. r1 - 1 of a V tile (kKT rows of CH bytes a chunk) become 0. Warp-wide; out of line, as
+// the tiles at the end of a sequence are few.
+template <int HD, int CH>
+__device__ __noinline__ void clear_rows(uint8_t* vt, int r0, int r1, int lane) {
+#pragma unroll 1
+  for (int e = lane; e < (r1 - r0) * (HD / 16); e += 32) {
+    const int r = r0 + e / (HD / 16), x = e % (HD / 16) * 16;
+    *reinterpret_cast<uint4*>(vt + x / CH * (kKT * CH) + r * CH + x % CH) =
+        make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+// NaN codes in the rows r0 .. r1 - 1 of a V tile, keys that some query rows of the block do not see
+// (a weight of 0 would not keep a NaN out of O): the codes become 0, and the key's weight NaN for
+// the query rows q that see it (n0 + r < lim[q]): byte q of the key's row of NP bytes in `pt`.
+template <int HD, int CH, int RL, int NP>
+__device__ __noinline__ void clear_nan(uint8_t* vt, uint8_t* pt, int r0, int r1, int n0,
+                                       const int* lim, int lane) {
+#pragma unroll 1
+  for (int e = lane; e < (r1 - r0) * (HD / 16); e += 32) {
+    const int r = r0 + e / (HD / 16), x = e % (HD / 16) * 16;
+    uint4* at = reinterpret_cast<uint4*>(vt + x / CH * (kKT * CH) + r * CH + x % CH);
+    uint4 v = *at;
+    const uint4 z = make_uint4(nan_bytes(v.x), nan_bytes(v.y), nan_bytes(v.z), nan_bytes(v.w));
+    if (z.x | z.y | z.z | z.w) {
+      v.x &= ~((z.x >> 7) * 0xffu);
+      v.y &= ~((z.y >> 7) * 0xffu);
+      v.z &= ~((z.z >> 7) * 0xffu);
+      v.w &= ~((z.w >> 7) * 0xffu);
+      *at = v;
+#pragma unroll 1
+      for (int q = 0; q < RL; ++q)
+        if (n0 + r < lim[q]) pt[r * NP + swz<NP>(0, r) * 16 + q] = 0x7f;
+    }
+  }
+}
+
 struct Q8K {
   const __nv_bfloat16* q;  // [B, H, lq, HD]
   const float* k_scale;
@@ -248,7 +288,7 @@ struct Q8K {
   float* o_part;   // [2 * grid, R, HD]: O of a share, in units of 2^m
   float* ml_part;  // [2 * grid, 2, R]: m and the sum
   int* status;
-  int B, H, Hk, G, lq, rows, rb, max_pages, num_pages, ps_shift, sb_shift, causal;
+  int B, H, Hk, G, lq, rows, rb, max_pages, num_pages, ps_shift, sb_shift;
   float scale_log2;
   unsigned long long wait_limit_ns;
 };
@@ -321,6 +361,7 @@ struct Walk {
     cost = q8_cost(p, b);
   }
 
+  template <bool MULTI>
   __device__ __forceinline__ bool next(const Q8K& p, int R) {
     const unsigned U = (unsigned)(p.Hk * p.rb);
     int je;
@@ -350,7 +391,7 @@ struct Walk {
     whole = first && je == cost - kUnitCost;
     // keys that any row of the block sees
     jb = je;
-    if (p.causal && p.lq > 1) {
+    if (MULTI) {
       const int r0 = rb * R, r1 = min(p.rows, r0 + R) - 1;
       const int imax = r0 / p.lq == r1 / p.lq ? r1 % p.lq : p.lq - 1;
       const int seen = max(0, len - p.lq + imax + 1);
@@ -384,7 +425,8 @@ __device__ __forceinline__ bool take_unit(UnitRing* ring, int un, Unit& u, bool&
 
 // RL: the rows of a unit that there can be (of the R that a tile has columns for): the softmax's
 // arithmetic runs on these alone.
-template <int HD, int R, int RL>
+// MULTI: several new positions under the causal rule, so that the rows of a block see different keys.
+template <int HD, int R, int RL, bool MULTI>
 __global__ void __launch_bounds__(Q8Layout<HD, R, RL>::THREADS, Q8Layout<HD, R, RL>::CTAS)
     q8_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
                    const Q8K p) {
@@ -593,14 +635,12 @@ __global__ void __launch_bounds__(Q8Layout<HD, R, RL>::THREADS, Q8Layout<HD, R, 
              wait_warp(&p_full[buf], (g >> 1) & 1, &wctl);
         if (!ok) break;
         uint8_t* vt = smem + LY::OFF_V + st * LY::KV_BYTES;
-        if (n0 + kKT > w.len) {  // rows behind the sequence's end
-          const int r0 = w.len - n0;
-#pragma unroll 1
-          for (int e = lane; e < (kKT - r0) * (HD / 16); e += 32) {
-            const int r = r0 + e / (HD / 16), x = e % (HD / 16);
-            *reinterpret_cast<uint4*>(vt + x * 16 / CH * (kKT * CH) + r * CH + x * 16 % CH) =
-                make_uint4(0u, 0u, 0u, 0u);
-          }
+        if (n0 + kKT > w.len - (MULTI ? p.lq - 1 : 0)) {
+          const int tail = min(w.len - n0, kKT), hidden = max(w.len - p.lq + 1 - n0, 0);
+          if (MULTI && hidden < tail)
+            clear_nan<HD, CH, RL, NP>(vt, smem + LY::OFF_P + buf * LY::P_BYTES, hidden, tail, n0,
+                                      lim_s[un & 1], lane);
+          if (tail < kKT) clear_rows<HD, CH>(vt, tail, kKT, lane);  // behind the sequence's end
           fence_proxy_async();
           __syncwarp();
         }
@@ -658,8 +698,8 @@ __global__ void __launch_bounds__(Q8Layout<HD, R, RL>::THREADS, Q8Layout<HD, R, 
                      : make_uint4(0u, 0u, 0u, 0u);
         };
         if (lane < R) {
-          const int i = p.lq == 1 ? 0 : (r0 + lane) % p.lq;
-          lim_s[qb][lane] = min(p.causal ? max(0, len - p.lq + i + 1) : len, jb * kKT);
+          const int i = MULTI ? (r0 + lane) % p.lq : 0;
+          lim_s[qb][lane] = min(MULTI ? max(0, len - p.lq + i + 1) : len, jb * kKT);
         }
         uint4 x = load(0), x1 = QSTEPS > 1 ? load(1) : x;
 #pragma unroll 1
@@ -709,7 +749,7 @@ __global__ void __launch_bounds__(Q8Layout<HD, R, RL>::THREADS, Q8Layout<HD, R, 
         if (published >= kUnits)
           ok = wait_warp(&units.free[slot], (published / kUnits - 1) & 1, &wctl);
         if (!ok) break;
-        ended = !w.next(p, R);
+        ended = !w.template next<MULTI>(p, R);
         if (lane == 0) {
           units.at[slot][0] = make_int4(w.b, w.kh, w.rb, w.ja);
           units.at[slot][1] = make_int4(w.jb, w.len, ended ? -1 : w.whole | w.first << 1, 0);
@@ -792,7 +832,7 @@ __global__ void __launch_bounds__(Q8Layout<HD, R, RL>::THREADS, Q8Layout<HD, R, 
       if (softmax_any(wg, !ok) || end) break;
       const int r0 = w.rb * R + row0, live = min(RW, p.rows - r0);
       // tiles below lim_min need no test of the keys
-      const int lim_min = min(p.causal ? max(0, w.len - p.lq + 1) : w.len, w.jb * kKT);
+      const int lim_min = min(MULTI ? max(0, w.len - p.lq + 1) : w.len, w.jb * kKT);
       float l[RW];
 #pragma unroll
       for (int r = 0; r < RW; ++r) l[r] = 0.0f;
@@ -825,7 +865,7 @@ __global__ void __launch_bounds__(Q8Layout<HD, R, RL>::THREADS, Q8Layout<HD, R, 
         if (j * kKT + kKT > lim_min) {
 #pragma unroll
           for (int r = 0; r < RW; ++r)
-            if (j * kKT + key >= lim_s[qb][row0 + r]) t[r] = -INFINITY;
+            if (j * kKT + key >= (MULTI ? lim_s[qb][row0 + r] : lim_min)) t[r] = -INFINITY;
         }
         float top = t[0];
 #pragma unroll
@@ -1119,11 +1159,11 @@ Plan make_plan(const Q8AttnArgs& a) {
   return pl;
 }
 
-template <int HD, int R, int RL>
-cudaError_t attn_t(const Q8AttnArgs& a, const Q8AttnMaps& m, const Plan& pl, void* ws,
+template <int HD, int R, int RL, bool MULTI>
+cudaError_t attn_m(const Q8AttnArgs& a, const Q8AttnMaps& m, const Plan& pl, void* ws,
                    cudaStream_t s) {
   using LY = Q8Layout<HD, R, RL>;
-  auto kern = q8_attn_kernel<HD, R, RL>;
+  auto kern = q8_attn_kernel<HD, R, RL, MULTI>;
   static OncePerKey<> smem_attr;
   cudaError_t e = set_smem_once(smem_attr, kern, LY::SMEM_BYTES);
   if (e != cudaSuccess) return e;
@@ -1149,7 +1189,6 @@ cudaError_t attn_t(const Q8AttnArgs& a, const Q8AttnMaps& m, const Plan& pl, voi
   p.num_pages = a.num_pages;
   p.ps_shift = a.ps_shift;
   p.sb_shift = a.sb_shift;
-  p.causal = a.causal;
   p.scale_log2 = a.scale * kLog2e;
   p.wait_limit_ns = a.wait_limit_ns;
   profile_mark(kKernQ8Attn, 0, s);
@@ -1164,6 +1203,13 @@ cudaError_t attn_t(const Q8AttnArgs& a, const Q8AttnMaps& m, const Plan& pl, voi
                  dim3((unsigned)(32 * (rows < 8 ? rows : 8))), 0, s, p, pl.grid);
   profile_mark(kKernQ8Combine, 1, s);
   return e;
+}
+
+template <int HD, int R, int RL>
+cudaError_t attn_t(const Q8AttnArgs& a, const Q8AttnMaps& m, const Plan& pl, void* ws,
+                   cudaStream_t s) {
+  return a.causal && a.lq > 1 ? attn_m<HD, R, RL, true>(a, m, pl, ws, s)
+                              : attn_m<HD, R, RL, false>(a, m, pl, ws, s);
 }
 
 template <int HD>

@@ -427,7 +427,8 @@ int fa_q8_cache_read(const fa_q8_cache* cache, const fa_q8_rows* rows, void* str
 /* fa_paged_attention over the 8-bit cache: same q, block_table, lengths, o, lse, params and
  * checks (p's n_kv_heads, head_dim, page_size and num_pages must equal the cache's, num_splits
  * must be 0). Sums and softmax statistics are f32. A query row with an element that is not finite
- * gives NaN. At most 2^30 tiles of work: batch * n_kv_heads * ceil(max_pages * page_size / 128),
+ * gives NaN; a NaN code reaches the rows that see its key and no others (in a value of the last
+ * q_len - 1 keys it makes all of such a row NaN, elsewhere its own column). At most 2^30 tiles of work: batch * n_kv_heads * ceil(max_pages * page_size / 128),
  * times ceil((n_heads / n_kv_heads) * q_len / 16), or FA_ERR_INVALID. */
 int fa_q8_paged_attention(const void* q, const fa_q8_cache* cache, const int32_t* block_table,
                           const int32_t* lengths, void* o, float* lse, const fa_paged_params* p,

@@ -490,6 +490,33 @@ def test_attention_nan_stays_in_its_rows():
     assert torch.equal(o.isnan(), hit) and torch.equal(lse, l0)
 
 
+@pytest.mark.parametrize("d,H,lq", [(128, 8, 3), (64, 2, 5), (256, 8, 4)])
+def test_attention_nan_behind_a_row_does_not_reach_it(d, H, lq):
+    """NaN in keys and values that only the later of the new positions see."""
+    import torch
+
+    c = A("hidden", 2, H, 2, lq, d, 16, 16, [300, 129])
+    _, table, P, cache, q = make_attend(c)
+    qt, _ = bf16(q)
+    o0, l0 = attend(c, table, dev_cache(*cache), qt)
+    for which in (0, 1):
+        bad = [x.copy() for x in cache]
+        for b, n in enumerate(c["lengths"]):  # the last position, and the one two before it
+            bad[which][table[b, (n - 1) // 16], 1, (n - 1) % 16, 5] = 0x7F
+            bad[which][table[b, (n - 3) // 16], 0, (n - 3) % 16, 9:12] = 0xFF
+        o, lse = attend(c, table, dev_cache(*bad), qt)
+        sees = torch.zeros(2, H, lq, dtype=torch.bool, device="cuda")
+        sees[:, H // 2:, lq - 1] = True
+        sees[:, :H // 2, lq - 3:] = True
+        assert torch.equal(o[~sees], o0[~sees]) and torch.equal(lse[~sees], l0[~sees])
+        if which == 0:
+            assert o[sees].isnan().all() and lse[sees].isnan().all()
+        else:
+            assert torch.equal(lse, l0)
+            assert o[:, H // 2:, lq - 1, 5].isnan().all()
+            assert o[:, :H // 2, lq - 3:, 9:12].isnan().all()
+
+
 def test_attention_is_bitwise_reproducible():
     import torch
 
