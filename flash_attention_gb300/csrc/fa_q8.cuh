@@ -45,7 +45,8 @@ __host__ __device__ inline long long q8_unit_slots(long long total, int batch, i
 // start(b) / unit + 2 b <= slot, found 32 candidates at a time. `start` reads the offset of a
 // sequence's first row; whatever it returns, the answer lies in [0, batch).
 template <class F>
-__device__ __forceinline__ int q8_slot_owner(long long slot, int batch, int unit, int lane, F start) {
+__device__ __forceinline__ int q8_slot_owner(long long slot, int batch, int unit, int lane,
+                                             F start) {
   int lo = 0, n = batch;  // the answer is in [lo, lo + n)
   while (n > 1) {
     const int step = (n + 31) / 32;

@@ -19,21 +19,29 @@
 //    small weights beside a key that takes nearly all still count (with the pieces unscaled the
 //    steps are 2^-27, and a case like that was off by 1.3 times its tolerance).
 // S^T = K q^T has the keys as the M = 128 rows of a tile and R query rows as 2 R columns: a thread
-// owns a key, whose two scales are then the thread's constants, and sees the R scores of it.
+// owns a key, whose two scales are then the thread's constants, and holds its scores.
 // O^T = V^T w^T has the head dim as M (V is read transposed, MN-major) and 3 R columns; the value
 // scale is part of the weight: w = exp2(score + log2(v_scale) - m), m the running maximum of that
-// sum less 11, so that neither the weights nor O lose range whatever the
-// scales are; the softmax's sum takes w / v_scale.
+// sum less 11, so that neither the weights nor O lose range whatever the scales are; the softmax's
+// sum takes w / v_scale. All sums are f32.
 //
 // Work: the (sequence, kv head, block of R rows) units, each ceil(len / 128) key tiles, form one
-// list of tiles, cut evenly over persistent CTAs (the lengths are on the device; each CTA finds
-// its part from them). A unit counts kUnitCost tiles more than it has, what its start and end cost. A CTA writes the units it has whole; of the others it leaves its share's
-// O, m and sum, which a second kernel joins in the order of the keys.
+// list of tiles, cut evenly over persistent CTAs (the lengths are on the device; each CTA finds its
+// part from them). A unit counts kUnitCost tiles more than it has, what its start and end cost. A
+// CTA writes the units it has whole; of the others it leaves its share's O, m and sum, which a
+// second kernel joins in the order of the keys.
 //
 // Warps of a CTA: one or two softmax warpgroups of 8 rows (thread = key of the tile, and head-dim
 // row of O^T), then one warp each for the TMA copies of K and V pages (boxes of min(page_size, 128)
-// rows), for issuing S^T, for O^T (it zeroes what a last page holds behind the sequence's end, so
-// that NaN there meets no weight), and for the list: it walks it, splits q and fetches the scales. All waits on barriers are bounded.
+// rows), for issuing S^T, for O^T (it also clears what must not meet a weight: rows behind the
+// sequence's end, NaN behind a query row), and for the list: it walks it, splits q and fetches the
+// scales. All waits on barriers are bounded.
+//
+// Measured (device time of a call with both kernels): 64 sequences of 1k to 16k keys, head_dim 128,
+// 32:8 heads, 963 MB: 149 us, 95 % of the measured copy rate (6787 GB/s); 16 sequences of 2k to 16k
+// keys, 351 MB: 63 us (82 %), the start, the joining kernel and the last CTAs being the rest; with
+// 16 rows a kv head 69 us for 322 MB, bound by the softmax's latency and issue; 128 sequences of up
+// to 2047 keys at head_dim 64, 132 MB: 37 us, bound by instructions.
 #include <float.h>
 
 #include <algorithm>
@@ -46,8 +54,8 @@ namespace fa {
 
 namespace {
 constexpr int kKT = 128;          // keys of a tile (the MMA M of S^T)
-// Tiles' worth of a unit's start and end (128 sequences of up to 2k keys, head_dim 64: 51 us with 0,
-// 40 with 2, 37 with 4; long sequences do not tell).
+// Tiles' worth of a unit's start and end (128 sequences of up to 2k keys, head_dim 64: 51 us with
+// 0, 40 with 2, 37 with 4; long sequences do not tell).
 constexpr int kUnitCost = 4;
 constexpr int kPageChunk = 128;   // block-table entries staged at a time
 constexpr float kLog2e = 1.4426950408889634f;
@@ -192,11 +200,11 @@ __device__ __forceinline__ bool softmax_any(int wg, bool v) {
   return r != 0;
 }
 // Bounded waits of this kernel. A first poll in line (suspended for as long as the hardware likes);
-// what follows is out of line, with polls suspended for up to 20 us. (8 warps a CTA, most of which
-// wait most of the time: short polls were the larger part of all instructions, and share the SM's
-// instruction cache with the softmax.) Under a limit below 100 us, which exists to make waits run
-// out, those polls are not suspended, and S^T's wait for a unit's q, which always lasts a while at
-// the start, begins with one that is not (elsewhere that costs 2 %).
+// what follows is out of line, with polls suspended for up to 20 us. (Most warps wait most of the
+// time; short polls in line cost issue and the SM's instruction cache, which the softmax needs.)
+// Under a limit below 100 us, which exists to make waits run out, those polls are not suspended,
+// and S^T's wait for a unit's q, which always lasts a while at the start, begins with one that is
+// not (elsewhere that costs 2 %).
 __device__ __noinline__ bool wait_more(uint64_t* bar, uint32_t parity, WaitCtl* w) {
   const uint64_t t0 = globaltimer();
   const bool brief = w->limit_ns < 100000ull;
@@ -316,8 +324,8 @@ __device__ __forceinline__ unsigned q8_share(unsigned all, unsigned grid) {
   return (all + grid - 1) / grid;
 }
 
-// The units of a CTA's share [t, t1) of the list, in order: the last warp walks it and publishes the
-// units in shared memory, where the other roles take them from.
+// The units of a CTA's share [t, t1) of the list, in order: the last warp walks it and publishes
+// the units in shared memory, where the other roles take them from.
 struct Walk {
   unsigned t, t1;    // next place in the list, end of the share
   unsigned pre;      // the list before sequence b
@@ -425,7 +433,7 @@ __device__ __forceinline__ bool take_unit(UnitRing* ring, int un, Unit& u, bool&
 
 // RL: the rows of a unit that there can be (of the R that a tile has columns for): the softmax's
 // arithmetic runs on these alone.
-// MULTI: several new positions under the causal rule, so that the rows of a block see different keys.
+// MULTI: several new positions under the causal rule: the rows of a block see different keys.
 template <int HD, int R, int RL, bool MULTI>
 __global__ void __launch_bounds__(Q8Layout<HD, R, RL>::THREADS, Q8Layout<HD, R, RL>::CTAS)
     q8_attn_kernel(const __grid_constant__ CUtensorMap mK, const __grid_constant__ CUtensorMap mV,
@@ -445,8 +453,8 @@ __global__ void __launch_bounds__(Q8Layout<HD, R, RL>::THREADS, Q8Layout<HD, R, 
   __shared__ int bad_input;
   __shared__ int page_s[kPageChunk];
   __shared__ __align__(16) float sc_s[2][2][kKT];  // key scale, log2 of the value scale
-  __shared__ __align__(16) float qs_s[2][R];   // rows: score factor, key limit
-  __shared__ __align__(16) int lim_s[2][R];
+  __shared__ __align__(16) float qs_s[2][R];       // rows: score factor
+  __shared__ __align__(16) int lim_s[2][R];        // and the keys they see: those below it
   __shared__ __align__(16) float nm_s[2][R], red_s[4][R];  // -m; maxima or sums of the warps
   __shared__ __align__(16) float up_s[R], f_s[R];  // how far m moves, and O's factors then
 
@@ -513,7 +521,7 @@ __global__ void __launch_bounds__(Q8Layout<HD, R, RL>::THREADS, Q8Layout<HD, R, 
     const int z_oob = p.num_pages * p.Hk;       // a page past the cache: zero fill
     const int sub = lane / KCH, c = lane % KCH; // this lane's box
     int g = 0, gk = 0, gv = 0;                  // tiles, and copies of K and V, so far
-    int page_b = -1, page_lo = 0;               // page_s holds entries page_lo .. of sequence page_b
+    int page_b = -1, page_lo = 0;               // page_s: entries page_lo .. of sequence page_b
     Unit w;
     bool ok = true, end = false;
 #pragma unroll 1
@@ -791,7 +799,7 @@ __global__ void __launch_bounds__(Q8Layout<HD, R, RL>::THREADS, Q8Layout<HD, R, 
             if (lane == 0) mbar_arrive(&s_full[buf]);
           }
           const int key = (j + h + 2) * kKT + lane * 4;
-          const bool have = page[h] >= 0 && page[h] < p.num_pages;  // (else a key of zeros, or none)
+          const bool have = page[h] >= 0 && page[h] < p.num_pages;  // (else zeros, or no key)
           const size_t at = (size_t)(unsigned)page[h] * page_scales +
                             (head_scales + ((key & ps_mask) >> p.sb_shift));
           ks[h][0] = have ? __ldg(p.k_scale + at) : 0.0f;
@@ -812,10 +820,10 @@ __global__ void __launch_bounds__(Q8Layout<HD, R, RL>::THREADS, Q8Layout<HD, R, 
   } else {
     // ------------------------------------------------------------------ softmax, and O out.
     // A warpgroup has the rows row0 .. row0 + 7 of the block (RW of them at most; with 16 rows two
-    // groups share the latency of a tile: one group of 16 took 69 us for four new positions of 16
-    // sequences). Rows that are not there (live of the RW are) have the score factor 0, and columns of q, S, w
-    // and O that hold anything (NaN too) and are never used. A wait that runs out shows at the
-    // next softmax_any, where all threads leave together.
+    // groups share the latency of a tile: 46 us for a chunk of 32 positions, 49 with one group of
+    // 16 rows). Rows that are not there (live of the RW are) have columns of q, S, w and O that
+    // hold anything (NaN too) and are never used. A wait that runs out shows at the next
+    // softmax_any, where all threads leave together.
     constexpr int RW = RL < 8 ? RL : 8;
     const int wg = LY::NWG == 1 ? 0 : warp >> 2, wl = warp & 3, row0 = wg * 8;
     const int key = threadIdx.x & 127;  // key of the tile
@@ -884,7 +892,8 @@ __global__ void __launch_bounds__(Q8Layout<HD, R, RL>::THREADS, Q8Layout<HD, R, 
           }
           if (key < RW) {
             const int r = row0 + key;
-            const float mx = fmaxf(fmaxf(red_s[0][r], red_s[1][r]), fmaxf(red_s[2][r], red_s[3][r]));
+            const float mx =
+                fmaxf(fmaxf(red_s[0][r], red_s[1][r]), fmaxf(red_s[2][r], red_s[3][r]));
             float up = mx - kTop;
             if (first ? mx == -INFINITY : !(up > 0.0f)) up = 0.0f;
             nm_s[qb][r] = first ? -up : nm_s[qb][r] - up;
@@ -1034,7 +1043,8 @@ __global__ void __launch_bounds__(Q8Layout<HD, R, RL>::THREADS, Q8Layout<HD, R, 
 // Joins the shares of the units that were cut, and writes those of sequences without keys: a warp
 // for each row, a CTA for (up to) 8 rows of a unit. Launched early: what it needs to know of the
 // lengths it works out while the attention still runs. Then only latency counts (a few KB): a lane
-// reads one share's m and sum, and the first shares' O is on its way before their weights are known.
+// reads one share's m and sum, and the first shares' O is on its way before their weights are
+// known.
 template <int HD, int R>
 __global__ void __launch_bounds__(256) q8_combine_kernel(const Q8K p, int grid) {
   const int warp = warp_id(), lane = lane_id();
@@ -1144,8 +1154,8 @@ struct Plan {
 
 // Rows of a unit: the smallest block that holds the G * q_len rows of a kv head, 16 at most; more
 // rows take further passes over the keys, from L2 (blocks of 32, with one CTA an SM: 83 us against
-// 74 for 128 rows a kv head). Grid: every CTA slot of the GPU, or one CTA
-// for each tile there can be.
+// 74 for 128 rows a kv head). Grid: every CTA slot of the GPU, or one CTA for each tile there can
+// be.
 Plan make_plan(const Q8AttnArgs& a) {
   Plan pl;
   const int rows = a.G * a.lq;

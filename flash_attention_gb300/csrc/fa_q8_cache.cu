@@ -68,8 +68,8 @@ __device__ __forceinline__ bool seq_rows(const Q8RowsK& p, int b, int& start, in
 // Pages of a warp's `rows` rows from position p0 on: lane i holds that of entry
 // (p0 >> ps_shift) + i, -1 where the table names none of the cache. Entries whose positions all
 // lie outside [from, end) are not read.
-__device__ __forceinline__ int lane_page(const Q8RowsK& p, int b, int p0, int rows, int from, int end,
-                                         int lane, bool& bad) {
+__device__ __forceinline__ int lane_page(const Q8RowsK& p, int b, int p0, int rows, int from,
+                                         int end, int lane, bool& bad) {
   const int entry = (p0 >> p.ps_shift) + lane;
   if (lane > (rows - 1) >> p.ps_shift || (long long)entry << p.ps_shift >= end ||
       (long long)(entry + 1) << p.ps_shift <= from)
@@ -186,7 +186,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1)
 #pragma unroll
   for (int t = 0; t < kSteps; ++t) {
     const int pos = p0 + t * RL::RPS + r;
-    const int pg = __shfl_sync(0xffffffffu, lane_pg, ONE ? 0 : (pos >> p.ps_shift) - (p0 >> p.ps_shift));
+    const int pg =
+        __shfl_sync(0xffffffffu, lane_pg, ONE ? 0 : (pos >> p.ps_shift) - (p0 >> p.ps_shift));
     page[ONE ? 0 : t] = pg;
     isnew |= (uint32_t)(live && pos >= lo && pos < len) << t;
     look |= (uint32_t)(live && pos < len && (pos | (sb - 1)) >= lo && pg >= 0) << t;
@@ -214,7 +215,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1)
 #pragma unroll
       for (int t = 0; t < kSteps; ++t) {
         x[t] = make_uint4(0u, 0u, 0u, 0u);
-        if (on && (isnew >> t & 1)) x[t] = __ldg(reinterpret_cast<const uint4*>(src + t * row_step));
+        if (on && (isnew >> t & 1))
+          x[t] = __ldg(reinterpret_cast<const uint4*>(src + t * row_step));
       }
     }
     uint32_t odd = 0;
@@ -284,7 +286,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1)
         for (int t = g * SPB; t < (g + 1) * SPB; ++t)
           *reinterpret_cast<uint2*>(dst + t * (RL::RPS * HD)) = quantise8(x[t], inv);
         // (a block of several steps begins with the first one's first row)
-        if (col == 0 && (SPB > 1 ? r == 0 : (r & (sb - 1)) == 0) && ((p0 & (sb - 1)) == 0 || SPB < 8))
+        if (col == 0 && (SPB > 1 ? r == 0 : (r & (sb - 1)) == 0) &&
+            ((p0 & (sb - 1)) == 0 || SPB < 8))
           *scale(g * SPB) = s;
       }
       continue;

@@ -366,8 +366,8 @@ int fa_paged_attention_bwd(const void* q, const void* k_cache, const void* v_cac
  * pages.
  *
  * Scales must lie in (0, 2^100] wherever a key is read (value scales below 2^-100, the writer's
- * smallest, are read as 2^-100); what the slots past a sequence's end
- * hold (codes and scales, NaN included) reaches no result. */
+ * smallest, are read as 2^-100); what the slots past a sequence's end hold (codes and scales, NaN
+ * included) reaches no result. */
 typedef struct fa_q8_cache {
   void* k;              /* e4m3 [num_pages, n_kv_heads, page_size, head_dim], 16-byte aligned */
   void* v;              /* same */
@@ -428,8 +428,9 @@ int fa_q8_cache_read(const fa_q8_cache* cache, const fa_q8_rows* rows, void* str
  * checks (p's n_kv_heads, head_dim, page_size and num_pages must equal the cache's, num_splits
  * must be 0). Sums and softmax statistics are f32. A query row with an element that is not finite
  * gives NaN; a NaN code reaches the rows that see its key and no others (in a value of the last
- * q_len - 1 keys it makes all of such a row NaN, elsewhere its own column). At most 2^30 tiles of work: batch * n_kv_heads * ceil(max_pages * page_size / 128),
- * times ceil((n_heads / n_kv_heads) * q_len / 16), or FA_ERR_INVALID. */
+ * q_len - 1 keys it makes all of such a row NaN, elsewhere its own column). FA_ERR_INVALID above
+ * 2^30 tiles of work: batch * n_kv_heads * ceil((n_heads / n_kv_heads) * q_len / 16), times
+ * ceil(max_pages * page_size / 128) + 4. */
 int fa_q8_paged_attention(const void* q, const fa_q8_cache* cache, const int32_t* block_table,
                           const int32_t* lengths, void* o, float* lse, const fa_paged_params* p,
                           void* stream);
