@@ -1,5 +1,6 @@
-// fa_q8_attn.cu -- attention of a few new queries per sequence over the 8-bit paged key/value
-// cache, sm_103a.
+// fa_q8_attn.cu -- attention of new queries over the 8-bit paged key/value cache, sm_103a: the
+// kernel for up to 32 query rows a kv head (at head_dim 256 for any number), the joining kernel and
+// the launches; fa_q8_chunk.cuh has the kernel for more rows.
 //
 // Key j of sequence b is slot j % page_size of page table[b][j / page_size]; its key is
 // k_scale * k codes, its value v_scale * v codes, and query i of the q_len new positions sees key
@@ -287,6 +288,7 @@ __device__ __noinline__ void clear_nan(uint8_t* vt, uint8_t* pt, int r0, int r1,
 
 struct Q8K {
   const __nv_bfloat16* q;  // [B, H, lq, HD]
+  const uint8_t* codes[2];  // K, V (where no tensor map is used)
   const float* k_scale;
   const float* v_scale;
   const int32_t* table;
@@ -1040,6 +1042,14 @@ __global__ void __launch_bounds__(Q8Layout<HD, R, RL>::THREADS, Q8Layout<HD, R, 
   }
 }
 
+}  // namespace
+}  // namespace fa
+
+#include "fa_q8_chunk.cuh"
+
+namespace fa {
+namespace {
+
 // Joins the shares of the units that were cut, and writes those of sequences without keys: a warp
 // for each row, a CTA for (up to) 8 rows of a unit. Launched early: what it needs to know of the
 // lengths it works out while the attention still runs. Then only latency counts (a few KB): a lane
@@ -1065,7 +1075,8 @@ __global__ void __launch_bounds__(256) q8_combine_kernel(const Q8K p, int grid) 
   if (cost == 0 && blockIdx.y == 0) {
     for (int e = threadIdx.x; e < live * HD; e += blockDim.x)
       p.o[unit_row * HD + e] = __float2bfloat16(0.f);
-    if (p.lse && lane < live && warp == 0) p.lse[unit_row + lane] = -INFINITY;
+    if (p.lse)
+      for (int e = threadIdx.x; e < live; e += blockDim.x) p.lse[unit_row + e] = -INFINITY;
   }
   // (by every CTA: what follows this kernel must find the attention done)
   grid_dep_wait();
@@ -1148,21 +1159,28 @@ __global__ void __launch_bounds__(256) q8_combine_kernel(const Q8K p, int grid) 
     p.lse[unit_row + r] = sum == 0.0f ? -INFINITY : fmaf(m + kSumExp, kLn2, logf(sum));
 }
 
+// Rows a kv head from which blocks of 128 rows are taken (head_dim 64 and 128; 256 columns of O
+// would not leave tensor memory for the rest). A tile of 128 keys takes the same time for any
+// number of its rows, and a block of 16 a bit more than a third of it. 16 sequences of 4k to 16k
+// keys, 8 kv heads, head_dim 128, blocks of 16 against one of 128: 32 rows 115 / 142 us, 40 rows
+// 156 / 143, 64 211 / 144, 128 399 / 152, 512 1461 / 550; head_dim 64: 100 / 110, 141 / 111,
+// 184 / 111, 355 / 115, 1369 / 411.
+constexpr int kChunkRows = 33;
+
 struct Plan {
   int R, RL, rb, grid;
 };
 
-// Rows of a unit: the smallest block that holds the G * q_len rows of a kv head, 16 at most; more
-// rows take further passes over the keys, from L2 (blocks of 32, with one CTA an SM: 83 us against
-// 74 for 128 rows a kv head). Grid: every CTA slot of the GPU, or one CTA for each tile there can
-// be.
+// Rows of a unit: the smallest block of 8, 16 or 128 that holds the G * q_len rows of a kv head,
+// but 16 up to 32 rows; more rows take further passes over the keys, from L2. Grid: every CTA slot
+// of the GPU, or one CTA for each tile there can be.
 Plan make_plan(const Q8AttnArgs& a) {
   Plan pl;
   const int rows = a.G * a.lq;
-  pl.R = rows <= 8 ? 8 : 16;
+  pl.R = rows <= 8 ? 8 : rows < kChunkRows || a.d > 128 ? 16 : 128;
   pl.RL = rows <= 2 ? 2 : rows <= 4 ? 4 : pl.R;
   pl.rb = (rows + pl.R - 1) / pl.R;
-  const int ctas = 152 * (a.d > 128 ? 1 : a.d == 64 && pl.RL <= 4 ? 3 : 2);
+  const int ctas = 152 * (a.d > 128 || pl.R > 16 ? 1 : a.d == 64 && pl.RL <= 4 ? 3 : 2);
   const long long cap = (long long)a.max_pages << a.ps_shift;
   const long long tiles = ((cap + kKT - 1) / kKT + kUnitCost) * a.B * a.Hk * pl.rb;
   pl.grid = (int)std::min<long long>(ctas, tiles);
@@ -1172,13 +1190,12 @@ Plan make_plan(const Q8AttnArgs& a) {
 template <int HD, int R, int RL, bool MULTI>
 cudaError_t attn_m(const Q8AttnArgs& a, const Q8AttnMaps& m, const Plan& pl, void* ws,
                    cudaStream_t s) {
-  using LY = Q8Layout<HD, R, RL>;
-  auto kern = q8_attn_kernel<HD, R, RL, MULTI>;
   static OncePerKey<> smem_attr;
-  cudaError_t e = set_smem_once(smem_attr, kern, LY::SMEM_BYTES);
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
   Q8K p;
   p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.codes[0] = a.k;
+  p.codes[1] = a.v;
   p.k_scale = a.k_scale;
   p.v_scale = a.v_scale;
   p.table = a.table;
@@ -1201,8 +1218,19 @@ cudaError_t attn_m(const Q8AttnArgs& a, const Q8AttnMaps& m, const Plan& pl, voi
   p.sb_shift = a.sb_shift;
   p.scale_log2 = a.scale * kLog2e;
   p.wait_limit_ns = a.wait_limit_ns;
-  profile_mark(kKernQ8Attn, 0, s);
-  kern<<<pl.grid, LY::THREADS, LY::SMEM_BYTES, s>>>(m.k, m.v, p);
+  if constexpr (R == 128) {
+    using LY = Q8Chunk<HD>;
+    auto kern = q8_chunk_kernel<HD, MULTI>;
+    if ((e = set_smem_once(smem_attr, kern, LY::SMEM_BYTES)) != cudaSuccess) return e;
+    profile_mark(kKernQ8Attn, 0, s);
+    kern<<<pl.grid, LY::THREADS, LY::SMEM_BYTES, s>>>(p);
+  } else {
+    using LY = Q8Layout<HD, R, RL>;
+    auto kern = q8_attn_kernel<HD, R, RL, MULTI>;
+    if ((e = set_smem_once(smem_attr, kern, LY::SMEM_BYTES)) != cudaSuccess) return e;
+    profile_mark(kKernQ8Attn, 0, s);
+    kern<<<pl.grid, LY::THREADS, LY::SMEM_BYTES, s>>>(m.k, m.v, p);
+  }
   e = cudaGetLastError();
   profile_mark(kKernQ8Attn, 1, s);
   if (e != cudaSuccess) return e;
@@ -1229,8 +1257,11 @@ cudaError_t attn_d(const Q8AttnArgs& a, const Q8AttnMaps& m, const Plan& pl, voi
     case 2: return attn_t<HD, 8, 2>(a, m, pl, ws, s);
     case 4: return attn_t<HD, 8, 4>(a, m, pl, ws, s);
     case 8: return attn_t<HD, 8, 8>(a, m, pl, ws, s);
-    default: return attn_t<HD, 16, 16>(a, m, pl, ws, s);
+    case 16: return attn_t<HD, 16, 16>(a, m, pl, ws, s);
+    default: break;
   }
+  if constexpr (HD <= 128) return attn_t<HD, 128, 128>(a, m, pl, ws, s);
+  return cudaErrorInvalidValue;
 }
 }  // namespace
 
@@ -1239,7 +1270,8 @@ int q8_box_cols(int head_dim) { return head_dim < 128 ? head_dim : 128; }
 
 long long q8_attn_tiles(const Q8AttnArgs& a) {
   const long long cap = (long long)a.max_pages << a.ps_shift;
-  return (long long)a.B * a.Hk * make_plan(a).rb * ((cap + kKT - 1) / kKT + kUnitCost);
+  const int blocks = (a.G * a.lq + 15) / 16;  // (fewer with larger blocks)
+  return (long long)a.B * a.Hk * blocks * ((cap + kKT - 1) / kKT + kUnitCost);
 }
 
 size_t q8_attn_workspace_bytes(const Q8AttnArgs& a) {
