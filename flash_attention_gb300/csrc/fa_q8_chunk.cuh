@@ -262,15 +262,13 @@ __global__ void __launch_bounds__(Q8Chunk<HD>::THREADS, 1) q8_chunk_kernel(const
       const int end_key = min(w.len, w.jb * kKT);
       const unsigned in_page = ((unsigned)w.kh * HD << p.ps_shift) + col;
       const unsigned head_scales = (unsigned)w.kh << nb_shift;
-      auto page_of = [&](int j) {  // of this lane's key of tile j; -1: no key, or no page
+      // The page of this lane's key of tile j (-1: there is no key), not looked at before it is
+      // used: a test here would wait for the load.
+      auto page_of = [&](int j) {
         const int key = j * kKT + row0 + lane;
-        int pg = key < end_key ? table[key >> p.ps_shift] : -1;
-        if (key < end_key && (pg < 0 || pg >= p.num_pages)) {
-          pg = -1;
-          bad_input = 1;
-        }
-        return pg;
+        return key < end_key ? table[key >> p.ps_shift] : -1;
       };
+      auto is_page = [&](int pg) { return (unsigned)pg < (unsigned)p.num_pages; };
       // K and V of the g-th tile, j of the unit, whose pages are pg, into slots 2 g and 2 g + 1
       auto fetch = [&](int g, int j, int pg) {
         const uint32_t dk = raw + 2 * g % LY::SLOTS * (kKT * HD);
@@ -280,17 +278,20 @@ __global__ void __launch_bounds__(Q8Chunk<HD>::THREADS, 1) q8_chunk_kernel(const
           for (int s = 0; s < STEPS; ++s) {
             const int r = s * RPS + rr, page = __shfl_sync(0xffffffffu, pg, r);
             const unsigned in = (unsigned)(j * kKT + row0 + r) & ps_mask;
-            const size_t at = (unsigned)max(page, 0) * page_bytes + (in * HD + in_page);
-            copy16_async(dk + s * 512, p.codes[0] + at, page >= 0);
-            copy16_async(dv + s * 512, p.codes[1] + at, page >= 0);
+            const bool have = is_page(page);  // (else zeros)
+            const size_t at = (have ? (unsigned)page : 0u) * page_bytes + (in * HD + in_page);
+            copy16_async(dk + s * 512, p.codes[0] + at, have);
+            copy16_async(dv + s * 512, p.codes[1] + at, have);
           }
         }
         copies_commit();
       };
       auto scale_of = [&](const float* scales, int j, int pg) {  // (keys that are not there have
-        const int in = (j * kKT + row0 + lane) & ps_mask;        // codes of 0 and no weight)
-        return pg >= 0 ? __ldg(scales + pg * page_scales + (head_scales + (in >> p.sb_shift)))
-                       : 1.0f;
+        const int key = j * kKT + row0 + lane, in = key & ps_mask;  // codes of 0 and no weight)
+        if (is_page(pg))
+          return __ldg(scales + pg * page_scales + (head_scales + (in >> p.sb_shift)));
+        if (key < end_key) bad_input = 1;
+        return 1.0f;
       };
       int pg[LY::AHEAD + 2];  // of tiles j, j + 1, ..
 #pragma unroll
@@ -326,9 +327,11 @@ __global__ void __launch_bounds__(Q8Chunk<HD>::THREADS, 1) q8_chunk_kernel(const
         ks = scale_of(p.k_scale, j + 1, pg[1]);
         vs = scale_of(p.v_scale, j + 1, pg[1]);
         copies_wait<LY::AHEAD - 1>();
+        uint4 x[STEPS];
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s)
-          store(smem + LY::OFF_K + buf * LY::KV_BYTES, s, codes_of(2 * g, s));
+        for (int s = 0; s < STEPS; ++s) x[s] = codes_of(2 * g, s);
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) store(smem + LY::OFF_K + buf * LY::KV_BYTES, s, x[s]);
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&k_full[buf]);
@@ -337,9 +340,8 @@ __global__ void __launch_bounds__(Q8Chunk<HD>::THREADS, 1) q8_chunk_kernel(const
         fetch(g + LY::AHEAD, j + LY::AHEAD, pg[LY::AHEAD]);
         if (g >= 2) ok = wait_warp(&p_done[buf], ((g >> 1) - 1) & 1, &wctl);
         if (!ok) break;
-        uint4 xv[STEPS];
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s) xv[s] = codes_of(2 * g + 1, s);
+        for (int s = 0; s < STEPS; ++s) x[s] = codes_of(2 * g + 1, s);
         unsigned nans = 0;
         if (MULTI && (j + 1) * kKT > w.len - p.lq + 1) {
           // Keys that not every row sees: NaN in a value must meet no weight there, not even 0.
@@ -348,13 +350,13 @@ __global__ void __launch_bounds__(Q8Chunk<HD>::THREADS, 1) q8_chunk_kernel(const
 #pragma unroll
           for (int s = 0; s < STEPS; ++s) {
             const int r = s * RPS + rr;
-            const uint4 z = make_uint4(nan_bytes(xv[s].x), nan_bytes(xv[s].y),
-                                       nan_bytes(xv[s].z), nan_bytes(xv[s].w));
+            const uint4 z = make_uint4(nan_bytes(x[s].x), nan_bytes(x[s].y),
+                                       nan_bytes(x[s].z), nan_bytes(x[s].w));
             if (r >= hidden && (z.x | z.y | z.z | z.w)) {
-              xv[s].x &= ~((z.x >> 7) * 0xffu);
-              xv[s].y &= ~((z.y >> 7) * 0xffu);
-              xv[s].z &= ~((z.z >> 7) * 0xffu);
-              xv[s].w &= ~((z.w >> 7) * 0xffu);
+              x[s].x &= ~((z.x >> 7) * 0xffu);
+              x[s].y &= ~((z.y >> 7) * 0xffu);
+              x[s].z &= ~((z.z >> 7) * 0xffu);
+              x[s].w &= ~((z.w >> 7) * 0xffu);
               nans |= 1u << r;
             }
           }
@@ -362,7 +364,7 @@ __global__ void __launch_bounds__(Q8Chunk<HD>::THREADS, 1) q8_chunk_kernel(const
         }
         if (lane == 0) vn_s[buf][warp - LY::SOFT] = nans;
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s) store(smem + LY::OFF_V + buf * LY::KV_BYTES, s, xv[s]);
+        for (int s = 0; s < STEPS; ++s) store(smem + LY::OFF_V + buf * LY::KV_BYTES, s, x[s]);
 #pragma unroll
         for (int i = 0; i < LY::AHEAD + 1; ++i) pg[i] = pg[i + 1];
         fence_proxy_async();
