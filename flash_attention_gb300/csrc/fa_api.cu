@@ -779,7 +779,7 @@ static int log2_of(int x) {
 }
 
 // Scratch of the 8-bit attention comes from a pool of the library's own on each device that keeps
-// what is freed (a few MB at most): the device's default pool gives memory back whenever the
+// what is freed (20 MB at most for a call): the device's default pool gives memory back whenever the
 // stream has been waited for, and the next call then takes 200 us to get it again, many times
 // what a decoding step's attention runs.
 static cudaError_t scratch_pool(int dev, cudaMemPool_t* out) {

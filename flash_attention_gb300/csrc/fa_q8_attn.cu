@@ -1161,10 +1161,10 @@ __global__ void __launch_bounds__(256) q8_combine_kernel(const Q8K p, int grid) 
 
 // Rows a kv head from which blocks of 128 rows are taken (head_dim 64 and 128; 256 columns of O
 // would not leave tensor memory for the rest). A tile of 128 keys takes the same time for any
-// number of its rows, and a block of 16 a bit more than a third of it. 16 sequences of 4k to 16k
-// keys, 8 kv heads, head_dim 128, blocks of 16 against one of 128: 32 rows 115 / 142 us, 40 rows
-// 156 / 143, 64 211 / 144, 128 399 / 152, 512 1461 / 550; head_dim 64: 100 / 110, 141 / 111,
-// 184 / 111, 355 / 115, 1369 / 411.
+// number of its rows, a block of 16 not half of that. 16 sequences of 4k to 16k keys, 8 kv heads,
+// head_dim 128, blocks of 16 against those of 128: 32 rows 115 / 128 us, 40 rows 156 / 128,
+// 128 rows 399 / 139, 512 rows 1461 / 500; head_dim 64: 100 / 107, 141 / 108, 355 / 112,
+// 1369 / 411.
 constexpr int kChunkRows = 33;
 
 struct Plan {

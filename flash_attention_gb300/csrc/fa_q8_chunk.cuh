@@ -19,9 +19,9 @@
 // What bounds it: the softmax's warps, which wait for little (at head_dim 64 7 % of their time for
 // scores, 3 % at their votes, 5 % for a free half of w): two of them on a scheduler, with their
 // exponentials and the chain from scores to weights; at head_dim 128 the widening's shared-memory
-// traffic too. A tile takes about 3000 cycles at head_dim 64 and 4000 at 128, for any number of
-// its 128 rows: 16 sequences of 4k to 16k keys, 8 kv heads of 128 rows, 168 M scores: 115 us and
-// 152 us. Tried: codes through registers instead of cp.async (they spilled: 410 us for 48 rows at
+// traffic too. A tile takes about 3000 cycles at head_dim 64 and 3600 at 128, for any number of
+// its 128 rows: 16 sequences of 4k to 16k keys, 8 kv heads of 128 rows, 168 M scores: 112 us and
+// 139 us. Tried: codes through registers instead of cp.async (they spilled: 410 us for 48 rows at
 // head_dim 128 where cp.async took 185), scores 32 columns and scales 8 keys at a time (no faster).
 //
 // Warps: 0-7 softmax (two warpgroups, half the keys of a tile each, and half the columns of O),
