@@ -792,10 +792,15 @@ static cudaError_t scratch_pool(int dev, cudaMemPool_t* out) {
     props.location.type = cudaMemLocationTypeDevice;
     props.location.id = dev;
     cudaMemPool_t pool = nullptr;
-    cudaError_t err = cudaMemPoolCreate(&pool, &props);
+    // (no work on any stream: a capture, in which the first call may come, need not end for it)
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaError_t err = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (err != cudaSuccess) return err;
+    err = cudaMemPoolCreate(&pool, &props);
     uint64_t keep = UINT64_MAX;
     if (err == cudaSuccess)
       err = cudaMemPoolSetAttribute(pool, cudaMemPoolAttrReleaseThreshold, &keep);
+    cudaThreadExchangeStreamCaptureMode(&mode);
     if (err == cudaSuccess) pools[dev] = pool;
     return err;
   });

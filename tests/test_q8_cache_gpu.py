@@ -738,3 +738,47 @@ def test_two_streams_at_once():
         for a, b in zip(outs, want):
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     assert fa.fa_device_status(True) == fa.FA_OK
+
+
+FIRST_CALLS = """
+import torch
+import flash_attention_gb300 as fa
+
+B, Hk, d, ps = 2, 2, 128, 16
+table = torch.randperm(80, device="cuda").to(torch.int32).view(B, 40).contiguous()
+lens = torch.tensor([300, 600], device="cuda", dtype=torch.int32)
+cu = torch.tensor([0, 300, 900], device="cuda", dtype=torch.int32)
+x = torch.randn(2, Hk, 900, d, device="cuda").bfloat16()
+q = [torch.randn(B, 8, n, d, device="cuda").bfloat16() for n in (1, 16)]
+cache = fa.make_q8_cache(80, Hk, ps, d)
+
+
+def step():
+    out = []
+    fa.q8_cache_write(x[0], x[1], *cache, table, lens, cu_seqlens=cu)
+    for y in q:
+        out += fa.q8_paged_attention(y, *cache, table, lens, scale=0.1)
+    return out + list(fa.q8_cache_read(*cache, table, cu, 900))
+
+
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = step()
+g.replay()
+torch.cuda.synchronize()
+want = step()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, want)) and fa.fa_device_status(True) == 0
+"""
+
+
+def test_a_process_whose_first_calls_are_captured():
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
