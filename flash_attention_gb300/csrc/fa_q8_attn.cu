@@ -23,8 +23,9 @@
 // owns a key, whose two scales are then the thread's constants, and holds its scores.
 // O^T = V^T w^T has the head dim as M (V is read transposed, MN-major) and 3 R columns; the value
 // scale is part of the weight: w = exp2(score + log2(v_scale) - m), m the running maximum of that
-// sum less 11, so that neither the weights nor O lose range whatever the scales are; the softmax's
-// sum takes w / v_scale. All sums are f32.
+// sum less 11, so that a value counts down to 2^-33 of the row's largest weight times scale; the
+// softmax's sum takes w / v_scale, or, in a tile with a scale 2^-96 of one that came before, an
+// exponential of its own (there w may be 0 where w / v_scale is not). All sums are f32.
 //
 // Work: the (sequence, kv head, block of R rows) units, each ceil(len / 128) key tiles, form one
 // list of tiles, cut evenly over persistent CTAs (the lengths are on the device; each CTA finds its
@@ -65,8 +66,13 @@ constexpr float kLn2 = 0.6931471805599453f;
 // 2^kMost (where f16 would not hold 8 times what the first piece leaves).
 constexpr float kTop = 11.0f, kMost = 15.0f;
 // The softmax's sums are held in units of 2^16: with value scales from 2^-100 to 2^100 neither
-// w / v_scale nor 2^22 of them leave f32.
+// w / v_scale nor 2^22 of them leave f32, and a row's sum is 2^-105 at least (its m less its largest
+// score is at most 100 - 11). A factor between two m's may be any, so sums are scaled by its root
+// twice (scale_sum).
 constexpr float kSumExp = 16.0f, kSumUnit = 65536.0f;
+// Value scales of a unit's keys (log2) may be this far below the largest up to their tile for
+// w / v_scale to serve: a w below f32 (2^-126) is then that of a score 2^-41 of the largest one's.
+constexpr float kApart = 96.0f;
 
 // R query rows of a unit at a time. KST, VST: stages of the K and V rings; V has more, as a V tile
 // stays until the weights of its keys are there (3 and 3 of 16 KB: 167 us, 2 and 4: 162 us for 64
@@ -150,6 +156,17 @@ __device__ __forceinline__ float lg2(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// 2^x, subnormal results included.
+__device__ __forceinline__ float ex2_full(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// A sum times 2^-up, also where 2^-up is below f32 and the product is not.
+__device__ __forceinline__ float scale_sum(float sum, float up) {
+  const float root = ex2(-0.5f * up);
+  return sum * root * root;
 }
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
@@ -455,6 +472,9 @@ __global__ void __launch_bounds__(Q8Layout<HD, R, RL>::THREADS, Q8Layout<HD, R, 
   __shared__ int bad_input;
   __shared__ int page_s[kPageChunk];
   __shared__ __align__(16) float sc_s[2][2][kKT];  // key scale, log2 of the value scale
+  // One of a tile's value scales is kApart below another. Read after s_free, so four tiles deep: when
+  // the scores of two tiles before are read, the weights of three before are done.
+  __shared__ int apart_s[4];
   __shared__ __align__(16) float qs_s[2][R];       // rows: score factor
   __shared__ __align__(16) int lim_s[2][R];        // and the keys they see: those below it
   __shared__ __align__(16) float nm_s[2][R], red_s[4][R];  // -m; maxima or sums of the warps
@@ -777,6 +797,7 @@ __global__ void __launch_bounds__(Q8Layout<HD, R, RL>::THREADS, Q8Layout<HD, R, 
       const int end_key = min(len, jb * kKT);
       const bool wide = p.sb_shift >= 2;  // the four keys have one scale
       float ks[2][4], vs[2][4];
+      float most = -INFINITY;  // log2 of the unit's largest value scale so far
       int page[2] = {-1, -1};
 #pragma unroll 1
       for (int j = ja - 4; j < jb && ok; j += 2) {
@@ -784,17 +805,23 @@ __global__ void __launch_bounds__(Q8Layout<HD, R, RL>::THREADS, Q8Layout<HD, R, 
         for (int h = 0; h < 2; ++h) {
           if (j + h >= ja && j + h < jb) {
             const int buf = g & 1;
-            if (g >= 2) ok = ok && wait_warp(&s_free[buf], ((g >> 1) - 1) & 1, &wctl);
-            ++g;
             const float least = __int_as_float((kQ8MinExp + 127) << 23);
             float4 k4 = make_float4(ks[h][0], ks[h][0], ks[h][0], ks[h][0]);
             const float l0 = lg2(fmaxf(vs[h][0], least));
             float4 l4 = make_float4(l0, l0, l0, l0);
+            float lo = l0, hi = l0;
             if (!wide) {
               k4 = make_float4(ks[h][0], ks[h][1], ks[h][2], ks[h][3]);
               l4 = make_float4(l0, lg2(fmaxf(vs[h][1], least)), lg2(fmaxf(vs[h][2], least)),
                                lg2(fmaxf(vs[h][3], least)));
+              lo = fminf(fminf(l4.x, l4.y), fminf(l4.z, l4.w));
+              hi = fmaxf(fmaxf(l4.x, l4.y), fmaxf(l4.z, l4.w));
             }
+            most = fmaxf(most, warp_max(hi));
+            const float below = warp_max(-lo) + most;
+            if (g >= 2) ok = ok && wait_warp(&s_free[buf], ((g >> 1) - 1) & 1, &wctl);
+            if (lane == 0) apart_s[g & 3] = below > kApart;
+            ++g;
             *reinterpret_cast<float4*>(&sc_s[buf][0][lane * 4]) = k4;
             *reinterpret_cast<float4*>(&sc_s[buf][1][lane * 4]) = l4;
             __syncwarp();
@@ -910,7 +937,7 @@ __global__ void __launch_bounds__(Q8Layout<HD, R, RL>::THREADS, Q8Layout<HD, R, 
 #pragma unroll
           for (int r = 0; r < RW; ++r) {
             t[r] -= up_s[row0 + r];
-            if (!first) l[r] *= f_s[row0 + r];
+            if (!first) l[r] = scale_sum(l[r], up_s[row0 + r]);
           }
           if (!first) {
 #pragma unroll 1
@@ -928,7 +955,12 @@ __global__ void __launch_bounds__(Q8Layout<HD, R, RL>::THREADS, Q8Layout<HD, R, 
           }
         }
         // weights, their sum, and their pieces into shared memory, a key's row of NP bytes
-        const float inv = ex2(-lsv - kSumExp);  // 1 / value scale, in the sum's unit
+        float inv = ex2(-lsv - kSumExp);  // 1 / value scale, in the sum's unit
+        if (apart_s[g & 3]) {
+          inv = 0.0f;
+#pragma unroll
+          for (int r = 0; r < RW; ++r) l[r] += ex2_full(t[r] - lsv - kSumExp);
+        }
         if (g >= 2) ok = ok && wait_warp(&p_done[buf], ph ^ 1, &wctl);
         uint32_t pc[3][2];
 #pragma unroll
@@ -1124,11 +1156,12 @@ __global__ void __launch_bounds__(256) q8_combine_kernel(const Q8K p, int grid) 
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float f = li == 0.0f ? 0.0f : ex2(mi - top), old = ex2(m - top);
+    float part = scale_sum(li, top - mi);  // (0 stays 0)
+    sum = scale_sum(sum, top - m);
     m = top;
-    float part = li * f;
 #pragma unroll
     for (int o = 16; o > 0; o /= 2) part += __shfl_xor_sync(0xffffffffu, part, o);
-    sum = fmaf(sum, old, part);
+    sum += part;
 #pragma unroll
     for (int e = 0; e < CPL; ++e) acc[e] *= old;
 #pragma unroll 1

@@ -46,7 +46,7 @@ struct Q8Chunk {
   static constexpr int SOFT = 8, CONV = 4, MMA_WARP = 12, LIST_WARP = 13;
   static constexpr int THREADS = 32 * 14;
   static_assert(HD <= 128, "O has 128 columns");
-  static_assert(SMEM_BYTES + 8192 <= 228 * 1024, "shared memory budget");
+  static_assert(SMEM_BYTES + 9216 + 1024 <= 228 * 1024, "shared memory budget");  // (and static)
 };
 
 // kind::f16 with f16 operands, f32 accumulator.
@@ -125,13 +125,18 @@ __global__ void __launch_bounds__(Q8Chunk<HD>::THREADS, 1) q8_chunk_kernel(const
   // when the scores of two tiles before are read, so that the weights of three before are done.
   __shared__ __align__(16) float ks_s[4][kKT];
   __shared__ __align__(16) float lv_s[4][kKT];
-  __shared__ __align__(16) float iv_s[4][kKT];
+  __shared__ __align__(16) float iv_s[5][kKT];  // (the last: zeros)
+  // Largest and least of the value scales' log2 that each of the warps has: of the unit's tiles so
+  // far, of this one.
+  __shared__ __align__(16) float most_s[2][LY::CONV], least_s[2][LY::CONV];
+  __shared__ int iv_at[4];  // where in iv_s the sum of a tile takes its factors
   __shared__ unsigned vn_s[2][kKT / 32];  // keys whose value has a NaN, where some rows see it
   __shared__ float qs_s[R], red_s[2][R];  // rows: score factor; maxima or sums of the two halves
 
   const int warp = warp_id(), lane = lane_id();
   Walk list;
   if (warp == LY::LIST_WARP) list.init(p, blockIdx.x, gridDim.x, lane);
+  if (threadIdx.x < kKT) iv_s[4][threadIdx.x] = 0.0f;
   if (threadIdx.x == 0) {
     wait_ctl_init(&wctl, p.wait_limit_ns);
     bad_input = 0;
@@ -197,7 +202,6 @@ __global__ void __launch_bounds__(Q8Chunk<HD>::THREADS, 1) q8_chunk_kernel(const
       if (!ok) return;
       tc_fence_after();
       if (lane == 0) {
-        mbar_arrive(&s_full[buf]);
         const Desc kb = make_desc(smem_u32(smem + LY::OFF_K + buf * LY::KV_BYTES), 16, 1024);
 #pragma unroll
         for (int ks = 0; ks < HD / 16; ++ks) {
@@ -206,6 +210,13 @@ __global__ void __launch_bounds__(Q8Chunk<HD>::THREADS, 1) q8_chunk_kernel(const
                   ks > 0 ? 1u : 0u);
         }
         mma_commit(&s_full[buf]);
+        // value scales too far apart for w / v_scale: the sum takes exponentials of its own
+        const float4 hi = *reinterpret_cast<const float4*>(most_s[buf]);
+        const float4 lo = *reinterpret_cast<const float4*>(least_s[buf]);
+        const float most = fmaxf(fmaxf(hi.x, hi.y), fmaxf(hi.z, hi.w));
+        const float least = fminf(fminf(lo.x, lo.y), fminf(lo.z, lo.w));
+        iv_at[g & 3] = most - least > kApart ? 4 : g & 3;
+        mbar_arrive(&s_full[buf]);
       }
       __syncwarp();
     };
@@ -293,6 +304,7 @@ __global__ void __launch_bounds__(Q8Chunk<HD>::THREADS, 1) q8_chunk_kernel(const
         if (key < end_key) bad_input = 1;
         return 1.0f;
       };
+      float most = -INFINITY;
       int pg[LY::AHEAD + 2];  // of tiles j, j + 1, ..
 #pragma unroll
       for (int i = 0; i < LY::AHEAD + 1; ++i) pg[i] = page_of(w.ja + i);
@@ -324,6 +336,12 @@ __global__ void __launch_bounds__(Q8Chunk<HD>::THREADS, 1) q8_chunk_kernel(const
         ks_s[g & 3][row0 + lane] = ks;
         lv_s[g & 3][row0 + lane] = l;
         iv_s[g & 3][row0 + lane] = ex2(-l - kSumExp);
+        most = fmaxf(most, warp_max(l));
+        const float least = -warp_max(-l);
+        if (lane == 0) {
+          most_s[buf][warp - LY::SOFT] = most;
+          least_s[buf][warp - LY::SOFT] = least;
+        }
         ks = scale_of(p.k_scale, j + 1, pg[1]);
         vs = scale_of(p.v_scale, j + 1, pg[1]);
         copies_wait<LY::AHEAD - 1>();
@@ -444,6 +462,7 @@ __global__ void __launch_bounds__(Q8Chunk<HD>::THREADS, 1) q8_chunk_kernel(const
         ok = ok && wait_warp(&s_full[buf], ph, &wctl);
         tc_fence_after();
         const bool first = j == w.ja;
+        const int at = iv_at[g & 3];
         const uint64_t nm2 = f2_pack(nm, nm);
         float t[64];
         uint32_t sr[2][16];  // scores of 16 keys, and of the next 16 on their way
@@ -499,7 +518,8 @@ __global__ void __launch_bounds__(Q8Chunk<HD>::THREADS, 1) q8_chunk_kernel(const
 #pragma unroll
           for (int c = 0; c < 64; ++c) t[c] -= up;
           if (!first) {  // O is scaled too, once the last O MMA is done
-            l2 = f2_mul(l2, f2_pack(f, f));
+            const float root = ex2(-0.5f * up);  // (scale_sum)
+            l2 = f2_mul(f2_mul(l2, f2_pack(root, root)), f2_pack(root, root));
             ok = wait_warp(&p_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &wctl);
             tc_fence_after();
 #pragma unroll 1
@@ -515,6 +535,18 @@ __global__ void __launch_bounds__(Q8Chunk<HD>::THREADS, 1) q8_chunk_kernel(const
             tmem_wait_st();
           }
         }
+        if (at == 4) {
+          // (rare, and a loop through local memory: unrolled it made every tile slower)
+          float4 y[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            y[c] = make_float4(t[4 * c], t[4 * c + 1], t[4 * c + 2], t[4 * c + 3]);
+          float x = 0.0f;
+#pragma unroll 1
+          for (int c = 0; c < 64; ++c)
+            x += ex2_full(reinterpret_cast<const float*>(y)[c] - lv_s[g & 3][col0 + c] - kSumExp);
+          l2 = f2_add(l2, f2_pack(x, 0.0f));
+        }
         // weights and their sum; to the tensor cores as f16
         if (g >= 2) ok = ok && wait_warp(&p_done[buf], ph ^ 1, &wctl);
         uint32_t pw[32];
@@ -523,7 +555,7 @@ __global__ void __launch_bounds__(Q8Chunk<HD>::THREADS, 1) q8_chunk_kernel(const
           ulonglong2 i4[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            i4[c] = *reinterpret_cast<const ulonglong2*>(&iv_s[g & 3][col0 + c0 + 4 * c]);
+            i4[c] = *reinterpret_cast<const ulonglong2*>(&iv_s[at][col0 + c0 + 4 * c]);
 #pragma unroll
           for (int c = c0; c < c0 + 16; c += 4) {
             const float a = ex2(t[c]), b = ex2(t[c + 1]), d = ex2(t[c + 2]), e = ex2(t[c + 3]);

@@ -426,7 +426,9 @@ int fa_q8_cache_read(const fa_q8_cache* cache, const fa_q8_rows* rows, void* str
 
 /* fa_paged_attention over the 8-bit cache: same q, block_table, lengths, o, lse, params and
  * checks (p's n_kv_heads, head_dim, page_size and num_pages must equal the cache's, num_splits
- * must be 0). Sums and softmax statistics are f32. A query row with an element that is not finite
+ * must be 0). Sums and softmax statistics are f32. Value scales may differ by any factor: every key
+ * has its share of the softmax's sum, and its value counts in O down to 2^-33 of the row's largest
+ * softmax weight times value scale. A query row with an element that is not finite
  * gives NaN; a NaN code reaches the rows that see its key and no others (in a value of the last
  * q_len - 1 keys it makes all of such a row NaN, elsewhere its own column). FA_ERR_INVALID above
  * 2^30 tiles of work: batch * n_kv_heads * ceil((n_heads / n_kv_heads) * q_len / 16), times
