@@ -192,10 +192,13 @@ __device__ __forceinline__ void load_scores(uint32_t taddr, uint32_t (&s)[16]) {
     }
   }
 }
-// Two weights (>= 0, at most 2^15) -> two f16 rounded to 9 bits (half up).
+// Two weights (>= 0, at most 2^15) -> two f16 rounded to 9 bits: cut to f16's 11, then the nearest
+// of 9 (half up), which together is the nearest of the f32 value. (With f16's own rounding first,
+// one weight in four was a tie and went up: O was 3.4e-4 too large, the sum being of the weights
+// as they are.)
 __device__ __forceinline__ uint32_t weight_f16x2(float lo, float hi) {
   uint32_t h;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
+  asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
   return (h + 0x00020002u) & 0xfffcfffcu;
 }
 // 8 times what their upper bytes (the e5m2 pieces) leave; exact, and below 2^16.
