@@ -706,6 +706,7 @@ __global__ void __launch_bounds__(Q8Layout<HD, R, RL>::THREADS, Q8Layout<HD, R, 
     const int nb_shift = p.ps_shift - p.sb_shift, ps_mask = (1 << p.ps_shift) - 1;
     const unsigned page_scales = (unsigned)p.Hk << nb_shift;  // of a page's heads
     int g = 0, published = 0;
+    uint32_t largest = 0;  // bits of the scales read
     bool ok = true, ended = false;
 #pragma unroll 1
     for (int un = -1; ok; ++un) {  // (-1: nothing but the first unit's publication)
@@ -813,7 +814,12 @@ __global__ void __launch_bounds__(Q8Layout<HD, R, RL>::THREADS, Q8Layout<HD, R, 
             const float l0 = lg2(fmaxf(vs[h][0], least));
             float4 l4 = make_float4(l0, l0, l0, l0);
             float lo = l0, hi = l0;
+            largest = max(largest, max(__float_as_uint(ks[h][0]), __float_as_uint(vs[h][0])));
             if (!wide) {
+#pragma unroll
+              for (int e = 1; e < 4; ++e)
+                largest =
+                    max(largest, max(__float_as_uint(ks[h][e]), __float_as_uint(vs[h][e])));
               k4 = make_float4(ks[h][0], ks[h][1], ks[h][2], ks[h][3]);
               l4 = make_float4(l0, lg2(fmaxf(vs[h][1], least)), lg2(fmaxf(vs[h][2], least)),
                                lg2(fmaxf(vs[h][3], least)));
@@ -849,6 +855,7 @@ __global__ void __launch_bounds__(Q8Layout<HD, R, RL>::THREADS, Q8Layout<HD, R, 
         }
       }
     }
+    if (largest > kQ8MaxScale) bad_input = 1;
   } else {
     // ------------------------------------------------------------------ softmax, and O out.
     // A warpgroup has the rows row0 .. row0 + 7 of the block (RW of them at most; with 16 rows two

@@ -265,6 +265,7 @@ __global__ void __launch_bounds__(Q8Chunk<HD>::THREADS, 1) q8_chunk_kernel(const
     const size_t page_scales = (size_t)p.Hk << nb_shift;
     const uint32_t raw = smem_u32(smem + LY::OFF_C) + (warp - LY::SOFT) * (32 * HD) + lane * 16;
     int g = 0;
+    uint32_t largest = 0;  // bits of the scales read
     Unit w;
     bool ok = true, end = false;
 #pragma unroll 1
@@ -333,6 +334,7 @@ __global__ void __launch_bounds__(Q8Chunk<HD>::THREADS, 1) q8_chunk_kernel(const
         if (g >= 2) ok = wait_warp(&s_free[buf], ((g >> 1) - 1) & 1, &wctl);
         if (!ok) break;
         const float l = lg2(fmaxf(vs, __int_as_float((kQ8MinExp + 127) << 23)));
+        largest = max(largest, max(__float_as_uint(ks), __float_as_uint(vs)));
         ks_s[g & 3][row0 + lane] = ks;
         lv_s[g & 3][row0 + lane] = l;
         iv_s[g & 3][row0 + lane] = ex2(-l - kSumExp);
@@ -391,6 +393,7 @@ __global__ void __launch_bounds__(Q8Chunk<HD>::THREADS, 1) q8_chunk_kernel(const
       }
     }
     copies_wait<0>();
+    if (largest > kQ8MaxScale) bad_input = 1;
   } else {
     // ------------------------------------------------------------------ q, softmax, and O out
     // Rows that are not there have q = 0. A row is two threads', and its 32 rows two warps': these

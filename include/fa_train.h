@@ -82,7 +82,8 @@ typedef struct fa_params {
                                    exists for the requested option */
 #define FA_ERR_TOO_LARGE 5      /* the problem needs more scratch than fa_train_bwd_noalloc has */
 #define FA_ERR_BAD_INPUT 6      /* (fa_device_status) a paged call met a sequence length or a
-                                   block-table entry out of range; those keys were read as 0 */
+                                   block-table entry out of range (those keys were read as 0), or
+                                   a call on the 8-bit cache offsets or scales out of range */
 
 /* Mask element types of fa_options.mask_type. */
 #define FA_MASK_F32 0  /* additive, natural log, float (an entry -inf hides the key) */
@@ -365,9 +366,10 @@ int fa_paged_attention_bwd(const void* q, const void* k_cache, const void* v_cac
  * fa_train_fwd_ex takes them (a long prompt against what is cached). No counterpart on the
  * pages.
  *
- * Scales must lie in (0, 2^100] wherever a key is read (value scales below 2^-100, the writer's
- * smallest, are read as 2^-100); what the slots past a sequence's end hold (codes and scales, NaN
- * included) reaches no result. */
+ * The attention takes scales in [0, 2^100] (value scales below 2^-100, the writer's smallest, are read
+ * as 2^-100); another one where a key is read, as the writer makes of finite values above
+ * 448 * 2^100, makes fa_device_status return FA_ERR_BAD_INPUT. What the slots past a sequence's end
+ * hold (codes and scales, NaN included) reaches no result. */
 typedef struct fa_q8_cache {
   void* k;              /* e4m3 [num_pages, n_kv_heads, page_size, head_dim], 16-byte aligned */
   void* v;              /* same */
@@ -462,8 +464,9 @@ int fa_debug_ex2(const float* x, float* y_poly, float* y_mufu, float* y_ref, int
 int fa_debug_wait_timeout(uint64_t* waited_ns, void* stream);
 
 /* Synchronises the current device, then returns FA_OK, FA_ERR_DEVICE_TIMEOUT if any kernel of
- * this library on it gave up a bounded wait, or FA_ERR_BAD_INPUT if a paged call met a length
- * or block-table entry out of range, since the last call with clear != 0. */
+ * this library on it gave up a bounded wait, or FA_ERR_BAD_INPUT if a paged call met a length,
+ * a block-table entry, or (8-bit cache) an offset or a scale out of range, since the last call with
+ * clear != 0. */
 int fa_device_status(int clear);
 
 /* Human-readable text of a return code (static storage). */

@@ -97,3 +97,58 @@ def test_a_zero_block_before_large_values():
             assert fa.fa_device_status(True) == fa.FA_OK
             assert (o == 2.0 ** 39).all(), o.float().flatten()[:4]
             assert (lse - np.log(n)).abs().max() < 2.0 ** -14
+
+
+# --------------------------------------------------------------------- scales out of range
+@pytest.mark.parametrize("lq,d,block", [(1, 128, 16), (1, 128, 1), (1, 64, 8), (3, 256, 2),
+                                        (4, 128, 1), (20, 64, 16), (20, 128, 1)])
+def test_scales_out_of_range_are_reported(lq, d, block):
+    """The attention admits scales in [0, 2^100]: another one is reported where a key that is read
+    has it, for keys and for values, and nowhere else."""
+    import flash_attention_gb300 as fa
+
+    c = A("range", 2, 4, 2, lq, d, 16, block, [300, 133])
+    _, table, P, cache, q = make_attend(c)
+    qt, _ = bf16(q)
+    nb = 16 // block
+    for which in (2, 3):
+        for value in (2.0 ** 101, np.inf, np.nan, -1.0):
+            for b, pos in ((0, 0), (0, 299), (1, 77)):
+                bad = [x.copy() for x in cache]
+                bad[which][table[b, pos // 16], 1, pos % 16 // block] = value
+                attend(c, table, dev_cache(*bad), qt)
+                assert fa.fa_device_status(True) == fa.FA_ERR_BAD_INPUT, (which, value, b, pos)
+            bad = [x.copy() for x in cache]  # behind the end: 133 keys end in the 9th page
+            first = 133 % 16 // block + 1  # the first block without a key
+            bad[which][table[1, 8], :, first:nb] = value
+            bad[which][np.setdiff1d(np.arange(P), np.concatenate(
+                [table[0, :19], table[1, :9]]))] = value
+            attend(c, table, dev_cache(*bad), qt)
+            assert fa.fa_device_status(True) == fa.FA_OK, (which, value)
+    edge = [x.copy() for x in cache]
+    edge[2][:, :, 0], edge[3][:, :, 0] = 0.0, 0.0
+    attend(c, table, dev_cache(*edge), qt)
+    edge[3][:, :, 0] = 2.0 ** 100
+    attend(c, table, dev_cache(*edge), qt)
+    assert fa.fa_device_status(True) == fa.FA_OK
+
+
+def test_values_that_the_attention_does_not_admit():
+    """The writer takes any finite value (up to a scale of 2^120); the attention over it says so."""
+    import torch
+
+    import flash_attention_gb300 as fa
+
+    for size, status in ((5e32, fa.FA_OK), (6e32, fa.FA_ERR_BAD_INPUT),
+                         (3e38, fa.FA_ERR_BAD_INPUT)):
+        for which in (0, 1):
+            for lq in (1, 40):
+                cache = fa.make_q8_cache(2, 1, 16, 64)
+                x = [torch.ones(1, 1, 5, 64, dtype=torch.bfloat16, device="cuda")
+                     for _ in range(2)]
+                x[which][0, 0, 3, 7] = size
+                fa.q8_cache_write(*x, *cache, ints([[1]]), ints([5]))
+                assert fa.fa_device_status(True) == fa.FA_OK
+                q = torch.zeros(1, 1, lq, 64, dtype=torch.bfloat16, device="cuda")
+                fa.q8_paged_attention(q, *cache, ints([[1]]), ints([5]), scale=1.0)
+                assert fa.fa_device_status(True) == status, (size, which, lq)
