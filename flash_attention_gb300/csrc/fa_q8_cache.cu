@@ -56,13 +56,18 @@ __device__ __forceinline__ void flag_bad(int* status) {
 }
 
 // Rows of sequence b: where they start in the packed batch, and how many there are.
-__device__ __forceinline__ bool seq_rows(const Q8RowsK& p, int b, int& start, int& n) {
-  if (!p.cu) {
-    start = 0;
-    n = p.new_len;
-    return false;
-  }
-  return varlen_seq(p.cu, b, p.total, p.total, start, n);
+__device__ __forceinline__ void seq_rows(const Q8RowsK& p, int b, int& start, int& n) {
+  start = 0;
+  n = p.new_len;
+  if (p.cu) varlen_seq(p.cu, b, p.total, p.total, start, n);
+}
+
+// The offsets of sequence `item` are out of range (item i looks at sequence i's; there are at least
+// four items a sequence). What finds a slot's owner takes offsets that do not decrease, and may pass
+// over a sequence where they do: no owner would report it.
+__device__ __forceinline__ bool bad_offsets(const Q8RowsK& p, long long item) {
+  int start, n;
+  return p.cu && item < p.B && varlen_seq(p.cu, (int)item, p.total, p.total, start, n);
 }
 
 // Pages of a warp's `rows` rows from position p0 on: lane i holds that of entry
@@ -159,13 +164,13 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1)
   const int hgroups = (p.Hk + heads - 1) / heads;
   const int h0 = (int)((item >> 1) % hgroups) * heads;
   const long long slot = (item >> 1) / hgroups;
-  bool live = item < items, bad = false;
+  bool live = item < items, bad = bad_offsets(p, item);
   int b = 0, start = 0, n = 0, len = 0, first = 0, p0 = 0;
   if (live) {
     auto offset = [&](int i) { return p.cu ? (long long)p.cu[i] : (long long)i * p.new_len; };
     b = q8_slot_owner(slot, p.B, unit, lane, offset);
     len = p.lens[b];
-    bad |= seq_rows(p, b, start, n);
+    seq_rows(p, b, start, n);
     if (len < 0 || len > (long long)p.max_pages << p.ps_shift) {  // no place is the right one
       bad = true;
       live = false;
@@ -331,7 +336,8 @@ __global__ void __launch_bounds__(256, 4)
   auto offset = [&](int i) { return (long long)p.cu[i]; };
   const int b = q8_slot_owner(slot, p.B, RL::TR, lane, offset);
   int start, n;
-  bool bad = varlen_seq(p.cu, b, p.total, p.total, start, n);
+  varlen_seq(p.cu, b, p.total, p.total, start, n);
+  bool bad = bad_offsets(p, item);
   const long long cap = (long long)p.max_pages << p.ps_shift;
   bad |= n > cap;
   const long long u = slot - (offset(b) / RL::TR + 2ll * b);

@@ -414,7 +414,9 @@ typedef struct fa_q8_rows {
  * read, such as a shared prefix, may be shared). Not checked: two sequences writing one slot race.
  * The table, lengths and offsets are checked on the device: a sequence whose length is outside
  * [0, max_pages * page_size] is not written, rows of a page outside the cache are left out,
- * offsets out of range are clamped, and each makes fa_device_status return FA_ERR_BAD_INPUT.
+ * offsets out of range are clamped (where they decrease, rows of any sequence may be left out, but
+ * nothing is written that is not the call's), and each makes fa_device_status return
+ * FA_ERR_BAD_INPUT.
  * Every output bit is determined by the inputs. Returns FA_OK, FA_ERR_INVALID,
  * FA_ERR_UNSUPPORTED or FA_ERR_CUDA. */
 int fa_q8_cache_write(const fa_q8_cache* cache, const fa_q8_rows* rows, void* stream);
@@ -423,7 +425,8 @@ int fa_q8_cache_write(const fa_q8_cache* cache, const fa_q8_rows* rows, void* st
  * bf16(code * scale) into rows->k and rows->v (packed: cu_seqlens is required; rows must not lie
  * on one another: head and row strides of head_dim or more). Rows of `total`
  * behind cu_seqlens[batch] are left as they were. Rows of a page outside the cache or past the
- * table's end become 0 and make fa_device_status return FA_ERR_BAD_INPUT. */
+ * table's end become 0 and make fa_device_status return FA_ERR_BAD_INPUT, as do offsets out of range
+ * (handled as by the writer: where they decrease, rows may be left as they were). */
 int fa_q8_cache_read(const fa_q8_cache* cache, const fa_q8_rows* rows, void* stream);
 
 /* fa_paged_attention over the 8-bit cache: same q, block_table, lengths, o, lse, params and
