@@ -752,7 +752,8 @@ def q8_cache_read(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, t
     """The keys and values of a batch back from an 8-bit paged cache: (k, v), bf16
     [Hk, total, d], packed as varlen_attention_fwd takes them. Sequence b's rows
     cu_seqlens[b] .. cu_seqlens[b + 1] - 1 are its first keys. `out`: a pair of such tensors of
-    any strides with contiguous rows (rows behind cu_seqlens[B] are left as they were)."""
+    any strides with contiguous rows that do not lie on one another, such as views of one tensor
+    (rows behind cu_seqlens[B] are left as they were)."""
     import torch
 
     cache = _q8_cache(k_cache, v_cache, k_scale, v_scale, torch)

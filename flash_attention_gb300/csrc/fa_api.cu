@@ -13,6 +13,7 @@
 
 #include "../../include/fa_train.h"
 #include "fa_launch.h"
+#include "fa_rows.h"
 
 namespace {
 
@@ -843,10 +844,10 @@ static int prepare_q8_rows(const fa_q8_cache* c, const fa_q8_rows* r, bool write
     if (r->k_stride[i] < 0 || r->v_stride[i] < 0 || r->k_stride[i] % 8 || r->v_stride[i] % 8)
       return FA_ERR_INVALID;
   if (!write) {  // rows that are written must not lie on one another
-    const int64_t d = c->head_dim;
-    if ((r->total > 1 && (r->k_stride[2] < d || r->v_stride[2] < d)) ||
-        (c->n_kv_heads > 1 && (r->k_stride[1] < d || r->v_stride[1] < d)))
-      return FA_ERR_INVALID;
+    const fa::RowGrid k = {c->n_kv_heads, r->total, r->k_stride[1], r->k_stride[2]};
+    const fa::RowGrid v = {c->n_kv_heads, r->total, r->v_stride[1], r->v_stride[2]};
+    const intptr_t bytes = reinterpret_cast<intptr_t>(r->v) - reinterpret_cast<intptr_t>(r->k);
+    if (!fa::rows_apart(k, v, bytes / 2, c->head_dim)) return FA_ERR_INVALID;
   }
   a->codes[0] = c->k;
   a->codes[1] = c->v;

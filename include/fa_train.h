@@ -422,8 +422,9 @@ typedef struct fa_q8_rows {
 int fa_q8_cache_write(const fa_q8_cache* cache, const fa_q8_rows* rows, void* stream);
 
 /* Reads the first cu_seqlens[b+1] - cu_seqlens[b] keys and values of every sequence back:
- * bf16(code * scale) into rows->k and rows->v (packed: cu_seqlens is required; rows must not lie
- * on one another: head and row strides of head_dim or more). Rows of `total`
+ * bf16(code * scale) into rows->k and rows->v (packed: cu_seqlens is required). Rows must not lie on
+ * one another: FA_ERR_INVALID where two rows of k or two of v do, or a row of k and one of v (that is
+ * not looked for where k and v have different strides, but for their first rows). Rows of `total`
  * behind cu_seqlens[batch] are left as they were. Rows of a page outside the cache or past the
  * table's end become 0 and make fa_device_status return FA_ERR_BAD_INPUT, as do offsets out of range
  * (handled as by the writer: where they decrease, rows may be left as they were). */
