@@ -924,7 +924,6 @@ int fa_q8_paged_attention(const void* q, const fa_q8_cache* cache, const int32_t
   a.lse = lse;
   a.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
   a.B = p->batch;
-  a.H = p->n_heads;
   a.Hk = p->n_kv_heads;
   a.G = p->n_heads / p->n_kv_heads;
   a.lq = p->q_len;

@@ -340,7 +340,7 @@ struct Q8AttnArgs {
   float* lse;            // [B, H, lq] or nullptr
   int* status;
   uint64_t wait_limit_ns;
-  int B, H, Hk, G, lq, d, max_pages, num_pages, causal;
+  int B, Hk, G, lq, d, max_pages, num_pages, causal;
   int ps_shift, sb_shift;
   float scale;
 };

@@ -318,7 +318,7 @@ struct Q8K {
   float* o_part;   // [2 * grid, R, HD]: O of a share, in units of 2^m
   float* ml_part;  // [2 * grid, 2, R]: m and the sum
   int* status;
-  int B, H, Hk, G, lq, rows, rb, max_pages, num_pages, ps_shift, sb_shift;
+  int B, Hk, lq, rows, rb, max_pages, num_pages, ps_shift, sb_shift;
   float scale_log2;
   unsigned long long wait_limit_ns;
 };
@@ -1249,9 +1249,7 @@ cudaError_t attn_m(const Q8AttnArgs& a, const Q8AttnMaps& m, const Plan& pl, voi
   p.o_part = p.ml_part + (size_t)2 * pl.grid * 2 * R;
   p.status = a.status;
   p.B = a.B;
-  p.H = a.H;
   p.Hk = a.Hk;
-  p.G = a.G;
   p.lq = a.lq;
   p.rows = a.G * a.lq;
   p.rb = pl.rb;

@@ -460,8 +460,9 @@ cudaError_t write_t(const Q8RowsArgs& a, cudaStream_t s) {
 
 template <int HD, int SPB>
 cudaError_t write_s(const Q8RowsArgs& a, cudaStream_t s) {
-  // (a block of 8 steps is all of a warp's rows, and a page holds whole blocks)
-  if constexpr (SPB < 8)
+  // (a block of 8 steps is all of a warp's rows, and a page holds whole blocks; at head_dim 256 a
+  // warp has 8 rows, the smallest page)
+  if constexpr (SPB < 8 && RowLanes<HD>::TR > 8)
     if ((1 << a.ps_shift) < RowLanes<HD>::TR) return write_t<HD, SPB, false>(a, s);
   return write_t<HD, SPB, true>(a, s);
 }
@@ -482,10 +483,12 @@ cudaError_t read_d(const Q8RowsArgs& a, cudaStream_t s) {
   const long long items = slots * ((a.Hk + heads - 1) / heads) * 2;
   const unsigned grid = (unsigned)((items + 7) / 8);
   profile_mark(kKernQ8Read, 0, s);
-  if ((1 << a.ps_shift) < RowLanes<HD>::TR)
-    q8_read_kernel<HD, false><<<grid, 256, 0, s>>>(rows_params(a), items, heads);
-  else
-    q8_read_kernel<HD, true><<<grid, 256, 0, s>>>(rows_params(a), items, heads);
+  bool one = true;
+  if constexpr (RowLanes<HD>::TR > 8) {
+    one = (1 << a.ps_shift) >= RowLanes<HD>::TR;
+    if (!one) q8_read_kernel<HD, false><<<grid, 256, 0, s>>>(rows_params(a), items, heads);
+  }
+  if (one) q8_read_kernel<HD, true><<<grid, 256, 0, s>>>(rows_params(a), items, heads);
   const cudaError_t e = cudaGetLastError();
   profile_mark(kKernQ8Read, 1, s);
   return e;
