@@ -782,7 +782,8 @@ static int log2_of(int x) {
 // Scratch of the 8-bit attention comes from a pool of the library's own on each device that keeps
 // what is freed (20 MB at most for a call): the device's default pool gives memory back whenever the
 // stream has been waited for, and the next call then takes 200 us to get it again, many times
-// what a decoding step's attention runs.
+// what a decoding step's attention runs. (The pool serves on after a device reset, as
+// tests/test_q8_reset_gpu.py shows.)
 static cudaError_t scratch_pool(int dev, cudaMemPool_t* out) {
   static cudaMemPool_t pools[64] = {};
   static fa::OncePerKey<> once;
