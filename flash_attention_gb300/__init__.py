@@ -717,7 +717,8 @@ def q8_cache_write(k, v, k_cache, v_cache, k_scale, v_scale, block_table, length
     [Hk, total, d]; any strides with contiguous rows. `lengths` (int32 [B]) counts each sequence's
     keys with the new rows, which become its last positions; block_table is int32 [B, max_pages].
     A page written to must belong to one sequence of the call. See fa_q8_cache_write in
-    include/fa_train.h for the rounding and the scales."""
+    include/fa_train.h for the rounding and the scales. With `stream`, the inputs have to stay as
+    they are until that stream has done the call."""
     import torch
 
     cache = _q8_cache(k_cache, v_cache, k_scale, v_scale, torch)
@@ -753,7 +754,8 @@ def q8_cache_read(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, t
     [Hk, total, d], packed as varlen_attention_fwd takes them. Sequence b's rows
     cu_seqlens[b] .. cu_seqlens[b + 1] - 1 are its first keys. `out`: a pair of such tensors of
     any strides with contiguous rows that do not lie on one another, such as views of one tensor
-    (rows behind cu_seqlens[B] are left as they were)."""
+    (rows behind cu_seqlens[B] are left as they were). With `stream`, the inputs have to stay as they
+    are until that stream has done the call, and new outputs belong to it."""
     import torch
 
     cache = _q8_cache(k_cache, v_cache, k_scale, v_scale, torch)
@@ -792,7 +794,11 @@ def q8_paged_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, lengt
     """paged_attention over an 8-bit paged cache: q bf16 [B, H, q_len, d], codes float8_e4m3fn
     [num_pages, Hk, page_size, d] with float32 scales [num_pages, Hk, page_size // scale_block],
     block_table [B, max_pages] and lengths [B] (int32): returns (o, lse). The q_len queries are
-    each sequence's last positions (causal: bottom-right per sequence)."""
+    each sequence's last positions (causal: bottom-right per sequence). Scales outside [0, 2^100]
+    are reported by fa_device_status. With `stream`, the inputs have to stay as they are until that
+    stream has done the call, and the outputs belong to it. For a long prompt against the cache
+    (more than about 640 query rows a kv head, 140 at head_dim 256) q8_cache_read and
+    varlen_attention_fwd are faster."""
     import torch
 
     cache = _q8_cache(k_cache, v_cache, k_scale, v_scale, torch)

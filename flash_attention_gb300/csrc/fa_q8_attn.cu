@@ -40,10 +40,11 @@
 // scales. All waits on barriers are bounded.
 //
 // Measured (device time of a call with both kernels): 64 sequences of 1k to 16k keys, head_dim 128,
-// 32:8 heads, 963 MB: 149 us, 95 % of the measured copy rate (6787 GB/s); 16 sequences of 2k to 16k
+// 32:8 heads, 963 MB: 150 us, 94 % of the measured copy rate (6787 GB/s); 16 sequences of 2k to 16k
 // keys, 351 MB: 63 us (82 %), the start, the joining kernel and the last CTAs being the rest; with
-// 16 rows a kv head 69 us for 322 MB, bound by the softmax's latency and issue; 128 sequences of up
-// to 2047 keys at head_dim 64, 132 MB: 37 us, bound by instructions.
+// 16 rows a kv head 70 us for 322 MB, bound by the softmax's latency and issue; 128 sequences of up
+// to 2047 keys at head_dim 64, 132 MB: 37 us, bound by latency and instruction fetch (issue active
+// 38 %; a unit has 8 tiles, and its start and end take as long as four).
 #include <float.h>
 
 #include <algorithm>
@@ -1202,9 +1203,12 @@ __global__ void __launch_bounds__(256) q8_combine_kernel(const Q8K p, int grid) 
     p.lse[unit_row + r] = sum == 0.0f ? -INFINITY : fmaf(m + kSumExp, kLn2, logf(sum));
 }
 
-// Rows a kv head from which blocks of 128 rows are taken (head_dim 64 and 128; 256 columns of O
-// would not leave tensor memory for the rest). A tile of 128 keys takes the same time for any
-// number of its rows, a block of 16 not half of that. 16 sequences of 4k to 16k keys, 8 kv heads,
+// Rows a kv head from which blocks of 128 rows are taken (head_dim 64 and 128 alone: at 256 that
+// kernel's layout, with weights beside the scores and tiles of 128 keys, has neither the tensor
+// memory nor the shared memory, and none with weights over their scores and tiles of 64 keys is
+// written; more rows there read the keys again for every 16: 128 rows 814 us, 512 rows 3172). A tile
+// of 128 keys takes the same time for any number of its rows, a block of 16 not half of that. 16
+// sequences of 4k to 16k keys, 8 kv heads,
 // head_dim 128, blocks of 16 against those of 128: 32 rows 115 / 128 us, 40 rows 156 / 128,
 // 128 rows 399 / 139, 512 rows 1461 / 500; head_dim 64: 100 / 107, 141 / 108, 355 / 112,
 // 1369 / 411.

@@ -21,8 +21,10 @@
 // exponentials and the chain from scores to weights; at head_dim 128 the widening's shared-memory
 // traffic too. A tile takes about 3000 cycles at head_dim 64 and 3600 at 128, for any number of
 // its 128 rows: 16 sequences of 4k to 16k keys, 8 kv heads of 128 rows, 168 M scores: 112 us and
-// 139 us. Tried: codes through registers instead of cp.async (they spilled: 410 us for 48 rows at
-// head_dim 128 where cp.async took 185), scores 32 columns and scales 8 keys at a time (no faster).
+// 139 us. (From about 640 rows a kv head on, reading the keys back as bf16 and the variable-length
+// attention are faster.) Tried: codes through registers instead of cp.async (they spilled: 410 us
+// for 48 rows at head_dim 128 where cp.async took 185), scores 32 columns and scales 8 keys at a
+// time (no faster).
 //
 // Warps: 0-7 softmax (two warpgroups, half the keys of a tile each, and half the columns of O),
 // 8-11 keys and values, 12 the MMAs, 13 the list of units. One CTA an SM.
