@@ -1208,10 +1208,9 @@ __global__ void __launch_bounds__(256) q8_combine_kernel(const Q8K p, int grid) 
 // memory nor the shared memory, and none with weights over their scores and tiles of 64 keys is
 // written; more rows there read the keys again for every 16: 128 rows 814 us, 512 rows 3172). A tile
 // of 128 keys takes the same time for any number of its rows, a block of 16 not half of that. 16
-// sequences of 4k to 16k keys, 8 kv heads,
-// head_dim 128, blocks of 16 against those of 128: 32 rows 115 / 128 us, 40 rows 156 / 128,
-// 128 rows 399 / 139, 512 rows 1461 / 500; head_dim 64: 100 / 107, 141 / 108, 355 / 112,
-// 1369 / 411.
+// sequences of 4k to 16k keys, 8 kv heads, head_dim 128, blocks of 16 against those of 128: 32 rows
+// 115 / 128 us, 40 rows 156 / 128, 128 rows 399 / 139, 512 rows 1461 / 500; head_dim 64: 100 / 107,
+// 141 / 108, 355 / 112, 1369 / 411.
 constexpr int kChunkRows = 33;
 
 struct Plan {
