@@ -16,8 +16,8 @@ namespace fa {
 // Exponent of the smallest scale that the writer uses (an all-zero block has it). The attention
 // reads smaller value scales as this one, so that log2 of a scale is always finite.
 constexpr int kQ8MinExp = -100;
-// The largest scale that the attention admits, 2^100, as its f32 bits: those of negative values and of
-// NaN are larger.
+// The largest scale that the attention admits, 2^100, as its f32 bits: those of negative values and
+// of NaN are larger.
 constexpr uint32_t kQ8MaxScale = 0x71800000u;
 
 // Two floats -> two e4m3 codes (round to nearest even, saturating; NaN -> 0x7F): `lo` in bits 0-7.

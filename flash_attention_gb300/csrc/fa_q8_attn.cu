@@ -67,9 +67,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 // 2^kMost (where f16 would not hold 8 times what the first piece leaves).
 constexpr float kTop = 11.0f, kMost = 15.0f;
 // The softmax's sums are held in units of 2^16: with value scales from 2^-100 to 2^100 neither
-// w / v_scale nor 2^22 of them leave f32, and a row's sum is 2^-105 at least (its m less its largest
-// score is at most 100 - 11). A factor between two m's may be any, so sums are scaled by its root
-// twice (scale_sum).
+// w / v_scale nor 2^22 of them leave f32, and a row's sum is 2^-105 at least (its m less its
+// largest score is at most 100 - 11). A factor between two m's may be any, so sums are scaled by
+// its root twice (scale_sum).
 constexpr float kSumExp = 16.0f, kSumUnit = 65536.0f;
 // Value scales of a unit's keys (log2) may be this far below the largest up to their tile for
 // w / v_scale to serve: a w below f32 (2^-126) is then that of a score 2^-41 of the largest one's.
@@ -476,8 +476,8 @@ __global__ void __launch_bounds__(Q8Layout<HD, R, RL>::THREADS, Q8Layout<HD, R, 
   __shared__ int bad_input;
   __shared__ int page_s[kPageChunk];
   __shared__ __align__(16) float sc_s[2][2][kKT];  // key scale, log2 of the value scale
-  // One of a tile's value scales is kApart below another. Read after s_free, so four tiles deep: when
-  // the scores of two tiles before are read, the weights of three before are done.
+  // One of a tile's value scales is kApart below another. Read after s_free, so four tiles deep:
+  // when the scores of two tiles before are read, the weights of three before are done.
   __shared__ int apart_s[4];
   __shared__ __align__(16) float qs_s[2][R];       // rows: score factor
   __shared__ __align__(16) int lim_s[2][R];        // and the keys they see: those below it

@@ -63,8 +63,8 @@ __device__ __forceinline__ void seq_rows(const Q8RowsK& p, int b, int& start, in
 }
 
 // The offsets of sequence `item` are out of range (item i looks at sequence i's; there are at least
-// four items a sequence). What finds a slot's owner takes offsets that do not decrease, and may pass
-// over a sequence where they do: no owner would report it.
+// four items a sequence). What finds a slot's owner takes offsets that do not decrease, and may
+// pass over a sequence where they do: no owner would report it.
 __device__ __forceinline__ bool bad_offsets(const Q8RowsK& p, long long item) {
   int start, n;
   return p.cu && item < p.B && varlen_seq(p.cu, (int)item, p.total, p.total, start, n);

@@ -367,8 +367,8 @@ int fa_paged_attention_bwd(const void* q, const void* k_cache, const void* v_cac
  * head on, (n_heads / n_kv_heads) * q_len, at head_dim 256 from 140, that is faster than
  * fa_q8_paged_attention, for a bf16 copy of the keys and values). No counterpart on the pages.
  *
- * The attention takes scales in [0, 2^100] (value scales below 2^-100, the writer's smallest, are read
- * as 2^-100); another one where a key is read, as the writer makes of finite values above
+ * The attention takes scales in [0, 2^100] (value scales below 2^-100, the writer's smallest, are
+ * read as 2^-100); another one where a key is read, as the writer makes of finite values above
  * 448 * 2^100, makes fa_device_status return FA_ERR_BAD_INPUT. What the slots past a sequence's end
  * hold (codes and scales, NaN included) reaches no result. */
 typedef struct fa_q8_cache {
@@ -423,12 +423,12 @@ typedef struct fa_q8_rows {
 int fa_q8_cache_write(const fa_q8_cache* cache, const fa_q8_rows* rows, void* stream);
 
 /* Reads the first cu_seqlens[b+1] - cu_seqlens[b] keys and values of every sequence back:
- * bf16(code * scale) into rows->k and rows->v (packed: cu_seqlens is required). Rows must not lie on
- * one another: FA_ERR_INVALID where two rows of k or two of v do, or a row of k and one of v (that is
- * not looked for where k and v have different strides, but for their first rows). Rows of `total`
- * behind cu_seqlens[batch] are left as they were. Rows of a page outside the cache or past the
- * table's end become 0 and make fa_device_status return FA_ERR_BAD_INPUT, as do offsets out of range
- * (handled as by the writer: where they decrease, rows may be left as they were). */
+ * bf16(code * scale) into rows->k and rows->v (packed: cu_seqlens is required). Rows must not lie
+ * on one another: FA_ERR_INVALID where two rows of k or two of v do, or a row of k and one of v
+ * (that is not looked for where k and v have different strides, but for their first rows). Rows of
+ * `total` behind cu_seqlens[batch] are left as they were. Rows of a page outside the cache or past the
+ * table's end become 0 and make fa_device_status return FA_ERR_BAD_INPUT, as do offsets out of
+ * range (clamped; where they decrease, rows may be left as they were or be another sequence's). */
 int fa_q8_cache_read(const fa_q8_cache* cache, const fa_q8_rows* rows, void* stream);
 
 /* fa_paged_attention over the 8-bit cache: same q, block_table, lengths, o, lse, params and
