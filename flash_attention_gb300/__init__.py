@@ -20,7 +20,9 @@ __all__ = [
     "FA_ERR_TOO_LARGE", "FA_ERR_BAD_INPUT", "FaOptions", "FaPagedParams", "paged_attention",
     "fa_paged_attention", "fa_paged_attention_bwd", "fa_train_fwd_ex", "fa_train_bwd_ex", "make_options",
     "FA_MASK_F32", "FA_MASK_BF16", "FA_MASK_BOOL", "FaQ8Cache", "FaQ8Rows", "make_q8_cache",
-    "q8_cache_write", "q8_cache_read", "q8_paged_attention",
+    "q8_cache_write", "q8_cache_read", "q8_paged_attention", "FA_TREE_MAX", "FaRotary",
+    "FaRotaryRows", "FaPagedRows", "FaPagedKept", "rotary_inv_freq", "rotary_fwd", "rotary_bwd",
+    "paged_cache_append", "paged_tree_attention", "paged_cache_keep",
 ]
 
 FA_OK = 0
@@ -37,6 +39,7 @@ FA_MASK_BF16 = 1
 FA_MASK_BOOL = 2
 FA_LAYOUT_Q_BSHD = 1   # q, o, dO, dq as [batch, seq, heads, dim] in memory
 FA_LAYOUT_KV_BSHD = 2  # k, v, dk, dv as [batch, seq, kv_heads, dim] in memory
+FA_TREE_MAX = 256      # nodes of a drafted tree
 
 
 class FaOptions(ctypes.Structure):
@@ -130,6 +133,93 @@ class FaQ8Rows(ctypes.Structure):
     ]
 
 
+class FaRotary(ctypes.Structure):
+    """Mirror of `fa_rotary` in include/fa_train.h."""
+
+    _fields_ = [
+        ("inv_freq", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+        ("pos_stride", ctypes.c_int64),
+        ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("offset", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class FaRotaryRows(ctypes.Structure):
+    """Mirror of `fa_rotary_rows` in include/fa_train.h."""
+
+    _fields_ = [
+        ("q", ctypes.c_void_p),
+        ("k", ctypes.c_void_p),
+        ("q_out", ctypes.c_void_p),
+        ("k_out", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64 * 3),
+        ("k_stride", ctypes.c_int64 * 3),
+        ("q_out_stride", ctypes.c_int64 * 3),
+        ("k_out_stride", ctypes.c_int64 * 3),
+        ("cu_seqlens", ctypes.c_void_p),
+        ("batch", ctypes.c_int32),
+        ("n_heads", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("rows", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class FaPagedRows(ctypes.Structure):
+    """Mirror of `fa_paged_rows` in include/fa_train.h."""
+
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("q", ctypes.c_void_p),
+        ("q_out", ctypes.c_void_p),
+        ("k_cache", ctypes.c_void_p),
+        ("v_cache", ctypes.c_void_p),
+        ("k_stride", ctypes.c_int64 * 3),
+        ("v_stride", ctypes.c_int64 * 3),
+        ("q_stride", ctypes.c_int64 * 3),
+        ("cu_seqlens", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p),
+        ("lengths", ctypes.c_void_p),
+        ("batch", ctypes.c_int32),
+        ("n_heads", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("total", ctypes.c_int32),
+        ("new_len", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class FaPagedKept(ctypes.Structure):
+    """Mirror of `fa_paged_kept` in include/fa_train.h."""
+
+    _fields_ = [
+        ("k_cache", ctypes.c_void_p),
+        ("v_cache", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p),
+        ("lengths", ctypes.c_void_p),
+        ("keep", ctypes.c_void_p),
+        ("counts", ctypes.c_void_p),
+        ("new_lengths", ctypes.c_void_p),
+        ("batch", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("tree_len", ctypes.c_int32),
+        ("max_keep", ctypes.c_int32),
+    ]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -177,6 +267,17 @@ def load_library():
             lib.fa_q8_paged_attention.argtypes = [vp, pc, vp, vp, vp, vp,
                                                   ctypes.POINTER(FaPagedParams), vp]
             lib.fa_q8_paged_attention.restype = ctypes.c_int
+            lib.fa_rotary_apply.argtypes = [ctypes.POINTER(FaRotaryRows),
+                                            ctypes.POINTER(FaRotary), ctypes.c_int, vp]
+            lib.fa_rotary_apply.restype = ctypes.c_int
+            lib.fa_paged_append.argtypes = [ctypes.POINTER(FaPagedRows),
+                                            ctypes.POINTER(FaRotary), vp]
+            lib.fa_paged_append.restype = ctypes.c_int
+            lib.fa_paged_keep.argtypes = [ctypes.POINTER(FaPagedKept), vp]
+            lib.fa_paged_keep.restype = ctypes.c_int
+            lib.fa_paged_tree_attention.argtypes = [vp, vp, vp, vp, vp, vp, ctypes.c_int64, vp, fp,
+                                                    ctypes.POINTER(FaPagedParams), vp]
+            lib.fa_paged_tree_attention.restype = ctypes.c_int
             lib.fa_device_status.argtypes = [ctypes.c_int]
             lib.fa_device_status.restype = ctypes.c_int
             lib.fa_error_string.argtypes = [ctypes.c_int]
@@ -367,7 +468,7 @@ def fa_device_status(clear: bool = True) -> int:
     return load_library().fa_device_status(int(bool(clear)))
 
 
-FA_NUM_KERNELS = 14
+FA_NUM_KERNELS = 19
 
 
 def fa_profile_enable(on: bool) -> None:
@@ -828,3 +929,309 @@ def q8_paged_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, lengt
     if rc:
         raise FaError(rc, "fa_q8_paged_attention")
     return o, lse
+
+
+# ------------------------------------------------------------------------- rotary positions
+def rotary_inv_freq(rotary_dim, base=10000.0, *, factor=1.0, method=None, original_len=None,
+                    beta_fast=32.0, beta_slow=1.0, device="cuda"):
+    """Frequencies for rotary_fwd and its like, and the scale that goes with them: (inv_freq, scale),
+    inv_freq float64 [rotary_dim // 2], base ** (-2 i / rotary_dim) radians a position, stretched for
+    contexts `factor` times as long by `method`:
+      None      not at all (factor must be 1)
+      "linear"  all of them divided by factor
+      "base"    base * factor ** (rotary_dim / (rotary_dim - 2)) for base: the slowest frequency is
+                divided by factor, the fastest stays
+      "parts"   those that turn less than beta_slow times in original_len positions divided by factor,
+                those that turn more than beta_fast times as they are, a linear mixture by i between;
+                the scale becomes 0.1 ln(factor) + 1
+    A setup step: computed in 64 bits on the host, once."""
+    import math
+
+    import torch
+
+    n = int(rotary_dim)
+    if n < 16 or n % 16:
+        raise ValueError("rotary_dim must be a multiple of 16")
+    if not (base > 0 and factor > 0 and math.isfinite(base) and math.isfinite(factor)):
+        raise ValueError("base and factor must be finite and positive")
+    if method not in (None, "linear", "base", "parts"):
+        raise ValueError("method must be None, 'linear', 'base' or 'parts'")
+    if method is None and factor != 1.0:
+        raise ValueError("a factor needs a method")
+    if method == "base":
+        base = base * factor ** (n / (n - 2))
+    i = torch.arange(n // 2, dtype=torch.float64)
+    freq = torch.pow(torch.tensor(float(base), dtype=torch.float64), -2.0 * i / n)
+    scale = 1.0
+    if method == "linear":
+        freq = freq / factor
+    elif method == "parts":
+        if original_len is None or original_len < 1 or not 0 < beta_slow < beta_fast or base <= 1:
+            raise ValueError("'parts' needs original_len, 0 < beta_slow < beta_fast and base > 1")
+
+        def pair_of(turns):  # the pair that turns so many times in original_len positions
+            return n * math.log(original_len / (2 * math.pi * turns)) / (2 * math.log(base))
+
+        low = max(math.floor(pair_of(beta_fast)), 0)
+        high = min(math.ceil(pair_of(beta_slow)), n - 1)
+        slow = ((i - low) / max(high - low, 1e-3)).clamp(0, 1)
+        freq = freq * (1 - slow) + freq / factor * slow
+        scale = 0.1 * math.log(factor) + 1 if factor > 1 else 1.0
+    return freq.to(device), scale
+
+
+def _rotary(inv_freq, positions, batch, rows, interleaved, offset, scale, packed, torch):
+    """FaRotary for rows of a batch (batch x rows, or `rows` packed ones)."""
+    if not (inv_freq.dtype is torch.float64 and inv_freq.dim() == 1 and inv_freq.is_contiguous()):
+        raise ValueError("inv_freq must be a contiguous float64 tensor [rotary_dim // 2]")
+    pos, stride = None, 0
+    if positions is not None:
+        shape = positions.shape
+        if positions.dtype is not torch.int32 or not (
+                shape == (rows,) or not packed and shape == (batch, rows)):
+            raise ValueError("positions must be int32, one for each row: [B, n], [n] for all "
+                             "sequences alike, or packed [total]")
+        if rows > 1 and positions.stride(-1) != 1:
+            raise ValueError("the positions of a sequence must be contiguous")
+        pos = positions.data_ptr()
+        stride = positions.stride(0) if len(shape) == 2 and batch > 1 else 0
+    return FaRotary(inv_freq.data_ptr(), pos, stride, 2 * inv_freq.shape[0],
+                    1 if interleaved else 0, int(offset), float(scale))
+
+
+def _rows_like(x, torch):
+    """An output for x [.., heads, rows, d]: contiguous where the rows of a head follow one another
+    in x, else [.., rows, heads, d] in memory."""
+    if x.stride(-2) == x.shape[-1] or x.shape[-2] == 1:
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    return torch.empty((*x.shape[:-3], x.shape[-2], x.shape[-3], x.shape[-1]), dtype=x.dtype,
+                       device=x.device).transpose(-3, -2)
+
+
+def _rotate(q, k, inv_freq, back, positions, cu_seqlens, offset, interleaved, scale, out, stream):
+    import torch
+
+    shape, packed = q.shape, q.dim() == 3
+    if not packed and q.dim() != 4:
+        raise ValueError("q must be [B, H, n, d] or packed [H, total, d]")
+    B, n, d = 1 if packed else shape[0], shape[-2], shape[-1]
+    if k is not None and not (k.dim() == q.dim() and k.shape[-2:] == shape[-2:]
+                              and (packed or k.shape[0] == B)):
+        raise ValueError("q and k must have the same batch, rows and head dim")
+    cu = None
+    if cu_seqlens is not None:
+        if not packed or positions is not None:
+            raise ValueError("cu_seqlens goes with packed rows, and without positions")
+        B = cu_seqlens.shape[0] - 1 if cu_seqlens.dim() == 1 else 0
+        cu = _q8_index(cu_seqlens, B + 1, "cu_seqlens", torch)
+        if B < 1:
+            raise ValueError("cu_seqlens must be a contiguous int32 tensor of B + 1 entries")
+    if positions is not None and offset:
+        raise ValueError("offset is for rows without positions")
+    rot = _rotary(inv_freq, positions, B, n, interleaved, offset, scale, packed, torch)
+    zero = (0, 0, 0)
+    qs = _q8_rows(q, "q", torch)
+    ks = zero if k is None else _q8_rows(k, "k", torch)
+    outs = () if out is None else tuple(t for t in out if t is not None)
+    handle, ctx = _q8_stream(stream, torch, q, inv_freq,
+                             *(t for t in (k, positions, cu_seqlens) if t is not None), *outs)
+    if out is not None:
+        qo, ko = out
+        if qo.shape != shape or (ko is None) != (k is None) or (k is not None
+                                                                and ko.shape != k.shape):
+            raise ValueError("out must be two tensors like q and k")
+    elif ctx is None:
+        qo, ko = _rows_like(q, torch), None if k is None else _rows_like(k, torch)
+    else:
+        with ctx:
+            qo, ko = _rows_like(q, torch), None if k is None else _rows_like(k, torch)
+    if q.numel() == 0:
+        return qo, ko
+    rows = FaRotaryRows(q.data_ptr(), None if k is None else k.data_ptr(), qo.data_ptr(),
+                        None if k is None else ko.data_ptr(), qs, ks, _q8_rows(qo, "out[0]", torch),
+                        zero if k is None else _q8_rows(ko, "out[1]", torch), cu, B, shape[-3],
+                        0 if k is None else k.shape[-3], n, d, 0)
+    rc = (_lib or load_library()).fa_rotary_apply(ctypes.byref(rows), ctypes.byref(rot), back,
+                                                  handle)
+    if rc:
+        raise FaError(rc, "fa_rotary_apply")
+    return qo, ko
+
+
+def rotary_fwd(q, k, inv_freq, *, positions=None, cu_seqlens=None, offset=0, interleaved=False,
+               scale=1.0, out=None, stream=None):
+    """Queries and keys turned by their positions, for attention_fwd or varlen_attention_fwd: returns
+    (q, k). q [B, H, n, d] and k [B, Hk, n, d], or packed [H, total, d] and [Hk, total, d], bf16, any
+    strides with contiguous rows (views of a fused projection's output serve as they are); k may be
+    None. inv_freq: float64 [rotary_dim // 2], radians a position (rotary_inv_freq); the elements of a
+    row from rotary_dim on stay. Positions: int32 [B, n] or [n] (packed: [total]); without them, that
+    of row i is i + offset, in a packed batch with cu_seqlens (int32 [B + 1]) counted from each
+    sequence's first row. Pairs are i and i + rotary_dim / 2, or neighbours (interleaved); `scale`
+    multiplies what turns. `out`: a pair of tensors, q and k themselves for turning in place. New
+    outputs are contiguous, or [.., rows, heads, d] in memory where the inputs are laid out like that.
+    Rows behind cu_seqlens[B] are left as they were. With `stream`, the inputs have to stay as they
+    are until that stream has done the call, and new outputs belong to it."""
+    return _rotate(q, k, inv_freq, 0, positions, cu_seqlens, offset, interleaved, scale, out, stream)
+
+
+def rotary_bwd(dq, dk, inv_freq, *, positions=None, cu_seqlens=None, offset=0, interleaved=False,
+               scale=1.0, out=None, stream=None):
+    """Gradients of rotary_fwd's q and k from those of its results (dq, dk, as attention_bwd returns
+    them): the same turn backwards, the same arguments. Returns (dq, dk)."""
+    return _rotate(dq, dk, inv_freq, 1, positions, cu_seqlens, offset, interleaved, scale, out,
+                   stream)
+
+
+# --------------------------------------------------------- appending, and trees of drafted tokens
+def _bf16_cache(k, v, torch):
+    shape = k.shape
+    if not (k.dtype is v.dtype is torch.bfloat16 and len(shape) == 4 and v.shape == shape
+            and k.is_contiguous() and v.is_contiguous()):
+        raise ValueError("k_cache and v_cache must be contiguous bfloat16 [num_pages, Hk, page_size, d]")
+    return shape
+
+
+def paged_cache_append(k, v, k_cache, v_cache, block_table, lengths, *, q=None, inv_freq=None,
+                       positions=None, interleaved=False, rotary_scale=1.0, cu_seqlens=None,
+                       stream=None):
+    """Append new keys and values to a paged cache [num_pages, Hk, page_size, d], in place; with
+    inv_freq the keys are turned by their positions on the way, and with q the queries of the same
+    rows too: returns those (contiguous, as paged_attention and paged_tree_attention take them), or
+    None without q. k, v: bf16 [B, Hk, n, d], n new rows for each sequence, or with cu_seqlens (int32
+    [B + 1]) packed [Hk, total, d], q alike with its heads; any strides with contiguous rows.
+    `lengths` (int32 [B]) counts each sequence's keys with the new rows, which become its last
+    positions; block_table is int32 [B, max_pages]. Rows turn by their positions in the cache, or by
+    `positions` (int32 [B, n] or [n], packed [total]): a drafted tree's nodes by their depth. inv_freq,
+    interleaved and rotary_scale as in rotary_fwd. A page written to must belong to one sequence of
+    the call. With `stream`, the inputs have to stay as they are until that stream has done the call,
+    and what is returned belongs to it."""
+    import torch
+
+    P, Hk, ps, d = _bf16_cache(k_cache, v_cache, torch)
+    B, per = _q8_table(block_table, torch)
+    shape = k.shape
+    if v.shape != shape:
+        raise ValueError("k and v must have the same shape")
+    if cu_seqlens is None:
+        if not (len(shape) == 4 and shape[0] == B and shape[1] == Hk and shape[3] == d):
+            raise ValueError("k and v must be [B, Hk, n, d]")
+        cu, total, n = None, 0, shape[2]
+    else:
+        if not (len(shape) == 3 and shape[0] == Hk and shape[2] == d):
+            raise ValueError("packed k and v must be [Hk, total, d]")
+        cu, total, n = _q8_index(cu_seqlens, B + 1, "cu_seqlens", torch), shape[1], 0
+    if q is not None:
+        if inv_freq is None:
+            raise ValueError("q is turned with the keys: it needs inv_freq")
+        if len(q.shape) != len(shape) or q.shape[-2:] != shape[-2:] or (
+                cu is None and q.shape[0] != B):
+            raise ValueError("q must have the rows and head dim of k")
+    rot = None
+    if inv_freq is not None:
+        rot = _rotary(inv_freq, positions, B, shape[-2], interleaved, 0, rotary_scale,
+                      cu is not None, torch)
+    elif positions is not None:
+        raise ValueError("positions need inv_freq")
+    zero = (0, 0, 0)
+    ks, vs = _q8_rows(k, "k", torch), _q8_rows(v, "v", torch)
+    qs = zero if q is None else _q8_rows(q, "q", torch)
+    lens = _q8_index(lengths, B, "lengths", torch)
+    handle, ctx = _q8_stream(stream, torch, k, v, k_cache, v_cache, block_table, lengths, *(
+        t for t in (q, inv_freq, positions, cu_seqlens) if t is not None))
+    out = None
+    if q is not None:
+        if ctx is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        else:
+            with ctx:
+                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if total == 0 and n == 0:
+        return out
+    rows = FaPagedRows(k.data_ptr(), v.data_ptr(), None if q is None else q.data_ptr(),
+                       None if q is None else out.data_ptr(), k_cache.data_ptr(),
+                       v_cache.data_ptr(), ks, vs, qs, cu, block_table.data_ptr(), lens, B,
+                       0 if q is None else q.shape[-3], Hk, d, ps, per, P, total, n, 0)
+    rc = (_lib or load_library()).fa_paged_append(
+        ctypes.byref(rows), None if rot is None else ctypes.byref(rot), handle)
+    if rc:
+        raise FaError(rc, "fa_paged_append")
+    return out
+
+
+def paged_tree_attention(q, k_cache, v_cache, block_table, lengths, tree_mask, *, scale,
+                         stream=None):
+    """paged_attention for trees of drafted tokens: q bf16 [B, H, T, d] are a sequence's last T
+    positions, the nodes of its tree; each sees every key before them, and of the last T keys those
+    that its row of tree_mask names (bool or uint8 [T, T] for all sequences, or [B, T, T]; its
+    ancestors and itself): returns (o, lse). T is at most FA_TREE_MAX. A smaller tree stands at the
+    end of the T, with the columns before it (keys of the sequence) named for every node. A node that
+    sees no key gives o = 0 and lse = -inf. With `stream`, the inputs have to stay as they are until
+    that stream has done the call, and the outputs belong to it."""
+    import torch
+
+    P, Hk, ps, d = _bf16_cache(k_cache, v_cache, torch)
+    shape = q.shape
+    if not (q.dtype is torch.bfloat16 and len(shape) == 4 and q.is_contiguous()
+            and shape[3] == d):
+        raise ValueError("q must be contiguous bfloat16 [B, H, T, d]")
+    B, H, T, _ = shape
+    rows, per = _q8_table(block_table, torch)
+    if rows != B:
+        raise ValueError("block_table must have a row for each sequence of q")
+    lens = _q8_index(lengths, B, "lengths", torch)
+    if tree_mask.dtype not in (torch.bool, torch.uint8) or tree_mask.shape not in ((T, T),
+                                                                                   (B, T, T)):
+        raise ValueError("tree_mask must be bool or uint8 [T, T] or [B, T, T]")
+    st = tree_mask.stride()
+    if T > 1 and st[-2:] != (T, 1):
+        raise ValueError("the mask of a tree must be contiguous")
+    mask_stride = st[0] if len(st) == 3 and B > 1 else 0
+    handle, ctx = _q8_stream(stream, torch, q, k_cache, v_cache, block_table, lengths, tree_mask)
+    params = FaPagedParams(B, H, Hk, T, d, ps, per, P, float(scale), 0, 0, 0)
+    if ctx is None:
+        o = torch.empty_like(q)
+        lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device)
+    else:
+        with ctx:
+            o = torch.empty_like(q)
+            lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device)
+    rc = (_lib or load_library()).fa_paged_tree_attention(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), lens,
+        tree_mask.data_ptr(), mask_stride, o.data_ptr(), lse.data_ptr(), ctypes.byref(params),
+        handle)
+    if rc:
+        raise FaError(rc, "fa_paged_tree_attention")
+    return o, lse
+
+
+def paged_cache_keep(k_cache, v_cache, block_table, lengths, keep, counts, tree_len, *,
+                     stream=None):
+    """Keep the accepted nodes of drafted trees: of each sequence's last tree_len keys, the first
+    counts[b] that keep[b] names (int32 [B, M], nodes 0 .. tree_len - 1, ascending; counts int32 [B])
+    move, in that order, to the front of the tree_len, in both caches, in place. Returns the new
+    lengths, max(0, lengths - tree_len + counts), as a new tensor. A node that keeps its place does
+    not move (a smaller tree at the end of the tree_len names the columns before it first). A page
+    that is moved in must belong to one sequence of the call. See fa_paged_keep in include/fa_train.h
+    for what is refused on the device."""
+    import torch
+
+    P, Hk, ps, d = _bf16_cache(k_cache, v_cache, torch)
+    B, per = _q8_table(block_table, torch)
+    lens = _q8_index(lengths, B, "lengths", torch)
+    if not (keep.dtype is torch.int32 and keep.dim() == 2 and keep.shape[0] == B
+            and keep.is_contiguous()):
+        raise ValueError("keep must be a contiguous int32 tensor [B, M]")
+    n = _q8_index(counts, B, "counts", torch)
+    handle, ctx = _q8_stream(stream, torch, k_cache, v_cache, block_table, lengths, keep, counts)
+    if ctx is None:
+        new = torch.empty_like(lengths)
+    else:
+        with ctx:
+            new = torch.empty_like(lengths)
+    kept = FaPagedKept(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), lens,
+                       keep.data_ptr(), n, new.data_ptr(), B, Hk, d, ps, per, P, int(tree_len),
+                       keep.shape[1])
+    rc = (_lib or load_library()).fa_paged_keep(ctypes.byref(kept), handle)
+    if rc:
+        raise FaError(rc, "fa_paged_keep")
+    return new

@@ -18,9 +18,10 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libfa_gb300.so")
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_bwd_strided.cu", "fa_bwd_pair.cu",
            "fa_bwd_dq.cu", "fa_paged.cu", "fa_paged_bwd.cu", "fa_q8_cache.cu", "fa_q8_attn.cu",
+           "fa_rotary.cu", "fa_tree.cu",
            "fa_diag.cu"]
 HEADERS = ["fa_common.cuh", "fa_launch.h", "fa_band.cuh", "fa_once.h", "fa_bwd_common.cuh",
-           "fa_bwd_main.cuh", "fa_q8.cuh", "fa_q8_chunk.cuh", "fa_rows.h"]
+           "fa_bwd_main.cuh", "fa_q8.cuh", "fa_q8_chunk.cuh", "fa_rows.h", "fa_rotary.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -312,6 +312,11 @@ const char* fa_kernel_name(int id) {
     case FA_KERNEL_Q8_READ: return "q8_read_kernel";
     case FA_KERNEL_Q8_ATTN: return "q8_attn_kernel";
     case FA_KERNEL_Q8_COMBINE: return "q8_combine_kernel";
+    case FA_KERNEL_ROTARY: return "rotary_kernel";
+    case FA_KERNEL_PAGED_APPEND: return "paged_append_kernel";
+    case FA_KERNEL_PAGED_KEEP: return "paged_keep_kernel";
+    case FA_KERNEL_TREE_ATTN: return "tree_attn_kernel";
+    case FA_KERNEL_TREE_COMBINE: return "tree_combine_kernel";
     default: return "unknown";
   }
 }
@@ -961,6 +966,302 @@ int fa_q8_paged_attention(const void* q, const fa_q8_cache* cache, const int32_t
   return FA_OK;
 }
 
+// ---------------------------------------------------------------- rotary positions, paged rows
+// The addresses from a strided tensor's first element to its last, as a half-open range.
+struct Extent {
+  uintptr_t lo, hi;
+  bool meets(const Extent& o) const { return lo < o.hi && o.lo < hi; }
+};
+
+// Rows [batch, heads, rows, d] of bf16 with strides; whether they make sense, and what they span.
+static bool row_extent(const void* base, const int64_t* st, int64_t batch, int64_t heads,
+                       int64_t rows, int d, Extent* out) {
+  if (check_bf16(base) != FA_OK) return false;
+  const int64_t n[3] = {batch, heads, rows};
+  double span = d;
+  for (int i = 0; i < 3; ++i) {
+    if (st[i] < 0 || st[i] % 8) return false;
+    span += (double)(n[i] - 1) * (double)st[i];
+  }
+  if (span > 1e15) return false;  // no memory has as many elements (and nothing below overflows)
+  out->lo = reinterpret_cast<uintptr_t>(base);
+  out->hi = out->lo + 2 * (uintptr_t)(d + (batch - 1) * st[0] + (heads - 1) * st[1] +
+                                      (rows - 1) * st[2]);
+  return true;
+}
+
+// Whether no two rows of such a tensor share memory: from the smallest stride on, each dimension's
+// step passes all that the ones before it span.
+static bool rows_nest(const int64_t* st, int64_t batch, int64_t heads, int64_t rows, int d) {
+  int64_t n[3] = {batch, heads, rows}, s[3] = {st[0], st[1], st[2]};
+  int64_t span = d;
+  for (int k = 0; k < 3; ++k) {
+    int at = -1;
+    for (int i = 0; i < 3; ++i)
+      if (n[i] > 1 && (at < 0 || s[i] < s[at])) at = i;
+    if (at < 0) return true;
+    if (s[at] < span) return false;
+    span += (n[at] - 1) * s[at];
+    n[at] = 1;
+  }
+  return true;
+}
+
+static int check_rotary(const fa_rotary* r, int head_dim, bool append) {
+  if (!r || !r->inv_freq || !aligned(r->inv_freq, 8)) return FA_ERR_INVALID;
+  if (r->positions && !aligned(r->positions, 4)) return FA_ERR_INVALID;
+  if (r->pos_stride < 0 || (!r->positions && r->pos_stride != 0)) return FA_ERR_INVALID;
+  if (r->rotary_dim < 16 || r->rotary_dim % 16 || r->rotary_dim > head_dim) return FA_ERR_INVALID;
+  if (r->interleaved != 0 && r->interleaved != 1) return FA_ERR_INVALID;
+  if (r->offset != 0 && (append || r->positions)) return FA_ERR_INVALID;
+  return std::isfinite(r->scale) ? FA_OK : FA_ERR_INVALID;
+}
+
+static fa::Rope rope_of(const fa_rotary* r, int back) {
+  fa::Rope o = {};
+  if (!r) return o;
+  o.inv_freq = r->inv_freq;
+  o.pos = r->positions;
+  o.pos_stride = r->pos_stride;
+  o.offset = r->offset;
+  o.half = r->rotary_dim / 2;
+  o.inter = r->interleaved;
+  o.scale = r->scale;
+  o.sign = back ? -1.0f : 1.0f;
+  return o;
+}
+
+static fa::RowSeg row_seg(const void* src, void* dst, const int64_t* ss, const int64_t* ds,
+                          int heads, bool turn, bool paged) {
+  fa::RowSeg g = {};
+  g.src = static_cast<const __nv_bfloat16*>(src);
+  g.dst = static_cast<__nv_bfloat16*>(dst);
+  for (int i = 0; i < 3; ++i) {
+    g.ss[i] = ss[i];
+    g.ds[i] = ds ? ds[i] : 0;
+  }
+  g.heads = heads;
+  g.turn = turn;
+  g.paged = paged;
+  return g;
+}
+
+static int rows_call(fa::RowsArgs* a, void* stream, const char* where) {
+  int rc = check_device();
+  if (rc) return rc;
+  if (a->rows == 0) return FA_OK;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  cudaError_t e = device_status_word(dev, &a->status);
+  if (e != cudaSuccess) return cuda_fail(e, "status word");
+  e = fa::launch_rows(*a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail(e, where);
+}
+
+int fa_rotary_apply(const fa_rotary_rows* r, const fa_rotary* rotary, int back, void* stream) {
+  if (!r || r->batch <= 0 || r->n_heads <= 0 || r->n_kv_heads < 0 || r->rows < 0 ||
+      r->reserved != 0 || (back != 0 && back != 1))
+    return FA_ERR_INVALID;
+  const int d = r->head_dim;
+  if (d != 64 && d != 128 && d != 256) return FA_ERR_INVALID;
+  int rc = check_rotary(rotary, d, false);
+  if (rc) return rc;
+  const bool packed = r->cu_seqlens != nullptr;
+  if (packed && (!aligned(r->cu_seqlens, 4) || rotary->positions)) return FA_ERR_INVALID;
+  const int64_t rows = (packed ? 1 : (int64_t)r->batch) * r->rows;
+  if (rows > INT32_MAX || (int64_t)r->n_heads + r->n_kv_heads > 65535) return FA_ERR_INVALID;
+  if ((r->k == nullptr) != (r->n_kv_heads == 0) || (r->k == nullptr) != (r->k_out == nullptr))
+    return FA_ERR_INVALID;
+  const int64_t B = packed ? 1 : r->batch, n = r->rows > 0 ? r->rows : 1;
+  const int segs = r->k ? 2 : 1;
+  const void* src[2] = {r->q, r->k};
+  void* dst[2] = {r->q_out, r->k_out};
+  const int64_t* ss[2] = {r->q_stride, r->k_stride};
+  const int64_t* ds[2] = {r->q_out_stride, r->k_out_stride};
+  const int heads[2] = {r->n_heads, r->n_kv_heads};
+  Extent in[2], out[2];
+  for (int i = 0; i < segs; ++i) {
+    if (!row_extent(src[i], ss[i], B, heads[i], n, d, &in[i]) ||
+        !row_extent(dst[i], ds[i], B, heads[i], n, d, &out[i]) ||
+        !rows_nest(ds[i], B, heads[i], n, d))
+      return FA_ERR_INVALID;
+  }
+  for (int i = 0; i < segs; ++i) {
+    for (int j = 0; j < segs; ++j) {
+      bool same = i == j && src[i] == dst[i];  // in place: every element stays where it is
+      const int64_t ext[3] = {B, heads[i], n};
+      for (int k = 0; k < 3; ++k) same = same && (ext[k] == 1 || ss[i][k] == ds[i][k]);
+      if (!same && out[i].meets(in[j])) return FA_ERR_INVALID;
+      if (i != j && out[i].meets(out[j])) return FA_ERR_INVALID;
+    }
+  }
+  fa::RowsArgs a = {};
+  for (int i = 0; i < segs; ++i)
+    a.seg[i] = row_seg(src[i], dst[i], ss[i], ds[i], heads[i], true, false);
+  a.rope = rope_of(rotary, back);
+  a.cu = r->cu_seqlens;
+  a.B = r->batch;
+  a.n = r->rows;
+  a.rows = (int)rows;
+  a.d = d;
+  return rows_call(&a, stream, "rotary launch");
+}
+
+// What the calls that write a paged bf16 cache have in common.
+static int check_cache(const void* k_cache, const void* v_cache, const int32_t* block_table,
+                       const int32_t* lengths, int batch, int n_kv_heads, int head_dim,
+                       int page_size, int max_pages, int num_pages) {
+  if (batch <= 0 || n_kv_heads <= 0 || max_pages <= 0 || num_pages <= 0) return FA_ERR_INVALID;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return FA_ERR_INVALID;
+  if (page_size < 8 || page_size > 256 || (page_size & (page_size - 1))) return FA_ERR_INVALID;
+  if ((int64_t)max_pages * page_size > kMaxLen) return FA_ERR_INVALID;
+  if ((int64_t)num_pages * n_kv_heads > INT32_MAX / 2) return FA_ERR_INVALID;
+  if (!block_table || !lengths || !aligned(block_table, 4) || !aligned(lengths, 4))
+    return FA_ERR_INVALID;
+  const int rc = check_bf16(k_cache);
+  return rc ? rc : check_bf16(v_cache);
+}
+
+int fa_paged_append(const fa_paged_rows* r, const fa_rotary* rotary, void* stream) {
+  if (!r) return FA_ERR_INVALID;
+  const int d = r->head_dim;
+  int rc = check_cache(r->k_cache, r->v_cache, r->block_table, r->lengths, r->batch, r->n_kv_heads,
+                       d, r->page_size, r->max_pages, r->num_pages);
+  if (rc) return rc;
+  if (r->reserved != 0 || r->n_heads < 0) return FA_ERR_INVALID;
+  if (rotary ? (rc = check_rotary(rotary, d, true)) != FA_OK : r->q != nullptr)
+    return FA_ERR_INVALID;
+  const bool packed = r->cu_seqlens != nullptr;
+  if (packed) {
+    if (!aligned(r->cu_seqlens, 4) || r->total < 0 || r->new_len != 0) return FA_ERR_INVALID;
+    if (rotary && rotary->pos_stride != 0) return FA_ERR_INVALID;
+  } else if (r->total != 0 || r->new_len < 1 || r->new_len > kMaxLen) {
+    return FA_ERR_INVALID;
+  }
+  const int64_t B = packed ? 1 : r->batch, n = packed ? (r->total > 0 ? r->total : 1) : r->new_len;
+  if (B * n > INT32_MAX || (int64_t)r->n_heads + 2 * (int64_t)r->n_kv_heads > 65535)
+    return FA_ERR_INVALID;
+  if ((r->q == nullptr) != (r->n_heads == 0) || (r->q == nullptr) != (r->q_out == nullptr))
+    return FA_ERR_INVALID;
+  Extent k, v, q;
+  if (!row_extent(r->k, r->k_stride, B, r->n_kv_heads, n, d, &k) ||
+      !row_extent(r->v, r->v_stride, B, r->n_kv_heads, n, d, &v))
+    return FA_ERR_INVALID;
+  const int64_t q_out_stride[3] = {(int64_t)r->n_heads * n * d, n * d, d};
+  if (r->q) {
+    Extent out, kc, vc;
+    const int64_t cache_rows = (int64_t)r->n_kv_heads * r->page_size;
+    const int64_t flat[3] = {0, cache_rows * d, d};
+    if (!row_extent(r->q, r->q_stride, B, r->n_heads, n, d, &q) ||
+        !row_extent(r->q_out, q_out_stride, B, r->n_heads, n, d, &out) ||
+        !row_extent(r->k_cache, flat, 1, r->num_pages, cache_rows, d, &kc) ||
+        !row_extent(r->v_cache, flat, 1, r->num_pages, cache_rows, d, &vc) || out.meets(q) ||
+        out.meets(k) || out.meets(v) || out.meets(kc) || out.meets(vc))
+      return FA_ERR_INVALID;
+  }
+  fa::RowsArgs a = {};
+  a.seg[0] = row_seg(r->k, r->k_cache, r->k_stride, nullptr, r->n_kv_heads, rotary != nullptr, true);
+  a.seg[1] = row_seg(r->v, r->v_cache, r->v_stride, nullptr, r->n_kv_heads, false, true);
+  if (r->q) a.seg[2] = row_seg(r->q, r->q_out, r->q_stride, q_out_stride, r->n_heads, true, false);
+  a.rope = rope_of(rotary, 0);
+  a.cu = r->cu_seqlens;
+  a.table = r->block_table;
+  a.lens = r->lengths;
+  a.B = r->batch;
+  a.n = packed ? r->total : r->new_len;
+  a.rows = packed ? r->total : (int)(B * n);
+  a.d = d;
+  a.Hk = r->n_kv_heads;
+  a.max_pages = r->max_pages;
+  a.num_pages = r->num_pages;
+  a.ps_shift = log2_of(r->page_size);
+  return rows_call(&a, stream, "paged append launch");
+}
+
+int fa_paged_keep(const fa_paged_kept* r, void* stream) {
+  if (!r) return FA_ERR_INVALID;
+  int rc = check_cache(r->k_cache, r->v_cache, r->block_table, r->lengths, r->batch, r->n_kv_heads,
+                       r->head_dim, r->page_size, r->max_pages, r->num_pages);
+  if (rc) return rc;
+  if (r->tree_len < 1 || r->tree_len > FA_TREE_MAX || r->max_keep < 1 || r->max_keep > r->tree_len)
+    return FA_ERR_INVALID;
+  if ((int64_t)r->n_kv_heads * r->head_dim > 4 << 20) return FA_ERR_INVALID;  // grid y
+  if (!r->keep || !r->counts || !r->new_lengths || !aligned(r->keep, 4) || !aligned(r->counts, 4) ||
+      !aligned(r->new_lengths, 4))
+    return FA_ERR_INVALID;
+  auto ints = [](const int32_t* p, int64_t n) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    return Extent{lo, lo + 4 * (uintptr_t)n};
+  };
+  const Extent out = ints(r->new_lengths, r->batch);
+  if (out.meets(ints(r->lengths, r->batch)) || out.meets(ints(r->counts, r->batch)) ||
+      out.meets(ints(r->keep, (int64_t)r->batch * r->max_keep)) ||
+      out.meets(ints(r->block_table, (int64_t)r->batch * r->max_pages)))
+    return FA_ERR_INVALID;
+  if ((rc = check_device())) return rc;
+  fa::KeepArgs a;
+  a.k_cache = r->k_cache;
+  a.v_cache = r->v_cache;
+  a.table = r->block_table;
+  a.lens = r->lengths;
+  a.keep = r->keep;
+  a.counts = r->counts;
+  a.new_lens = r->new_lengths;
+  a.B = r->batch;
+  a.Hk = r->n_kv_heads;
+  a.d = r->head_dim;
+  a.max_pages = r->max_pages;
+  a.num_pages = r->num_pages;
+  a.ps_shift = log2_of(r->page_size);
+  a.T = r->tree_len;
+  a.M = r->max_keep;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  cudaError_t e = device_status_word(dev, &a.status);
+  if (e != cudaSuccess) return cuda_fail(e, "status word");
+  e = fa::launch_keep(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail(e, "paged keep launch");
+}
+
+int fa_paged_tree_attention(const void* q, const void* k_cache, const void* v_cache,
+                            const int32_t* block_table, const int32_t* lengths,
+                            const uint8_t* tree_mask, int64_t mask_stride, void* o, float* lse,
+                            const fa_paged_params* p, void* stream) {
+  int rc;
+  if ((rc = check_paged(p, q, k_cache, v_cache, block_table, lengths)) || (rc = check_bf16(o)))
+    return rc;
+  if (lse && !aligned(lse, 4)) return FA_ERR_INVALID;
+  if (p->causal != 0 || p->num_splits != 0 || p->q_len > FA_TREE_MAX) return FA_ERR_INVALID;
+  if (!tree_mask || mask_stride < 0) return FA_ERR_INVALID;
+  fa::TreeArgs a;
+  a.q = q;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.table = block_table;
+  a.lens = lengths;
+  a.mask = tree_mask;
+  a.mask_stride = mask_stride;
+  a.o = o;
+  a.lse = lse;
+  a.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  a.B = p->batch;
+  a.Hk = p->n_kv_heads;
+  a.G = p->n_heads / p->n_kv_heads;
+  a.T = p->q_len;
+  a.d = p->head_dim;
+  a.max_pages = p->max_pages;
+  a.num_pages = p->num_pages;
+  a.ps_shift = log2_of(p->page_size);
+  a.scale = p->scale;
+  if ((rc = check_device())) return rc;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  cudaError_t e = device_status_word(dev, &a.status);
+  if (e != cudaSuccess) return cuda_fail(e, "status word");
+  e = fa::launch_tree(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail(e, "tree attention launch");
+}
+
 int fa_device_status(int clear) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1030,7 +1331,7 @@ const char* fa_error_string(int code) {
       return "unsupported: the device is not compute capability 10.3 (the library holds sm_103a code only), or no kernel exists for this head-dim pair";
     case FA_ERR_TOO_LARGE: return "problem needs more scratch than the fixed no-allocation array holds";
     case FA_ERR_BAD_INPUT:
-      return "a paged call met a sequence length or block-table entry out of range";
+      return "a paged call met a sequence length, block-table entry, offset or kept node out of range";
     default: return "unknown error code";
   }
 }

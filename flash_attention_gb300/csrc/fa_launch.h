@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -51,7 +52,12 @@ enum KernelId {
   kKernQ8Read = 11,
   kKernQ8Attn = 12,
   kKernQ8Combine = 13,
-  kNumKernels = 14
+  kKernRotary = 14,
+  kKernPagedAppend = 15,
+  kKernPagedKeep = 16,
+  kKernTreeAttn = 17,
+  kKernTreeCombine = 18,
+  kNumKernels = 19
 };
 
 // Records a timing event before (end = 0) or after (end = 1) a launch on `s` when timing is
@@ -353,5 +359,72 @@ long long q8_attn_tiles(const Q8AttnArgs& a);  // key tiles of all units, at mos
 size_t q8_attn_workspace_bytes(const Q8AttnArgs& a);
 cudaError_t launch_q8_attn(const Q8AttnArgs& a, const Q8AttnMaps& m, void* ws,
                            cudaStream_t stream);
+
+// Rotary positions and the appending of rows to a paged bf16 cache (fa_rotary.cu).
+struct Rope {
+  const double* inv_freq;  // [half], radians per position
+  const int32_t* pos;      // positions of the rows, or nullptr: given by the rows' places
+  long long pos_stride;    // between sequences
+  int offset;              // added to positions that the rows' places give
+  int half;                // rotary_dim / 2, a multiple of 8
+  int inter;               // interleaved pairs
+  float scale;
+  float sign;              // 1, or -1: turn back
+};
+struct RowSeg {  // rows of a number of heads on their way
+  const __nv_bfloat16* src;
+  __nv_bfloat16* dst;            // rows of a tensor, or a cache
+  long long ss[3], ds[3];        // strides (sequence, head, row) in elements
+  int heads;                     // 0: no such segment
+  int turn;                      // by the rotation
+  int paged;                     // dst is a cache [num_pages, Hk, page_size, d]
+  int groups;                    // (set by the launch)
+};
+struct RowsArgs {
+  RowSeg seg[3];
+  Rope rope;
+  const int32_t* cu;     // packed batch: [B + 1] row offsets, or nullptr: n rows each
+  const int32_t* table;  // [B, max_pages] and [B], nullptr without paged segments
+  const int32_t* lens;
+  int* status;
+  int B, n, rows, d;     // rows: of the batch, B * n or the packed total
+  int Hk, max_pages, num_pages, ps_shift;
+};
+cudaError_t launch_rows(const RowsArgs& a, cudaStream_t stream);
+
+// Nodes of a drafted tree, at most (a query row's mask is held in 8 words).
+constexpr int kTreeMax = 256;
+
+// Kept rows of a sequence's last T (fa_rotary.cu).
+struct KeepArgs {
+  void* k_cache;          // bf16 [num_pages, Hk, page_size, d]
+  void* v_cache;
+  const int32_t* table;   // [B, max_pages]
+  const int32_t* lens;    // [B]
+  const int32_t* keep;    // [B, M]
+  const int32_t* counts;  // [B]
+  int32_t* new_lens;      // [B]
+  int* status;
+  int B, Hk, d, max_pages, num_pages, ps_shift, T, M;
+};
+cudaError_t launch_keep(const KeepArgs& a, cudaStream_t stream);
+
+// Attention for a tree of drafted tokens over the paged bf16 cache (fa_tree.cu).
+struct TreeArgs {
+  const void* q;         // bf16 [B, H, T, d]
+  const void* k_cache;   // bf16 [num_pages, Hk, page_size, d]
+  const void* v_cache;
+  const int32_t* table;  // [B, max_pages]
+  const int32_t* lens;   // [B]
+  const uint8_t* mask;   // [T, T] of each sequence, mask_stride apart
+  long long mask_stride;
+  void* o;               // bf16 [B, H, T, d]
+  float* lse;            // [B, H, T] or nullptr
+  int* status;
+  uint64_t wait_limit_ns;
+  int B, Hk, G, T, d, max_pages, num_pages, ps_shift;
+  float scale;
+};
+cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream);
 
 }  // namespace fa

@@ -82,8 +82,9 @@ typedef struct fa_params {
                                    exists for the requested option */
 #define FA_ERR_TOO_LARGE 5      /* the problem needs more scratch than fa_train_bwd_noalloc has */
 #define FA_ERR_BAD_INPUT 6      /* (fa_device_status) a paged call met a sequence length or a
-                                   block-table entry out of range (those keys were read as 0), or
-                                   a call on the 8-bit cache offsets or scales out of range */
+                                   block-table entry out of range (those keys were read as 0), a
+                                   call on the 8-bit cache offsets or scales out of range, or a
+                                   call on rows offsets or kept nodes out of range */
 
 /* Mask element types of fa_options.mask_type. */
 #define FA_MASK_F32 0  /* additive, natural log, float (an entry -inf hides the key) */
@@ -225,7 +226,12 @@ int fa_train_bwd(const void* q, const void* k, const void* v, const void* o, con
 #define FA_KERNEL_Q8_READ 11    /* fa_q8_cache_read */
 #define FA_KERNEL_Q8_ATTN 12    /* fa_q8_paged_attention */
 #define FA_KERNEL_Q8_COMBINE 13 /* merge of the key ranges of fa_q8_paged_attention */
-#define FA_NUM_KERNELS 14
+#define FA_KERNEL_ROTARY 14       /* fa_rotary_apply */
+#define FA_KERNEL_PAGED_APPEND 15 /* fa_paged_append */
+#define FA_KERNEL_PAGED_KEEP 16   /* fa_paged_keep */
+#define FA_KERNEL_TREE_ATTN 17    /* fa_paged_tree_attention */
+#define FA_KERNEL_TREE_COMBINE 18 /* merge of the key ranges of fa_paged_tree_attention */
+#define FA_NUM_KERNELS 19
 
 /* Turns timing on (1) or off (0). Returns FA_OK. */
 int fa_profile_enable(int on);
@@ -444,6 +450,157 @@ int fa_q8_paged_attention(const void* q, const fa_q8_cache* cache, const int32_t
                           const int32_t* lengths, void* o, float* lse, const fa_paged_params* p,
                           void* stream);
 
+/* ------------------------------------------------------------------ rotary positions
+ * Queries and keys turned by their positions on their way to attention, and the gradients' way back.
+ * No counterpart on the pages. Pair i of the first rotary_dim elements of a row at position p, (x1,
+ * x2), turns by the angle a = p * inv_freq[i]:
+ *   y1 = scale * (x1 cos a - x2 sin a),  y2 = scale * (x1 sin a + x2 cos a)
+ * and the elements from rotary_dim on stay as they are. Pair i is the elements i and
+ * i + rotary_dim / 2, or 2 i and 2 i + 1 (interleaved). The angle is that of the 64-bit inv_freq for
+ * any 32-bit position, less than 2^-30 of a turn off for |inv_freq| <= 1 (2^k times that below 2^k).
+ * Stretched contexts are other frequencies and a scale. A frequency that is not finite makes its pairs
+ * NaN. */
+typedef struct fa_rotary {
+  const double* inv_freq;   /* f64 [rotary_dim / 2] on the device, 8-byte aligned: radians a position */
+  const int32_t* positions; /* NULL: given by the rows' places; or int32 on the device, 4-byte aligned:
+                               that of row i of sequence b at b * pos_stride + i (packed: of row i at i) */
+  int64_t pos_stride;       /* >= 0 (0: the same positions for every sequence) */
+  int32_t rotary_dim;       /* a multiple of 16, at most head_dim */
+  int32_t interleaved;      /* 0 or 1 */
+  int32_t offset;           /* added to the places; 0 with positions and in fa_paged_append */
+  float scale;              /* finite; of the turned elements */
+} fa_rotary;
+
+/* Rows of queries and keys, bf16: row i of head h of sequence b at
+ * b * stride[0] + h * stride[1] + i * stride[2] elements. The head_dim elements of a row are
+ * contiguous; strides are multiples of 8 elements and pointers 16-byte aligned, so views into a larger
+ * tensor (a fused projection's output) serve as they are. */
+typedef struct fa_rotary_rows {
+  const void* q;
+  const void* k;            /* NULL with n_kv_heads = 0: queries alone */
+  void* q_out;
+  void* k_out;
+  int64_t q_stride[3];
+  int64_t k_stride[3];
+  int64_t q_out_stride[3];
+  int64_t k_out_stride[3];
+  const int32_t* cu_seqlens; /* NULL, or int32 [batch + 1] on the device: a packed batch of `rows` rows
+                                in all (stride[0] unused), sequence b's being cu_seqlens[b] ..
+                                cu_seqlens[b + 1] - 1, whose places begin at 0 */
+  int32_t batch;             /* >= 1 */
+  int32_t n_heads;           /* >= 1 */
+  int32_t n_kv_heads;        /* >= 0 */
+  int32_t rows;              /* of each sequence (its places are 0 .. rows - 1), or of the packed batch;
+                                >= 0; batch * rows < 2^31 */
+  int32_t head_dim;          /* 64, 128 or 256 */
+  int32_t reserved;          /* must be 0 */
+} fa_rotary_rows;
+
+/* Turns the rows (back = 0), or turns them back by the same angles with the same scale (back = 1): the
+ * gradients of q and k from those of the turned ones. Outputs may be their inputs (same pointer and
+ * strides); otherwise they must not share memory with any input, and rows of outputs must not lie on
+ * one another (looked for as ranges of addresses and by nesting strides: FA_ERR_INVALID). Rows of a
+ * packed batch behind cu_seqlens[batch] are left as they were; offsets that decrease or pass `rows`
+ * make fa_device_status return FA_ERR_BAD_INPUT (then rows may be left out, or have another place).
+ * Returns FA_OK, FA_ERR_INVALID, FA_ERR_UNSUPPORTED or FA_ERR_CUDA. */
+int fa_rotary_apply(const fa_rotary_rows* rows, const fa_rotary* rotary, int back, void* stream);
+
+/* ------------------------------------------------------------------ appending to the paged cache
+ * New keys and values into the bf16 cache of fa_paged_attention, the keys turned by their positions on
+ * the way, and the queries of the same rows turned with them. The rows are those of
+ * fa_q8_cache_write: of `new_len` rows for each sequence, or packed (cu_seqlens non-NULL, sequence b's
+ * being cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of `total`). lengths[b] counts the sequence's keys with
+ * the new rows: its n rows become the positions lengths[b] - n .. lengths[b] - 1 (those below 0 are left
+ * out, so a padded entry of length 0 writes nothing). Strides as for fa_rotary_rows. */
+typedef struct fa_paged_rows {
+  const void* k;
+  const void* v;
+  const void* q;             /* NULL: no queries (n_heads = 0) */
+  void* q_out;               /* bf16 [batch, n_heads, new_len, head_dim], packed [n_heads, total, head_dim];
+                                shares no memory with k, v, q and the caches */
+  void* k_cache;             /* bf16 [num_pages, n_kv_heads, page_size, head_dim], 16-byte aligned */
+  void* v_cache;             /* same */
+  int64_t k_stride[3];
+  int64_t v_stride[3];
+  int64_t q_stride[3];
+  const int32_t* cu_seqlens;  /* NULL, or int32 [batch + 1] on the device, 4-byte aligned */
+  const int32_t* block_table; /* int32 [batch, max_pages] on the device, 4-byte aligned */
+  const int32_t* lengths;     /* int32 [batch] on the device, 4-byte aligned */
+  int32_t batch;              /* >= 1 */
+  int32_t n_heads;            /* >= 0 */
+  int32_t n_kv_heads;         /* >= 1; num_pages * n_kv_heads < 2^30 */
+  int32_t head_dim;           /* 64, 128 or 256 */
+  int32_t page_size;          /* a power of two in [8, 256] */
+  int32_t max_pages;          /* columns of the table; max_pages * page_size <= 2^22 */
+  int32_t num_pages;          /* >= 1 */
+  int32_t total;              /* packed: rows for each head, >= 0; otherwise 0 */
+  int32_t new_len;            /* not packed: rows of each sequence, >= 1; packed: 0 */
+  int32_t reserved;           /* must be 0 */
+} fa_paged_rows;
+
+/* rotary: NULL (keys as they are; then no queries), or the rotation. Its positions are those of the new
+ * rows; NULL: their positions in the cache (for a tree of drafted tokens they are not the same). A page
+ * that a call writes must belong to one sequence of the call. Not checked: two sequences writing one
+ * slot race. A sequence whose length is outside [0, max_pages * page_size] is not written, rows of a
+ * page outside the cache are left out, and both, and offsets that decrease or pass `total`, make
+ * fa_device_status return FA_ERR_BAD_INPUT. Slots of no new row keep what they hold, and rows of q_out
+ * behind cu_seqlens[batch] too. Returns FA_OK, FA_ERR_INVALID, FA_ERR_UNSUPPORTED or FA_ERR_CUDA. */
+int fa_paged_append(const fa_paged_rows* rows, const fa_rotary* rotary, void* stream);
+
+/* ------------------------------------------------------------------ trees of drafted tokens
+ * fa_paged_attention where the q_len new positions are the nodes of a tree: a sequence's last q_len
+ * keys, of which a node sees those that its row of the mask names (its ancestors and itself, say),
+ * and every key before them:
+ *   visible(i, j) = j < lengths[b] - q_len  or  mask[b][i][j - (lengths[b] - q_len)] != 0
+ * for 0 <= j < lengths[b]. O = softmax(scale * q k^T) v; L = natural-log logsumexp; a node that sees no
+ * key gives O = 0 and L = -inf. Trees of fewer than q_len nodes stand at the end of the q_len: the
+ * columns before them, keys of the sequence, are named for every node, and the rows before them give
+ * what nobody reads. What hidden keys and values hold (NaN and infinities included) reaches no row that
+ * does not see them.
+ *   q, o            bf16 [batch, n_heads, q_len, head_dim] (device, 16-byte aligned)
+ *   k_cache, v_cache, block_table, lengths: as for fa_paged_attention
+ *   tree_mask       uint8 [q_len, q_len] for each sequence (device), contiguous, mask_stride bytes apart
+ *                   (0: one tree for all; otherwise >= 0)
+ *   lse             output or NULL: f32 [batch, n_heads, q_len]
+ *   p               causal and num_splits must be 0, q_len at most FA_TREE_MAX
+ * Lengths and table entries out of range as for fa_paged_attention (clamped, read as zeros, reported).
+ * Returns FA_OK, FA_ERR_INVALID, FA_ERR_UNSUPPORTED or FA_ERR_CUDA. */
+#define FA_TREE_MAX 256
+int fa_paged_tree_attention(const void* q, const void* k_cache, const void* v_cache,
+                            const int32_t* block_table, const int32_t* lengths,
+                            const uint8_t* tree_mask, int64_t mask_stride, void* o, float* lse,
+                            const fa_paged_params* p, void* stream);
+
+/* What stays of a tree: of a sequence's last tree_len keys, the counts[b] that keep[b] names move, in
+ * that order, to the front of the tree_len, in both caches, and the sequence's length becomes
+ * max(0, lengths[b] - tree_len + counts[b]). keep names nodes 0 .. tree_len - 1, ascending, so that what
+ * moves never moves up; a node that keeps its place need not exist (a short tree's columns before it).
+ * Keys were turned by their positions when they were appended, and keep them. The rest of the tree's
+ * slots hold anything afterwards. Pages that are moved in must belong to one sequence of the call. */
+typedef struct fa_paged_kept {
+  void* k_cache;              /* bf16 [num_pages, n_kv_heads, page_size, head_dim], 16-byte aligned */
+  void* v_cache;              /* same */
+  const int32_t* block_table; /* int32 [batch, max_pages] on the device, 4-byte aligned */
+  const int32_t* lengths;     /* int32 [batch] on the device, 4-byte aligned */
+  const int32_t* keep;        /* int32 [batch, max_keep] on the device, 4-byte aligned */
+  const int32_t* counts;      /* int32 [batch] on the device: 0 .. max_keep */
+  int32_t* new_lengths;       /* output, int32 [batch] on the device; not one of the inputs */
+  int32_t batch;              /* >= 1 */
+  int32_t n_kv_heads;         /* >= 1; num_pages * n_kv_heads < 2^30 */
+  int32_t head_dim;           /* 64, 128 or 256 */
+  int32_t page_size;          /* a power of two in [8, 256] */
+  int32_t max_pages;          /* max_pages * page_size <= 2^22 */
+  int32_t num_pages;          /* >= 1 */
+  int32_t tree_len;           /* 1 .. FA_TREE_MAX */
+  int32_t max_keep;           /* 1 .. tree_len */
+} fa_paged_kept;
+
+/* A sequence whose length, count or nodes are out of range, whose nodes do not ascend, or of which a
+ * node would move from or to a place before the sequence's start, is left as it was, its length too; a
+ * row of a page outside the cache is left out. Either makes fa_device_status return FA_ERR_BAD_INPUT.
+ * Returns FA_OK, FA_ERR_INVALID, FA_ERR_UNSUPPORTED or FA_ERR_CUDA. */
+int fa_paged_keep(const fa_paged_kept* kept, void* stream);
+
 /* ------------------------------------------------------------------ bounded waits, diagnostics
  * Sets the limit of one barrier wait inside the kernels launched after this call, from any
  * thread (default 2 s; ns = 0 restores it; more than 60 s gives FA_ERR_INVALID). A wait that
@@ -470,8 +627,8 @@ int fa_debug_wait_timeout(uint64_t* waited_ns, void* stream);
 
 /* Synchronises the current device, then returns FA_OK, FA_ERR_DEVICE_TIMEOUT if any kernel of
  * this library on it gave up a bounded wait, or FA_ERR_BAD_INPUT if a paged call met a length,
- * a block-table entry, or (8-bit cache) an offset or a scale out of range, since the last call with
- * clear != 0. */
+ * a block-table entry, an offset, a kept node or (8-bit cache) a scale out of range, since the last
+ * call with clear != 0. */
 int fa_device_status(int clear);
 
 /* Human-readable text of a return code (static storage). */
