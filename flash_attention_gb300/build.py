@@ -21,7 +21,7 @@ SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_bwd_strided.cu", "fa_bwd_p
            "fa_rotary.cu", "fa_tree.cu",
            "fa_diag.cu"]
 HEADERS = ["fa_common.cuh", "fa_launch.h", "fa_band.cuh", "fa_once.h", "fa_bwd_common.cuh",
-           "fa_bwd_main.cuh", "fa_q8.cuh", "fa_q8_chunk.cuh", "fa_rows.h", "fa_rotary.cuh"]
+           "fa_bwd_main.cuh", "fa_q8.cuh", "fa_q8_chunk.cuh", "fa_rows.h", "fa_rotary.cuh", "fa_wait.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -1234,8 +1234,6 @@ int fa_paged_tree_attention(const void* q, const void* k_cache, const void* v_ca
   if (p->causal != 0 || p->num_splits != 0 || p->q_len > FA_TREE_MAX) return FA_ERR_INVALID;
   if (!tree_mask || mask_stride < 0) return FA_ERR_INVALID;
   fa::TreeArgs a;
-  a.q = q;
-  a.k_cache = k_cache;
   a.v_cache = v_cache;
   a.table = block_table;
   a.lens = lengths;
@@ -1253,13 +1251,31 @@ int fa_paged_tree_attention(const void* q, const void* k_cache, const void* v_ca
   a.num_pages = p->num_pages;
   a.ps_shift = log2_of(p->page_size);
   a.scale = p->scale;
+  if (fa::tree_tiles(a) > INT32_MAX / 2) return FA_ERR_INVALID;
   if ((rc = check_device())) return rc;
+  cudaError_t e = get_encoder();
+  if (e != cudaSuccess) return cuda_fail(e, "cuTensorMapEncodeTiled entry point");
   int dev = 0;
   cudaGetDevice(&dev);
-  cudaError_t e = device_status_word(dev, &a.status);
+  e = device_status_word(dev, &a.status);
   if (e != cudaSuccess) return cuda_fail(e, "status word");
-  e = fa::launch_tree(a, static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? FA_OK : cuda_fail(e, "tree attention launch");
+  fa::TreeMaps m;
+  const int box = fa::tree_box_rows(p->page_size);
+  if (!encode_bf16_3d(&m.q, q, a.B * a.Hk, a.G * a.T, a.d, fa::kTreeQRows) ||
+      !encode_bf16_3d(&m.k, k_cache, a.num_pages * a.Hk, p->page_size, a.d, box) ||
+      !encode_bf16_3d(&m.v, v_cache, a.num_pages * a.Hk, p->page_size, a.d, box))
+    return cuda_fail(cudaErrorInvalidValue, "cuTensorMapEncodeTiled");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  void* ws = nullptr;
+  cudaMemPool_t pool = nullptr;
+  if ((e = scratch_pool(dev, &pool)) != cudaSuccess) return cuda_fail(e, "scratch pool");
+  if ((e = cudaMallocFromPoolAsync(&ws, fa::tree_workspace_bytes(a), pool, s)) != cudaSuccess)
+    return cuda_fail(e, "cudaMallocFromPoolAsync (tree attention workspace)");
+  e = fa::launch_tree(a, m, ws, s);
+  const cudaError_t e2 = cudaFreeAsync(ws, s);
+  if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
+  if (e2 != cudaSuccess) return cuda_fail(e2, "cudaFreeAsync (tree attention workspace)");
+  return FA_OK;
 }
 
 int fa_device_status(int clear) {

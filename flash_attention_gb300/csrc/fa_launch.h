@@ -411,9 +411,7 @@ cudaError_t launch_keep(const KeepArgs& a, cudaStream_t stream);
 
 // Attention for a tree of drafted tokens over the paged bf16 cache (fa_tree.cu).
 struct TreeArgs {
-  const void* q;         // bf16 [B, H, T, d]
-  const void* k_cache;   // bf16 [num_pages, Hk, page_size, d]
-  const void* v_cache;
+  const void* v_cache;   // bf16 [num_pages, Hk, page_size, d]
   const int32_t* table;  // [B, max_pages]
   const int32_t* lens;   // [B]
   const uint8_t* mask;   // [T, T] of each sequence, mask_stride apart
@@ -425,6 +423,13 @@ struct TreeArgs {
   int B, Hk, G, T, d, max_pages, num_pages, ps_shift;
   float scale;
 };
-cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream);
+struct TreeMaps {
+  CUtensorMap q, k, v;  // q as [B*Hk, G*T, d]; caches as [num_pages*Hk, page_size, d]
+};
+int tree_box_rows(int page_size);
+constexpr int kTreeQRows = 128;            // rows of q's box
+long long tree_tiles(const TreeArgs& a);   // key tiles of all units, at most
+size_t tree_workspace_bytes(const TreeArgs& a);
+cudaError_t launch_tree(const TreeArgs& a, const TreeMaps& m, void* ws, cudaStream_t stream);
 
 }  // namespace fa

@@ -347,3 +347,26 @@ def test_on_another_stream():
     got = fa.paged_tree_attention(*args, scale=0.1, stream=s)
     s.synchronize()
     assert all(map(torch.equal, got, want))
+
+
+@pytest.mark.parametrize("d,T", [(64, 9), (64, 80), (128, 9), (128, 80), (256, 9)])
+def test_waits_that_run_out_are_reported(d, T):
+    """With a limit of 1 ns the kernel's ordinary waits run out: it winds down, the status says so, and
+    with the limit restored the same call is right."""
+    import torch
+
+    import flash_attention_gb300 as fa
+
+    lengths = [3000, 700]
+    rng, table, (kc, kx), (vc, vx), (q, qx) = make(d, 2, 4, 2, T, d, 16, lengths)
+    m = masks(rng, 2, T, "trees")
+    args = q, kc, vc, ints(table), ints(lengths), torch.from_numpy(m).cuda()
+    try:
+        fa.fa_set_wait_limit_ns(1)
+        fa.paged_tree_attention(*args, scale=0.1)
+        assert fa.fa_device_status(True) == fa.FA_ERR_DEVICE_TIMEOUT
+    finally:
+        fa.fa_set_wait_limit_ns(0)
+    got = fa.paged_tree_attention(*args, scale=0.1)
+    assert fa.fa_device_status(True) == fa.FA_OK
+    check(got, plain.tree_attention(qx, kx, vx, table, lengths, m, 0.1))
