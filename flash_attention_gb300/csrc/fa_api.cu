@@ -87,6 +87,22 @@ bool encode_bf16_3d(CUtensorMap* m, const void* base, int bh, int rows, int d, i
   return r == CUDA_SUCCESS;
 }
 
+// 5-D map over a paged bf16 cache [num_pages * heads, page_size, d] in which one box is up to 64 rows of
+// a page, whole: (64 columns, 8 rows, d / 64 column chunks, page_size / 8 row groups, pages). In shared
+// memory that is [row group][chunk][8 rows][128 bytes], 128-byte swizzled. Pages outside fill with zeros.
+bool encode_bf16_pages(CUtensorMap* m, const void* base, int ph, int page_size, int d, int box_rows) {
+  cuuint64_t dims[5] = {64, 8, (cuuint64_t)d / 64, (cuuint64_t)page_size / 8, (cuuint64_t)ph};
+  cuuint64_t strides[4] = {(cuuint64_t)d * 2, 128, (cuuint64_t)d * 16,
+                           (cuuint64_t)page_size * (cuuint64_t)d * 2};
+  cuuint32_t box[5] = {64, 8, (cuuint32_t)d / 64, (cuuint32_t)box_rows / 8, 1};
+  cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims,
+                        strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // 3-D map over the bytes of a contiguous [bh, rows, d] tensor of 8-bit codes, box (cols, box_rows,
 // 1), rows of cols = 64 or 128 bytes swizzled by their width; reads outside fill with zeros.
 bool encode_u8_3d(CUtensorMap* m, const void* base, int bh, int rows, int d, int cols,
@@ -1261,9 +1277,9 @@ int fa_paged_tree_attention(const void* q, const void* k_cache, const void* v_ca
   if (e != cudaSuccess) return cuda_fail(e, "status word");
   fa::TreeMaps m;
   const int box = fa::tree_box_rows(p->page_size);
-  if (!encode_bf16_3d(&m.q, q, a.B * a.Hk, a.G * a.T, a.d, fa::kTreeQRows) ||
-      !encode_bf16_3d(&m.k, k_cache, a.num_pages * a.Hk, p->page_size, a.d, box) ||
-      !encode_bf16_3d(&m.v, v_cache, a.num_pages * a.Hk, p->page_size, a.d, box))
+  if (!encode_bf16_3d(&m.q, q, a.B * a.Hk, a.G * a.T, a.d, fa::tree_q_rows(a)) ||
+      !encode_bf16_pages(&m.k, k_cache, a.num_pages * a.Hk, p->page_size, a.d, box) ||
+      !encode_bf16_pages(&m.v, v_cache, a.num_pages * a.Hk, p->page_size, a.d, box))
     return cuda_fail(cudaErrorInvalidValue, "cuTensorMapEncodeTiled");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   void* ws = nullptr;

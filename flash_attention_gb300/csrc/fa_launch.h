@@ -424,10 +424,10 @@ struct TreeArgs {
   float scale;
 };
 struct TreeMaps {
-  CUtensorMap q, k, v;  // q as [B*Hk, G*T, d]; caches as [num_pages*Hk, page_size, d]
+  CUtensorMap q, k, v;  // q as [B*Hk, G*T, d]; caches by pages (a box: rows of one page, whole)
 };
 int tree_box_rows(int page_size);
-constexpr int kTreeQRows = 128;            // rows of q's box
+int tree_q_rows(const TreeArgs& a);        // rows of q's box
 long long tree_tiles(const TreeArgs& a);   // key tiles of all units, at most
 size_t tree_workspace_bytes(const TreeArgs& a);
 cudaError_t launch_tree(const TreeArgs& a, const TreeMaps& m, void* ws, cudaStream_t stream);

@@ -10,22 +10,27 @@
 // for all of them; with 4 d bytes and 4 d flops a row for each key, HBM bounds it up to some 280 rows
 // a kv head. Up to that the work beside the bytes has to fit in the time of the bytes, 700 cycles for a
 // tile of 64 keys at head_dim 64, 1400 at 128: two softmax warpgroups (thread = row), which alternate.
-//  * up to 128 rows (PAIR): each has every other key tile, with an O, a maximum and a sum of its own;
-//    they are joined at a unit's end, in tensor memory, where a thread of either can read both O's;
-//  * more rows: each has 128 of a block's 256, on the same key tiles. (At head_dim 256 tensor memory
-//    holds one O: one warpgroup, blocks of 128 rows.)
-// S = Q K^T (M = 128 rows, N = 64 keys) and O += P V, with P in bf16 over S in tensor memory (two S
-// buffers for each warpgroup); the lazy rescale of the training forward. Sums are f32.
+//  * up to 128 rows (PAIR): tiles of 128 keys, of which each has a half, with an O, a maximum and a sum
+//    of its own; they are joined at a unit's end, in tensor memory, where a thread of either can read
+//    both O's;
+//  * more rows: each has 128 of a block's 256, on the same tiles of 64 keys. (At head_dim 256 tensor
+//    memory holds one O: one warpgroup, blocks of 128 rows.)
+// S = Q K^T (M = 128 rows; N = 128 keys for a pair, whose halves' scores lie side by side, else 64) and
+// O += P V, with P in bf16 over S in tensor memory (two S buffers for each warpgroup); the lazy rescale
+// of the training forward. Sums are f32.
 //
-// Work: the (sequence, kv head, row block) units, each ceil(len / 64) key tiles, form one list of
+// Work: the (sequence, kv head, row block) units, each with its key tiles, form one list of
 // tiles, cut evenly over persistent CTAs, one on an SM (the lengths are on the device; each CTA finds
 // its part from them). A unit counts kUnitCost tiles more than it has, what its start and end cost. A
 // CTA writes the units it has whole; of the others it leaves its share's O, m and sum, which a second
 // kernel joins in the order of the keys.
 //
-// Warps: 0-3 (0-7) softmax, then one each for the copies of K and V pages (TMA boxes of
-// min(page_size, 64) rows), for S, for O, and for the list: it walks the list two units ahead, packs
-// the tree's mask into words and loads Q. The mask is tested in the tiles of the last T keys alone.
+// Warps: 0-3 (0-7) softmax, then one each for the copies of K pages, of V pages, for S, for O, and for
+// the list: it walks the list two units ahead, packs the tree's mask into words and loads Q. A page's
+// part of a tile is one TMA box, min(page_size, 64) rows of all columns: what limits small copies is
+// the number of them a warp can issue (copies alone, 131072 keys of 8 heads, head_dim 128, pages of 16:
+// 4.6 TB/s with a box for each 64 columns, 5.7 with one box, 6.3 with a warp each for K and V; pages of 8:
+// 3.0, 4.2, 5.7). The mask is tested in the tiles of the last T keys alone.
 // There a value that is not finite must meet no weight of a row that does not see it, not even 0: the
 // O warp clears it, and rows that see it get it added at the end (tree_odd).
 #include <float.h>
@@ -39,35 +44,52 @@
 namespace fa {
 
 namespace {
-constexpr int kKT = 64;          // keys of a tile
-constexpr int kUnitCost = 4;     // tiles' worth of a unit's start and end
+constexpr int kHT = 64;          // keys of a stage of the rings: of a tile, or half of one (PAIR)
+constexpr int kUnitCost = 3;     // tiles' worth of a unit's start and end
 constexpr int kPageChunk = 128;  // block-table entries staged at a time
 constexpr int kUnits = 3;        // units published
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;
 
-template <int HD, bool PAIR>
+template <int HD, bool PAIR, int C>
 struct TreeLayout {
   static constexpr int NWG = HD <= 128 ? 2 : 1;      // softmax warpgroups
-  static constexpr int ROWS = PAIR ? 128 : 128 * NWG;  // query rows of a unit
-  static constexpr int ST = HD == 64 ? 8 : HD == 128 ? 4 : 2;  // stages of the K ring and the V ring
+  static constexpr int RC = 128 / C;                 // query rows of a copy
+  static constexpr int ROWS = PAIR ? RC : 128 * NWG;  // of a unit
+  static constexpr int KT = PAIR ? 2 * kHT : kHT;    // keys of a tile
+  static constexpr int HALVES = KT / kHT;
+  // stages of the rings; V has more where there is room, as a V stage stays until the weights of its
+  // keys are there (K's are even: the halves of a tile are one operand)
+  static constexpr int KST = HD == 64 ? 8 : HD == 128 ? (PAIR ? 6 : 4) : 2;
+  static constexpr int VST = HD == 64 ? 12 : HD == 128 ? (PAIR ? 5 : 4) : 2;
   static constexpr int KCH = HD / 64;
-  static constexpr int Q_BYTES = 128 * HD * 2;       // of 128 rows; PAIR: two units' Q, else a unit's
-  static constexpr int KV_BYTES = kKT * HD * 2;
-  static constexpr int OFF_K = NWG * Q_BYTES;
-  static constexpr int OFF_V = OFF_K + ST * KV_BYTES;
-  static constexpr int OFF_BITS = OFF_V + ST * KV_BYTES;  // mask words, kUnits * T * ceil(T / 32)
-  static constexpr int COL_S = NWG * HD;             // O of each warpgroup, then its two S
+  static constexpr int Q_BYTES = 128 * HD * 2;       // of 128 rows
+  // Units whose Q is held: a second one costs stages. (Its load runs beside a unit's last softmax.)
+  static constexpr int QB = PAIR && HD == 64 ? 2 : 1;
+  static constexpr int ST_BYTES = kHT * HD * 2;
+  static constexpr int OFF_K = (PAIR ? QB : NWG) * Q_BYTES;
+  static constexpr int OFF_V = OFF_K + KST * ST_BYTES;
+  static constexpr int OFF_JOIN = OFF_V + VST * ST_BYTES;  // 16 columns of the copies' O
+  static constexpr int OFF_BITS = OFF_JOIN + (C > 1 ? NWG * 128 * 64 : 0);  // the masks' words
+  static constexpr int COL_S = NWG * HD;             // O of each warpgroup, then S
   static constexpr int TMEM_COLS = 512;
   static constexpr int SOFT = 4 * NWG;
-  static constexpr int TMA_WARP = SOFT, S_WARP = SOFT + 1, O_WARP = SOFT + 2, LIST_WARP = SOFT + 3;
-  static constexpr int THREADS = 32 * (SOFT + 4);
-  static_assert(!PAIR || NWG == 2, "pairs need two warpgroups");
-  static_assert(COL_S + NWG * 2 * kKT <= TMEM_COLS, "TMEM budget");
-  static int smem_bytes(int T) { return OFF_BITS + kUnits * T * ((T + 31) / 32) * 4 + 1024; }
-  static_assert(OFF_BITS + kUnits * kTreeMax * (kTreeMax / 32) * 4 + 1024 + 8192 <= 227 * 1024,
-                "shared memory budget");
+  static constexpr int K_WARP = SOFT, V_WARP = SOFT + 1, S_WARP = SOFT + 2, O_WARP = SOFT + 3,
+                       LIST_WARP = SOFT + 4;
+  static constexpr int THREADS = 32 * (SOFT + 5);
+  // columns of S (and P) of warpgroup w in its buffer b: for a pair the two lie side by side
+  static __device__ __forceinline__ uint32_t col_s(int w, int b) {
+    return COL_S + (PAIR ? b * 2 + w : w * 2 + b) * kHT;
+  }
+  static_assert(!PAIR || (NWG == 2 && KST % 2 == 0), "pairs need two warpgroups");
+  static_assert(C == 1 || PAIR, "copies are of a pair's rows");
+  static_assert(COL_S + NWG * 2 * kHT <= TMEM_COLS, "TMEM budget");
+  static constexpr int T_MAX = PAIR ? RC : kTreeMax;
+  static constexpr int smem_bytes(int T) {
+    return OFF_BITS + kUnits * T * ((T + 31) / 32) * 4 + 1024;
+  }
+  static_assert(smem_bytes(T_MAX) + 8192 <= 227 * 1024, "shared memory budget");
 };
 
 struct TreeK {
@@ -81,7 +103,7 @@ struct TreeK {
   float* o_part;   // [2 * grid, HD / 4, ROWS, 4]: O of a share, in units of 2^m
   float* ml_part;  // [2 * grid, 2, ROWS]: m and the sum
   int* status;
-  int B, Hk, T, words, rows, rb, max_pages, num_pages, ps_shift;
+  int B, Hk, T, words, rows, rb, max_pages, num_pages, ps_shift, kt_shift;
   float scale_log2;
   unsigned long long wait_limit_ns;
 };
@@ -94,7 +116,7 @@ __device__ __forceinline__ int tree_len(const TreeK& p, int b) {
 // What a unit of sequence b counts in the list; 0 without keys.
 __device__ __forceinline__ int tree_cost(const TreeK& p, int b) {
   const int len = tree_len(p, b);
-  return len > 0 ? (len + kKT - 1) / kKT + kUnitCost : 0;
+  return len > 0 ? ((len - 1) >> p.kt_shift) + 1 + kUnitCost : 0;
 }
 // The sum over all sequences (of one unit each), by one warp that has that of sequence `lane`. The
 // host has checked that the whole list, Hk * rb times as long, fits 31 bits.
@@ -187,6 +209,7 @@ struct TreeUnit {
 struct TreeRing {
   int4 at[kUnits][2];
   uint64_t full[kUnits], free[kUnits];
+  uint64_t bits_full[kUnits];       // the mask's words are there
   uint64_t odd_full[kUnits];        // the O warp has looked at all the unit's tiles
   unsigned odd[kUnits][kTreeMax / 32];  // nodes whose values are not all finite
 };
@@ -204,6 +227,14 @@ __device__ __forceinline__ bool take_unit(TreeRing* ring, int un, TreeUnit& u, b
   end = c.z < 0;
   return true;
 }
+// The tiles of the next unit, for a single thread: 0 at the end, -1 where a wait ran out.
+__device__ __forceinline__ int take_tiles(TreeRing* ring, int un, WaitCtl* wctl) {
+  const int slot = un % kUnits;
+  if (!wait(&ring->full[slot], (un / kUnits) & 1, wctl)) return -1;
+  const int ja = ring->at[slot][0].w, jb = ring->at[slot][1].x, c = ring->at[slot][1].z;
+  mbar_arrive(&ring->free[slot]);
+  return c < 0 ? 0 : jb - ja;
+}
 
 // Bits [s, s + 32) of a node's row of mask words: ones before it, zeros behind it.
 __device__ __forceinline__ uint32_t mask_bits(const unsigned* row, int words, int s) {
@@ -213,30 +244,32 @@ __device__ __forceinline__ uint32_t mask_bits(const unsigned* row, int words, in
   return __funnelshift_r(lo, hi, s & 31);
 }
 
-// Packs a tree's mask [T, T] into words, 32 of them in flight (warp-wide).
+// Packs a tree's mask [T, T] into words, a lane a word (warp-wide).
 __device__ __forceinline__ void pack_mask(const uint8_t* mask, unsigned* out, int T, int words,
                                           int lane) {
-  const int n = T * words;
+  const bool wide = (T & 3) == 0 && (reinterpret_cast<uintptr_t>(mask) & 3) == 0;
 #pragma unroll 1
-  for (int f0 = 0; f0 < n; f0 += 32) {
-    uint8_t x[32];
-    int i = f0 / words, w = f0 - i * words;
+  for (int f = lane; f < T * words; f += 32) {
+    const int i = f / words, c0 = (f - i * words) * 32;
+    const uint8_t* x = mask + (size_t)i * T + c0;
+    const int n = min(32, T - c0);
+    unsigned m = 0;
+    if (wide) {  // 4 bytes at once (n is a multiple of 4 then)
+      uint32_t y[8];
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const int c = 32 * w + lane;
-      x[e] = f0 + e < n && c < T ? mask[(size_t)i * T + c] : (uint8_t)0;
-      if (++w == words) {
-        w = 0;
-        ++i;
-      }
-    }
-    unsigned mine = 0;
+      for (int e = 0; e < 8; ++e)
+        y[e] = 4 * e < n ? *reinterpret_cast<const uint32_t*>(x + 4 * e) : 0u;
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const unsigned m = __ballot_sync(0xffffffffu, x[e] != 0);
-      if (lane == e) mine = m;
+      for (int e = 0; e < 8; ++e)  // bytes that are not 0, as 1, gathered into the top four bits
+        m |= ((__vcmpne4(y[e], 0u) & 0x01010101u) * 0x10204080u >> 28) << (4 * e);
+    } else {
+      uint8_t y[32];
+#pragma unroll
+      for (int e = 0; e < 32; ++e) y[e] = e < n ? x[e] : (uint8_t)0;
+#pragma unroll
+      for (int e = 0; e < 32; ++e) m |= (unsigned)(y[e] != 0) << e;
     }
-    if (f0 + lane < n) out[f0 + lane] = mine;
+    out[f] = m;
   }
 }
 
@@ -245,6 +278,8 @@ __device__ __forceinline__ uint32_t odd_halves(uint32_t x) {
   return __vcmpgeu2(x & 0x7fff7fffu, 0x7f807f80u);
 }
 
+// Tiles of K and V lie in shared memory as [8 rows][64 columns] blocks of 1024 bytes, swizzled, those
+// of 8 rows one after another.
 // A V tile that has keys of the tree or rows behind the sequence's end: clears those rows, and values
 // of the tree's keys that are not finite, whose nodes go into `odd`. Warp-wide; out of line, as such
 // tiles are few.
@@ -253,39 +288,75 @@ __device__ __noinline__ void tree_tile(uint8_t* vt, int n0, int tree0, int len, 
                                        int lane) {
   constexpr int G8 = HD / 8;  // 16-byte groups of a row
   auto at = [&](int r, int g) {
-    return reinterpret_cast<uint4*>(vt + g / 8 * (kKT * 128) + r * 128 + ((g % 8) ^ (r & 7)) * 16);
+    return reinterpret_cast<uint4*>(vt + (r / 8 * (HD / 64) + g / 8) * 1024 + (r & 7) * 128 +
+                                    ((g % 8) ^ (r & 7)) * 16);
   };
-  const int end = min(kKT, len - n0);
+  const int end = min(kHT, len - n0);
 #pragma unroll 1
-  for (int e = lane + max(0, tree0 - n0) * G8; e < end * G8; e += 32) {
-    const int r = e / G8;
-    uint4* x = at(r, e % G8);
-    uint4 v = *x;
-    const uint4 z = make_uint4(odd_halves(v.x), odd_halves(v.y), odd_halves(v.z), odd_halves(v.w));
-    if (z.x | z.y | z.z | z.w) {
-      *x = make_uint4(v.x & ~z.x, v.y & ~z.y, v.z & ~z.z, v.w & ~z.w);
-      const int node = n0 + r - tree0;
-      atomicOr(&odd[node >> 5], 1u << (node & 31));
+  for (int e0 = lane + max(0, tree0 - n0) * G8; e0 < end * G8; e0 += 4 * 32) {
+    uint4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int e = e0 + 32 * k;
+      v[k] = e < end * G8 ? *at(e / G8, e % G8) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint4 x = v[k];
+      const uint4 z = make_uint4(odd_halves(x.x), odd_halves(x.y), odd_halves(x.z), odd_halves(x.w));
+      if (z.x | z.y | z.z | z.w) {
+        const int e = e0 + 32 * k, node = n0 + e / G8 - tree0;
+        *at(e / G8, e % G8) = make_uint4(x.x & ~z.x, x.y & ~z.y, x.z & ~z.z, x.w & ~z.w);
+        atomicOr(&odd[node >> 5], 1u << (node & 31));
+      }
     }
   }
-#pragma unroll 1
-  for (int e = lane + end * G8; e < kKT * G8; e += 32) *at(e / G8, e % G8) = make_uint4(0, 0, 0, 0);
+#pragma unroll 4
+  for (int e = lane + end * G8; e < kHT * G8; e += 32) *at(e / G8, e % G8) = make_uint4(0, 0, 0, 0);
 }
 
-// Values that tree_tile has cleared, of the nodes that a row sees, added to 8 of its columns.
-__device__ __noinline__ void tree_odd(const TreeK& p, float* x, const unsigned* odd,
-                                      const unsigned* sees, const TreeUnit& u, int HD, int c) {
-  const int tree0 = u.len - p.T;
+// Values that tree_tile has cleared, of the nodes that a row sees, added to N of its columns.
+template <int HD, int N>
+__device__ __forceinline__ void tree_odd(const TreeK& p, float (&x)[N], const unsigned* odd,
+                                         const unsigned* sees, const TreeUnit& u, int c) {
+#pragma unroll 1
   for (int n = 0; n < p.T; ++n) {
     if (!(odd[n >> 5] >> (n & 31) & sees[n >> 5] >> (n & 31) & 1)) continue;
-    const int key = tree0 + n, slot = key & ((1 << p.ps_shift) - 1);
+    const int key = u.len - p.T + n, slot = key & ((1 << p.ps_shift) - 1);
     const int page = p.table[(size_t)u.b * p.max_pages + (key >> p.ps_shift)];  // (it has been read)
     const __nv_bfloat16* v = p.v + ((((size_t)page * p.Hk + u.kh) << p.ps_shift) + slot) * HD + c;
-    for (int e = 0; e < 8; ++e) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
       const float f = __bfloat162float(v[e]);
       if (!isfinite(f)) x[e] += f;
     }
   }
+}
+
+// The weights of a copy's keys, zeros for the others.
+template <int C>
+__device__ __forceinline__ void store_weights(uint32_t at, const uint32_t (&pk)[32 / C], int copy) {
+#pragma unroll
+  for (int k = 0; k < C; ++k) {
+    uint32_t x[32 / C];
+#pragma unroll
+    for (int e = 0; e < 32 / C; ++e) x[e] = k == copy ? pk[e] : 0u;
+    if constexpr (C == 2)
+      tmem_st16(at + k * 16, x);
+    else
+      asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(
+                       at + k * 8),
+                   "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]),
+                   "r"(x[7])
+                   : "memory");
+  }
+}
+// The barrier of a warpgroup's threads.
+__device__ __forceinline__ void group_sync(int wg) {
+  if (wg == 0)
+    asm volatile("barrier.cta.sync 2, 128;" ::: "memory");
+  else
+    asm volatile("barrier.cta.sync 3, 128;" ::: "memory");
 }
 
 // The barrier of the softmax's threads; true where any of them came with `v`.
@@ -301,24 +372,26 @@ __device__ __forceinline__ bool soft_any(bool v) {
   return r != 0;
 }
 
-template <int HD, bool PAIR>
-__global__ void __launch_bounds__(TreeLayout<HD, PAIR>::THREADS, 1)
+template <int HD, bool PAIR, int C>
+__global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, 1)
     tree_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                 const __grid_constant__ CUtensorMap mV, const TreeK p) {
-  using LY = TreeLayout<HD, PAIR>;
-  constexpr int ST = LY::ST, KCH = LY::KCH, NWG = LY::NWG;
+  using LY = TreeLayout<HD, PAIR, C>;
+  constexpr int KCH = LY::KCH, NWG = LY::NWG, HALVES = LY::HALVES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  // Item n of a warpgroup: its n-th tile. S and P of it are in its buffer n & 1.
-  __shared__ uint64_t k_full[ST], v_full[ST], k_empty[ST], v_empty[ST];
+  // Tile g's S is in buffer g & 1. s_full: it is there (a pair's, of both, in [0]); p_full: P is, of a
+  // warpgroup; p_done: O has it. (The rings' empty barriers are their own: a stage may be filled again
+  // when the phase of p_done or s_full that freed it is two phases old.)
+  __shared__ uint64_t k_full[LY::KST], v_full[LY::VST], k_empty[LY::KST], v_empty[LY::VST];
   __shared__ uint64_t s_full[NWG][2], p_full[NWG][2], p_done[NWG][2], q_full[2], q_free[2];
   __shared__ uint64_t o_free, drain_s, drain_o;
   __shared__ __align__(16) TreeRing units;
   __shared__ uint32_t tmem_base_s;
   __shared__ WaitCtl wctl;
   __shared__ int bad_input;
-  __shared__ int page_s[kPageChunk];
+  __shared__ int page_s[2][kPageChunk];
   __shared__ float2 ml_s[2][2][128];  // of a unit (even, odd): m and the sum of each warpgroup's rows
   unsigned* bits = reinterpret_cast<unsigned*>(smem + LY::OFF_BITS);
 
@@ -327,10 +400,13 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR>::THREADS, 1)
     wait_ctl_init(&wctl, p.wait_limit_ns);
     bad_input = 0;
 #pragma unroll 1
-    for (int s = 0; s < ST; ++s) {
+    for (int s = 0; s < LY::KST; ++s) {
       mbar_init(&k_full[s], 1);
-      mbar_init(&v_full[s], 1);
       mbar_init(&k_empty[s], 1);
+    }
+#pragma unroll 1
+    for (int s = 0; s < LY::VST; ++s) {
+      mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], 1);
     }
 #pragma unroll 1
@@ -346,7 +422,8 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR>::THREADS, 1)
 #pragma unroll 1
     for (int s = 0; s < kUnits; ++s) {
       mbar_init(&units.full[s], 1);
-      mbar_init(&units.free[s], 3 + LY::SOFT);
+      mbar_init(&units.free[s], 4 + LY::SOFT);
+      mbar_init(&units.bits_full[s], 1);
       mbar_init(&units.odd_full[s], 1);
     }
     mbar_init(&o_free, LY::SOFT);
@@ -364,19 +441,20 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR>::THREADS, 1)
   const uint32_t tbase = tmem_base_s;
   grid_dep_trigger();
 
-  if (warp == LY::TMA_WARP) {
-    // ------------------------------------------------------------------ K and V copies
-    const bool leader = lane == 0;
-    if (leader) {
-      tma_prefetch_desc(&mK);
-      tma_prefetch_desc(&mV);
-    }
-    const int box = min(1 << p.ps_shift, kKT);  // rows of a box
-    const int boxes = kKT / box * KCH;          // of a tile (at most 32)
+  if (warp == LY::K_WARP || warp == LY::V_WARP) {
+    // ------------------------------------------------------------------ K or V copies
+    const bool leader = lane == 0, is_v = warp == LY::V_WARP;
+    const CUtensorMap* map = is_v ? &mV : &mK;
+    uint64_t* full = is_v ? v_full : k_full;
+    uint8_t* ring = smem + (is_v ? LY::OFF_V : LY::OFF_K);
+    const int ST = is_v ? LY::VST : LY::KST;
+    int* pages = page_s[is_v];
+    if (leader) tma_prefetch_desc(map);
+    const int box = min(1 << p.ps_shift, kHT);  // rows of a box
+    const int boxes = kHT / box;                // of a tile (at most 8)
     const int z_oob = p.num_pages * p.Hk;       // a page past the cache: zero fill
-    const int sub = lane / KCH, c = lane % KCH; // this lane's box
-    int g = 0, gk = 0, gv = 0;                  // tiles, and copies of K and V, so far
-    int page_b = -1, page_lo = 0;               // page_s: entries page_lo .. of sequence page_b
+    int g = 0, st = 0;                          // copies so far, the next one's stage
+    int page_b = -1, page_lo = 0;               // pages: entries page_lo .. of sequence page_b
     TreeUnit w;
     bool ok = true, end = false;
 #pragma unroll 1
@@ -384,9 +462,9 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR>::THREADS, 1)
       const int used = (w.len + (1 << p.ps_shift) - 1) >> p.ps_shift;
       const int32_t* row = p.table + (size_t)w.b * p.max_pages;
 #pragma unroll 1
-      for (int j = w.ja; j < w.jb && ok; ++j, ++g) {
-        const int n0 = j * kKT;
-        const int p_lo = n0 >> p.ps_shift, p_hi = min(used - 1, (n0 + kKT - 1) >> p.ps_shift);
+      for (int j = w.ja * HALVES; j < w.jb * HALVES; ++j, ++g) {
+        const int n0 = j * kHT;  // (past the sequence's end: zeros, and no page)
+        const int p_lo = n0 >> p.ps_shift, p_hi = min(used - 1, (n0 + kHT - 1) >> p.ps_shift);
         if (page_b != w.b || p_lo < page_lo || p_hi >= page_lo + kPageChunk) {
           page_b = w.b;
           page_lo = p_lo;
@@ -399,84 +477,80 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR>::THREADS, 1)
               pg = -1;
               bad_input = 1;
             }
-            page_s[e] = pg;
+            pages[e] = pg;
           }
           __syncwarp();
         }
-        const int key = n0 + sub * box;
+        const int key = n0 + lane * box;  // of this lane's box
         int z = z_oob, y = 0;
         if (lane < boxes && key < w.len) {
-          const int pg = page_s[(key >> p.ps_shift) - page_lo];
+          const int pg = pages[(key >> p.ps_shift) - page_lo];
           if (pg >= 0) {
             z = pg * p.Hk + w.kh;
-            y = key & ((1 << p.ps_shift) - 1);
+            y = (key & ((1 << p.ps_shift) - 1)) >> 3;
           }
         }
-        const int st = g % ST;
-        const uint32_t use = g / ST;
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-          uint64_t* full = which ? &v_full[st] : &k_full[st];
-          if (leader) {
-            if (use > 0) ok = wait(which ? &v_empty[st] : &k_empty[st], (use - 1) & 1, &wctl);
-            if (ok) mbar_arrive_expect_tx(full, LY::KV_BYTES);
-          }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) break;
-          uint8_t* dst = smem + (which ? LY::OFF_V : LY::OFF_K) + st * LY::KV_BYTES +
-                         c * (kKT * 128) + sub * box * 128;
-          if (lane < boxes) tma_load_3d(dst, which ? &mV : &mK, full, c * 64, y, z);
-          ++(which ? gv : gk);
+        if (leader) {
+          // (of K, a tile's stages are freed as one)
+          uint64_t* empty = is_v ? &v_empty[st] : &k_empty[st / HALVES * HALVES];
+          if (g >= ST) ok = wait(empty, (g / ST - 1) & 1, &wctl);
+          if (ok) mbar_arrive_expect_tx(&full[st], LY::ST_BYTES);
         }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        if (lane < boxes)
+          tma_load_5d(ring + st * LY::ST_BYTES + lane * box * (HD * 2), map, &full[st], 0, 0, 0, y,
+                      z);
+        if (++st == ST) st = 0;
       }
     }
     if (leader) {  // no copy may be in flight when the CTA ends
 #pragma unroll 1
       for (int s = 0; s < ST; ++s) {
-        const int nk = (gk - s + ST - 1) / ST, nv = (gv - s + ST - 1) / ST;  // copies into stage s
-        if (nk > 0) mbar_wait_drain(&k_full[s], (nk - 1) & 1);
-        if (nv > 0) mbar_wait_drain(&v_full[s], (nv - 1) & 1);
+        const int n = (g - s + ST - 1) / ST;  // copies into stage s
+        if (n > 0) mbar_wait_drain(&full[s], (n - 1) & 1);
       }
     }
   } else if (warp == LY::S_WARP) {
     // ------------------------------------------------------------------ S = Q K^T
-    const uint32_t id = idesc_bf16(128, kKT, 0, 0);
-    int g = 0;
-    TreeUnit w;
-    bool ok = true, end = false;
+    if (lane == 0) {
+      const uint32_t id = idesc_bf16(128, LY::KT, 0, 0);
+      const Desc k0 = make_desc(smem_u32(smem + LY::OFF_K), 16, KCH * 1024);
+      int g = 0, st = 0;
+      bool ok = true;
 #pragma unroll 1
-    for (int un = 0; ok && (ok = take_unit<true>(&units, un, w, end, lane, &wctl)) && !end; ++un) {
-      const int qs = PAIR ? un & 1 : 0;
-      ok = wait_warp<false>(&q_full[qs], (PAIR ? un >> 1 : un) & 1, &wctl);
+      for (int un = 0; ok; ++un) {
+        const int tiles = take_tiles(&units, un, &wctl);
+        if (tiles <= 0) break;
+        const int qs = un % LY::QB;
+        const uint32_t qp = un / LY::QB & 1;
+        // (a poll that is not suspended first: where a short limit runs out)
+        ok = mbar_test_wait(&q_full[qs], qp) || wait_more(&q_full[qs], qp, &wctl);
 #pragma unroll 1
-      for (int j = w.ja; j < w.jb && ok; ++j, ++g) {
-        const int st = g % ST;
-        ok = wait_warp(&k_full[st], (g / ST) & 1, &wctl);
-#pragma unroll
-        for (int i = 0; i < (PAIR ? 1 : NWG); ++i) {
-          const int wg = PAIR ? g & 1 : i, n = PAIR ? g >> 1 : g, buf = n & 1;
-          // the buffer's last P is done with
-          if (ok && n >= 2) ok = wait_warp(&p_done[wg][buf], ((n >> 1) - 1) & 1, &wctl);
+        for (int e = g + tiles; ok && g < e; ++g) {
+          const int buf = g & 1;
+          const uint32_t before = ((g >> 1) - 1) & 1;  // the buffer's last P is done with
+          for (int w = 0; w < NWG; ++w)
+            if (ok && g >= 2) ok = wait(&p_done[w][buf], before, &wctl);
+          for (int h = 0; h < HALVES; ++h)
+            ok = ok && wait(&k_full[st + h], (g * HALVES / LY::KST) & 1, &wctl);
           if (!ok) break;
           tc_fence_after();
-          if (lane == 0) {
-            const Desc qa = make_desc(smem_u32(smem + (PAIR ? qs : i) * LY::Q_BYTES), 16, 1024);
-            const Desc kb = make_desc(smem_u32(smem + LY::OFF_K + st * LY::KV_BYTES), 16, 1024);
-            const uint32_t tS = tbase + LY::COL_S + (wg * 2 + buf) * kKT;
+          const Desc kb{k0.at(st * LY::ST_BYTES), k0.hi};
+#pragma unroll
+          for (int w = 0; w < (PAIR ? 1 : NWG); ++w) {
+            const Desc qa = make_desc(smem_u32(smem + (PAIR ? qs : w) * LY::Q_BYTES), 16, 1024);
 #pragma unroll
             for (int ks = 0; ks < HD / 16; ++ks)
-              mma_ss2(tS, qa.at((ks / 4) * (128 * 128) + (ks % 4) * 32), qa.hi,
-                      kb.at((ks / 4) * (kKT * 128) + (ks % 4) * 32), kb.hi, id, ks > 0 ? 1u : 0u);
-            mma_commit(&s_full[wg][buf]);
+              mma_ss2(tbase + LY::col_s(w, buf), qa.at((ks / 4) * (128 * 128) + (ks % 4) * 32), qa.hi,
+                      kb.at((ks / 4) * 1024 + (ks % 4) * 32), kb.hi, id, ks > 0 ? 1u : 0u);
+            mma_commit(&s_full[w][buf]);
           }
-          __syncwarp();
+          mma_commit(&k_empty[st]);
+          st = st + HALVES == LY::KST ? 0 : st + HALVES;
         }
-        if (ok && lane == 0) mma_commit(&k_empty[st]);
+        if (ok) mma_commit(&q_free[qs]);
       }
-      if (ok && lane == 0) mma_commit(&q_free[qs]);
-      __syncwarp();
-    }
-    if (lane == 0) {
       mma_commit(&drain_s);
       mbar_wait_drain(&drain_s, 0);
     }
@@ -484,7 +558,8 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR>::THREADS, 1)
   } else if (warp == LY::O_WARP) {
     // ------------------------------------------------------------------ O += P V
     const uint32_t id = idesc_bf16(128, HD, 0, 1);
-    int g = 0;
+    int g = 0, st = 0;
+    uint32_t vp = 0;  // stage of V, and its phase
     TreeUnit w;
     bool ok = true, end = false;
 #pragma unroll 1
@@ -492,38 +567,44 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR>::THREADS, 1)
       const int slot = un % kUnits, tree0 = w.len - p.T;
 #pragma unroll 1
       for (int j = w.ja; j < w.jb && ok; ++j, ++g) {
-        const int st = g % ST, n0 = j * kKT;
-        uint8_t* vt = smem + LY::OFF_V + st * LY::KV_BYTES;
-        ok = wait_warp(&v_full[st], (g / ST) & 1, &wctl);
-        if (!ok) break;
-        if (n0 + kKT > tree0) {
-          tree_tile<HD>(vt, n0, tree0, w.len, units.odd[slot], lane);
-          fence_proxy_async();
-          __syncwarp();
-        }
-        if (j == w.jb - 1 && lane == 0) mbar_arrive(&units.odd_full[slot]);
-        // a unit's first O is written over the last one's when both warpgroups have read that
+        const int buf = g & 1;
+        // a pair's first O is written over the last unit's when both warpgroups have read that
         if (PAIR && j == w.ja && un > 0) ok = wait_warp(&o_free, (un - 1) & 1, &wctl);
+        uint8_t* vt = smem;
+        int vst = 0;
 #pragma unroll
-        for (int i = 0; i < (PAIR ? 1 : NWG); ++i) {
-          const int wg = PAIR ? g & 1 : i, n = PAIR ? g >> 1 : g, buf = n & 1;
-          ok = ok && wait_warp(&p_full[wg][buf], (n >> 1) & 1, &wctl);
+        for (int i = 0; i < NWG; ++i) {
+          if (PAIR || i == 0) {
+            const int n0 = j * LY::KT + i * kHT;
+            vst = st;
+            vt = smem + LY::OFF_V + st * LY::ST_BYTES;
+            ok = ok && wait_warp(&v_full[st], vp, &wctl);
+            if (!ok) break;
+            if (n0 + kHT > tree0 && n0 < w.len) {
+              tree_tile<HD>(vt, n0, tree0, w.len, units.odd[slot], lane);
+              fence_proxy_async();
+              __syncwarp();
+            }
+            if (j == w.jb - 1 && i == HALVES - 1 && lane == 0) mbar_arrive(&units.odd_full[slot]);
+            if (++st == LY::VST) {
+              st = 0;
+              vp ^= 1;
+            }
+          }
+          ok = ok && wait_warp(&p_full[i][buf], (g >> 1) & 1, &wctl);
           if (!ok) break;
           tc_fence_after();
           if (lane == 0) {
-            const uint32_t tP = tbase + LY::COL_S + (wg * 2 + buf) * kKT;
-            const Desc vb = make_desc(smem_u32(vt), kKT * 128, 1024);  // V, MN-major
-            const bool more = j - w.ja >= (PAIR ? 2 : 1);
+            const Desc vb = make_desc(smem_u32(vt), 1024, KCH * 1024);  // V, MN-major
 #pragma unroll
-            for (int ks = 0; ks < kKT / 16; ++ks)
-              mma_ts2(tbase + wg * HD, tP + ks * 8, vb.at(ks * 2048), vb.hi, id,
-                      more || ks > 0 ? 1u : 0u);
-            mma_commit(&p_done[wg][buf]);
+            for (int ks = 0; ks < kHT / 16; ++ks)
+              mma_ts2(tbase + i * HD, tbase + LY::col_s(i, buf) + ks * 8,
+                      vb.at(ks * (2 * KCH * 1024)), vb.hi, id, j > w.ja || ks > 0 ? 1u : 0u);
+            mma_commit(&p_done[i][buf]);
+            if (PAIR || i == NWG - 1) mma_commit(&v_empty[vst]);
           }
           __syncwarp();
         }
-        if (ok && lane == 0) mma_commit(&v_empty[st]);
-        __syncwarp();
       }
     }
     if (lane == 0) {
@@ -552,22 +633,8 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR>::THREADS, 1)
       if (un >= kUnits) ok = wait_warp(&units.free[slot], (un / kUnits - 1) & 1, &wctl);
       if (!ok) break;
       ended = !list.next(p);
-      if (!ended) {
-        const int whose = p.mask_stride == 0 ? 0 : list.b;
-        bool have = false;
-#pragma unroll
-        for (int s = 0; s < kUnits; ++s) {
-          if (s == slot) {
-            have = packed[s] == whose;
-            packed[s] = whose;
-          }
-        }
-        if (!have)
-          pack_mask(p.mask + list.b * p.mask_stride, bits + slot * p.T * p.words, p.T, p.words,
-                    lane);
-        if (lane < kTreeMax / 32) units.odd[slot][lane] = 0;
-        __syncwarp();
-      }
+      if (lane < kTreeMax / 32) units.odd[slot][lane] = 0;
+      __syncwarp();
       if (lane == 0) {
         units.at[slot][0] = make_int4(list.b, list.kh, list.rb, list.ja);
         units.at[slot][1] =
@@ -576,26 +643,39 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR>::THREADS, 1)
       }
       __syncwarp();
       if (ended) break;
-      const int qs = PAIR ? un & 1 : 0, turn = PAIR ? un >> 1 : un;
+      const int qs = un % LY::QB, turn = un / LY::QB;
       if (turn > 0) ok = wait_warp(&q_free[qs], (turn - 1) & 1, &wctl);
       if (!ok) break;
       if (lane == 0) {
         constexpr int tiles = PAIR ? 1 : NWG;
         mbar_arrive_expect_tx(&q_full[qs], tiles * LY::Q_BYTES);
-        for (int i = 0; i < tiles; ++i)
+        for (int i = 0; i < tiles * C; ++i)
           for (int c = 0; c < KCH; ++c)
-            tma_load_3d(smem + (PAIR ? qs : i) * LY::Q_BYTES + c * (128 * 128), &mQ, &q_full[qs],
-                        c * 64, list.rb * LY::ROWS + i * 128, list.b * p.Hk + list.kh);
+            tma_load_3d(smem + (PAIR ? qs * LY::Q_BYTES + i * LY::RC * 128 : i * LY::Q_BYTES) +
+                            c * (128 * 128),
+                        &mQ, &q_full[qs], c * 64, list.rb * LY::ROWS + (PAIR ? 0 : i * 128),
+                        list.b * p.Hk + list.kh);
       }
       ++loads;
+      const int whose = p.mask_stride == 0 ? 0 : list.b;
+      bool have = false;
+#pragma unroll
+      for (int s = 0; s < kUnits; ++s) {
+        if (s == slot) {
+          have = packed[s] == whose;
+          packed[s] = whose;
+        }
+      }
+      if (!have)
+        pack_mask(p.mask + list.b * p.mask_stride, bits + slot * p.T * p.words, p.T, p.words, lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&units.bits_full[slot]);
       __syncwarp();
     }
     if (lane == 0) {  // no copy may be in flight when the CTA ends
-      if (PAIR) {
-        if (loads > 0) mbar_wait_drain(&q_full[0], ((loads - 1) >> 1) & 1);
-        if (loads > 1) mbar_wait_drain(&q_full[1], ((loads - 2) >> 1) & 1);
-      } else if (loads > 0) {
-        mbar_wait_drain(&q_full[0], (loads - 1) & 1);
+      for (int i = 0; i < LY::QB; ++i) {
+        const int n = (loads - i + LY::QB - 1) / LY::QB;  // of this buffer
+        if (n > 0) mbar_wait_drain(&q_full[i], (n - 1) & 1);
       }
     }
   } else {
@@ -605,9 +685,12 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR>::THREADS, 1)
     // warpgroups meet (PAIR) both leave together.
     const int wg = warp >> 2, wl = warp & 3, row = threadIdx.x & 127;
     const uint32_t lanes = tbase + ((uint32_t)(wl * 32) << 16);
-    const uint32_t tO = lanes + wg * HD, tS = lanes + LY::COL_S + wg * 2 * kKT;
-    const float c2 = p.scale_log2;
-    int g = 0;  // PAIR: tiles of the CTA so far, this warpgroup's are those of its parity
+    const uint32_t tO = lanes + wg * HD;
+    // copy `copy` of row r: NC of the warpgroup's 64 keys of a tile
+    constexpr int NC = kHT / C;
+    const int copy = C == 1 ? 0 : row / LY::RC, r = row % LY::RC;
+    const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
+    int g = 0;
     TreeUnit w;
     bool ok = true, end = false;
 #pragma unroll 1
@@ -616,48 +699,59 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR>::THREADS, 1)
       if (PAIR ? soft_any<32 * LY::SOFT>(!ok) || end : !ok || end) break;
       const int slot = un % kUnits;
       const int r0 = w.rb * LY::ROWS + (PAIR ? 0 : wg * 128);
-      const bool live = r0 + wl * 32 < p.rows, mine = r0 + row < p.rows;
-      const int node = mine ? (r0 + row) % p.T : 0;
+      const bool live = r0 + wl * 32 % LY::RC < p.rows, mine = r0 + r < p.rows;
+      const int node = mine ? (r0 + r) % p.T : 0;
       const unsigned* sees = bits + (slot * p.T + node) * p.words;
-      const int tree0 = w.len - p.T;
+      // the first key of the tree, counted from this thread's first of tile 0
+      const int tree0 = w.len - p.T - (PAIR ? wg * kHT : 0) - copy * NC;
       float m = -FLT_MAX / 2.0f, l = 0.0f;
-      bool any = false;  // a tile of the unit was this warpgroup's
 #pragma unroll 1
-      for (int j = w.ja + (PAIR ? (g ^ wg) & 1 : 0); j < w.jb; j += PAIR ? 2 : 1) {
-        const int n = PAIR ? (g + j - w.ja) >> 1 : g + j - w.ja, buf = n & 1;
-        const uint32_t at = tS + buf * kKT;
-        ok = wait_warp(&s_full[wg][buf], (n >> 1) & 1, &wctl);
+      for (int j = w.ja; j < w.jb; ++j, ++g) {
+        const int buf = g & 1, first = j * LY::KT - tree0;  // node of this thread's first key
+        const uint32_t ph = (g >> 1) & 1, at = lanes + LY::col_s(wg, buf);
+        ok = wait_warp(&s_full[PAIR ? 0 : wg][buf], ph, &wctl);
+        // (every warp that is asked for has seen the words that it looks at)
+        if (ok && first + NC > 0) ok = wait_warp(&units.bits_full[slot], (un / kUnits) & 1, &wctl);
         if (!ok) break;
         if (live) {
           tc_fence_after();
-          uint32_t s[2][32];
-          tmem_ld32(at, s[0]);
-          tmem_ld32(at + 32, s[1]);
+          uint32_t s[NC];
+          if constexpr (NC == 16) {
+            tmem_ld16(at + copy * NC, s);
+          } else {
+#pragma unroll
+            for (int h = 0; h < NC / 32; ++h)
+              tmem_ld32(at + copy * NC + h * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[h * 32]));
+          }
           tmem_wait_ld();
-          const int first = j * kKT - tree0;  // node of the tile's first key
-          if (first + kKT > 0) {
+          if (first + NC > 0) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t vis = mask_bits(sees, p.words, first + h * 32);
+            for (int h = 0; h < NC; h += 32) {
+              const uint32_t vis = mask_bits(sees, p.words, first + h);
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!(vis >> e & 1)) s[h][e] = 0xff800000u;  // -inf
+              for (int e = 0; e < 32 && e < NC; ++e)
+                if (!(vis >> e & 1)) s[h + e] = 0xff800000u;  // -inf
             }
           }
-          float mx = -INFINITY;
+          float mx[4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int k = 0; k < 4; ++k) {
+            mx[k] = __uint_as_float(s[k]);
 #pragma unroll
-            for (int e = 0; e < 32; e += 2)
-              mx = fmax3(mx, __uint_as_float(s[h][e]), __uint_as_float(s[h][e + 1]));
-          const float m_new = fmaxf(m, mx * c2);
-          if (!any) {
+            for (int e = 4 + 2 * k; e < NC - 4; e += 8)
+              mx[k] = fmax3(mx[k], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+          }
+          mx[0] = fmax3(mx[0], __uint_as_float(s[NC - 4]), __uint_as_float(s[NC - 3]));
+          mx[1] = fmax3(mx[1], __uint_as_float(s[NC - 2]), __uint_as_float(s[NC - 1]));
+          const float m_new =
+              fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2);
+          if (j == w.ja) {
             m = m_new;
           } else if (__any_sync(0xffffffffu, m_new > m + kRescale)) {
             // O holds P V of this warpgroup's tiles before; only the last can be outstanding
             const float f = ex2(m - m_new);
             l *= f;
-            ok = wait_warp(&p_done[wg][(n - 1) & 1], ((n - 1) >> 1) & 1, &wctl);
+            ok = wait_warp(&p_done[wg][(g - 1) & 1], ((g - 1) >> 1) & 1, &wctl);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
@@ -672,46 +766,57 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR>::THREADS, 1)
             tmem_wait_st();
             m = m_new;
           }
-          float sum = 0.0f;
+          const uint64_t nm = f2_pack(-m, -m);
+          uint64_t sum[2] = {0ull, 0ull};
+          constexpr int PN = NC < 32 ? NC : 32;  // keys whose weights are stored at once
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t pk[16];
+          for (int h = 0; h < NC / PN; ++h) {
+            uint32_t pk[PN / 2];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float a = ex2(fmaf(__uint_as_float(s[h][2 * e]), c2, -m));
-              const float b = ex2(fmaf(__uint_as_float(s[h][2 * e + 1]), c2, -m));
-              sum += a + b;
-              pk[e] = pack_bf16(a, b);
+            for (int e = 0; e < PN; e += 2) {
+              const uint32_t* x = &s[h * PN + e];
+              float a, b;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(x[0]), __uint_as_float(x[1])), c2, nm), a, b);
+              a = ex2(a);
+              b = ex2(b);
+              sum[e / 2 & 1] = f2_add(sum[e / 2 & 1], f2_pack(a, b));
+              pk[e / 2] = pack_bf16(a, b);
             }
-            tmem_st16(at + h * 16, pk);
+            if constexpr (C == 1)
+              tmem_st16(at + h * 16, pk);
+            else
+              store_weights<C>(at, pk, copy);
           }
-          l += sum;
+          float a, b;
+          f2_unpack(f2_add(sum[0], sum[1]), a, b);
+          l += a + b;
           tmem_wait_st();
           tc_fence_before();
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[wg][buf]);
-        any = true;
       }
       // ---- the unit's end: O of all its tiles, of both warpgroups where they share the rows
-      const int tiles = w.jb - w.ja;
-      const int mine_last = PAIR ? g + tiles - 1 - ((g + tiles - 1 - wg) & 1) : g + tiles - 1;
-      g += tiles;
-      if (ok && any) {
-        const int n = PAIR ? mine_last >> 1 : mine_last;  // this warpgroup's last item
-        ok = wait_warp(&p_done[wg][n & 1], (n >> 1) & 1, &wctl);
-      }
+      if (ok) ok = wait_warp(&p_done[wg][(g - 1) & 1], ((g - 1) >> 1) & 1, &wctl);
       if (ok) ok = wait_warp(&units.odd_full[slot], (un / kUnits) & 1, &wctl);
       float f0 = 1.0f, f1 = 0.0f;  // factors of O (this warpgroup's, or the first's) and the second's
       if (PAIR) {
         ml_s[un & 1][wg][row] = make_float2(m, l);
         tc_fence_before();  // (the other warpgroup reads this one's O too)
         if (soft_any<32 * LY::SOFT>(!ok)) break;
-        const float2 a = ml_s[un & 1][0][row], b = ml_s[un & 1][1][row];
-        m = fmaxf(a.x, b.x);
+        const auto& ml = ml_s[un & 1];
+#pragma unroll
+        for (int k = 0; k < C; ++k)
+          m = fmaxf(m, fmaxf(ml[0][r + k * LY::RC].x, ml[1][r + k * LY::RC].x));
+        l = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 2 * C; ++k) {
+          const float2 x = ml[k & 1][r + k / 2 * LY::RC];
+          if (x.y != 0.0f) l = fmaf(x.y, ex2(x.x - m), l);
+        }
+        const float2 a = ml[0][row], b = ml[1][row];
         f0 = a.y == 0.0f ? 0.0f : ex2(a.x - m);
         f1 = b.y == 0.0f ? 0.0f : ex2(b.x - m);
-        l = a.y * f0 + b.y * f1;
       } else if (!ok) {
         break;
       } else if (l == 0.0f) {
@@ -721,15 +826,38 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR>::THREADS, 1)
       bool odd = false;
 #pragma unroll
       for (int k = 0; k < kTreeMax / 32; ++k) odd |= units.odd[slot][k] != 0;
-      const size_t unit_row = ((size_t)w.b * p.Hk + w.kh) * p.rows + r0 + row;
+      const size_t unit_row = ((size_t)w.b * p.Hk + w.kh) * p.rows + r0 + r;
       const size_t part = 2 * (size_t)blockIdx.x + (w.first ? 1 : 0);
-      const int prow = PAIR ? row : wg * 128 + row;  // of the unit's rows
+      const int prow = PAIR ? r : wg * 128 + row;  // of the unit's rows
       float4* o_part = reinterpret_cast<float4*>(p.o_part) + part * (HD / 4) * LY::ROWS + prow;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       if (w.whole) {
         f0 *= inv;
         f1 *= inv;
       }
+      // N columns from c on of this thread's row, where they go
+      auto out = [&](auto& o, int c) {
+        constexpr int N = sizeof(o) / 4;
+        if (!mine) return;
+        if (odd) tree_odd<HD>(p, o, units.odd[slot], sees, w, c);
+        if (w.whole) {
+          __nv_bfloat16* dst = p.o + unit_row * HD + c;
+          if constexpr (N == 4)
+            *reinterpret_cast<uint2*>(dst) =
+                make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
+          else
+#pragma unroll
+            for (int k = 0; k < N; k += 8)
+              *reinterpret_cast<uint4*>(dst + k) =
+                  make_uint4(pack_bf16(o[k], o[k + 1]), pack_bf16(o[k + 2], o[k + 3]),
+                             pack_bf16(o[k + 4], o[k + 5]), pack_bf16(o[k + 6], o[k + 7]));
+        } else {
+#pragma unroll
+          for (int k = 0; k < N; k += 4)
+            o_part[(size_t)((c + k) / 4) * LY::ROWS] =
+                make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+        }
+      };
       if (live) {
         constexpr int COLS = PAIR ? HD / 2 : HD;
 #pragma unroll 1
@@ -744,27 +872,33 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR>::THREADS, 1)
             o[e] = f0 == 0.0f ? 0.0f : __uint_as_float(x[e]) * f0;  // (O of no weight holds anything)
             if (PAIR) o[e] += f1 == 0.0f ? 0.0f : __uint_as_float(y[e]) * f1;
           }
-          if (odd && mine) {
-            tree_odd(p, o, units.odd[slot], sees, w, HD, c);
-            tree_odd(p, o + 8, units.odd[slot], sees, w, HD, c + 8);
-          }
-          if (!mine) {
-          } else if (w.whole) {
-            uint4* dst = reinterpret_cast<uint4*>(p.o + unit_row * HD + c);
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              dst[k] = make_uint4(pack_bf16(o[8 * k], o[8 * k + 1]), pack_bf16(o[8 * k + 2], o[8 * k + 3]),
-                                  pack_bf16(o[8 * k + 4], o[8 * k + 5]),
-                                  pack_bf16(o[8 * k + 6], o[8 * k + 7]));
+          if constexpr (C == 1) {
+            out(o, c);
+            __syncwarp();
           } else {
+            // the copies' sums, through shared memory; a thread has 16 / C of the 16 columns then
+            float4* join = reinterpret_cast<float4*>(smem + LY::OFF_JOIN) + wg * (128 * 4);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              o_part[(size_t)(c / 4 + k) * LY::ROWS] =
+              join[row * 4 + (k ^ (row & 3))] =
                   make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            group_sync(wg);
+            constexpr int N = 16 / C;
+            float z[N] = {};
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+              const int from = r + i * LY::RC;
+#pragma unroll
+              for (int k = 0; k < N; k += 4) {
+                const float4 v = join[from * 4 + ((copy * (N / 4) + k / 4) ^ (from & 3))];
+                z[k] += v.x, z[k + 1] += v.y, z[k + 2] += v.z, z[k + 3] += v.w;
+              }
+            }
+            group_sync(wg);
+            out(z, c + copy * N);
           }
-          __syncwarp();
         }
-        if (mine && (!PAIR || wg == 0)) {
+        if (mine && copy == 0 && (!PAIR || wg == 0)) {
           if (!w.whole) {
             p.ml_part[part * 2 * LY::ROWS + prow] = m;
             p.ml_part[(part * 2 + 1) * LY::ROWS + prow] = l;
@@ -868,26 +1002,28 @@ __global__ void __launch_bounds__(32 * HD / 8) tree_combine_kernel(const TreeK p
 }
 
 struct TreePlan {
-  int ROWS, rb, grid;
+  int pair, C, ROWS, rb, grid;
 };
 TreePlan tree_plan(const TreeArgs& a) {
   TreePlan pl;
   const int rows = a.G * a.T;
-  pl.ROWS = rows <= 128 || a.d > 128 ? 128 : 256;
+  pl.pair = rows <= 128 && a.d <= 128;
+  pl.C = a.d > 64 || rows > 64 ? 1 : rows > 32 ? 2 : 4;
+  pl.ROWS = pl.pair ? 128 / pl.C : a.d <= 128 ? 256 : 128;
   pl.rb = (rows + pl.ROWS - 1) / pl.ROWS;
   const long long cap = (long long)a.max_pages << a.ps_shift;
-  const long long tiles = ((cap + kKT - 1) / kKT + kUnitCost) * a.B * a.Hk * pl.rb;
+  const long long tiles = ((cap + kHT - 1) / kHT + kUnitCost) * a.B * a.Hk * pl.rb;  // (at most)
   pl.grid = (int)std::min<long long>(152, tiles);
   return pl;
 }
 
-template <int HD, bool PAIR>
-cudaError_t launch_tree_t(const TreeArgs& a, const TreeMaps& m, void* ws, cudaStream_t s) {
-  using LY = TreeLayout<HD, PAIR>;
+template <int HD, bool PAIR, int C>
+cudaError_t launch_tree_t(const TreeArgs& a, const TreeMaps& m, const TreePlan& pl, void* ws,
+                          cudaStream_t s) {
+  using LY = TreeLayout<HD, PAIR, C>;
   static OncePerKey<> smem_attr;
-  const TreePlan pl = tree_plan(a);
-  auto kern = tree_kernel<HD, PAIR>;
-  cudaError_t e = set_smem_once(smem_attr, kern, LY::smem_bytes(kTreeMax));
+  auto kern = tree_kernel<HD, PAIR, C>;
+  cudaError_t e = set_smem_once(smem_attr, kern, LY::smem_bytes(LY::T_MAX));
   if (e != cudaSuccess) return e;
   TreeK p;
   p.v = static_cast<const __nv_bfloat16*>(a.v_cache);
@@ -909,6 +1045,7 @@ cudaError_t launch_tree_t(const TreeArgs& a, const TreeMaps& m, void* ws, cudaSt
   p.max_pages = a.max_pages;
   p.num_pages = a.num_pages;
   p.ps_shift = a.ps_shift;
+  p.kt_shift = PAIR ? 7 : 6;
   p.scale_log2 = a.scale * kLog2e;
   p.wait_limit_ns = a.wait_limit_ns;
   profile_mark(kKernTreeAttn, 0, s);
@@ -926,11 +1063,11 @@ cudaError_t launch_tree_t(const TreeArgs& a, const TreeMaps& m, void* ws, cudaSt
 }
 }  // namespace
 
-int tree_box_rows(int page_size) { return page_size < kKT ? page_size : kKT; }
+int tree_box_rows(int page_size) { return page_size < kHT ? page_size : kHT; }
 
 long long tree_tiles(const TreeArgs& a) {
   const long long cap = (long long)a.max_pages << a.ps_shift;
-  return ((cap + kKT - 1) / kKT + kUnitCost) * a.B * a.Hk * tree_plan(a).rb;
+  return ((cap + kHT - 1) / kHT + kUnitCost) * a.B * a.Hk * tree_plan(a).rb;
 }
 
 size_t tree_workspace_bytes(const TreeArgs& a) {
@@ -938,13 +1075,20 @@ size_t tree_workspace_bytes(const TreeArgs& a) {
   return (size_t)2 * pl.grid * pl.ROWS * (a.d + 2) * 4;
 }
 
+int tree_q_rows(const TreeArgs& a) { return 128 / tree_plan(a).C; }
+
 cudaError_t launch_tree(const TreeArgs& a, const TreeMaps& m, void* ws, cudaStream_t s) {
-  const bool pair = a.G * a.T <= 128;
+  const TreePlan pl = tree_plan(a);
   switch (a.d) {
-    case 64: return pair ? launch_tree_t<64, true>(a, m, ws, s) : launch_tree_t<64, false>(a, m, ws, s);
+    case 64:
+      if (!pl.pair) return launch_tree_t<64, false, 1>(a, m, pl, ws, s);
+      return pl.C == 1   ? launch_tree_t<64, true, 1>(a, m, pl, ws, s)
+             : pl.C == 2 ? launch_tree_t<64, true, 2>(a, m, pl, ws, s)
+                         : launch_tree_t<64, true, 4>(a, m, pl, ws, s);
     case 128:
-      return pair ? launch_tree_t<128, true>(a, m, ws, s) : launch_tree_t<128, false>(a, m, ws, s);
-    case 256: return launch_tree_t<256, false>(a, m, ws, s);
+      return pl.pair ? launch_tree_t<128, true, 1>(a, m, pl, ws, s)
+                     : launch_tree_t<128, false, 1>(a, m, pl, ws, s);
+    case 256: return launch_tree_t<256, false, 1>(a, m, pl, ws, s);
     default: return cudaErrorInvalidValue;
   }
 }

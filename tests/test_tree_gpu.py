@@ -70,6 +70,10 @@ CASES = [
     (2, 4, 2, 7, 128, 16, [6, 200], "all"),
     (70, 2, 2, 3, 64, 16, list(range(70)), "one tree"),
     (1, 40, 1, 8, 64, 16, [333], "trees"),
+    (3, 8, 8, 17, 64, 64, [17, 1000, 130], "trees"),
+    (3, 8, 1, 4, 64, 8, [200, 4, 131], "any"),
+    (2, 4, 2, 31, 64, 32, [900, 129], "any"),
+    (2, 1, 1, 64, 64, 16, [64, 192], "trees"),
 ]
 
 
@@ -94,16 +98,16 @@ def test_matches_the_definition(case):
     assert fa.fa_device_status(True) == fa.FA_OK
 
 
-@pytest.mark.parametrize("d", [64, 128, 256])
-def test_long_sequences_of_mixed_lengths(d):
+@pytest.mark.parametrize("d,T", [(64, 12), (64, 9), (64, 40), (64, 50), (128, 12), (128, 50), (256, 12)])
+def test_long_sequences_of_mixed_lengths(d, T):
     """Sequences that are cut over many CTAs beside some of a few keys."""
     import torch
 
     import flash_attention_gb300 as fa
 
-    lengths = [9000, 40, 5000, 41, 12345]
-    rng, table, (kc, kx), (vc, vx), (q, qx) = make(d, 5, 6, 2, 12, d, 32, lengths)
-    m = masks(rng, 5, 12, "trees")
+    lengths = [9000, 50, 5000, 51, 12345]
+    rng, table, (kc, kx), (vc, vx), (q, qx) = make(d, 5, 6, 2, T, d, 32, lengths)
+    m = masks(rng, 5, T, "trees")
     want = plain.tree_attention(qx, kx, vx, table, lengths, m, 0.1)
     got = fa.paged_tree_attention(q, kc, vc, ints(table), ints(lengths), torch.from_numpy(m).cuda(),
                                   scale=0.1)
@@ -168,9 +172,9 @@ def test_short_trees_stand_at_the_end():
         check((o[b:b + 1, :, T - n:], lse[b:b + 1, :, T - n:]), alone[b])
 
 
-@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("d,H", [(64, 2), (64, 4), (64, 6), (64, 12), (128, 6), (128, 12), (256, 6)])
 @pytest.mark.parametrize("what", ["nan", "inf", "-inf"])
-def test_what_a_node_does_not_see_stays_out(d, what):
+def test_what_a_node_does_not_see_stays_out(d, what, H):
     """NaN and infinities in the keys and values of some nodes, and everywhere behind the sequences:
     rows that do not see them are as if they were not there; rows that do are what the formula gives."""
     import torch
@@ -178,7 +182,7 @@ def test_what_a_node_does_not_see_stays_out(d, what):
     import flash_attention_gb300 as fa
 
     lengths, T = [24, 200, 1000, 131], 24
-    rng, table, (kc, kx), (vc, vx), (q, qx) = make(d, 4, 6, 2, T, d, 16, lengths)
+    rng, table, (kc, kx), (vc, vx), (q, qx) = make(d, 4, H, 2, T, d, 16, lengths)
     m = masks(rng, 4, T, "trees")
     bad = float(what)
     used = np.zeros(kx.shape[:1] + kx.shape[2:3], bool)
@@ -349,7 +353,8 @@ def test_on_another_stream():
     assert all(map(torch.equal, got, want))
 
 
-@pytest.mark.parametrize("d,T", [(64, 9), (64, 80), (128, 9), (128, 80), (256, 9)])
+@pytest.mark.parametrize("d,T", [(64, 9), (64, 30), (64, 60), (64, 80), (128, 9), (128, 80),
+                                 (256, 9)])
 def test_waits_that_run_out_are_reported(d, T):
     """With a limit of 1 ns the kernel's ordinary waits run out: it winds down, the status says so, and
     with the limit restored the same call is right."""
