@@ -26,13 +26,14 @@
 // kernel joins in the order of the keys.
 //
 // Warps: 0-3 (0-7) softmax, then one each for the copies of K pages, of V pages, for S, for O, and for
-// the list: it walks the list two units ahead, packs the tree's mask into words and loads Q. A page's
+// the list: it walks the list two units ahead, loads Q and packs the tree's mask into words. A page's
 // part of a tile is one TMA box, min(page_size, 64) rows of all columns: what limits small copies is
 // the number of them a warp can issue (copies alone, 131072 keys of 8 heads, head_dim 128, pages of 16:
 // 4.6 TB/s with a box for each 64 columns, 5.7 with one box, 6.3 with a warp each for K and V; pages of 8:
 // 3.0, 4.2, 5.7). The mask is tested in the tiles of the last T keys alone.
-// There a value that is not finite must meet no weight of a row that does not see it, not even 0: the
-// O warp clears it, and rows that see it get it added at the end (tree_odd).
+// There a value that is not finite must meet no weight of a row that does not see it, not even 0: a
+// last warp looks those tiles over as they land and clears it, and rows that see it get it added at the
+// end (tree_odd).
 #include <float.h>
 
 #include <algorithm>
@@ -62,7 +63,7 @@ struct TreeLayout {
   // stages of the rings; V has more where there is room, as a V stage stays until the weights of its
   // keys are there (K's are even: the halves of a tile are one operand)
   static constexpr int KST = HD == 64 ? 8 : HD == 128 ? (PAIR ? 6 : 4) : 2;
-  static constexpr int VST = HD == 64 ? 12 : HD == 128 ? (PAIR ? 5 : 4) : 2;
+  static constexpr int VST = HD == 64 ? (C > 1 ? 10 : 12) : HD == 128 ? (PAIR ? 5 : 4) : 2;
   static constexpr int KCH = HD / 64;
   static constexpr int Q_BYTES = 128 * HD * 2;       // of 128 rows
   // Units whose Q is held: a second one costs stages. (Its load runs beside a unit's last softmax.)
@@ -70,20 +71,20 @@ struct TreeLayout {
   static constexpr int ST_BYTES = kHT * HD * 2;
   static constexpr int OFF_K = (PAIR ? QB : NWG) * Q_BYTES;
   static constexpr int OFF_V = OFF_K + KST * ST_BYTES;
-  static constexpr int OFF_JOIN = OFF_V + VST * ST_BYTES;  // 16 columns of the copies' O
-  static constexpr int OFF_BITS = OFF_JOIN + (C > 1 ? NWG * 128 * 64 : 0);  // the masks' words
+  static constexpr int OFF_JOIN = OFF_V + VST * ST_BYTES;  // the copies' O, 32 columns a warpgroup
+  static constexpr int OFF_BITS = OFF_JOIN + (C > 1 ? NWG * 128 * 128 : 0);  // the masks' words
   static constexpr int COL_S = NWG * HD;             // O of each warpgroup, then S
   static constexpr int TMEM_COLS = 512;
   static constexpr int SOFT = 4 * NWG;
   static constexpr int K_WARP = SOFT, V_WARP = SOFT + 1, S_WARP = SOFT + 2, O_WARP = SOFT + 3,
-                       LIST_WARP = SOFT + 4;
-  static constexpr int THREADS = 32 * (SOFT + 5);
+                       LIST_WARP = SOFT + 4, FIX_WARP = SOFT + 5;
+  static constexpr int THREADS = 32 * (SOFT + 6);
   // columns of S (and P) of warpgroup w in its buffer b: for a pair the two lie side by side
   static __device__ __forceinline__ uint32_t col_s(int w, int b) {
     return COL_S + (PAIR ? b * 2 + w : w * 2 + b) * kHT;
   }
   static_assert(!PAIR || (NWG == 2 && KST % 2 == 0), "pairs need two warpgroups");
-  static_assert(C == 1 || PAIR, "copies are of a pair's rows");
+  static_assert(C == 1 || (PAIR && HD == 64), "copies are of a pair's rows");
   static_assert(COL_S + NWG * 2 * kHT <= TMEM_COLS, "TMEM budget");
   static constexpr int T_MAX = PAIR ? RC : kTreeMax;
   static constexpr int smem_bytes(int T) {
@@ -210,7 +211,7 @@ struct TreeRing {
   int4 at[kUnits][2];
   uint64_t full[kUnits], free[kUnits];
   uint64_t bits_full[kUnits];       // the mask's words are there
-  uint64_t odd_full[kUnits];        // the O warp has looked at all the unit's tiles
+  uint64_t odd_full[kUnits];        // the unit's tree has been looked over
   unsigned odd[kUnits][kTreeMax / 32];  // nodes whose values are not all finite
 };
 template <bool FREE>
@@ -385,6 +386,9 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, 1)
   // warpgroup; p_done: O has it. (The rings' empty barriers are their own: a stage may be filled again
   // when the phase of p_done or s_full that freed it is two phases old.)
   __shared__ uint64_t k_full[LY::KST], v_full[LY::VST], k_empty[LY::KST], v_empty[LY::VST];
+  // of stages with V of the tree's keys: asked for (only then is v_full's phase the one of that copy),
+  // and looked over
+  __shared__ uint64_t v_tail[LY::VST], v_fixed[LY::VST];
   __shared__ uint64_t s_full[NWG][2], p_full[NWG][2], p_done[NWG][2], q_full[2], q_free[2];
   __shared__ uint64_t o_free, drain_s, drain_o;
   __shared__ __align__(16) TreeRing units;
@@ -408,6 +412,8 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, 1)
     for (int s = 0; s < LY::VST; ++s) {
       mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], 1);
+      mbar_init(&v_tail[s], 1);
+      mbar_init(&v_fixed[s], 1);
     }
 #pragma unroll 1
     for (int s = 0; s < 2; ++s) {
@@ -422,7 +428,7 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, 1)
 #pragma unroll 1
     for (int s = 0; s < kUnits; ++s) {
       mbar_init(&units.full[s], 1);
-      mbar_init(&units.free[s], 4 + LY::SOFT);
+      mbar_init(&units.free[s], 5 + LY::SOFT);
       mbar_init(&units.bits_full[s], 1);
       mbar_init(&units.odd_full[s], 1);
     }
@@ -495,6 +501,7 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, 1)
           uint64_t* empty = is_v ? &v_empty[st] : &k_empty[st / HALVES * HALVES];
           if (g >= ST) ok = wait(empty, (g / ST - 1) & 1, &wctl);
           if (ok) mbar_arrive_expect_tx(&full[st], LY::ST_BYTES);
+          if (ok && is_v && n0 + kHT > w.len - p.T && n0 < w.len) mbar_arrive(&v_tail[st]);
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
@@ -559,12 +566,12 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, 1)
     // ------------------------------------------------------------------ O += P V
     const uint32_t id = idesc_bf16(128, HD, 0, 1);
     int g = 0, st = 0;
-    uint32_t vp = 0;  // stage of V, and its phase
+    uint32_t vp = 0, fixed = 0;  // stage of V, and its phase; phases of v_fixed
     TreeUnit w;
     bool ok = true, end = false;
 #pragma unroll 1
     for (int un = 0; ok && (ok = take_unit<true>(&units, un, w, end, lane, &wctl)) && !end; ++un) {
-      const int slot = un % kUnits, tree0 = w.len - p.T;
+      const int tree0 = w.len - p.T;
 #pragma unroll 1
       for (int j = w.ja; j < w.jb && ok; ++j, ++g) {
         const int buf = g & 1;
@@ -581,11 +588,10 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, 1)
             ok = ok && wait_warp(&v_full[st], vp, &wctl);
             if (!ok) break;
             if (n0 + kHT > tree0 && n0 < w.len) {
-              tree_tile<HD>(vt, n0, tree0, w.len, units.odd[slot], lane);
-              fence_proxy_async();
-              __syncwarp();
+              ok = wait_warp(&v_fixed[st], fixed >> st & 1, &wctl);
+              if (!ok) break;
+              fixed ^= 1u << st;
             }
-            if (j == w.jb - 1 && i == HALVES - 1 && lane == 0) mbar_arrive(&units.odd_full[slot]);
             if (++st == LY::VST) {
               st = 0;
               vp ^= 1;
@@ -612,6 +618,33 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, 1)
       mbar_wait_drain(&drain_o, 0);
     }
     __syncwarp();
+  } else if (warp == LY::FIX_WARP) {
+    // ------------------------------------------------------------------ V of the tree's keys, as soon
+    // as it has landed: what is not finite, and what lies behind the sequence's end
+    int g = 0;
+    uint32_t asked = 0;  // phases of v_tail
+    TreeUnit w;
+    bool ok = true, end = false;
+#pragma unroll 1
+    for (int un = 0; ok && (ok = take_unit<true>(&units, un, w, end, lane, &wctl)) && !end; ++un) {
+      const int slot = un % kUnits, tree0 = w.len - p.T;
+      const int h0 = w.ja * HALVES, h1 = w.jb * HALVES;  // stages
+#pragma unroll 1
+      for (int h = max(h0, max(tree0, 0) / kHT); h < h1 && h * kHT < w.len; ++h) {
+        const int st = (g + h - h0) % LY::VST;
+        ok = wait_warp(&v_tail[st], asked >> st & 1, &wctl) &&
+             wait_warp(&v_full[st], (g + h - h0) / LY::VST & 1, &wctl);
+        if (!ok) break;
+        asked ^= 1u << st;
+        tree_tile<HD>(smem + LY::OFF_V + st * LY::ST_BYTES, h * kHT, tree0, w.len, units.odd[slot],
+                      lane);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_fixed[st]);
+      }
+      g += h1 - h0;
+      if (lane == 0) mbar_arrive(&units.odd_full[slot]);
+    }
   } else if (warp == LY::LIST_WARP) {
     // ------------------------------------------------------------------ units, masks and Q
     if (blockIdx.x == 0) {  // lengths out of range are clamped, and reported here
@@ -695,8 +728,12 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, 1)
     bool ok = true, end = false;
 #pragma unroll 1
     for (int un = 0;; ++un) {
+      // (a pair meets once for each unit, whatever a warp has come upon: here, or at the unit's end)
       ok = take_unit<false>(&units, un, w, end, lane, &wctl);
-      if (PAIR ? soft_any<32 * LY::SOFT>(!ok) || end : !ok || end) break;
+      if (!ok || end) {
+        if (PAIR) soft_any<32 * LY::SOFT>(true);
+        break;
+      }
       const int slot = un % kUnits;
       const int r0 = w.rb * LY::ROWS + (PAIR ? 0 : wg * 128);
       const bool live = r0 + wl * 32 % LY::RC < p.rows, mine = r0 + r < p.rows;
@@ -797,13 +834,17 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, 1)
         if (lane == 0) mbar_arrive(&p_full[wg][buf]);
       }
       // ---- the unit's end: O of all its tiles, of both warpgroups where they share the rows
-      if (ok) ok = wait_warp(&p_done[wg][(g - 1) & 1], ((g - 1) >> 1) & 1, &wctl);
-      if (ok) ok = wait_warp(&units.odd_full[slot], (un / kUnits) & 1, &wctl);
-      float f0 = 1.0f, f1 = 0.0f;  // factors of O (this warpgroup's, or the first's) and the second's
       if (PAIR) {
         ml_s[un & 1][wg][row] = make_float2(m, l);
-        tc_fence_before();  // (the other warpgroup reads this one's O too)
         if (soft_any<32 * LY::SOFT>(!ok)) break;
+        // (both warpgroups have given their last P; neither's next O can come before o_free)
+        ok = wait_warp(&p_done[wg ^ 1][(g - 1) & 1], ((g - 1) >> 1) & 1, &wctl);
+      }
+      ok = ok && wait_warp(&p_done[wg][(g - 1) & 1], ((g - 1) >> 1) & 1, &wctl) &&
+           wait_warp(&units.odd_full[slot], (un / kUnits) & 1, &wctl);
+      // A wait that has run out here: O is left undefined, as the status says.
+      float f0 = 1.0f, f1 = 0.0f;  // factors of O (this warpgroup's, or the first's) and the second's
+      if (PAIR) {
         const auto& ml = ml_s[un & 1];
 #pragma unroll
         for (int k = 0; k < C; ++k)
@@ -842,15 +883,11 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, 1)
         if (odd) tree_odd<HD>(p, o, units.odd[slot], sees, w, c);
         if (w.whole) {
           __nv_bfloat16* dst = p.o + unit_row * HD + c;
-          if constexpr (N == 4)
-            *reinterpret_cast<uint2*>(dst) =
-                make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
-          else
 #pragma unroll
-            for (int k = 0; k < N; k += 8)
-              *reinterpret_cast<uint4*>(dst + k) =
-                  make_uint4(pack_bf16(o[k], o[k + 1]), pack_bf16(o[k + 2], o[k + 3]),
-                             pack_bf16(o[k + 4], o[k + 5]), pack_bf16(o[k + 6], o[k + 7]));
+          for (int k = 0; k < N; k += 8)
+            *reinterpret_cast<uint4*>(dst + k) =
+                make_uint4(pack_bf16(o[k], o[k + 1]), pack_bf16(o[k + 2], o[k + 3]),
+                           pack_bf16(o[k + 4], o[k + 5]), pack_bf16(o[k + 6], o[k + 7]));
         } else {
 #pragma unroll
           for (int k = 0; k < N; k += 4)
@@ -876,27 +913,29 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, 1)
             out(o, c);
             __syncwarp();
           } else {
-            // the copies' sums, through shared memory; a thread has 16 / C of the 16 columns then
-            float4* join = reinterpret_cast<float4*>(smem + LY::OFF_JOIN) + wg * (128 * 4);
+            // into shared memory
+            float4* join = reinterpret_cast<float4*>(smem + LY::OFF_JOIN) + wg * (128 * 8);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              join[row * 4 + (k ^ (row & 3))] =
+              join[row * 8 + ((c / 4 & 7) + k ^ (row & 7))] =
                   make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-            group_sync(wg);
-            constexpr int N = 16 / C;
-            float z[N] = {};
-#pragma unroll
-            for (int i = 0; i < C; ++i) {
-              const int from = r + i * LY::RC;
-#pragma unroll
-              for (int k = 0; k < N; k += 4) {
-                const float4 v = join[from * 4 + ((copy * (N / 4) + k / 4) ^ (from & 3))];
-                z[k] += v.x, z[k + 1] += v.y, z[k + 2] += v.z, z[k + 3] += v.w;
-              }
-            }
-            group_sync(wg);
-            out(z, c + copy * N);
           }
+        }
+        if constexpr (C > 1) {  // the copies' sums: a thread has 32 / C of the 32 columns
+          group_sync(wg);
+          const float4* join = reinterpret_cast<const float4*>(smem + LY::OFF_JOIN) + wg * (128 * 8);
+          constexpr int N = 32 / C;
+          float z[N] = {};
+#pragma unroll
+          for (int i = 0; i < C; ++i) {
+            const int from = r + i * LY::RC;
+#pragma unroll
+            for (int k = 0; k < N; k += 4) {
+              const float4 v = join[from * 8 + ((copy * (N / 4) + k / 4) ^ (from & 7))];
+              z[k] += v.x, z[k + 1] += v.y, z[k + 2] += v.z, z[k + 3] += v.w;
+            }
+          }
+          out(z, wg * COLS + copy * N);
         }
         if (mine && copy == 0 && (!PAIR || wg == 0)) {
           if (!w.whole) {
