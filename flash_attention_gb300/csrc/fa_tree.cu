@@ -55,26 +55,27 @@ constexpr float kRescale = 8.0f;
 
 template <int HD, bool PAIR, int C>
 struct TreeLayout {
-  static constexpr int NWG = HD <= 128 ? 2 : 1;      // softmax warpgroups
+  static constexpr int NWG = HD <= 128 && C == 1 ? 2 : 1;  // softmax warpgroups
+  static constexpr int CTAS = C > 1 ? 2 : 1;         // resident on an SM
   static constexpr int RC = 128 / C;                 // query rows of a copy
-  static constexpr int ROWS = PAIR ? RC : 128 * NWG;  // of a unit
+  static constexpr int ROWS = PAIR ? 128 : RC * NWG;  // of a unit
   static constexpr int KT = PAIR ? 2 * kHT : kHT;    // keys of a tile
   static constexpr int HALVES = KT / kHT;
   // stages of the rings; V has more where there is room, as a V stage stays until the weights of its
-  // keys are there (K's are even: the halves of a tile are one operand)
-  static constexpr int KST = HD == 64 ? 8 : HD == 128 ? (PAIR ? 6 : 4) : 2;
-  static constexpr int VST = HD == 64 ? (C > 1 ? 10 : 12) : HD == 128 ? (PAIR ? 5 : 4) : 2;
+  // keys are there (a pair's K are even: the halves of a tile are one operand)
+  static constexpr int KST = HD == 64 ? (C > 1 ? 3 : 8) : HD == 128 ? (PAIR ? 6 : 4) : 2;
+  static constexpr int VST = HD == 64 ? (C > 1 ? 4 : 12) : HD == 128 ? (PAIR ? 5 : 4) : 2;
   static constexpr int KCH = HD / 64;
   static constexpr int Q_BYTES = 128 * HD * 2;       // of 128 rows
   // Units whose Q is held: a second one costs stages. (Its load runs beside a unit's last softmax.)
-  static constexpr int QB = PAIR && HD == 64 ? 2 : 1;
+  static constexpr int QB = HD == 64 && (PAIR || C > 1) ? 2 : 1;
   static constexpr int ST_BYTES = kHT * HD * 2;
-  static constexpr int OFF_K = (PAIR ? QB : NWG) * Q_BYTES;
+  static constexpr int OFF_K = (NWG == 1 || PAIR ? QB : NWG) * Q_BYTES;
   static constexpr int OFF_V = OFF_K + KST * ST_BYTES;
-  static constexpr int OFF_JOIN = OFF_V + VST * ST_BYTES;  // the copies' O, 32 columns a warpgroup
-  static constexpr int OFF_BITS = OFF_JOIN + (C > 1 ? NWG * 128 * 128 : 0);  // the masks' words
+  static constexpr int OFF_JOIN = OFF_V + VST * ST_BYTES;  // 32 columns of the copies' O
+  static constexpr int OFF_BITS = OFF_JOIN + (C > 1 ? 128 * 128 : 0);  // the masks' words
   static constexpr int COL_S = NWG * HD;             // O of each warpgroup, then S
-  static constexpr int TMEM_COLS = 512;
+  static constexpr int TMEM_COLS = 512 / CTAS;
   static constexpr int SOFT = 4 * NWG;
   static constexpr int K_WARP = SOFT, V_WARP = SOFT + 1, S_WARP = SOFT + 2, O_WARP = SOFT + 3,
                        LIST_WARP = SOFT + 4, FIX_WARP = SOFT + 5;
@@ -84,13 +85,15 @@ struct TreeLayout {
     return COL_S + (PAIR ? b * 2 + w : w * 2 + b) * kHT;
   }
   static_assert(!PAIR || (NWG == 2 && KST % 2 == 0), "pairs need two warpgroups");
-  static_assert(C == 1 || (PAIR && HD == 64), "copies are of a pair's rows");
+  static_assert(C == 1 || (!PAIR && HD == 64), "two CTAs an SM at head_dim 64 alone");
   static_assert(COL_S + NWG * 2 * kHT <= TMEM_COLS, "TMEM budget");
-  static constexpr int T_MAX = PAIR ? RC : kTreeMax;
+  static constexpr int T_MAX = PAIR || C > 1 ? RC : kTreeMax;
   static constexpr int smem_bytes(int T) {
     return OFF_BITS + kUnits * T * ((T + 31) / 32) * 4 + 1024;
   }
-  static_assert(smem_bytes(T_MAX) + 8192 <= 227 * 1024, "shared memory budget");
+  // (and what is static, and the driver's 1 KB)
+  static_assert((smem_bytes(T_MAX) + (PAIR ? 6400 : 4096) + 1024) * CTAS <= 228 * 1024,
+                "shared memory budget");
 };
 
 struct TreeK {
@@ -292,22 +295,28 @@ __device__ __noinline__ void tree_tile(uint8_t* vt, int n0, int tree0, int len, 
     return reinterpret_cast<uint4*>(vt + (r / 8 * (HD / 64) + g / 8) * 1024 + (r & 7) * 128 +
                                     ((g % 8) ^ (r & 7)) * 16);
   };
-  const int end = min(kHT, len - n0);
+  const int begin = max(0, tree0 - n0), end = min(kHT, len - n0);
+  // A value times 0 is 0 or, of one that is not finite, NaN.
+  const __nv_bfloat162 zero = __float2bfloat162_rn(0.0f);
+  __nv_bfloat162 test[2] = {zero, zero};
+#pragma unroll 4
+  for (int e = lane + begin * G8; e < end * G8; e += 32) {
+    const uint4 x = *at(e / G8, e % G8);
+    test[0] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.x), zero, test[0]);
+    test[1] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.y), zero, test[1]);
+    test[0] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.z), zero, test[0]);
+    test[1] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x.w), zero, test[1]);
+  }
+  const float2 t = __bfloat1622float2(__hadd2(test[0], test[1]));
+  if (__any_sync(0xffffffffu, t.x != t.x || t.y != t.y)) {
 #pragma unroll 1
-  for (int e0 = lane + max(0, tree0 - n0) * G8; e0 < end * G8; e0 += 4 * 32) {
-    uint4 v[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int e = e0 + 32 * k;
-      v[k] = e < end * G8 ? *at(e / G8, e % G8) : make_uint4(0u, 0u, 0u, 0u);
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint4 x = v[k];
-      const uint4 z = make_uint4(odd_halves(x.x), odd_halves(x.y), odd_halves(x.z), odd_halves(x.w));
+    for (int e = lane + begin * G8; e < end * G8; e += 32) {
+      uint4* x = at(e / G8, e % G8);
+      const uint4 v = *x;
+      const uint4 z = make_uint4(odd_halves(v.x), odd_halves(v.y), odd_halves(v.z), odd_halves(v.w));
       if (z.x | z.y | z.z | z.w) {
-        const int e = e0 + 32 * k, node = n0 + e / G8 - tree0;
-        *at(e / G8, e % G8) = make_uint4(x.x & ~z.x, x.y & ~z.y, x.z & ~z.z, x.w & ~z.w);
+        *x = make_uint4(v.x & ~z.x, v.y & ~z.y, v.z & ~z.z, v.w & ~z.w);
+        const int node = n0 + e / G8 - tree0;
         atomicOr(&odd[node >> 5], 1u << (node & 31));
       }
     }
@@ -353,11 +362,8 @@ __device__ __forceinline__ void store_weights(uint32_t at, const uint32_t (&pk)[
   }
 }
 // The barrier of a warpgroup's threads.
-__device__ __forceinline__ void group_sync(int wg) {
-  if (wg == 0)
-    asm volatile("barrier.cta.sync 2, 128;" ::: "memory");
-  else
-    asm volatile("barrier.cta.sync 3, 128;" ::: "memory");
+__device__ __forceinline__ void soft_sync() {
+  asm volatile("barrier.cta.sync 2, 128;" ::: "memory");
 }
 
 // The barrier of the softmax's threads; true where any of them came with `v`.
@@ -374,11 +380,12 @@ __device__ __forceinline__ bool soft_any(bool v) {
 }
 
 template <int HD, bool PAIR, int C>
-__global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, 1)
+__global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, TreeLayout<HD, PAIR, C>::CTAS)
     tree_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                 const __grid_constant__ CUtensorMap mV, const TreeK p) {
   using LY = TreeLayout<HD, PAIR, C>;
   constexpr int KCH = LY::KCH, NWG = LY::NWG, HALVES = LY::HALVES;
+  constexpr bool JOIN = PAIR || C > 1;  // a row's O lies in several places
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -396,7 +403,7 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, 1)
   __shared__ WaitCtl wctl;
   __shared__ int bad_input;
   __shared__ int page_s[2][kPageChunk];
-  __shared__ float2 ml_s[2][2][128];  // of a unit (even, odd): m and the sum of each warpgroup's rows
+  __shared__ float2 ml_s[2][PAIR ? 2 : 1][JOIN ? 128 : 1];  // of a unit (even, odd): m and the sum of each warpgroup's rows
   unsigned* bits = reinterpret_cast<unsigned*>(smem + LY::OFF_BITS);
 
   const int warp = warp_id(), lane = lane_id();
@@ -546,7 +553,8 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, 1)
           const Desc kb{k0.at(st * LY::ST_BYTES), k0.hi};
 #pragma unroll
           for (int w = 0; w < (PAIR ? 1 : NWG); ++w) {
-            const Desc qa = make_desc(smem_u32(smem + (PAIR ? qs : w) * LY::Q_BYTES), 16, 1024);
+            const Desc qa =
+                make_desc(smem_u32(smem + (NWG == 1 || PAIR ? qs : w) * LY::Q_BYTES), 16, 1024);
 #pragma unroll
             for (int ks = 0; ks < HD / 16; ++ks)
               mma_ss2(tbase + LY::col_s(w, buf), qa.at((ks / 4) * (128 * 128) + (ks % 4) * 32), qa.hi,
@@ -684,9 +692,9 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, 1)
         mbar_arrive_expect_tx(&q_full[qs], tiles * LY::Q_BYTES);
         for (int i = 0; i < tiles * C; ++i)
           for (int c = 0; c < KCH; ++c)
-            tma_load_3d(smem + (PAIR ? qs * LY::Q_BYTES + i * LY::RC * 128 : i * LY::Q_BYTES) +
-                            c * (128 * 128),
-                        &mQ, &q_full[qs], c * 64, list.rb * LY::ROWS + (PAIR ? 0 : i * 128),
+            tma_load_3d(smem + (NWG == 1 || PAIR ? qs : i) * LY::Q_BYTES +
+                            (C > 1 ? i * LY::RC * 128 : 0) + c * (128 * 128),
+                        &mQ, &q_full[qs], c * 64, list.rb * LY::ROWS + (C > 1 ? 0 : i * 128),
                         list.b * p.Hk + list.kh);
       }
       ++loads;
@@ -728,10 +736,10 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, 1)
     bool ok = true, end = false;
 #pragma unroll 1
     for (int un = 0;; ++un) {
-      // (a pair meets once for each unit, whatever a warp has come upon: here, or at the unit's end)
+      // (those that join meet once for each unit, whatever a warp has come upon: here, or at its end)
       ok = take_unit<false>(&units, un, w, end, lane, &wctl);
       if (!ok || end) {
-        if (PAIR) soft_any<32 * LY::SOFT>(true);
+        if (JOIN) soft_any<32 * LY::SOFT>(true);
         break;
       }
       const int slot = un % kUnits;
@@ -834,9 +842,11 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, 1)
         if (lane == 0) mbar_arrive(&p_full[wg][buf]);
       }
       // ---- the unit's end: O of all its tiles, of both warpgroups where they share the rows
-      if (PAIR) {
+      if (JOIN) {
         ml_s[un & 1][wg][row] = make_float2(m, l);
         if (soft_any<32 * LY::SOFT>(!ok)) break;
+      }
+      if (PAIR) {
         // (both warpgroups have given their last P; neither's next O can come before o_free)
         ok = wait_warp(&p_done[wg ^ 1][(g - 1) & 1], ((g - 1) >> 1) & 1, &wctl);
       }
@@ -844,20 +854,25 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, 1)
            wait_warp(&units.odd_full[slot], (un / kUnits) & 1, &wctl);
       // A wait that has run out here: O is left undefined, as the status says.
       float f0 = 1.0f, f1 = 0.0f;  // factors of O (this warpgroup's, or the first's) and the second's
-      if (PAIR) {
-        const auto& ml = ml_s[un & 1];
+      if (JOIN) {
+        constexpr int N = PAIR ? 2 : C;  // the warpgroups, or the copies
+        const float2* ml = &ml_s[un & 1][0][PAIR ? row : r];
+        constexpr int STEP = PAIR ? 128 : LY::RC;
+        const float mine_m = m, mine_l = l;
 #pragma unroll
-        for (int k = 0; k < C; ++k)
-          m = fmaxf(m, fmaxf(ml[0][r + k * LY::RC].x, ml[1][r + k * LY::RC].x));
+        for (int k = 0; k < N; ++k) m = fmaxf(m, ml[k * STEP].x);
         l = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 2 * C; ++k) {
-          const float2 x = ml[k & 1][r + k / 2 * LY::RC];
+        for (int k = 0; k < N; ++k) {
+          const float2 x = ml[k * STEP];
           if (x.y != 0.0f) l = fmaf(x.y, ex2(x.x - m), l);
         }
-        const float2 a = ml[0][row], b = ml[1][row];
-        f0 = a.y == 0.0f ? 0.0f : ex2(a.x - m);
-        f1 = b.y == 0.0f ? 0.0f : ex2(b.x - m);
+        if (PAIR) {
+          f0 = ml[0].y == 0.0f ? 0.0f : ex2(ml[0].x - m);
+          f1 = ml[STEP].y == 0.0f ? 0.0f : ex2(ml[STEP].x - m);
+        } else {
+          f0 = mine_l == 0.0f ? 0.0f : ex2(mine_m - m);
+        }
       } else if (!ok) {
         break;
       } else if (l == 0.0f) {
@@ -869,7 +884,7 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, 1)
       for (int k = 0; k < kTreeMax / 32; ++k) odd |= units.odd[slot][k] != 0;
       const size_t unit_row = ((size_t)w.b * p.Hk + w.kh) * p.rows + r0 + r;
       const size_t part = 2 * (size_t)blockIdx.x + (w.first ? 1 : 0);
-      const int prow = PAIR ? r : wg * 128 + row;  // of the unit's rows
+      const int prow = (PAIR ? 0 : wg * 128) + r;  // of the unit's rows
       float4* o_part = reinterpret_cast<float4*>(p.o_part) + part * (HD / 4) * LY::ROWS + prow;
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       if (w.whole) {
@@ -898,44 +913,48 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, 1)
       if (live) {
         constexpr int COLS = PAIR ? HD / 2 : HD;
 #pragma unroll 1
-        for (int c = PAIR ? wg * COLS : 0, ce = c + COLS; c < ce; c += 16) {
-          uint32_t x[16], y[16];
-          tmem_ld16((PAIR ? lanes : tO) + c, x);
-          if (PAIR) tmem_ld16(lanes + HD + c, y);
-          tmem_wait_ld();
-          float o[16];
+        for (int c = PAIR ? wg * COLS : 0, ce = c + COLS; c < ce; c += 32) {
+          float o[32];
+          {
+            uint32_t x[32];
+            tmem_ld32((PAIR ? lanes : tO) + c, x);
+            tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            o[e] = f0 == 0.0f ? 0.0f : __uint_as_float(x[e]) * f0;  // (O of no weight holds anything)
-            if (PAIR) o[e] += f1 == 0.0f ? 0.0f : __uint_as_float(y[e]) * f1;
+            for (int e = 0; e < 32; ++e)  // (O of no weight holds anything)
+              o[e] = f0 == 0.0f ? 0.0f : __uint_as_float(x[e]) * f0;
+          }
+          if (PAIR) {
+            uint32_t x[32];
+            tmem_ld32(lanes + HD + c, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] += f1 == 0.0f ? 0.0f : __uint_as_float(x[e]) * f1;
           }
           if constexpr (C == 1) {
             out(o, c);
             __syncwarp();
           } else {
-            // into shared memory
-            float4* join = reinterpret_cast<float4*>(smem + LY::OFF_JOIN) + wg * (128 * 8);
+            // the copies' sums, through shared memory: a thread has 32 / C of the 32 columns
+            float4* join = reinterpret_cast<float4*>(smem + LY::OFF_JOIN);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              join[row * 8 + ((c / 4 & 7) + k ^ (row & 7))] =
+            for (int k = 0; k < 8; ++k)
+              join[row * 8 + (k ^ (row & 7))] =
                   make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-          }
-        }
-        if constexpr (C > 1) {  // the copies' sums: a thread has 32 / C of the 32 columns
-          group_sync(wg);
-          const float4* join = reinterpret_cast<const float4*>(smem + LY::OFF_JOIN) + wg * (128 * 8);
-          constexpr int N = 32 / C;
-          float z[N] = {};
+            soft_sync();
+            constexpr int N = 32 / C;
+            float z[N] = {};
 #pragma unroll
-          for (int i = 0; i < C; ++i) {
-            const int from = r + i * LY::RC;
+            for (int i = 0; i < C; ++i) {
+              const int from = r + i * LY::RC;
 #pragma unroll
-            for (int k = 0; k < N; k += 4) {
-              const float4 v = join[from * 8 + ((copy * (N / 4) + k / 4) ^ (from & 7))];
-              z[k] += v.x, z[k + 1] += v.y, z[k + 2] += v.z, z[k + 3] += v.w;
+              for (int k = 0; k < N; k += 4) {
+                const float4 v = join[from * 8 + ((copy * (N / 4) + k / 4) ^ (from & 7))];
+                z[k] += v.x, z[k + 1] += v.y, z[k + 2] += v.z, z[k + 3] += v.w;
+              }
             }
+            soft_sync();
+            out(z, c + copy * N);
           }
-          out(z, wg * COLS + copy * N);
         }
         if (mine && copy == 0 && (!PAIR || wg == 0)) {
           if (!w.whole) {
@@ -1046,13 +1065,13 @@ struct TreePlan {
 TreePlan tree_plan(const TreeArgs& a) {
   TreePlan pl;
   const int rows = a.G * a.T;
-  pl.pair = rows <= 128 && a.d <= 128;
   pl.C = a.d > 64 || rows > 64 ? 1 : rows > 32 ? 2 : 4;
-  pl.ROWS = pl.pair ? 128 / pl.C : a.d <= 128 ? 256 : 128;
+  pl.pair = rows <= 128 && a.d <= 128 && pl.C == 1;
+  pl.ROWS = pl.pair || pl.C > 1 ? 128 / pl.C : a.d <= 128 ? 256 : 128;
   pl.rb = (rows + pl.ROWS - 1) / pl.ROWS;
   const long long cap = (long long)a.max_pages << a.ps_shift;
   const long long tiles = ((cap + kHT - 1) / kHT + kUnitCost) * a.B * a.Hk * pl.rb;  // (at most)
-  pl.grid = (int)std::min<long long>(152, tiles);
+  pl.grid = (int)std::min<long long>(pl.C > 1 ? 304 : 152, tiles);
   return pl;
 }
 
@@ -1120,10 +1139,10 @@ cudaError_t launch_tree(const TreeArgs& a, const TreeMaps& m, void* ws, cudaStre
   const TreePlan pl = tree_plan(a);
   switch (a.d) {
     case 64:
-      if (!pl.pair) return launch_tree_t<64, false, 1>(a, m, pl, ws, s);
-      return pl.C == 1   ? launch_tree_t<64, true, 1>(a, m, pl, ws, s)
-             : pl.C == 2 ? launch_tree_t<64, true, 2>(a, m, pl, ws, s)
-                         : launch_tree_t<64, true, 4>(a, m, pl, ws, s);
+      return pl.pair     ? launch_tree_t<64, true, 1>(a, m, pl, ws, s)
+             : pl.C == 1 ? launch_tree_t<64, false, 1>(a, m, pl, ws, s)
+             : pl.C == 2 ? launch_tree_t<64, false, 2>(a, m, pl, ws, s)
+                         : launch_tree_t<64, false, 4>(a, m, pl, ws, s);
     case 128:
       return pl.pair ? launch_tree_t<128, true, 1>(a, m, pl, ws, s)
                      : launch_tree_t<128, false, 1>(a, m, pl, ws, s);

@@ -83,12 +83,20 @@ def lib():
     return fa.load_library()
 
 
+def rope(**kw):
+    return ctypes.byref(fa.FaRotary(**dict(ROPE, **kw)))
+
+
+def params(**kw):
+    return ctypes.byref(fa.FaPagedParams(**dict(PARAMS, **kw)))
+
+
 def struct(cls, base, **kw):
     d = dict(base, **kw)
     for n in d:
         if n.endswith("_stride") and n != "pos_stride":
             d[n] = (ctypes.c_int64 * 3)(*d[n])
-    return cls(**d)
+    return ctypes.byref(cls(**d))
 
 
 def ids(kw):
@@ -97,7 +105,7 @@ def ids(kw):
 
 @pytest.mark.parametrize("kw", BAD_ROPE, ids=ids)
 def test_bad_rotations_are_refused(lib, kw):
-    r = fa.FaRotary(**dict(ROPE, **kw))
+    r = rope(**kw)
     assert lib.fa_rotary_apply(struct(fa.FaRotaryRows, ROTATE), r, 0, None) == fa.FA_ERR_INVALID
     assert lib.fa_paged_append(struct(fa.FaPagedRows, APPEND), r, None) == fa.FA_ERR_INVALID
 
@@ -105,13 +113,13 @@ def test_bad_rotations_are_refused(lib, kw):
 @pytest.mark.parametrize("kw", BAD_ROTATE, ids=ids)
 def test_bad_rows_are_refused(lib, kw):
     rows = struct(fa.FaRotaryRows, ROTATE, **kw)
-    assert lib.fa_rotary_apply(rows, fa.FaRotary(**ROPE), 0, None) == fa.FA_ERR_INVALID
+    assert lib.fa_rotary_apply(rows, rope(), 0, None) == fa.FA_ERR_INVALID
 
 
 @pytest.mark.parametrize("kw", BAD_APPEND, ids=ids)
 def test_bad_appends_are_refused(lib, kw):
     rows = struct(fa.FaPagedRows, APPEND, **kw)
-    assert lib.fa_paged_append(rows, fa.FaRotary(**ROPE), None) == fa.FA_ERR_INVALID
+    assert lib.fa_paged_append(rows, rope(), None) == fa.FA_ERR_INVALID
 
 
 @pytest.mark.parametrize("kw", BAD_KEPT, ids=ids)
@@ -121,7 +129,7 @@ def test_bad_keeps_are_refused(lib, kw):
 
 @pytest.mark.parametrize("kw", BAD_PARAMS, ids=ids)
 def test_bad_tree_parameters_are_refused(lib, kw):
-    p = fa.FaPagedParams(**dict(PARAMS, **kw))
+    p = params(**kw)
     assert lib.fa_paged_tree_attention(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 0, FAKE, None, p,
                                        None) == fa.FA_ERR_INVALID
 
@@ -129,26 +137,26 @@ def test_bad_tree_parameters_are_refused(lib, kw):
 @pytest.mark.parametrize("i,value", [(0, None), (1, FAKE + 8), (2, None), (3, FAKE + 2), (4, None),
                                      (5, None), (6, -1), (7, FAKE + 2), (8, FAKE + 1), (9, None)])
 def test_bad_tree_arguments_are_refused(lib, i, value):
-    args = [FAKE] * 6 + [0, FAKE, None, fa.FaPagedParams(**PARAMS), None]
+    args = [FAKE] * 6 + [0, FAKE, None, params(), None]
     args[i] = value
     assert lib.fa_paged_tree_attention(*args) == fa.FA_ERR_INVALID
 
 
 def test_other_bad_calls(lib):
-    rope, bad = fa.FaRotary(**ROPE), fa.FA_ERR_INVALID
-    assert lib.fa_rotary_apply(None, rope, 0, None) == bad
+    turn, bad = rope(), fa.FA_ERR_INVALID
+    assert lib.fa_rotary_apply(None, turn, 0, None) == bad
     assert lib.fa_rotary_apply(struct(fa.FaRotaryRows, ROTATE), None, 0, None) == bad
-    assert lib.fa_rotary_apply(struct(fa.FaRotaryRows, ROTATE), rope, 2, None) == bad
-    own = fa.FaRotary(**dict(ROPE, positions=at(9)))
+    assert lib.fa_rotary_apply(struct(fa.FaRotaryRows, ROTATE), turn, 2, None) == bad
+    own = rope(positions=at(9))
     packed = struct(fa.FaRotaryRows, ROTATE, cu_seqlens=at(8))
     assert lib.fa_rotary_apply(packed, own, 0, None) == bad
-    assert lib.fa_paged_append(None, rope, None) == bad
+    assert lib.fa_paged_append(None, turn, None) == bad
     # queries, and an offset, where nothing turns them or the cache says where they are
     assert lib.fa_paged_append(struct(fa.FaPagedRows, APPEND), None, None) == bad
-    shifted = fa.FaRotary(**dict(ROPE, offset=1))
+    shifted = rope(offset=1)
     assert lib.fa_paged_append(struct(fa.FaPagedRows, APPEND), shifted, None) == bad
     packed = struct(fa.FaPagedRows, APPEND, cu_seqlens=at(8), total=8, new_len=0)
-    strided = fa.FaRotary(**dict(ROPE, positions=at(9), pos_stride=8))
+    strided = rope(positions=at(9), pos_stride=8)
     assert lib.fa_paged_append(packed, strided, None) == bad
     assert lib.fa_paged_keep(None, None) == bad
 
@@ -158,19 +166,19 @@ def test_good_calls_get_past_the_checks(lib):
     torch = pytest.importorskip("torch")
     if torch.cuda.is_available():
         pytest.skip("the pointers are not real")
-    rope = fa.FaRotary(**ROPE)
+    turn = rope()
     good = [dict(), dict(k=None, k_out=None, n_kv_heads=0), dict(q_out=at(0), k_out=at(1)),
             dict(q_out_stride=(4096, 128, 512)), dict(cu_seqlens=at(8)), dict(rows=0)]
     for kw in good:
         rows = struct(fa.FaRotaryRows, ROTATE, **kw)
-        assert lib.fa_rotary_apply(rows, rope, 1, None) != fa.FA_ERR_INVALID, kw
+        assert lib.fa_rotary_apply(rows, turn, 1, None) != fa.FA_ERR_INVALID, kw
     for kw in (dict(), dict(cu_seqlens=at(8), total=8, new_len=0)):
         rows = struct(fa.FaPagedRows, APPEND, **kw)
-        assert lib.fa_paged_append(rows, rope, None) != fa.FA_ERR_INVALID, kw
+        assert lib.fa_paged_append(rows, turn, None) != fa.FA_ERR_INVALID, kw
     rows = struct(fa.FaPagedRows, APPEND, q=None, q_out=None, n_heads=0)
     assert lib.fa_paged_append(rows, None, None) != fa.FA_ERR_INVALID
     assert lib.fa_paged_keep(struct(fa.FaPagedKept, KEPT), None) != fa.FA_ERR_INVALID
-    p = fa.FaPagedParams(**PARAMS)
+    p = params()
     assert lib.fa_paged_tree_attention(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 64, FAKE, None, p,
                                        None) != fa.FA_ERR_INVALID
 
