@@ -1040,6 +1040,8 @@ def _rotate(q, k, inv_freq, back, positions, cu_seqlens, offset, interleaved, sc
             raise ValueError("cu_seqlens must be a contiguous int32 tensor of B + 1 entries")
     if positions is not None and offset:
         raise ValueError("offset is for rows without positions")
+    if not -2 ** 31 <= offset <= 2 ** 31 - max(n, 1):
+        raise ValueError("positions must fit 32 bits")
     rot = _rotary(inv_freq, positions, B, n, interleaved, offset, scale, packed, torch)
     qs = _q8_rows(q, "q", torch)
     ks = _NO_STRIDES if k is None else _q8_rows(k, "k", torch)

@@ -1089,6 +1089,7 @@ int fa_rotary_apply(const fa_rotary_rows* r, const fa_rotary* rotary, int back, 
   if ((r->k == nullptr) != (r->n_kv_heads == 0) || (r->k == nullptr) != (r->k_out == nullptr))
     return FA_ERR_INVALID;
   const int64_t B = packed ? 1 : r->batch, n = r->rows > 0 ? r->rows : 1;
+  if ((int64_t)rotary->offset + n - 1 > INT32_MAX) return FA_ERR_INVALID;
   const int segs = r->k ? 2 : 1;
   const void* src[2] = {r->q, r->k};
   void* dst[2] = {r->q_out, r->k_out};
@@ -1164,15 +1165,20 @@ int fa_paged_append(const fa_paged_rows* r, const fa_rotary* rotary, void* strea
       !row_extent(r->v, r->v_stride, B, r->n_kv_heads, n, d, &v))
     return FA_ERR_INVALID;
   const int64_t q_out_stride[3] = {(int64_t)r->n_heads * n * d, n * d, d};
+  // what is written shares no memory with what is read
+  Extent kc, vc;
+  const int64_t cache_rows = (int64_t)r->n_kv_heads * r->page_size;
+  const int64_t flat[3] = {0, cache_rows * d, d};
+  if (!row_extent(r->k_cache, flat, 1, r->num_pages, cache_rows, d, &kc) ||
+      !row_extent(r->v_cache, flat, 1, r->num_pages, cache_rows, d, &vc) || kc.meets(vc) ||
+      kc.meets(k) || kc.meets(v) || vc.meets(k) || vc.meets(v))
+    return FA_ERR_INVALID;
   if (r->q) {
-    Extent out, kc, vc;
-    const int64_t cache_rows = (int64_t)r->n_kv_heads * r->page_size;
-    const int64_t flat[3] = {0, cache_rows * d, d};
+    Extent out;
     if (!row_extent(r->q, r->q_stride, B, r->n_heads, n, d, &q) ||
-        !row_extent(r->q_out, q_out_stride, B, r->n_heads, n, d, &out) ||
-        !row_extent(r->k_cache, flat, 1, r->num_pages, cache_rows, d, &kc) ||
-        !row_extent(r->v_cache, flat, 1, r->num_pages, cache_rows, d, &vc) || out.meets(q) ||
-        out.meets(k) || out.meets(v) || out.meets(kc) || out.meets(vc))
+        !row_extent(r->q_out, q_out_stride, B, r->n_heads, n, d, &out) || out.meets(q) ||
+        out.meets(k) || out.meets(v) || out.meets(kc) || out.meets(vc) || q.meets(kc) ||
+        q.meets(vc))
       return FA_ERR_INVALID;
   }
   fa::RowsArgs a = {};

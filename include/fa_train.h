@@ -467,7 +467,8 @@ typedef struct fa_rotary {
   int64_t pos_stride;       /* >= 0 (0: the same positions for every sequence) */
   int32_t rotary_dim;       /* a multiple of 16, at most head_dim */
   int32_t interleaved;      /* 0 or 1 */
-  int32_t offset;           /* added to the places; 0 with positions and in fa_paged_append */
+  int32_t offset;           /* added to the places (the last is below 2^31); 0 with positions and in
+                               fa_paged_append */
   float scale;              /* finite; of the turned elements */
 } fa_rotary;
 
@@ -516,10 +517,9 @@ typedef struct fa_paged_rows {
   const void* k;
   const void* v;
   const void* q;             /* NULL: no queries (n_heads = 0) */
-  void* q_out;               /* bf16 [batch, n_heads, new_len, head_dim], packed [n_heads, total, head_dim];
-                                shares no memory with k, v, q and the caches */
+  void* q_out;               /* bf16 [batch, n_heads, new_len, head_dim], packed [n_heads, total, head_dim] */
   void* k_cache;             /* bf16 [num_pages, n_kv_heads, page_size, head_dim], 16-byte aligned */
-  void* v_cache;             /* same */
+  void* v_cache;             /* same (q_out and the caches share no memory with k, v, q and one another) */
   int64_t k_stride[3];
   int64_t v_stride[3];
   int64_t q_stride[3];

@@ -61,6 +61,8 @@ BAD_APPEND = [
     dict(cu_seqlens=at(8), total=-1, new_len=0), dict(cu_seqlens=at(8), total=8, new_len=8),
     dict(batch=1 << 20, new_len=1 << 20), dict(reserved=1), dict(n_heads=65534),
     dict(q_out=at(2)), dict(q_out=at(0)), dict(q_out=at(1)), dict(q_out=at(4)), dict(q_out=at(5)),
+    dict(k=at(4)), dict(k=at(5)), dict(v=at(4) + 16), dict(v=at(5)), dict(q=at(4)), dict(q=at(5)),
+    dict(v_cache=at(4)),
 ]
 BAD_KEPT = [
     dict(k_cache=None), dict(v_cache=at(1) + 8), dict(block_table=None), dict(lengths=at(3) + 1),
@@ -156,6 +158,8 @@ def test_other_bad_calls(lib):
     shifted = rope(offset=1)
     assert lib.fa_paged_append(struct(fa.FaPagedRows, APPEND), shifted, None) == bad
     packed = struct(fa.FaPagedRows, APPEND, cu_seqlens=at(8), total=8, new_len=0)
+    assert lib.fa_rotary_apply(struct(fa.FaRotaryRows, ROTATE), rope(offset=2 ** 31 - 7), 0,
+                               None) == bad  # its last row's position
     strided = rope(positions=at(9), pos_stride=8)
     assert lib.fa_paged_append(packed, strided, None) == bad
     assert lib.fa_paged_keep(None, None) == bad
@@ -229,6 +233,8 @@ def test_the_binding_refuses_what_it_cannot_pass_on():
     refused("contiguous", fa.rotary_fwd, q, x, f,
             positions=torch.zeros(1, 6, dtype=torch.int32)[:, ::2])
     refused("offset", fa.rotary_fwd, q, x, f, positions=pos, offset=1)
+    for n in (2 ** 31, 2 ** 31 - 2, -2 ** 31 - 1):
+        refused("32 bits", fa.rotary_fwd, q, x, f, offset=n)
     refused("cu_seqlens", fa.rotary_fwd, q, x, f, cu_seqlens=cu)
     refused("cu_seqlens", fa.rotary_fwd, q[0], x[0], f, cu_seqlens=cu, positions=pos[0])
     refused("cu_seqlens", fa.rotary_fwd, q[0], x[0], f, cu_seqlens=cu.long())
