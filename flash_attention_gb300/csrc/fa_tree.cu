@@ -527,7 +527,10 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, TreeLayout<H
     }
   } else if (warp == LY::S_WARP) {
     // ------------------------------------------------------------------ S = Q K^T
-    if (lane == 0) {
+    // (Inside elect_one the compiler keeps descriptors in uniform registers; behind a test of the lane
+    // an MMA takes 67 cycles to issue whatever its shape, so 45 for N = 64, 59 for 128, which is its
+    // arithmetic, and with A in tensor memory 29 for N = 64.)
+    if (elect_one()) {
       const uint32_t id = idesc_bf16(128, LY::KT, 0, 0);
       const Desc k0 = make_desc(smem_u32(smem + LY::OFF_K), 16, KCH * 1024);
       int g = 0, st = 0;
@@ -608,7 +611,7 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, TreeLayout<H
           ok = ok && wait_warp(&p_full[i][buf], (g >> 1) & 1, &wctl);
           if (!ok) break;
           tc_fence_after();
-          if (lane == 0) {
+          if (elect_one()) {
             const Desc vb = make_desc(smem_u32(vt), 1024, KCH * 1024);  // V, MN-major
 #pragma unroll
             for (int ks = 0; ks < kHT / 16; ++ks)
@@ -621,7 +624,7 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, TreeLayout<H
         }
       }
     }
-    if (lane == 0) {
+    if (elect_one()) {  // (the same thread)
       mma_commit(&drain_o);
       mbar_wait_drain(&drain_o, 0);
     }
