@@ -8,16 +8,20 @@
 //
 // The G query heads of a kv head and the T nodes are rows of one product, so that a key is read once
 // for all of them; with 4 d bytes and 4 d flops a row for each key, HBM bounds it up to some 280 rows
-// a kv head. Up to that the work beside the bytes has to fit in the time of the bytes, 700 cycles for a
-// tile of 64 keys at head_dim 64, 1400 at 128: two softmax warpgroups (thread = row), which alternate.
-//  * up to 128 rows (PAIR): tiles of 128 keys, of which each has a half, with an O, a maximum and a sum
-//    of its own; they are joined at a unit's end, in tensor memory, where a thread of either can read
-//    both O's;
-//  * more rows: each has 128 of a block's 256, on the same tiles of 64 keys. (At head_dim 256 tensor
-//    memory holds one O: one warpgroup, blocks of 128 rows.)
-// S = Q K^T (M = 128 rows; N = 128 keys for a pair, whose halves' scores lie side by side, else 64) and
-// O += P V, with P in bf16 over S in tensor memory (two S buffers for each warpgroup); the lazy rescale
-// of the training forward. Sums are f32.
+// a kv head. S = Q K^T (M = 128 rows, N = 64 keys) and O += P V, with P in bf16 over S in tensor memory
+// (two buffers); a thread of the softmax has a row; the lazy rescale of the training forward; sums are
+// f32. What has to fit beside the bytes of a tile is a chain of latencies (scores, softmax, weights), so:
+//  * up to 128 rows, head_dim 64 and 128: two CTAs an SM with 128 rows each, which fill each other's
+//    waits and the starts and ends of each other's units. (One CTA with two softmax warpgroups on the
+//    halves of 128-key tiles, an O each, joined at a unit's end, and rings 1.4 times as deep: 132 us for
+//    125 for 16 sequences of up to 16k keys with 128 rows, 350 for 342 for 64 with 48, 61 for 43 at
+//    head_dim 64.)
+//  * at head_dim 64 with up to 64 (32) rows these are there twice (four times): a copy has a half (a
+//    quarter) of a tile's keys, with a maximum, a sum and an O of its own; four warps share a tile's
+//    exponentials then instead of two or one. They are joined at a unit's end, through shared memory.
+//  * more rows: one CTA, whose two warpgroups have 128 of a block's 256 rows each, on the same keys (two
+//    CTAs of 128 rows, which read keys again: 101 us for 90 for 16 sequences of up to 8k keys). At head_dim 256
+//    tensor memory holds one O: one warpgroup, blocks of 128 rows, one CTA.
 //
 // Work: the (sequence, kv head, row block) units, each with its key tiles, form one list of
 // tiles, cut evenly over persistent CTAs, one on an SM (the lengths are on the device; each CTA finds
@@ -45,55 +49,51 @@
 namespace fa {
 
 namespace {
-constexpr int kHT = 64;          // keys of a stage of the rings: of a tile, or half of one (PAIR)
-constexpr int kUnitCost = 3;     // tiles' worth of a unit's start and end
+constexpr int kKT = 64;          // keys of a tile
+// Tiles' worth of a unit's start and end (16 sequences of up to 8k keys, 256 rows, head_dim 128: 92 us with 3,
+// 85 with 5, 82 with 8; 100 of up to 2k, 17 rows, head_dim 64: 51.0, 51.6, 53.2).
+constexpr int kUnitCost = 5;
 constexpr int kPageChunk = 128;  // block-table entries staged at a time
 constexpr int kUnits = 3;        // units published
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;
 
-template <int HD, bool PAIR, int C>
+// C copies of a unit's rows, CT CTAs on an SM.
+template <int HD, int C, int CT>
 struct TreeLayout {
-  static constexpr int NWG = HD <= 128 && C == 1 ? 2 : 1;  // softmax warpgroups
-  static constexpr int CTAS = C > 1 ? 2 : 1;         // resident on an SM
+  static constexpr int NWG = HD <= 128 && CT == 1 ? 2 : 1;  // softmax warpgroups
   static constexpr int RC = 128 / C;                 // query rows of a copy
-  static constexpr int ROWS = PAIR ? 128 : RC * NWG;  // of a unit
-  static constexpr int KT = PAIR ? 2 * kHT : kHT;    // keys of a tile
-  static constexpr int HALVES = KT / kHT;
-  // stages of the rings; V has more where there is room, as a V stage stays until the weights of its
-  // keys are there (a pair's K are even: the halves of a tile are one operand)
-  static constexpr int KST = HD == 64 ? (C > 1 ? 3 : 8) : HD == 128 ? (PAIR ? 6 : 4) : 2;
-  static constexpr int VST = HD == 64 ? (C > 1 ? 4 : 12) : HD == 128 ? (PAIR ? 5 : 4) : 2;
+  static constexpr int ROWS = RC * NWG;              // of a unit
+  static constexpr int NC = kKT / C;                 // keys of a tile that a thread has
+  // Stages of the rings; V has more where there is room, as a V stage stays until the weights of its
+  // keys are there.
+  static constexpr int KST = HD == 64 ? (C > 1 ? 3 : CT == 2 ? 4 : 8) : HD == 128 && CT == 1 ? 4 : 2;
+  static constexpr int VST = HD == 64 ? (CT == 2 ? 4 : 12) : KST;
+  // Units whose Q is held: a second one costs stages. (Its load runs beside a unit's last softmax.)
+  static constexpr int QB = HD == 64 && CT == 2 ? 2 : 1;
   static constexpr int KCH = HD / 64;
   static constexpr int Q_BYTES = 128 * HD * 2;       // of 128 rows
-  // Units whose Q is held: a second one costs stages. (Its load runs beside a unit's last softmax.)
-  static constexpr int QB = HD == 64 && (PAIR || C > 1) ? 2 : 1;
-  static constexpr int ST_BYTES = kHT * HD * 2;
-  static constexpr int OFF_K = (NWG == 1 || PAIR ? QB : NWG) * Q_BYTES;
+  static constexpr int ST_BYTES = kKT * HD * 2;
+  static constexpr int OFF_K = (NWG == 1 ? QB : NWG) * Q_BYTES;
   static constexpr int OFF_V = OFF_K + KST * ST_BYTES;
   static constexpr int OFF_JOIN = OFF_V + VST * ST_BYTES;  // 32 columns of the copies' O
   static constexpr int OFF_BITS = OFF_JOIN + (C > 1 ? 128 * 128 : 0);  // the masks' words
-  static constexpr int COL_S = NWG * HD;             // O of each warpgroup, then S
-  static constexpr int TMEM_COLS = 512 / CTAS;
+  static constexpr int COL_S = NWG * HD;             // O of each warpgroup, then its two S (and P)
+  static constexpr int TMEM_COLS = 512 / CT;
   static constexpr int SOFT = 4 * NWG;
   static constexpr int K_WARP = SOFT, V_WARP = SOFT + 1, S_WARP = SOFT + 2, O_WARP = SOFT + 3,
                        LIST_WARP = SOFT + 4, FIX_WARP = SOFT + 5;
   static constexpr int THREADS = 32 * (SOFT + 6);
-  // columns of S (and P) of warpgroup w in its buffer b: for a pair the two lie side by side
-  static __device__ __forceinline__ uint32_t col_s(int w, int b) {
-    return COL_S + (PAIR ? b * 2 + w : w * 2 + b) * kHT;
-  }
-  static_assert(!PAIR || (NWG == 2 && KST % 2 == 0), "pairs need two warpgroups");
-  static_assert(C == 1 || (!PAIR && HD == 64), "two CTAs an SM at head_dim 64 alone");
-  static_assert(COL_S + NWG * 2 * kHT <= TMEM_COLS, "TMEM budget");
-  static constexpr int T_MAX = PAIR || C > 1 ? RC : kTreeMax;
+  static __device__ __forceinline__ uint32_t col_s(int w, int b) { return COL_S + (w * 2 + b) * kKT; }
+  static_assert(C == 1 || (CT == 2 && HD == 64), "not a variant");
+  static_assert(COL_S + NWG * 2 * kKT <= TMEM_COLS, "TMEM budget");
+  static constexpr int T_MAX = CT == 2 ? RC : kTreeMax;
   static constexpr int smem_bytes(int T) {
     return OFF_BITS + kUnits * T * ((T + 31) / 32) * 4 + 1024;
   }
   // (and what is static, and the driver's 1 KB)
-  static_assert((smem_bytes(T_MAX) + (PAIR ? 6400 : 4096) + 1024) * CTAS <= 228 * 1024,
-                "shared memory budget");
+  static_assert((smem_bytes(T_MAX) + 4096 + 1024) * CT <= 228 * 1024, "shared memory budget");
 };
 
 struct TreeK {
@@ -107,7 +107,7 @@ struct TreeK {
   float* o_part;   // [2 * grid, HD / 4, ROWS, 4]: O of a share, in units of 2^m
   float* ml_part;  // [2 * grid, 2, ROWS]: m and the sum
   int* status;
-  int B, Hk, T, words, rows, rb, max_pages, num_pages, ps_shift, kt_shift;
+  int B, Hk, T, words, rows, rb, max_pages, num_pages, ps_shift;
   float scale_log2;
   unsigned long long wait_limit_ns;
 };
@@ -120,7 +120,7 @@ __device__ __forceinline__ int tree_len(const TreeK& p, int b) {
 // What a unit of sequence b counts in the list; 0 without keys.
 __device__ __forceinline__ int tree_cost(const TreeK& p, int b) {
   const int len = tree_len(p, b);
-  return len > 0 ? ((len - 1) >> p.kt_shift) + 1 + kUnitCost : 0;
+  return len > 0 ? (len + kKT - 1) / kKT + kUnitCost : 0;
 }
 // The sum over all sequences (of one unit each), by one warp that has that of sequence `lane`. The
 // host has checked that the whole list, Hk * rb times as long, fits 31 bits.
@@ -295,7 +295,7 @@ __device__ __noinline__ void tree_tile(uint8_t* vt, int n0, int tree0, int len, 
     return reinterpret_cast<uint4*>(vt + (r / 8 * (HD / 64) + g / 8) * 1024 + (r & 7) * 128 +
                                     ((g % 8) ^ (r & 7)) * 16);
   };
-  const int begin = max(0, tree0 - n0), end = min(kHT, len - n0);
+  const int begin = max(0, tree0 - n0), end = min(kKT, len - n0);
   // A value times 0 is 0 or, of one that is not finite, NaN.
   const __nv_bfloat162 zero = __float2bfloat162_rn(0.0f);
   __nv_bfloat162 test[2] = {zero, zero};
@@ -322,7 +322,7 @@ __device__ __noinline__ void tree_tile(uint8_t* vt, int n0, int tree0, int len, 
     }
   }
 #pragma unroll 4
-  for (int e = lane + end * G8; e < kHT * G8; e += 32) *at(e / G8, e % G8) = make_uint4(0, 0, 0, 0);
+  for (int e = lane + end * G8; e < kKT * G8; e += 32) *at(e / G8, e % G8) = make_uint4(0, 0, 0, 0);
 }
 
 // Values that tree_tile has cleared, of the nodes that a row sees, added to N of its columns.
@@ -366,44 +366,42 @@ __device__ __forceinline__ void soft_sync() {
   asm volatile("barrier.cta.sync 2, 128;" ::: "memory");
 }
 
-// The barrier of the softmax's threads; true where any of them came with `v`.
-template <int N>
+// The same; true where any of them came with `v`.
 __device__ __forceinline__ bool soft_any(bool v) {
   int r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, %2, p;\n"
+      "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, 128, p;\n"
       " selp.s32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
-      : "r"((int)v), "n"(N)
+      : "r"((int)v)
       : "memory");
   return r != 0;
 }
 
-template <int HD, bool PAIR, int C>
-__global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, TreeLayout<HD, PAIR, C>::CTAS)
+template <int HD, int C, int CT>
+__global__ void __launch_bounds__(TreeLayout<HD, C, CT>::THREADS, CT)
     tree_kernel(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
                 const __grid_constant__ CUtensorMap mV, const TreeK p) {
-  using LY = TreeLayout<HD, PAIR, C>;
-  constexpr int KCH = LY::KCH, NWG = LY::NWG, HALVES = LY::HALVES;
-  constexpr bool JOIN = PAIR || C > 1;  // a row's O lies in several places
+  using LY = TreeLayout<HD, C, CT>;
+  constexpr int KCH = LY::KCH, NWG = LY::NWG;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  // Tile g's S is in buffer g & 1. s_full: it is there (a pair's, of both, in [0]); p_full: P is, of a
-  // warpgroup; p_done: O has it. (The rings' empty barriers are their own: a stage may be filled again
+  // Tile g's S and P are in buffer g & 1 of each warpgroup. s_full: S is there; p_full: P is; p_done: O has
+  // it. (The rings' empty barriers are their own: a stage may be filled again
   // when the phase of p_done or s_full that freed it is two phases old.)
   __shared__ uint64_t k_full[LY::KST], v_full[LY::VST], k_empty[LY::KST], v_empty[LY::VST];
   // of stages with V of the tree's keys: asked for (only then is v_full's phase the one of that copy),
   // and looked over
   __shared__ uint64_t v_tail[LY::VST], v_fixed[LY::VST];
   __shared__ uint64_t s_full[NWG][2], p_full[NWG][2], p_done[NWG][2], q_full[2], q_free[2];
-  __shared__ uint64_t o_free, drain_s, drain_o;
+  __shared__ uint64_t drain_s, drain_o;
   __shared__ __align__(16) TreeRing units;
   __shared__ uint32_t tmem_base_s;
   __shared__ WaitCtl wctl;
   __shared__ int bad_input;
   __shared__ int page_s[2][kPageChunk];
-  __shared__ float2 ml_s[2][PAIR ? 2 : 1][JOIN ? 128 : 1];  // of a unit (even, odd): m and the sum of each warpgroup's rows
+  __shared__ float2 ml_s[2][C > 1 ? 128 : 1];  // of a unit (even, odd): m and the sum of each copy's rows
   unsigned* bits = reinterpret_cast<unsigned*>(smem + LY::OFF_BITS);
 
   const int warp = warp_id(), lane = lane_id();
@@ -439,7 +437,6 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, TreeLayout<H
       mbar_init(&units.bits_full[s], 1);
       mbar_init(&units.odd_full[s], 1);
     }
-    mbar_init(&o_free, LY::SOFT);
     mbar_init(&drain_s, 1);
     mbar_init(&drain_o, 1);
     fence_barrier_init();
@@ -459,12 +456,13 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, TreeLayout<H
     const bool leader = lane == 0, is_v = warp == LY::V_WARP;
     const CUtensorMap* map = is_v ? &mV : &mK;
     uint64_t* full = is_v ? v_full : k_full;
+    uint64_t* empty = is_v ? v_empty : k_empty;
     uint8_t* ring = smem + (is_v ? LY::OFF_V : LY::OFF_K);
     const int ST = is_v ? LY::VST : LY::KST;
     int* pages = page_s[is_v];
     if (leader) tma_prefetch_desc(map);
-    const int box = min(1 << p.ps_shift, kHT);  // rows of a box
-    const int boxes = kHT / box;                // of a tile (at most 8)
+    const int box = min(1 << p.ps_shift, kKT);  // rows of a box
+    const int boxes = kKT / box;                // of a tile (at most 8)
     const int z_oob = p.num_pages * p.Hk;       // a page past the cache: zero fill
     int g = 0, st = 0;                          // copies so far, the next one's stage
     int page_b = -1, page_lo = 0;               // pages: entries page_lo .. of sequence page_b
@@ -475,9 +473,9 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, TreeLayout<H
       const int used = (w.len + (1 << p.ps_shift) - 1) >> p.ps_shift;
       const int32_t* row = p.table + (size_t)w.b * p.max_pages;
 #pragma unroll 1
-      for (int j = w.ja * HALVES; j < w.jb * HALVES; ++j, ++g) {
-        const int n0 = j * kHT;  // (past the sequence's end: zeros, and no page)
-        const int p_lo = n0 >> p.ps_shift, p_hi = min(used - 1, (n0 + kHT - 1) >> p.ps_shift);
+      for (int j = w.ja; j < w.jb; ++j, ++g) {
+        const int n0 = j * kKT;
+        const int p_lo = n0 >> p.ps_shift, p_hi = min(used - 1, (n0 + kKT - 1) >> p.ps_shift);
         if (page_b != w.b || p_lo < page_lo || p_hi >= page_lo + kPageChunk) {
           page_b = w.b;
           page_lo = p_lo;
@@ -504,11 +502,9 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, TreeLayout<H
           }
         }
         if (leader) {
-          // (of K, a tile's stages are freed as one)
-          uint64_t* empty = is_v ? &v_empty[st] : &k_empty[st / HALVES * HALVES];
-          if (g >= ST) ok = wait(empty, (g / ST - 1) & 1, &wctl);
+          if (g >= ST) ok = wait(&empty[st], (g / ST - 1) & 1, &wctl);
           if (ok) mbar_arrive_expect_tx(&full[st], LY::ST_BYTES);
-          if (ok && is_v && n0 + kHT > w.len - p.T && n0 < w.len) mbar_arrive(&v_tail[st]);
+          if (ok && is_v && n0 + kKT > w.len - p.T) mbar_arrive(&v_tail[st]);
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
@@ -531,7 +527,7 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, TreeLayout<H
     // an MMA takes 67 cycles to issue whatever its shape, so 45 for N = 64, 59 for 128, which is its
     // arithmetic, and with A in tensor memory 29 for N = 64.)
     if (elect_one()) {
-      const uint32_t id = idesc_bf16(128, LY::KT, 0, 0);
+      const uint32_t id = idesc_bf16(128, kKT, 0, 0);
       const Desc k0 = make_desc(smem_u32(smem + LY::OFF_K), 16, KCH * 1024);
       int g = 0, st = 0;
       bool ok = true;
@@ -549,15 +545,13 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, TreeLayout<H
           const uint32_t before = ((g >> 1) - 1) & 1;  // the buffer's last P is done with
           for (int w = 0; w < NWG; ++w)
             if (ok && g >= 2) ok = wait(&p_done[w][buf], before, &wctl);
-          for (int h = 0; h < HALVES; ++h)
-            ok = ok && wait(&k_full[st + h], (g * HALVES / LY::KST) & 1, &wctl);
+          ok = ok && wait(&k_full[st], (g / LY::KST) & 1, &wctl);
           if (!ok) break;
           tc_fence_after();
           const Desc kb{k0.at(st * LY::ST_BYTES), k0.hi};
 #pragma unroll
-          for (int w = 0; w < (PAIR ? 1 : NWG); ++w) {
-            const Desc qa =
-                make_desc(smem_u32(smem + (NWG == 1 || PAIR ? qs : w) * LY::Q_BYTES), 16, 1024);
+          for (int w = 0; w < NWG; ++w) {
+            const Desc qa = make_desc(smem_u32(smem + (NWG == 1 ? qs : w) * LY::Q_BYTES), 16, 1024);
 #pragma unroll
             for (int ks = 0; ks < HD / 16; ++ks)
               mma_ss2(tbase + LY::col_s(w, buf), qa.at((ks / 4) * (128 * 128) + (ks % 4) * 32), qa.hi,
@@ -565,7 +559,7 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, TreeLayout<H
             mma_commit(&s_full[w][buf]);
           }
           mma_commit(&k_empty[st]);
-          st = st + HALVES == LY::KST ? 0 : st + HALVES;
+          if (++st == LY::KST) st = 0;
         }
         if (ok) mma_commit(&q_free[qs]);
       }
@@ -586,41 +580,32 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, TreeLayout<H
 #pragma unroll 1
       for (int j = w.ja; j < w.jb && ok; ++j, ++g) {
         const int buf = g & 1;
-        // a pair's first O is written over the last unit's when both warpgroups have read that
-        if (PAIR && j == w.ja && un > 0) ok = wait_warp(&o_free, (un - 1) & 1, &wctl);
-        uint8_t* vt = smem;
-        int vst = 0;
+        ok = wait_warp(&v_full[st], vp, &wctl);
+        if (ok && j * kKT + kKT > tree0) {
+          ok = wait_warp(&v_fixed[st], fixed >> st & 1, &wctl);
+          fixed ^= 1u << st;
+        }
 #pragma unroll
         for (int i = 0; i < NWG; ++i) {
-          if (PAIR || i == 0) {
-            const int n0 = j * LY::KT + i * kHT;
-            vst = st;
-            vt = smem + LY::OFF_V + st * LY::ST_BYTES;
-            ok = ok && wait_warp(&v_full[st], vp, &wctl);
-            if (!ok) break;
-            if (n0 + kHT > tree0 && n0 < w.len) {
-              ok = wait_warp(&v_fixed[st], fixed >> st & 1, &wctl);
-              if (!ok) break;
-              fixed ^= 1u << st;
-            }
-            if (++st == LY::VST) {
-              st = 0;
-              vp ^= 1;
-            }
-          }
           ok = ok && wait_warp(&p_full[i][buf], (g >> 1) & 1, &wctl);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            const Desc vb = make_desc(smem_u32(vt), 1024, KCH * 1024);  // V, MN-major
+            // V, MN-major
+            const Desc vb =
+                make_desc(smem_u32(smem + LY::OFF_V + st * LY::ST_BYTES), 1024, KCH * 1024);
 #pragma unroll
-            for (int ks = 0; ks < kHT / 16; ++ks)
+            for (int ks = 0; ks < kKT / 16; ++ks)
               mma_ts2(tbase + i * HD, tbase + LY::col_s(i, buf) + ks * 8,
                       vb.at(ks * (2 * KCH * 1024)), vb.hi, id, j > w.ja || ks > 0 ? 1u : 0u);
             mma_commit(&p_done[i][buf]);
-            if (PAIR || i == NWG - 1) mma_commit(&v_empty[vst]);
+            if (i == NWG - 1) mma_commit(&v_empty[st]);
           }
           __syncwarp();
+        }
+        if (++st == LY::VST) {
+          st = 0;
+          vp ^= 1;
         }
       }
     }
@@ -639,21 +624,20 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, TreeLayout<H
 #pragma unroll 1
     for (int un = 0; ok && (ok = take_unit<true>(&units, un, w, end, lane, &wctl)) && !end; ++un) {
       const int slot = un % kUnits, tree0 = w.len - p.T;
-      const int h0 = w.ja * HALVES, h1 = w.jb * HALVES;  // stages
 #pragma unroll 1
-      for (int h = max(h0, max(tree0, 0) / kHT); h < h1 && h * kHT < w.len; ++h) {
-        const int st = (g + h - h0) % LY::VST;
+      for (int j = max(w.ja, max(tree0, 0) / kKT); j < w.jb; ++j) {
+        const int n = g + j - w.ja, st = n % LY::VST;
         ok = wait_warp(&v_tail[st], asked >> st & 1, &wctl) &&
-             wait_warp(&v_full[st], (g + h - h0) / LY::VST & 1, &wctl);
+             wait_warp(&v_full[st], n / LY::VST & 1, &wctl);
         if (!ok) break;
         asked ^= 1u << st;
-        tree_tile<HD>(smem + LY::OFF_V + st * LY::ST_BYTES, h * kHT, tree0, w.len, units.odd[slot],
+        tree_tile<HD>(smem + LY::OFF_V + st * LY::ST_BYTES, j * kKT, tree0, w.len, units.odd[slot],
                       lane);
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&v_fixed[st]);
       }
-      g += h1 - h0;
+      g += w.jb - w.ja;
       if (lane == 0) mbar_arrive(&units.odd_full[slot]);
     }
   } else if (warp == LY::LIST_WARP) {
@@ -691,12 +675,11 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, TreeLayout<H
       if (turn > 0) ok = wait_warp(&q_free[qs], (turn - 1) & 1, &wctl);
       if (!ok) break;
       if (lane == 0) {
-        constexpr int tiles = PAIR ? 1 : NWG;
-        mbar_arrive_expect_tx(&q_full[qs], tiles * LY::Q_BYTES);
-        for (int i = 0; i < tiles * C; ++i)
+        mbar_arrive_expect_tx(&q_full[qs], NWG * LY::Q_BYTES);
+        for (int i = 0; i < NWG * C; ++i)  // row blocks, or copies of one
           for (int c = 0; c < KCH; ++c)
-            tma_load_3d(smem + (NWG == 1 || PAIR ? qs : i) * LY::Q_BYTES +
-                            (C > 1 ? i * LY::RC * 128 : 0) + c * (128 * 128),
+            tma_load_3d(smem + (NWG == 1 ? qs * LY::Q_BYTES + i * LY::RC * 128 : i * LY::Q_BYTES) +
+                            c * (128 * 128),
                         &mQ, &q_full[qs], c * 64, list.rb * LY::ROWS + (C > 1 ? 0 : i * 128),
                         list.b * p.Hk + list.kh);
       }
@@ -725,13 +708,15 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, TreeLayout<H
   } else {
     // ------------------------------------------------------------------ softmax, and O out
     // Rows that are not there have q = 0 and columns that hold anything; warps without any row keep
-    // the barriers going and do nothing else. A wait that runs out ends the warp's tiles; where the
-    // warpgroups meet (PAIR) both leave together.
+    // the barriers going and do nothing else. A wait that runs out ends the warp's tiles; where copies
+    // are joined all warps leave together.
     const int wg = warp >> 2, wl = warp & 3, row = threadIdx.x & 127;
     const uint32_t lanes = tbase + ((uint32_t)(wl * 32) << 16);
     const uint32_t tO = lanes + wg * HD;
-    // copy `copy` of row r: NC of the warpgroup's 64 keys of a tile
-    constexpr int NC = kHT / C;
+    // copy `copy` of row r, with NC of a tile's keys
+    constexpr int NC = LY::NC;
+    // Where registers are few (two CTAs an SM) scores are taken twice, 32 at a time.
+    constexpr bool LEAN = CT == 2 && NC == 64;
     const int copy = C == 1 ? 0 : row / LY::RC, r = row % LY::RC;
     const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
     int g = 0;
@@ -742,55 +727,67 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, TreeLayout<H
       // (those that join meet once for each unit, whatever a warp has come upon: here, or at its end)
       ok = take_unit<false>(&units, un, w, end, lane, &wctl);
       if (!ok || end) {
-        if (JOIN) soft_any<32 * LY::SOFT>(true);
+        if (C > 1) soft_any(true);
         break;
       }
       const int slot = un % kUnits;
-      const int r0 = w.rb * LY::ROWS + (PAIR ? 0 : wg * 128);
+      const int r0 = w.rb * LY::ROWS + wg * 128;
       const bool live = r0 + wl * 32 % LY::RC < p.rows, mine = r0 + r < p.rows;
       const int node = mine ? (r0 + r) % p.T : 0;
       const unsigned* sees = bits + (slot * p.T + node) * p.words;
       // the first key of the tree, counted from this thread's first of tile 0
-      const int tree0 = w.len - p.T - (PAIR ? wg * kHT : 0) - copy * NC;
+      const int tree0 = w.len - p.T - copy * NC;
       float m = -FLT_MAX / 2.0f, l = 0.0f;
 #pragma unroll 1
       for (int j = w.ja; j < w.jb; ++j, ++g) {
-        const int buf = g & 1, first = j * LY::KT - tree0;  // node of this thread's first key
+        const int buf = g & 1, first = j * kKT - tree0;  // node of this thread's first key
         const uint32_t ph = (g >> 1) & 1, at = lanes + LY::col_s(wg, buf);
-        ok = wait_warp(&s_full[PAIR ? 0 : wg][buf], ph, &wctl);
+        ok = wait_warp(&s_full[wg][buf], ph, &wctl);
         // (every warp that is asked for has seen the words that it looks at)
         if (ok && first + NC > 0) ok = wait_warp(&units.bits_full[slot], (un / kUnits) & 1, &wctl);
         if (!ok) break;
         if (live) {
           tc_fence_after();
-          uint32_t s[NC];
+          uint32_t s[LEAN ? 32 : NC];
+          auto scores = [&](int h) {  // 32 of them
+            tmem_ld32(at + copy * NC + h, *reinterpret_cast<uint32_t(*)[32]>(&s[LEAN ? 0 : h]));
+          };
+          auto hide = [&](int h) {
+            if (first + NC <= 0) return;
+            const uint32_t vis = mask_bits(sees, p.words, first + h);
+#pragma unroll
+            for (int e = 0; e < 32 && e < NC; ++e)
+              if (!(vis >> e & 1)) s[(LEAN ? 0 : h) + e] = 0xff800000u;  // -inf
+          };
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
           if constexpr (NC == 16) {
             tmem_ld16(at + copy * NC, s);
-          } else {
+            tmem_wait_ld();
+            hide(0);
 #pragma unroll
-            for (int h = 0; h < NC / 32; ++h)
-              tmem_ld32(at + copy * NC + h * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[h * 32]));
-          }
-          tmem_wait_ld();
-          if (first + NC > 0) {
+            for (int e = 0; e < 16; e += 2)
+              mx[e / 2 & 3] =
+                  fmax3(mx[e / 2 & 3], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+          } else {
+            if (!LEAN) {
+#pragma unroll
+              for (int h = 0; h < NC; h += 32) scores(h);
+              tmem_wait_ld();
+            }
 #pragma unroll
             for (int h = 0; h < NC; h += 32) {
-              const uint32_t vis = mask_bits(sees, p.words, first + h);
+              if (LEAN) {
+                scores(h);
+                tmem_wait_ld();
+              }
+              hide(h);
 #pragma unroll
-              for (int e = 0; e < 32 && e < NC; ++e)
-                if (!(vis >> e & 1)) s[h + e] = 0xff800000u;  // -inf
+              for (int e = 0; e < 32; e += 2) {
+                const uint32_t* x = &s[(LEAN ? 0 : h) + e];
+                mx[e / 2 & 3] = fmax3(mx[e / 2 & 3], __uint_as_float(x[0]), __uint_as_float(x[1]));
+              }
             }
           }
-          float mx[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            mx[k] = __uint_as_float(s[k]);
-#pragma unroll
-            for (int e = 4 + 2 * k; e < NC - 4; e += 8)
-              mx[k] = fmax3(mx[k], __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-          }
-          mx[0] = fmax3(mx[0], __uint_as_float(s[NC - 4]), __uint_as_float(s[NC - 3]));
-          mx[1] = fmax3(mx[1], __uint_as_float(s[NC - 2]), __uint_as_float(s[NC - 1]));
           const float m_new =
               fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2);
           if (j == w.ja) {
@@ -819,10 +816,15 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, TreeLayout<H
           constexpr int PN = NC < 32 ? NC : 32;  // keys whose weights are stored at once
 #pragma unroll
           for (int h = 0; h < NC / PN; ++h) {
+            if (LEAN) {  // (P of a half lies over scores that have been taken)
+              scores(h * PN);
+              tmem_wait_ld();
+              hide(h * PN);
+            }
             uint32_t pk[PN / 2];
 #pragma unroll
             for (int e = 0; e < PN; e += 2) {
-              const uint32_t* x = &s[h * PN + e];
+              const uint32_t* x = &s[(LEAN ? 0 : h * PN) + e];
               float a, b;
               f2_unpack(f2_fma(f2_pack(__uint_as_float(x[0]), __uint_as_float(x[1])), c2, nm), a, b);
               a = ex2(a);
@@ -844,42 +846,28 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, TreeLayout<H
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[wg][buf]);
       }
-      // ---- the unit's end: O of all its tiles, of both warpgroups where they share the rows
-      if (JOIN) {
-        ml_s[un & 1][wg][row] = make_float2(m, l);
-        if (soft_any<32 * LY::SOFT>(!ok)) break;
+      // ---- the unit's end
+      if (C > 1) {
+        ml_s[un & 1][row] = make_float2(m, l);
+        if (soft_any(!ok)) break;
       }
-      if (PAIR) {
-        // (both warpgroups have given their last P; neither's next O can come before o_free)
-        ok = wait_warp(&p_done[wg ^ 1][(g - 1) & 1], ((g - 1) >> 1) & 1, &wctl);
-      }
+      // (with copies a wait that runs out here leaves O undefined, as the status says)
       ok = ok && wait_warp(&p_done[wg][(g - 1) & 1], ((g - 1) >> 1) & 1, &wctl) &&
            wait_warp(&units.odd_full[slot], (un / kUnits) & 1, &wctl);
-      // A wait that has run out here: O is left undefined, as the status says.
-      float f0 = 1.0f, f1 = 0.0f;  // factors of O (this warpgroup's, or the first's) and the second's
-      if (JOIN) {
-        constexpr int N = PAIR ? 2 : C;  // the warpgroups, or the copies
-        const float2* ml = &ml_s[un & 1][0][PAIR ? row : r];
-        constexpr int STEP = PAIR ? 128 : LY::RC;
-        const float mine_m = m, mine_l = l;
+      if (C == 1 && !ok) break;
+      float f = l == 0.0f ? 0.0f : 1.0f;  // O's factor
+      if (C > 1) {
+        const float2* ml = &ml_s[un & 1][r];
+        const float mine_m = m;
 #pragma unroll
-        for (int k = 0; k < N; ++k) m = fmaxf(m, ml[k * STEP].x);
+        for (int k = 0; k < C; ++k) m = fmaxf(m, ml[k * LY::RC].x);
+        f = l == 0.0f ? 0.0f : ex2(mine_m - m);
         l = 0.0f;
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-          const float2 x = ml[k * STEP];
+        for (int k = 0; k < C; ++k) {
+          const float2 x = ml[k * LY::RC];
           if (x.y != 0.0f) l = fmaf(x.y, ex2(x.x - m), l);
         }
-        if (PAIR) {
-          f0 = ml[0].y == 0.0f ? 0.0f : ex2(ml[0].x - m);
-          f1 = ml[STEP].y == 0.0f ? 0.0f : ex2(ml[STEP].x - m);
-        } else {
-          f0 = mine_l == 0.0f ? 0.0f : ex2(mine_m - m);
-        }
-      } else if (!ok) {
-        break;
-      } else if (l == 0.0f) {
-        f0 = 0.0f;
       }
       tc_fence_after();
       bool odd = false;
@@ -887,13 +875,9 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, TreeLayout<H
       for (int k = 0; k < kTreeMax / 32; ++k) odd |= units.odd[slot][k] != 0;
       const size_t unit_row = ((size_t)w.b * p.Hk + w.kh) * p.rows + r0 + r;
       const size_t part = 2 * (size_t)blockIdx.x + (w.first ? 1 : 0);
-      const int prow = (PAIR ? 0 : wg * 128) + r;  // of the unit's rows
+      const int prow = wg * 128 + r;  // of the unit's rows
       float4* o_part = reinterpret_cast<float4*>(p.o_part) + part * (HD / 4) * LY::ROWS + prow;
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      if (w.whole) {
-        f0 *= inv;
-        f1 *= inv;
-      }
+      if (w.whole && l != 0.0f) f *= 1.0f / l;
       // N columns from c on of this thread's row, where they go
       auto out = [&](auto& o, int c) {
         constexpr int N = sizeof(o) / 4;
@@ -914,25 +898,15 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, TreeLayout<H
         }
       };
       if (live) {
-        constexpr int COLS = PAIR ? HD / 2 : HD;
 #pragma unroll 1
-        for (int c = PAIR ? wg * COLS : 0, ce = c + COLS; c < ce; c += 32) {
+        for (int c = 0; c < HD; c += 32) {
+          uint32_t x[32];
+          tmem_ld32(tO + c, x);
+          tmem_wait_ld();
           float o[32];
-          {
-            uint32_t x[32];
-            tmem_ld32((PAIR ? lanes : tO) + c, x);
-            tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e)  // (O of no weight holds anything)
-              o[e] = f0 == 0.0f ? 0.0f : __uint_as_float(x[e]) * f0;
-          }
-          if (PAIR) {
-            uint32_t x[32];
-            tmem_ld32(lanes + HD + c, x);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] += f1 == 0.0f ? 0.0f : __uint_as_float(x[e]) * f1;
-          }
+          for (int e = 0; e < 32; ++e)  // (O of no weight holds anything)
+            o[e] = f == 0.0f ? 0.0f : __uint_as_float(x[e]) * f;
           if constexpr (C == 1) {
             out(o, c);
             __syncwarp();
@@ -959,7 +933,7 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, TreeLayout<H
             out(z, c + copy * N);
           }
         }
-        if (mine && copy == 0 && (!PAIR || wg == 0)) {
+        if (mine && copy == 0) {
           if (!w.whole) {
             p.ml_part[part * 2 * LY::ROWS + prow] = m;
             p.ml_part[(part * 2 + 1) * LY::ROWS + prow] = l;
@@ -970,10 +944,7 @@ __global__ void __launch_bounds__(TreeLayout<HD, PAIR, C>::THREADS, TreeLayout<H
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        if (PAIR) mbar_arrive(&o_free);
-        mbar_arrive(&units.free[slot]);
-      }
+      if (lane == 0) mbar_arrive(&units.free[slot]);
     }
   }
 
@@ -1063,27 +1034,27 @@ __global__ void __launch_bounds__(32 * HD / 8) tree_combine_kernel(const TreeK p
 }
 
 struct TreePlan {
-  int pair, C, ROWS, rb, grid;
+  int C, CT, ROWS, rb, grid;
 };
 TreePlan tree_plan(const TreeArgs& a) {
   TreePlan pl;
   const int rows = a.G * a.T;
   pl.C = a.d > 64 || rows > 64 ? 1 : rows > 32 ? 2 : 4;
-  pl.pair = rows <= 128 && a.d <= 128 && pl.C == 1;
-  pl.ROWS = pl.pair || pl.C > 1 ? 128 / pl.C : a.d <= 128 ? 256 : 128;
+  pl.CT = rows <= 128 && a.d <= 128 ? 2 : 1;
+  pl.ROWS = pl.CT == 2 ? 128 / pl.C : a.d <= 128 ? 256 : 128;
   pl.rb = (rows + pl.ROWS - 1) / pl.ROWS;
   const long long cap = (long long)a.max_pages << a.ps_shift;
-  const long long tiles = ((cap + kHT - 1) / kHT + kUnitCost) * a.B * a.Hk * pl.rb;  // (at most)
-  pl.grid = (int)std::min<long long>(pl.C > 1 ? 304 : 152, tiles);
+  const long long tiles = ((cap + kKT - 1) / kKT + kUnitCost) * a.B * a.Hk * pl.rb;
+  pl.grid = (int)std::min<long long>(152 * pl.CT, tiles);
   return pl;
 }
 
-template <int HD, bool PAIR, int C>
+template <int HD, int C, int CT>
 cudaError_t launch_tree_t(const TreeArgs& a, const TreeMaps& m, const TreePlan& pl, void* ws,
                           cudaStream_t s) {
-  using LY = TreeLayout<HD, PAIR, C>;
+  using LY = TreeLayout<HD, C, CT>;
   static OncePerKey<> smem_attr;
-  auto kern = tree_kernel<HD, PAIR, C>;
+  auto kern = tree_kernel<HD, C, CT>;
   cudaError_t e = set_smem_once(smem_attr, kern, LY::smem_bytes(LY::T_MAX));
   if (e != cudaSuccess) return e;
   TreeK p;
@@ -1106,7 +1077,6 @@ cudaError_t launch_tree_t(const TreeArgs& a, const TreeMaps& m, const TreePlan& 
   p.max_pages = a.max_pages;
   p.num_pages = a.num_pages;
   p.ps_shift = a.ps_shift;
-  p.kt_shift = PAIR ? 7 : 6;
   p.scale_log2 = a.scale * kLog2e;
   p.wait_limit_ns = a.wait_limit_ns;
   profile_mark(kKernTreeAttn, 0, s);
@@ -1124,11 +1094,11 @@ cudaError_t launch_tree_t(const TreeArgs& a, const TreeMaps& m, const TreePlan& 
 }
 }  // namespace
 
-int tree_box_rows(int page_size) { return page_size < kHT ? page_size : kHT; }
+int tree_box_rows(int page_size) { return page_size < kKT ? page_size : kKT; }
 
 long long tree_tiles(const TreeArgs& a) {
   const long long cap = (long long)a.max_pages << a.ps_shift;
-  return ((cap + kHT - 1) / kHT + kUnitCost) * a.B * a.Hk * tree_plan(a).rb;
+  return ((cap + kKT - 1) / kKT + kUnitCost) * a.B * a.Hk * tree_plan(a).rb;
 }
 
 size_t tree_workspace_bytes(const TreeArgs& a) {
@@ -1142,14 +1112,14 @@ cudaError_t launch_tree(const TreeArgs& a, const TreeMaps& m, void* ws, cudaStre
   const TreePlan pl = tree_plan(a);
   switch (a.d) {
     case 64:
-      return pl.pair     ? launch_tree_t<64, true, 1>(a, m, pl, ws, s)
-             : pl.C == 1 ? launch_tree_t<64, false, 1>(a, m, pl, ws, s)
-             : pl.C == 2 ? launch_tree_t<64, false, 2>(a, m, pl, ws, s)
-                         : launch_tree_t<64, false, 4>(a, m, pl, ws, s);
+      return pl.CT == 1  ? launch_tree_t<64, 1, 1>(a, m, pl, ws, s)
+             : pl.C == 1 ? launch_tree_t<64, 1, 2>(a, m, pl, ws, s)
+             : pl.C == 2 ? launch_tree_t<64, 2, 2>(a, m, pl, ws, s)
+                         : launch_tree_t<64, 4, 2>(a, m, pl, ws, s);
     case 128:
-      return pl.pair ? launch_tree_t<128, true, 1>(a, m, pl, ws, s)
-                     : launch_tree_t<128, false, 1>(a, m, pl, ws, s);
-    case 256: return launch_tree_t<256, false, 1>(a, m, pl, ws, s);
+      return pl.CT == 1 ? launch_tree_t<128, 1, 1>(a, m, pl, ws, s)
+                        : launch_tree_t<128, 1, 2>(a, m, pl, ws, s);
+    case 256: return launch_tree_t<256, 1, 1>(a, m, pl, ws, s);
     default: return cudaErrorInvalidValue;
   }
 }
