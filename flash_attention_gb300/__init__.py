@@ -1011,13 +1011,15 @@ def _rotary(inv_freq, positions, batch, rows, interleaved, offset, scale, packed
 _NO_STRIDES = (0, 0, 0)
 
 
-def _rows_like(x, torch):
-    """An output for x [.., heads, rows, d]: contiguous where the rows of a head follow one another
-    in x, else [.., rows, heads, d] in memory."""
-    if x.stride(-2) == x.shape[-1] or x.shape[-2] == 1:
-        return torch.empty_like(x, memory_format=torch.contiguous_format)
-    return torch.empty_like(x.transpose(-3, -2),
-                            memory_format=torch.contiguous_format).transpose(-3, -2)
+def _rows_like(x, strides):
+    """(an output for x [.., heads, rows, d] of these row strides, its own): contiguous where the rows of
+    a head follow one another in x, else [.., rows, heads, d] in memory."""
+    shape = x.shape
+    H, n, d = shape[-3:]
+    st = (n * d, d) if strides[2] == d or n == 1 else (d, H * d)
+    if len(shape) == 3:
+        return x.new_empty_strided(shape, (*st, 1)), (0, *st)
+    return x.new_empty_strided(shape, (H * n * d, *st, 1)), (H * n * d, *st)
 
 
 def _rotate(q, k, inv_freq, back, positions, cu_seqlens, offset, interleaved, scale, out, stream):
@@ -1048,25 +1050,31 @@ def _rotate(q, k, inv_freq, back, positions, cu_seqlens, offset, interleaved, sc
     used = [q, inv_freq]
     used += [t for t in (k, positions, cu_seqlens, *(out or ())) if t is not None]
     handle, ctx = _q8_stream(stream, torch, *used)
+    ko, kos = None, _NO_STRIDES
     if out is not None:
         qo, ko = out
         if qo.shape != shape or (ko is None) != (k is None) or (k is not None
                                                                 and ko.shape != k.shape):
             raise ValueError("out must be two tensors like q and k")
+        qos = _q8_rows(qo, "out[0]", torch)
+        if k is not None:
+            kos = _q8_rows(ko, "out[1]", torch)
     elif ctx is None:
-        qo, ko = _rows_like(q, torch), None if k is None else _rows_like(k, torch)
+        qo, qos = _rows_like(q, qs)
+        if k is not None:
+            ko, kos = _rows_like(k, ks)
     else:
         with ctx:
-            qo, ko = _rows_like(q, torch), None if k is None else _rows_like(k, torch)
-    if q.numel() == 0:
+            qo, qos = _rows_like(q, qs)
+            if k is not None:
+                ko, kos = _rows_like(k, ks)
+    if n == 0 or q.numel() == 0:
         return qo, ko
-    if k is None:
-        kp = kop = Hk = 0
-        kos = _NO_STRIDES
-    else:
-        kp, kop, Hk, kos = k.data_ptr(), ko.data_ptr(), k.shape[-3], _q8_rows(ko, "out[1]", torch)
-    rows = _pack_rotary_rows(q.data_ptr(), kp, qo.data_ptr(), kop, *qs, *ks,
-                             *_q8_rows(qo, "out[0]", torch), *kos, cu, B, shape[-3], Hk, n, d, 0)
+    kp = kop = Hk = 0
+    if k is not None:
+        kp, kop, Hk = k.data_ptr(), ko.data_ptr(), k.shape[-3]
+    rows = _pack_rotary_rows(q.data_ptr(), kp, qo.data_ptr(), kop, *qs, *ks, *qos, *kos, cu, B,
+                             shape[-3], Hk, n, d, 0)
     rc = (_lib or load_library()).fa_rotary_apply(rows, rot, back, handle)
     if rc:
         raise FaError(rc, "fa_rotary_apply")

@@ -1289,12 +1289,15 @@ int fa_paged_tree_attention(const void* q, const void* k_cache, const void* v_ca
     return cuda_fail(cudaErrorInvalidValue, "cuTensorMapEncodeTiled");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   void* ws = nullptr;
-  cudaMemPool_t pool = nullptr;
-  if ((e = scratch_pool(dev, &pool)) != cudaSuccess) return cuda_fail(e, "scratch pool");
-  if ((e = cudaMallocFromPoolAsync(&ws, fa::tree_workspace_bytes(a), pool, s)) != cudaSuccess)
-    return cuda_fail(e, "cudaMallocFromPoolAsync (tree attention workspace)");
+  const size_t ws_bytes = fa::tree_workspace_bytes(a);
+  if (ws_bytes) {
+    cudaMemPool_t pool = nullptr;
+    if ((e = scratch_pool(dev, &pool)) != cudaSuccess) return cuda_fail(e, "scratch pool");
+    if ((e = cudaMallocFromPoolAsync(&ws, ws_bytes, pool, s)) != cudaSuccess)
+      return cuda_fail(e, "cudaMallocFromPoolAsync (tree attention workspace)");
+  }
   e = fa::launch_tree(a, m, ws, s);
-  const cudaError_t e2 = cudaFreeAsync(ws, s);
+  const cudaError_t e2 = ws ? cudaFreeAsync(ws, s) : cudaSuccess;
   if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
   if (e2 != cudaSuccess) return cuda_fail(e2, "cudaFreeAsync (tree attention workspace)");
   return FA_OK;

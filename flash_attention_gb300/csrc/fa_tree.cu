@@ -23,11 +23,13 @@
 //    CTAs of 128 rows, which read keys again: 101 us for 90 for 16 sequences of up to 8k keys). At head_dim 256
 //    tensor memory holds one O: one warpgroup, blocks of 128 rows, one CTA.
 //
-// Work: the (sequence, kv head, row block) units, each with its key tiles, form one list of
-// tiles, cut evenly over persistent CTAs, one on an SM (the lengths are on the device; each CTA finds
+// Work: the (sequence, kv head, row block) units, each ceil(len / 64) key tiles, form one list of
+// tiles, cut evenly over persistent CTAs (the lengths are on the device; each CTA finds
 // its part from them). A unit counts kUnitCost tiles more than it has, what its start and end cost. A
 // CTA writes the units it has whole; of the others it leaves its share's O, m and sum, which a second
-// kernel joins in the order of the keys.
+// kernel joins in the order of the keys. Where the table has room for a few tiles only (kWholeKeys) a
+// unit is its first tile's CTA's, whole: cutting it would cost more than it evens out, and the second
+// kernel and the scratch are saved.
 //
 // Warps: 0-3 (0-7) softmax, then one each for the copies of K pages, of V pages, for S, for O, and for
 // the list: it walks the list two units ahead, loads Q and packs the tree's mask into words. A page's
@@ -53,6 +55,8 @@ constexpr int kKT = 64;          // keys of a tile
 // Tiles' worth of a unit's start and end (16 sequences of up to 8k keys, 256 rows, head_dim 128: 92 us with 3,
 // 85 with 5, 82 with 8; 100 of up to 2k, 17 rows, head_dim 64: 51.0, 51.6, 53.2).
 constexpr int kUnitCost = 5;
+// Room of a table, in keys, up to which units are not cut.
+constexpr int kWholeKeys = 512;
 constexpr int kPageChunk = 128;  // block-table entries staged at a time
 constexpr int kUnits = 3;        // units published
 constexpr float kLog2e = 1.4426950408889634f;
@@ -108,6 +112,7 @@ struct TreeK {
   float* ml_part;  // [2 * grid, 2, ROWS]: m and the sum
   int* status;
   int B, Hk, T, words, rows, rb, max_pages, num_pages, ps_shift;
+  int cut;  // units may be shared by CTAs
   float scale_log2;
   unsigned long long wait_limit_ns;
 };
@@ -188,8 +193,13 @@ struct TreeWalk {
       }
       const unsigned in = t - pre, u = in / (unsigned)cost;
       kh = (int)u;
-      const int from = (int)(in - u * cost), to = min(cost, from + (int)(t1 - t));
+      const int from = (int)(in - u * cost);
+      const int to = p.cut ? min(cost, from + (int)(t1 - t)) : cost;
       t += to - from;
+      if (!p.cut && from > 0) {  // the CTA's before
+        jb = 0;
+        continue;
+      }
       ja = max(0, from - kUnitCost);
       jb = max(0, to - kUnitCost);
     } while (jb == 0);
@@ -617,6 +627,17 @@ __global__ void __launch_bounds__(TreeLayout<HD, C, CT>::THREADS, CT)
   } else if (warp == LY::FIX_WARP) {
     // ------------------------------------------------------------------ V of the tree's keys, as soon
     // as it has landed: what is not finite, and what lies behind the sequence's end
+    if (!p.cut) {  // (else the joining kernel does it) rows of sequences without keys
+#pragma unroll 1
+      for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+        if (tree_len(p, b) > 0) continue;
+        const size_t r0 = (size_t)b * p.Hk * p.rows, n = (size_t)p.Hk * p.rows;
+        for (size_t e = lane; e < n * (HD / 8); e += 32)
+          reinterpret_cast<uint4*>(p.o + r0 * HD)[e] = make_uint4(0u, 0u, 0u, 0u);
+        if (p.lse)
+          for (size_t e = lane; e < n; e += 32) p.lse[r0 + e] = -INFINITY;
+      }
+    }
     int g = 0;
     uint32_t asked = 0;  // phases of v_tail
     TreeUnit w;
@@ -1034,7 +1055,7 @@ __global__ void __launch_bounds__(32 * HD / 8) tree_combine_kernel(const TreeK p
 }
 
 struct TreePlan {
-  int C, CT, ROWS, rb, grid;
+  int C, CT, ROWS, rb, grid, cut;
 };
 TreePlan tree_plan(const TreeArgs& a) {
   TreePlan pl;
@@ -1044,6 +1065,7 @@ TreePlan tree_plan(const TreeArgs& a) {
   pl.ROWS = pl.CT == 2 ? 128 / pl.C : a.d <= 128 ? 256 : 128;
   pl.rb = (rows + pl.ROWS - 1) / pl.ROWS;
   const long long cap = (long long)a.max_pages << a.ps_shift;
+  pl.cut = cap > kWholeKeys;
   const long long tiles = ((cap + kKT - 1) / kKT + kUnitCost) * a.B * a.Hk * pl.rb;
   pl.grid = (int)std::min<long long>(152 * pl.CT, tiles);
   return pl;
@@ -1074,6 +1096,7 @@ cudaError_t launch_tree_t(const TreeArgs& a, const TreeMaps& m, const TreePlan& 
   p.words = (a.T + 31) / 32;
   p.rows = a.G * a.T;
   p.rb = pl.rb;
+  p.cut = pl.cut;
   p.max_pages = a.max_pages;
   p.num_pages = a.num_pages;
   p.ps_shift = a.ps_shift;
@@ -1083,7 +1106,7 @@ cudaError_t launch_tree_t(const TreeArgs& a, const TreeMaps& m, const TreePlan& 
   kern<<<pl.grid, LY::THREADS, LY::smem_bytes(a.T), s>>>(m.q, m.k, m.v, p);
   e = cudaGetLastError();
   profile_mark(kKernTreeAttn, 1, s);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || !pl.cut) return e;
   const int live = std::min(p.rows, LY::ROWS);
   profile_mark(kKernTreeCombine, 0, s);
   e = launch_pdl(tree_combine_kernel<HD, LY::ROWS>,
@@ -1103,7 +1126,7 @@ long long tree_tiles(const TreeArgs& a) {
 
 size_t tree_workspace_bytes(const TreeArgs& a) {
   const TreePlan pl = tree_plan(a);
-  return (size_t)2 * pl.grid * pl.ROWS * (a.d + 2) * 4;
+  return pl.cut ? (size_t)2 * pl.grid * pl.ROWS * (a.d + 2) * 4 : 0;
 }
 
 int tree_q_rows(const TreeArgs& a) { return 128 / tree_plan(a).C; }

@@ -74,6 +74,9 @@ CASES = [
     (3, 8, 1, 4, 64, 8, [200, 4, 131], "any"),
     (2, 4, 2, 31, 64, 32, [900, 129], "any"),
     (2, 1, 1, 64, 64, 16, [64, 192], "trees"),
+    (1, 8, 1, 200, 128, 16, [500], "trees"),
+    (2, 24, 2, 40, 64, 256, [40, 777], "any"),
+    (2, 5, 1, 26, 128, 8, [26, 1300], "any"),
 ]
 
 
@@ -375,3 +378,67 @@ def test_waits_that_run_out_are_reported(d, T):
     got = fa.paged_tree_attention(*args, scale=0.1)
     assert fa.fa_device_status(True) == fa.FA_OK
     check(got, plain.tree_attention(qx, kx, vx, table, lengths, m, 0.1))
+
+
+def test_a_batch_of_thousands():
+    """More sequences than any warp looks at at once, most of them empty or of a few keys."""
+    import torch
+
+    import flash_attention_gb300 as fa
+
+    B, T = 3000, 3
+    rng = np.random.default_rng(12)
+    lengths = np.where(rng.random(B) < 0.5, 0, rng.integers(1, 20, B))
+    lengths[[7, 1500, B - 1]] = [700, 300, 64]
+    per = 44
+    table = np.zeros((B, per), np.int32)
+    used = -(-lengths // 16)
+    pages = rng.permutation(int(used.sum()) + 2)
+    at = 0
+    for b in range(B):
+        table[b, :used[b]] = pages[at:at + used[b]]
+        at += used[b]
+    P = len(pages)
+    (kc, kx), (vc, vx) = (bf16(rng.standard_normal((P, 1, 16, 64))) for _ in range(2))
+    q, qx = bf16(rng.standard_normal((B, 2, T, 64)))
+    m = masks(rng, B, T, "one tree")
+    want = plain.tree_attention(qx, kx, vx, table, lengths, m, 0.125)
+    got = fa.paged_tree_attention(q, kc, vc, ints(table), ints(lengths), torch.from_numpy(m).cuda(),
+                                  scale=0.125)
+    check(got, want)
+    assert fa.fa_device_status(True) == fa.FA_OK
+
+
+def test_masks_of_any_batch_stride_and_alignment():
+    import torch
+
+    import flash_attention_gb300 as fa
+
+    for T in (7, 8, 33, 64):
+        lengths = [300, 70, 200]
+        rng, table, (kc, kx), (vc, vx), (q, qx) = make(T, 3, 2, 1, T, 128, 16, lengths)
+        m = masks(rng, 3, T, "any")
+        want = plain.tree_attention(qx, kx, vx, table, lengths, m, 0.1)
+        for stride, off in ((T * T, 0), (T * T + 3, 1), (2 * T * T, 2)):
+            flat = torch.ones(4 * stride + 8, dtype=torch.uint8, device="cuda")
+            view = flat.as_strided((3, T, T), (stride, T, 1), off)
+            view.copy_(torch.from_numpy(m).cuda())
+            check(fa.paged_tree_attention(q, kc, vc, ints(table), ints(lengths), view, scale=0.1), want)
+
+
+def test_a_captured_call_takes_the_lengths_of_its_replay():
+    import torch
+
+    import flash_attention_gb300 as fa
+
+    rng, table, (kc, kx), (vc, vx), (q, qx) = make(9, 3, 8, 2, 12, 128, 16, [2000, 2000, 2000])
+    m = masks(rng, 3, 12, "trees")
+    lens, mask, tb = ints([100, 2000, 0]), torch.from_numpy(m).cuda(), ints(table)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = fa.paged_tree_attention(q, kc, vc, tb, lens, mask, scale=0.1)
+    for lengths in ([100, 2000, 0], [12, 13, 14], [0, 0, 0], [2000, 5, 1999]):
+        lens.copy_(ints(lengths))
+        graph.replay()
+        check(got, plain.tree_attention(qx, kx, vx, table, lengths, m, 0.1))
+    assert fa.fa_device_status(True) == fa.FA_OK
