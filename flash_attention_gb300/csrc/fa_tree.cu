@@ -55,8 +55,7 @@ constexpr int kKT = 64;          // keys of a tile
 // Tiles' worth of a unit's start and end (16 sequences of up to 8k keys, 256 rows, head_dim 128: 92 us with 3,
 // 85 with 5, 82 with 8; 100 of up to 2k, 17 rows, head_dim 64: 51.0, 51.6, 53.2).
 constexpr int kUnitCost = 5;
-// Room of a table, in keys, up to which units are not cut.
-constexpr int kWholeKeys = 512;
+constexpr int kWholeKeys = 512;  // room of a table up to which units are not cut (see tree_plan)
 constexpr int kPageChunk = 128;  // block-table entries staged at a time
 constexpr int kUnits = 3;        // units published
 constexpr float kLog2e = 1.4426950408889634f;
@@ -1065,7 +1064,10 @@ TreePlan tree_plan(const TreeArgs& a) {
   pl.ROWS = pl.CT == 2 ? 128 / pl.C : a.d <= 128 ? 256 : 128;
   pl.rb = (rows + pl.ROWS - 1) / pl.ROWS;
   const long long cap = (long long)a.max_pages << a.ps_shift;
-  pl.cut = cap > kWholeKeys;
+  // 100 sequences of up to 1000 keys, 48 rows, head_dim 128, 800 units: cut 64 us, whole 60; 20 of them: 21
+  // and 23 us; 100 of up to 2k, 17 rows, head_dim 64: 52 and 54; 100 of up to 500 keys, 100 rows: 67 and 48.
+  const long long units = (long long)a.B * a.Hk * pl.rb;
+  pl.cut = cap > (units >= 152 * pl.CT ? 2 * kWholeKeys : kWholeKeys);
   const long long tiles = ((cap + kKT - 1) / kKT + kUnitCost) * a.B * a.Hk * pl.rb;
   pl.grid = (int)std::min<long long>(152 * pl.CT, tiles);
   return pl;
