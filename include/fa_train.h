@@ -564,7 +564,9 @@ int fa_paged_append(const fa_paged_rows* rows, const fa_rotary* rotary, void* st
  *   lse             output or NULL: f32 [batch, n_heads, q_len]
  *   p               causal and num_splits must be 0, q_len at most FA_TREE_MAX
  * Lengths and table entries out of range as for fa_paged_attention (clamped, read as zeros, reported).
- * Returns FA_OK, FA_ERR_INVALID, FA_ERR_UNSUPPORTED or FA_ERR_CUDA. */
+ * Where the table has room for more than 512 keys the call takes scratch (40 MB at most) from a pool of
+ * the library's own that keeps what is freed. Returns FA_OK, FA_ERR_INVALID, FA_ERR_UNSUPPORTED or
+ * FA_ERR_CUDA. */
 #define FA_TREE_MAX 256
 int fa_paged_tree_attention(const void* q, const void* k_cache, const void* v_cache,
                             const int32_t* block_table, const int32_t* lengths,
