@@ -343,7 +343,8 @@ cudaError_t launch_keep(const KeepArgs& a, cudaStream_t s) {
   p.M = a.M;
   const int cols = 2 * p.Hk * p.d8;
   profile_mark(kKernPagedKeep, 0, s);
-  keep_kernel<<<dim3((unsigned)a.B, (unsigned)((cols + kKeepThreads - 1) / kKeepThreads)), kKeepThreads, 0, s>>>(p);
+  const dim3 grid((unsigned)a.B, (unsigned)((cols + kKeepThreads - 1) / kKeepThreads));
+  keep_kernel<<<grid, kKeepThreads, 0, s>>>(p);
   const cudaError_t e = cudaGetLastError();
   profile_mark(kKernPagedKeep, 1, s);
   return e;

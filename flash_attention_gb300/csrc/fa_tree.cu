@@ -10,18 +10,19 @@
 // for all of them; with 4 d bytes and 4 d flops a row for each key, HBM bounds it up to some 280 rows
 // a kv head. S = Q K^T (M = 128 rows, N = 64 keys) and O += P V, with P in bf16 over S in tensor memory
 // (two buffers); a thread of the softmax has a row; the lazy rescale of the training forward; sums are
-// f32. What has to fit beside the bytes of a tile is a chain of latencies (scores, softmax, weights), so:
+// f32. What has to fit beside the bytes of a tile is a chain of latencies (scores, softmax, weights),
+// so:
 //  * up to 128 rows, head_dim 64 and 128: two CTAs an SM with 128 rows each, which fill each other's
 //    waits and the starts and ends of each other's units. (One CTA with two softmax warpgroups on the
-//    halves of 128-key tiles, an O each, joined at a unit's end, and rings 1.4 times as deep: 132 us for
-//    125 for 16 sequences of up to 16k keys with 128 rows, 350 for 342 for 64 with 48, 61 for 43 at
-//    head_dim 64.)
+//    halves of 128-key tiles, an O each, joined at a unit's end, and rings 1.4 times as deep: 132 us
+//    for 125 for 16 sequences of up to 16k keys with 128 rows, 350 for 342 for 64 with 48, 61 for 43
+//    at head_dim 64.)
 //  * at head_dim 64 with up to 64 (32) rows these are there twice (four times): a copy has a half (a
 //    quarter) of a tile's keys, with a maximum, a sum and an O of its own; four warps share a tile's
 //    exponentials then instead of two or one. They are joined at a unit's end, through shared memory.
-//  * more rows: one CTA, whose two warpgroups have 128 of a block's 256 rows each, on the same keys (two
-//    CTAs of 128 rows, which read keys again: 101 us for 90 for 16 sequences of up to 8k keys). At head_dim 256
-//    tensor memory holds one O: one warpgroup, blocks of 128 rows, one CTA.
+//  * more rows: one CTA, whose two warpgroups have 128 of a block's 256 rows each, on the same keys
+//    (two CTAs of 128 rows, which read keys again: 101 us for 90 for 16 sequences of up to 8k keys).
+//    At head_dim 256 tensor memory holds one O: one warpgroup, blocks of 128 rows, one CTA.
 //
 // Work: the (sequence, kv head, row block) units, each ceil(len / 64) key tiles, form one list of
 // tiles, cut evenly over persistent CTAs (the lengths are on the device; each CTA finds
@@ -34,9 +35,9 @@
 // Warps: 0-3 (0-7) softmax, then one each for the copies of K pages, of V pages, for S, for O, and for
 // the list: it walks the list two units ahead, loads Q and packs the tree's mask into words. A page's
 // part of a tile is one TMA box, min(page_size, 64) rows of all columns: what limits small copies is
-// the number of them a warp can issue (copies alone, 131072 keys of 8 heads, head_dim 128, pages of 16:
-// 4.6 TB/s with a box for each 64 columns, 5.7 with one box, 6.3 with a warp each for K and V; pages of 8:
-// 3.0, 4.2, 5.7). The mask is tested in the tiles of the last T keys alone.
+// the number of them a warp can issue (copies alone, 131072 keys of 8 heads, head_dim 128, pages of
+// 16: 4.6 TB/s with a box for each 64 columns, 5.7 with one box, 6.3 with a warp each for K and V;
+// pages of 8: 3.0, 4.2, 5.7). The mask is tested in the tiles of the last T keys alone.
 // There a value that is not finite must meet no weight of a row that does not see it, not even 0: a
 // last warp looks those tiles over as they land and clears it, and rows that see it get it added at the
 // end (tree_odd).
@@ -52,8 +53,8 @@ namespace fa {
 
 namespace {
 constexpr int kKT = 64;          // keys of a tile
-// Tiles' worth of a unit's start and end (16 sequences of up to 8k keys, 256 rows, head_dim 128: 92 us with 3,
-// 85 with 5, 82 with 8; 100 of up to 2k, 17 rows, head_dim 64: 51.0, 51.6, 53.2).
+// Tiles' worth of a unit's start and end (16 sequences of up to 8k keys, 256 rows, head_dim 128: 92 us
+// with 3, 85 with 5, 82 with 8; 100 of up to 2k, 17 rows, head_dim 64: 51.0, 51.6, 53.2).
 constexpr int kUnitCost = 5;
 constexpr int kWholeKeys = 512;  // room of a table up to which units are not cut (see tree_plan)
 constexpr int kPageChunk = 128;  // block-table entries staged at a time
