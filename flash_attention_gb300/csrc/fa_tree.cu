@@ -107,7 +107,7 @@ struct TreeK {
   const uint8_t* mask;
   long long mask_stride;
   __nv_bfloat16* o;
-  float* lse;
+  float* lse;      // [B, H, T]
   float* o_part;   // [2 * grid, HD / 4, ROWS, 4]: O of a share, in units of 2^m
   float* ml_part;  // [2 * grid, 2, ROWS]: m and the sum
   int* status;
@@ -353,6 +353,70 @@ __device__ __forceinline__ void tree_odd(const TreeK& p, float (&x)[N], const un
   }
 }
 
+// A value before the tree that is not finite has met weights of 0 (those that a copy has of the others'
+// keys, and those that are 0 in 32 bits), which made NaN of it. In what a CTA has written such elements
+// become what the values that are not finite come to: those of the share's keys before the tree, and of
+// its nodes that the row sees. Rows whose sum is NaN (their scores were) stay as they are. Done by all
+// warps, which have 8 columns each (a lane: one, of every fourth key and row), once everything else
+// is. It hardly ever runs, but its place and its size count: 300 sequences of up to 1000 keys, 17 rows,
+// head_dim 64 take 85 us without it and with this; 97 with a call in the softmax's warps or the list's
+// (registers), 89 with a call here, 90 with 8 columns a lane (the kernel's instructions lie farther
+// apart). At head_dim 128 looking for what is not finite costs 1 to 2 %.
+template <int HD, int ROWS, int WARPS>
+__device__ __forceinline__ void tree_mend(const TreeK& p) {
+  const int lane = lane_id();
+  TreeWalk u;
+  u.init(p, blockIdx.x, gridDim.x, lane);
+#pragma unroll 1
+  while (u.next(p)) {
+    const int tree0 = u.len - p.T, k0 = u.ja * kKT, k1 = min(u.jb * kKT, u.len);
+    const size_t part = 2 * (size_t)blockIdx.x + (u.first ? 1 : 0);
+    const size_t row0 = ((size_t)u.b * p.Hk + u.kh) * p.rows + u.rb * ROWS;
+#pragma unroll 1
+    for (int c = warp_id() * 8 + lane % 8; c < HD; c += WARPS * 8) {
+      // a key's value where it is not finite, else 0 (pages outside are zeros)
+      auto value = [&](int key) {
+        const int page = p.table[(size_t)u.b * p.max_pages + (key >> p.ps_shift)];
+        if (page < 0 || page >= p.num_pages) return 0.0f;
+        const int slot = key & ((1 << p.ps_shift) - 1);
+        const float x =
+            __bfloat162float(p.v[((((size_t)page * p.Hk + u.kh) << p.ps_shift) + slot) * HD + c]);
+        return isfinite(x) ? 0.0f : x;
+      };
+      float before = 0.0f;
+      bool known = false;
+#pragma unroll 1
+      for (int r = lane / 8; r - lane / 8 < min(ROWS, p.rows - u.rb * ROWS); r += 4) {
+        const bool mine = u.rb * ROWS + r < p.rows;
+        __nv_bfloat16* const whole = p.o + (row0 + r) * HD + c;
+        float* const share = p.o_part + ((part * (HD / 4) + c / 4) * ROWS + r) * 4 + c % 4;
+        const float o = !mine ? 0.0f : u.whole ? __bfloat162float(*whole) : *share;
+        bool nan = o != o;
+        if (nan) {
+          const float l = u.whole ? p.lse[row0 + r] : p.ml_part[(part * 2 + 1) * ROWS + r];
+          nan = l == l;
+        }
+        if (!__any_sync(0xffffffffu, nan)) continue;
+        if (!known) {  // what the keys before the tree come to, for all rows
+          known = true;
+#pragma unroll 1
+          for (int k = k0 + lane / 8; k < min(k1, tree0); k += 4) before += value(k);
+          before += __shfl_xor_sync(0xffffffffu, before, 8);
+          before += __shfl_xor_sync(0xffffffffu, before, 16);
+        }
+        if (!nan || before == 0.0f) continue;  // (NaN of something else)
+        const uint8_t* sees = p.mask + u.b * p.mask_stride + (size_t)((u.rb * ROWS + r) % p.T) * p.T;
+        float x = before;
+#pragma unroll 1
+        for (int k = max(k0, tree0); k < k1; ++k)
+          if (sees[k - tree0]) x += value(k);
+        if (u.whole) *whole = __float2bfloat16(x);
+        else *share = x;
+      }
+    }
+  }
+}
+
 // The weights of a copy's keys, zeros for the others.
 template <int C>
 __device__ __forceinline__ void store_weights(uint32_t at, const uint32_t (&pk)[32 / C], int copy) {
@@ -410,6 +474,7 @@ __global__ void __launch_bounds__(TreeLayout<HD, C, CT>::THREADS, CT)
   __shared__ uint32_t tmem_base_s;
   __shared__ WaitCtl wctl;
   __shared__ int bad_input;
+  __shared__ int mend_s;  // something that is not finite has been written
   __shared__ int page_s[2][kPageChunk];
   __shared__ float2 ml_s[2][C > 1 ? 128 : 1];  // of a unit (even, odd): m and the sum of each copy's rows
   unsigned* bits = reinterpret_cast<unsigned*>(smem + LY::OFF_BITS);
@@ -417,7 +482,7 @@ __global__ void __launch_bounds__(TreeLayout<HD, C, CT>::THREADS, CT)
   const int warp = warp_id(), lane = lane_id();
   if (threadIdx.x == 0) {
     wait_ctl_init(&wctl, p.wait_limit_ns);
-    bad_input = 0;
+    bad_input = mend_s = 0;
 #pragma unroll 1
     for (int s = 0; s < LY::KST; ++s) {
       mbar_init(&k_full[s], 1);
@@ -634,8 +699,7 @@ __global__ void __launch_bounds__(TreeLayout<HD, C, CT>::THREADS, CT)
         const size_t r0 = (size_t)b * p.Hk * p.rows, n = (size_t)p.Hk * p.rows;
         for (size_t e = lane; e < n * (HD / 8); e += 32)
           reinterpret_cast<uint4*>(p.o + r0 * HD)[e] = make_uint4(0u, 0u, 0u, 0u);
-        if (p.lse)
-          for (size_t e = lane; e < n; e += 32) p.lse[r0 + e] = -INFINITY;
+        for (size_t e = lane; e < n; e += 32) p.lse[r0 + e] = -INFINITY;
       }
     }
     int g = 0;
@@ -876,13 +940,14 @@ __global__ void __launch_bounds__(TreeLayout<HD, C, CT>::THREADS, CT)
       ok = ok && wait_warp(&p_done[wg][(g - 1) & 1], ((g - 1) >> 1) & 1, &wctl) &&
            wait_warp(&units.odd_full[slot], (un / kUnits) & 1, &wctl);
       if (C == 1 && !ok) break;
-      float f = l == 0.0f ? 0.0f : 1.0f;  // O's factor
+      const bool none = l == 0.0f;
+      float f = none ? 0.0f : 1.0f;  // O's factor
       if (C > 1) {
         const float2* ml = &ml_s[un & 1][r];
         const float mine_m = m;
 #pragma unroll
         for (int k = 0; k < C; ++k) m = fmaxf(m, ml[k * LY::RC].x);
-        f = l == 0.0f ? 0.0f : ex2(mine_m - m);
+        f = none ? 0.0f : ex2(mine_m - m);
         l = 0.0f;
 #pragma unroll
         for (int k = 0; k < C; ++k) {
@@ -903,6 +968,12 @@ __global__ void __launch_bounds__(TreeLayout<HD, C, CT>::THREADS, CT)
       auto out = [&](auto& o, int c) {
         constexpr int N = sizeof(o) / 4;
         if (!mine) return;
+        uint64_t test = 0ull;  // (a sum that is NaN is the scores' doing)
+#pragma unroll
+        for (int e = 0; e < N; e += 2) test = f2_fma(f2_pack(o[e], o[e + 1]), 0ull, test);
+        float t0, t1;
+        f2_unpack(test, t0, t1);
+        if (t0 + t1 != 0.0f && l == l) mend_s = 1;
         if (odd) tree_odd<HD>(p, o, units.odd[slot], sees, w, c);
         if (w.whole) {
           __nv_bfloat16* dst = p.o + unit_row * HD + c;
@@ -927,7 +998,7 @@ __global__ void __launch_bounds__(TreeLayout<HD, C, CT>::THREADS, CT)
           float o[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e)  // (O of no weight holds anything)
-            o[e] = f == 0.0f ? 0.0f : __uint_as_float(x[e]) * f;
+            o[e] = none ? 0.0f : __uint_as_float(x[e]) * f;
           if constexpr (C == 1) {
             out(o, c);
             __syncwarp();
@@ -958,7 +1029,7 @@ __global__ void __launch_bounds__(TreeLayout<HD, C, CT>::THREADS, CT)
           if (!w.whole) {
             p.ml_part[part * 2 * LY::ROWS + prow] = m;
             p.ml_part[(part * 2 + 1) * LY::ROWS + prow] = l;
-          } else if (p.lse) {
+          } else {
             p.lse[unit_row] = l == 0.0f ? -INFINITY : fmaf(m, kLn2, logf(l));
           }
         }
@@ -976,6 +1047,7 @@ __global__ void __launch_bounds__(TreeLayout<HD, C, CT>::THREADS, CT)
     report_abort(&wctl, p.status);
     if (bad_input && p.status) atomicCAS(p.status, kStatusOk, kStatusBadInput);
   }
+  if (mend_s && !wctl.abort) tree_mend<HD, LY::ROWS, LY::THREADS / 32>(p);
 }
 
 // Joins the shares of the units that were cut, and writes those of sequences without keys: a thread
@@ -1001,7 +1073,7 @@ __global__ void __launch_bounds__(32 * HD / 8) tree_combine_kernel(const TreeK p
   uint4* dst = reinterpret_cast<uint4*>(p.o + out * HD + warp * 8);
   if (cost == 0 && mine) {
     *dst = make_uint4(0u, 0u, 0u, 0u);
-    if (p.lse && warp == 0) p.lse[out] = -INFINITY;
+    if (warp == 0) p.lse[out] = -INFINITY;
   }
   // (by every CTA: what follows this kernel must find the attention done)
   grid_dep_wait();
@@ -1042,16 +1114,35 @@ __global__ void __launch_bounds__(32 * HD / 8) tree_combine_kernel(const TreeK p
       const float f = ex2(mi[k] - top);
       l = fmaf(li[k], f, l);
       const float* y = &x[k][0].x;
-      if (f != 0.0f) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = fmaf(y[e], f, acc[e]);
+      for (int e = 0; e < 8; ++e) acc[e] = fmaf(y[e], f, acc[e]);
+    }
+  }
+  // (what is not finite and met a factor of 0, as in tree_mend)
+  bool nan = false;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) nan |= acc[e] != acc[e];
+  if (nan && l == l) {
+    float x[8] = {};
+#pragma unroll 1
+    for (int c = c0; c <= c1; ++c) {
+      const size_t s = (size_t)2 * c + (c == c0 ? 1 : 0);
+      if (p.ml_part[(s * 2 + 1) * ROWS + row] == 0.0f) continue;
+      const float* src = p.o_part + ((s * (HD / 4) + warp * 2) * ROWS + row) * 4;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float y = src[e / 4 * ROWS * 4 + e % 4];
+        if (!isfinite(y)) x[e] += y;
       }
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (acc[e] != acc[e] && x[e] != 0.0f) acc[e] = x[e];
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   *dst = make_uint4(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv),
                     pack_bf16(acc[4] * inv, acc[5] * inv), pack_bf16(acc[6] * inv, acc[7] * inv));
-  if (p.lse && warp == 0) p.lse[out] = l == 0.0f ? -INFINITY : fmaf(m, kLn2, logf(l));
+  if (warp == 0) p.lse[out] = l == 0.0f ? -INFINITY : fmaf(m, kLn2, logf(l));
 }
 
 struct TreePlan {
@@ -1074,6 +1165,11 @@ TreePlan tree_plan(const TreeArgs& a) {
   return pl;
 }
 
+// Scratch for the shares' O, m and sums; L of the rows lies behind it where the caller wants none.
+size_t parts_floats(const TreePlan& pl, int d) {
+  return pl.cut ? (size_t)2 * pl.grid * pl.ROWS * (d + 2) : 0;
+}
+
 template <int HD, int C, int CT>
 cudaError_t launch_tree_t(const TreeArgs& a, const TreeMaps& m, const TreePlan& pl, void* ws,
                           cudaStream_t s) {
@@ -1089,9 +1185,9 @@ cudaError_t launch_tree_t(const TreeArgs& a, const TreeMaps& m, const TreePlan& 
   p.mask = a.mask;
   p.mask_stride = a.mask_stride;
   p.o = static_cast<__nv_bfloat16*>(a.o);
-  p.lse = a.lse;
   p.o_part = static_cast<float*>(ws);
   p.ml_part = p.o_part + (size_t)2 * pl.grid * LY::ROWS * HD;
+  p.lse = a.lse ? a.lse : p.o_part + parts_floats(pl, HD);
   p.status = a.status;
   p.B = a.B;
   p.Hk = a.Hk;
@@ -1129,7 +1225,8 @@ long long tree_tiles(const TreeArgs& a) {
 
 size_t tree_workspace_bytes(const TreeArgs& a) {
   const TreePlan pl = tree_plan(a);
-  return pl.cut ? (size_t)2 * pl.grid * pl.ROWS * (a.d + 2) * 4 : 0;
+  const size_t lse = a.lse ? 0 : (size_t)a.B * a.Hk * a.G * a.T;
+  return (parts_floats(pl, a.d) + lse) * 4;
 }
 
 int tree_q_rows(const TreeArgs& a) { return 128 / tree_plan(a).C; }

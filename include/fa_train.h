@@ -556,7 +556,8 @@ int fa_paged_append(const fa_paged_rows* rows, const fa_rotary* rotary, void* st
  * key gives O = 0 and L = -inf. Trees of fewer than q_len nodes stand at the end of the q_len: the
  * columns before them, keys of the sequence, are named for every node, and the rows before them give
  * what nobody reads. What hidden keys and values hold (NaN and infinities included) reaches no row that
- * does not see them.
+ * does not see them; a row that sees a value that is not finite has it added as it is, whatever its
+ * weight (a call whose NaN or infinities reach a row takes up to some milliseconds more).
  *   q, o            bf16 [batch, n_heads, q_len, head_dim] (device, 16-byte aligned)
  *   k_cache, v_cache, block_table, lengths: as for fa_paged_attention
  *   tree_mask       uint8 [q_len, q_len] for each sequence (device), contiguous, mask_stride bytes apart
@@ -564,8 +565,8 @@ int fa_paged_append(const fa_paged_rows* rows, const fa_rotary* rotary, void* st
  *   lse             output or NULL: f32 [batch, n_heads, q_len]
  *   p               causal and num_splits must be 0, q_len at most FA_TREE_MAX
  * Lengths and table entries out of range as for fa_paged_attention (clamped, read as zeros, reported).
- * Where the table has room for more than 512 keys the call takes scratch (40 MB at most) from a pool of
- * the library's own that keeps what is freed. Returns FA_OK, FA_ERR_INVALID, FA_ERR_UNSUPPORTED or
+ * Where the table has room for more than 512 keys the call takes scratch (40 MB at most; without lse 4
+ * bytes a row more, for any table) from a pool of the library's own that keeps what is freed. Returns FA_OK, FA_ERR_INVALID, FA_ERR_UNSUPPORTED or
  * FA_ERR_CUDA. */
 #define FA_TREE_MAX 256
 int fa_paged_tree_attention(const void* q, const void* k_cache, const void* v_cache,
