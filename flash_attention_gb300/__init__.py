@@ -1090,7 +1090,8 @@ def rotary_fwd(q, k, inv_freq, *, positions=None, cu_seqlens=None, offset=0, int
     row from rotary_dim on stay. Positions: int32 [B, n] or [n] (packed: [total]); without them, that
     of row i is i + offset, in a packed batch with cu_seqlens (int32 [B + 1]) counted from each
     sequence's first row. Pairs are i and i + rotary_dim / 2, or neighbours (interleaved); `scale`
-    multiplies what turns. `out`: a pair of tensors, q and k themselves for turning in place. New
+    multiplies what turns. `out`: a pair of tensors, q and k themselves for turning in place, views of
+    one tensor (a fused projection's, or its gradient's) too as long as their rows are apart. New
     outputs are contiguous, or [.., rows, heads, d] in memory where the inputs are laid out like that.
     Rows behind cu_seqlens[B] are left as they were. With `stream`, the inputs have to stay as they
     are until that stream has done the call, and new outputs belong to it."""

@@ -1006,6 +1006,15 @@ static bool row_extent(const void* base, const int64_t* st, int64_t batch, int64
   return true;
 }
 
+// Whether rows [B, heads, n, d] of two such tensors share memory.
+static bool rows_share(const void* a, const int64_t* sa, int ha, const Extent& ea, const void* b,
+                       const int64_t* sb, int hb, const Extent& eb, int64_t B, int64_t n, int d) {
+  if (!ea.meets(eb)) return false;
+  const int64_t offset = (reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a)) / 2;
+  return fa::boxes_meet({{B, ha, n}, {sa[0], sa[1], sa[2]}}, {{B, hb, n}, {sb[0], sb[1], sb[2]}},
+                        offset, d);
+}
+
 // Whether no two rows of such a tensor share memory: from the smallest stride on, each dimension's
 // step passes all that the ones before it span.
 static bool rows_nest(const int64_t* st, int64_t batch, int64_t heads, int64_t rows, int d) {
@@ -1108,8 +1117,10 @@ int fa_rotary_apply(const fa_rotary_rows* r, const fa_rotary* rotary, int back, 
       bool same = i == j && src[i] == dst[i];  // in place: every element stays where it is
       const int64_t ext[3] = {B, heads[i], n};
       for (int k = 0; k < 3; ++k) same = same && (ext[k] == 1 || ss[i][k] == ds[i][k]);
-      if (!same && out[i].meets(in[j])) return FA_ERR_INVALID;
-      if (i != j && out[i].meets(out[j])) return FA_ERR_INVALID;
+      if (!same && rows_share(dst[i], ds[i], heads[i], out[i], src[j], ss[j], heads[j], in[j], B, n, d))
+        return FA_ERR_INVALID;
+      if (i < j && rows_share(dst[i], ds[i], heads[i], out[i], dst[j], ds[j], heads[j], out[j], B, n, d))
+        return FA_ERR_INVALID;
     }
   }
   fa::RowsArgs a = {};

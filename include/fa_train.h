@@ -499,11 +499,14 @@ typedef struct fa_rotary_rows {
 
 /* Turns the rows (back = 0), or turns them back by the same angles with the same scale (back = 1): the
  * gradients of q and k from those of the turned ones. Outputs may be their inputs (same pointer and
- * strides); otherwise they must not share memory with any input, and rows of outputs must not lie on
- * one another (looked for as ranges of addresses and by nesting strides: FA_ERR_INVALID). Rows of a
- * packed batch behind cu_seqlens[batch] are left as they were; offsets that decrease or pass `rows`
- * make fa_device_status return FA_ERR_BAD_INPUT (then rows may be left out, or have another place).
- * Returns FA_OK, FA_ERR_INVALID, FA_ERR_UNSUPPORTED or FA_ERR_CUDA. */
+ * strides); otherwise their rows must share no memory with a row of an input, nor with one another's:
+ * FA_ERR_INVALID. Views of one tensor (q and k of a fused projection, turned in place) are looked at row
+ * by row, so that they may lie between one another. (An output's own strides have to nest: each passes
+ * all that the smaller ones span. Views whose strides are so unlike that the search for a common
+ * element takes more than some thousand steps count as sharing one.) Rows of a packed batch behind
+ * cu_seqlens[batch] are left as they were; offsets that decrease or pass `rows` make fa_device_status
+ * return FA_ERR_BAD_INPUT (then rows may be left out, or have another place). Returns FA_OK,
+ * FA_ERR_INVALID, FA_ERR_UNSUPPORTED or FA_ERR_CUDA. */
 int fa_rotary_apply(const fa_rotary_rows* rows, const fa_rotary* rotary, int back, void* stream);
 
 /* ------------------------------------------------------------------ appending to the paged cache
@@ -566,8 +569,8 @@ int fa_paged_append(const fa_paged_rows* rows, const fa_rotary* rotary, void* st
  *   p               causal and num_splits must be 0, q_len at most FA_TREE_MAX
  * Lengths and table entries out of range as for fa_paged_attention (clamped, read as zeros, reported).
  * Where the table has room for more than 512 keys the call takes scratch (40 MB at most; without lse 4
- * bytes a row more, for any table) from a pool of the library's own that keeps what is freed. Returns FA_OK, FA_ERR_INVALID, FA_ERR_UNSUPPORTED or
- * FA_ERR_CUDA. */
+ * bytes a row more, for any table) from a pool of the library's own that keeps what is freed. Returns
+ * FA_OK, FA_ERR_INVALID, FA_ERR_UNSUPPORTED or FA_ERR_CUDA. */
 #define FA_TREE_MAX 256
 int fa_paged_tree_attention(const void* q, const void* k_cache, const void* v_cache,
                             const int32_t* block_table, const int32_t* lengths,
