@@ -566,7 +566,10 @@ int fa_paged_append(const fa_paged_rows* rows, const fa_rotary* rotary, void* st
  *   tree_mask       uint8 [q_len, q_len] for each sequence (device), contiguous, mask_stride bytes apart
  *                   (0: one tree for all; otherwise >= 0)
  *   lse             output or NULL: f32 [batch, n_heads, q_len]
- *   p               causal and num_splits must be 0, q_len at most FA_TREE_MAX
+ *   p               causal and num_splits must be 0, q_len at most FA_TREE_MAX; the key tiles that the
+ *                   table has room for, batch * n_kv_heads * row blocks * (ceil(max_pages * page_size
+ *                   / 64) + 5), must be below 2^30, whatever the lengths. (Row blocks: of 256 rows, at
+ *                   head_dim 256 of 128, of a kv head's n_heads / n_kv_heads * q_len.)
  * Lengths and table entries out of range as for fa_paged_attention (clamped, read as zeros, reported).
  * Where the table has room for more than 512 keys the call takes scratch (40 MB at most; without lse 4
  * bytes a row more, for any table) from a pool of the library's own that keeps what is freed. Returns
