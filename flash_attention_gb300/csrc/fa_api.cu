@@ -1150,6 +1150,15 @@ static int check_cache(const void* k_cache, const void* v_cache, const int32_t* 
   return rc ? rc : check_bf16(v_cache);
 }
 
+// What the two caches span; whether they are apart.
+static bool cache_extents(const void* k_cache, const void* v_cache, int num_pages, int n_kv_heads,
+                          int page_size, int d, Extent* k, Extent* v) {
+  const int64_t rows = (int64_t)n_kv_heads * page_size;
+  const int64_t flat[3] = {0, rows * d, d};
+  return row_extent(k_cache, flat, 1, num_pages, rows, d, k) &&
+         row_extent(v_cache, flat, 1, num_pages, rows, d, v) && !k->meets(*v);
+}
+
 int fa_paged_append(const fa_paged_rows* r, const fa_rotary* rotary, void* stream) {
   if (!r) return FA_ERR_INVALID;
   const int d = r->head_dim;
@@ -1178,10 +1187,7 @@ int fa_paged_append(const fa_paged_rows* r, const fa_rotary* rotary, void* strea
   const int64_t q_out_stride[3] = {(int64_t)r->n_heads * n * d, n * d, d};
   // what is written shares no memory with what is read
   Extent kc, vc;
-  const int64_t cache_rows = (int64_t)r->n_kv_heads * r->page_size;
-  const int64_t flat[3] = {0, cache_rows * d, d};
-  if (!row_extent(r->k_cache, flat, 1, r->num_pages, cache_rows, d, &kc) ||
-      !row_extent(r->v_cache, flat, 1, r->num_pages, cache_rows, d, &vc) || kc.meets(vc) ||
+  if (!cache_extents(r->k_cache, r->v_cache, r->num_pages, r->n_kv_heads, r->page_size, d, &kc, &vc) ||
       kc.meets(k) || kc.meets(v) || vc.meets(k) || vc.meets(v))
     return FA_ERR_INVALID;
   if (r->q) {
@@ -1227,6 +1233,11 @@ int fa_paged_keep(const fa_paged_kept* r, void* stream) {
     return Extent{lo, lo + 4 * (uintptr_t)n};
   };
   const Extent out = ints(r->new_lengths, r->batch);
+  Extent kc, vc;  // (rows of the one would be moved while the other's are read)
+  if (!cache_extents(r->k_cache, r->v_cache, r->num_pages, r->n_kv_heads, r->page_size, r->head_dim,
+                     &kc, &vc) ||
+      out.meets(kc) || out.meets(vc))
+    return FA_ERR_INVALID;
   if (out.meets(ints(r->lengths, r->batch)) || out.meets(ints(r->counts, r->batch)) ||
       out.meets(ints(r->keep, (int64_t)r->batch * r->max_keep)) ||
       out.meets(ints(r->block_table, (int64_t)r->batch * r->max_pages)))

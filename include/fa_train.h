@@ -588,12 +588,12 @@ int fa_paged_tree_attention(const void* q, const void* k_cache, const void* v_ca
  * slots hold anything afterwards. Pages that are moved in must belong to one sequence of the call. */
 typedef struct fa_paged_kept {
   void* k_cache;              /* bf16 [num_pages, n_kv_heads, page_size, head_dim], 16-byte aligned */
-  void* v_cache;              /* same */
+  void* v_cache;              /* same (shares no memory with k_cache) */
   const int32_t* block_table; /* int32 [batch, max_pages] on the device, 4-byte aligned */
   const int32_t* lengths;     /* int32 [batch] on the device, 4-byte aligned */
   const int32_t* keep;        /* int32 [batch, max_keep] on the device, 4-byte aligned */
   const int32_t* counts;      /* int32 [batch] on the device: 0 .. max_keep */
-  int32_t* new_lengths;       /* output, int32 [batch] on the device; not one of the inputs */
+  int32_t* new_lengths;       /* output, int32 [batch] on the device; shares no memory with the others */
   int32_t batch;              /* >= 1 */
   int32_t n_kv_heads;         /* >= 1; num_pages * n_kv_heads < 2^30 */
   int32_t head_dim;           /* 64, 128 or 256 */

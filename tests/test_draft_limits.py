@@ -26,4 +26,3 @@ def test_room_of_the_table(lib, head_dim, heads, nodes):
                        num_pages=64, **ROOM)
             rc = lib.fa_paged_tree_attention(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 0, FAKE, None, p, None)
             assert (rc != fa.FA_ERR_INVALID) == good, (batch, kv)
-
