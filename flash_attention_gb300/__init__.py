@@ -1068,7 +1068,7 @@ def _rotate(q, k, inv_freq, back, positions, cu_seqlens, offset, interleaved, sc
             qo, qos = _rows_like(q, qs)
             if k is not None:
                 ko, kos = _rows_like(k, ks)
-    if n == 0 or q.numel() == 0:
+    if n == 0 or shape[0] == 0 and not packed:
         return qo, ko
     kp = kop = Hk = 0
     if k is not None:

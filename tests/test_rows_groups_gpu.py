@@ -68,3 +68,19 @@ def test_appending(case):
                                   (40, 64, 32, 5, 3, [5, 64, 100])], ids=str)
 def test_keeping(case):
     rows.test_keep_moves_the_accepted_rows(case)
+
+
+def test_no_rows_and_no_heads():
+    """Nothing to turn gives empty outputs; keys without queries are refused, not left unturned."""
+    import torch
+
+    import flash_attention_gb300 as fa
+
+    f, _ = fa.rotary_inv_freq(64)
+    x = torch.ones(2, 4, 6, 64, dtype=torch.bfloat16, device="cuda")
+    for q, k in ((x[:, :, :0], x[:, :2, :0]), (x[:0], x[:0, :2]), (x[0, :, :0], None)):
+        qo, ko = fa.rotary_fwd(q, k, f)
+        assert qo.shape == q.shape and (k is None or ko.shape == k.shape)
+    for q, k in ((x[:, :0], x), (x[0, :0], x[0]), (x[:, :0], None)):
+        with pytest.raises(fa.FaError):
+            fa.rotary_fwd(q, k, f)
