@@ -938,12 +938,14 @@ def rotary_inv_freq(rotary_dim, base=10000.0, *, factor=1.0, method=None, origin
     inv_freq float64 [rotary_dim // 2], base ** (-2 i / rotary_dim) radians a position, stretched for
     contexts `factor` times as long by `method`:
       None      not at all (factor must be 1)
-      "linear"  all of them divided by factor
+      "linear"  all of them divided by factor (position interpolation)
       "base"    base * factor ** (rotary_dim / (rotary_dim - 2)) for base: the slowest frequency is
-                divided by factor, the fastest stays
+                divided by factor, the fastest stays (known as NTK-aware scaling)
       "parts"   those that turn less than beta_slow times in original_len positions divided by factor,
                 those that turn more than beta_fast times as they are, a linear mixture by i between;
-                the scale becomes 0.1 ln(factor) + 1
+                the scale becomes 0.1 ln(factor) + 1 (YaRN; Peng et al. 2023, "YaRN: Efficient Context
+                Window Extension of Large Language Models", with the mixture over i in place of over
+                the turns, between whole numbers from 0 to rotary_dim - 1, as models are trained)
     A setup step: computed in 64 bits on the host, once."""
     import math
 
@@ -972,6 +974,8 @@ def rotary_inv_freq(rotary_dim, base=10000.0, *, factor=1.0, method=None, origin
         def pair_of(turns):  # the pair that turns so many times in original_len positions
             return n * math.log(original_len / (2 * math.pi * turns)) / (2 * math.log(base))
 
+        # Within 0 .. n - 1, though the pairs end at n / 2 - 1: the mixture's slope, and with it what
+        # models were trained with, depends on where it ends. 1e-3 makes a step of low = high.
         low = max(math.floor(pair_of(beta_fast)), 0)
         high = min(math.ceil(pair_of(beta_slow)), n - 1)
         slow = ((i - low) / max(high - low, 1e-3)).clamp(0, 1)

@@ -8,8 +8,9 @@
 // becomes turns per position in units of 2^-64, and p times that, in 64-bit integers that wrap, is
 // the fraction of a turn, at most p + 1 units off for |inv_freq| <= 1: 2^-32 of a turn at the last
 // 32-bit position. (An angle held in 32 bits is 2^-5 of a radian off at position 10^6.) Its upper 32
-// bits go to the hardware's sine and cosine, which are good to 2^-21 within pi: 2^-12 of what a bf16
-// is rounded by.
+// bits become radians in f32, whatever the position: below 2^-24.3 of a turn off by their rounding, the
+// constant's and the product's, 2^-21.6 of a radian. The hardware's sine and cosine of them are good to
+// 2^-21 within pi. Together that is 2^-12 of what a bf16 is rounded by.
 #pragma once
 
 #include <cuda_bf16.h>

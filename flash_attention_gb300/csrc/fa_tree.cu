@@ -8,10 +8,13 @@
 //
 // The G query heads of a kv head and the T nodes are rows of one product, so that a key is read once
 // for all of them; with 4 d bytes and 4 d flops a row for each key, HBM bounds it up to some 280 rows
-// a kv head. S = Q K^T (M = 128 rows, N = 64 keys) and O += P V, with P in bf16 over S in tensor memory
-// (two buffers); a thread of the softmax has a row; the lazy rescale of the training forward; sums are
-// f32. What has to fit beside the bytes of a tile is a chain of latencies (scores, softmax, weights),
-// so:
+// a kv head. S = Q K^T (M = 128 rows, N = 64 keys) and O += P V, with P over S in tensor memory (two
+// buffers); a thread of the softmax has a row; the lazy rescale of the training forward. Scores, maxima,
+// sums and O are f32. P is rounded to bf16, the type that the product takes beside V's; its sum is of
+// what was not rounded. (As in the training forward. O is off by 0.0021 to 0.0023, root mean square
+// relative to its formula in 64 bits; by 0.0017, its own rounding, were P exact, which would take a
+// second product for what the rounding leaves.) What has to fit beside the bytes of a tile is a chain of
+// latencies (scores, softmax, weights), so:
 //  * up to 128 rows, head_dim 64 and 128: two CTAs an SM with 128 rows each, which fill each other's
 //    waits and the starts and ends of each other's units. (One CTA with two softmax warpgroups on the
 //    halves of 128-key tiles, an O each, joined at a unit's end, and rings 1.4 times as deep: 132 us
@@ -33,14 +36,16 @@
 // kernel and the scratch are saved.
 //
 // Warps: 0-3 (0-7) softmax, then one each for the copies of K pages, of V pages, for S, for O, and for
-// the list: it walks the list two units ahead, loads Q and packs the tree's mask into words. A page's
+// the list: it walks the list ahead of the others (two units where two Q are held, else one), loads Q
+// and packs the tree's mask into words. A page's
 // part of a tile is one TMA box, min(page_size, 64) rows of all columns: what limits small copies is
 // the number of them a warp can issue (copies alone, 131072 keys of 8 heads, head_dim 128, pages of
 // 16: 4.6 TB/s with a box for each 64 columns, 5.7 with one box, 6.3 with a warp each for K and V;
 // pages of 8: 3.0, 4.2, 5.7). The mask is tested in the tiles of the last T keys alone.
 // There a value that is not finite must meet no weight of a row that does not see it, not even 0: a
 // last warp looks those tiles over as they land and clears it, and rows that see it get it added at the
-// end (tree_odd).
+// end (tree_odd). What every row sees, the values before the tree, is put right when all is done
+// (tree_mend).
 #include <float.h>
 
 #include <algorithm>

@@ -457,7 +457,8 @@ int fa_q8_paged_attention(const void* q, const fa_q8_cache* cache, const int32_t
  *   y1 = scale * (x1 cos a - x2 sin a),  y2 = scale * (x1 sin a + x2 cos a)
  * and the elements from rotary_dim on stay as they are. Pair i is the elements i and
  * i + rotary_dim / 2, or 2 i and 2 i + 1 (interleaved). The angle is that of the 64-bit inv_freq for
- * any 32-bit position, less than 2^-30 of a turn off for |inv_freq| <= 1 (2^k times that below 2^k).
+ * any 32-bit position: as a fraction of a turn it is less than 2^-30 off for |inv_freq| <= 1 (2^k times
+ * that below 2^k), and becomes radians in 32 bits, less than 2^-24 of a turn off.
  * Stretched contexts are other frequencies and a scale. A frequency that is not finite makes its pairs
  * NaN. */
 typedef struct fa_rotary {
