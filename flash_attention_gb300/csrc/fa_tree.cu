@@ -37,11 +37,11 @@
 //
 // Warps: 0-3 (0-7) softmax, then one each for the copies of K pages, of V pages, for S, for O, and for
 // the list: it walks the list ahead of the others (two units where two Q are held, else one), loads Q
-// and packs the tree's mask into words. A page's
-// part of a tile is one TMA box, min(page_size, 64) rows of all columns: what limits small copies is
-// the number of them a warp can issue (copies alone, 131072 keys of 8 heads, head_dim 128, pages of
-// 16: 4.6 TB/s with a box for each 64 columns, 5.7 with one box, 6.3 with a warp each for K and V;
-// pages of 8: 3.0, 4.2, 5.7). The mask is tested in the tiles of the last T keys alone.
+// and packs the tree's mask into words. A page's part of a tile is one TMA box, min(page_size, 64) rows
+// of all columns: what limits small copies is the number of them a warp can issue (copies alone, 131072
+// keys of 8 heads, head_dim 128, pages of 16: 4.6 TB/s with a box for each 64 columns, 5.7 with one
+// box, 6.3 with a warp each for K and V; pages of 8: 3.0, 4.2, 5.7). The mask is tested in the tiles of
+// the last T keys alone.
 // There a value that is not finite must meet no weight of a row that does not see it, not even 0: a
 // last warp looks those tiles over as they land and clears it, and rows that see it get it added at the
 // end (tree_odd). What every row sees, the values before the tree, is put right when all is done
